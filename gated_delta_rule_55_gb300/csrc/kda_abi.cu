@@ -29,6 +29,12 @@ int check_device() {
   return ok ? KDA_OK : KDA_ERR_DEVICE;
 }
 
+}  // namespace
+
+int kda::check_current_device() { return check_device(); }
+
+namespace {
+
 // Head dimensions and the query scale (scale <= 0 selects dk^-0.5).
 int check_dims_scale(float* scale, int dk, int dv) {
   if (!head_dim_ok(dk) || !head_dim_ok(dv)) return KDA_ERR_HEAD_DIM;
@@ -683,6 +689,9 @@ const char* kda_status_string(int status) {
     case KDA_ERR_TOO_LARGE: return "problem too large for the kernels' index limits";
     case KDA_ERR_WORKSPACE: return "workspace NULL, smaller than required or not 256-byte aligned";
     case KDA_ERR_FLAGS: return "unknown bits in the flags argument";
+    case KDA_ERR_PAGE_SIZE: return "page_size must be 16, 32, 64 or 128";
+    case KDA_ERR_ROTARY: return "the rotated part must be a multiple of 16 from 0 to the head dim";
+    case KDA_ERR_STRIDE: return "a token stride is shorter than a token or not a multiple of 16 bytes";
     default: return "unknown kda status";
   }
 }

@@ -76,7 +76,75 @@ struct DecodeArgs {
   int B, H, dk, dv;
 };
 
+// Serving form of the kernel_delta_attention call (kda_attention_step).
+struct StepArgs {
+  const void* q;               // [rows, Hk, dk], token stride q_stride elements
+  const void* k;               // [rows, Hk, dk]
+  const void* v;               // [rows, Hv, dv]
+  long long q_stride, k_stride, v_stride;
+  const float* beta;           // [rows, Hv]
+  const float* decay;          // [rows, Hv] or NULL
+  float* state;                // [num_slots, Hv, dk, dv]
+  const int32_t* slots;        // [N]
+  const int32_t* out_slots;    // [N] or NULL (in place)
+  const int32_t* cu_seqlens;   // [N + 1] or NULL (T tokens per request)
+  void* out;                   // [rows, Hv, dv]
+  float scale;
+  int N, T, Hk, Hv, dk, dv, num_slots;
+  int no_l2norm, literal;
+};
+
+// Head norms with rotation (kda_qk_norm_rope_*).
+struct NormRopeArgs {
+  const void* q;               // [T, Hq, D], token stride q_stride elements
+  const void* k;               // [T, Hkv, D]
+  const void* v;               // [T, Hkv, D] (append)
+  long long q_stride, k_stride, v_stride;
+  const float* q_weight;       // [D] or NULL
+  const float* k_weight;
+  const float* cos_table;      // [max_position, R / 2]
+  const float* sin_table;
+  const int32_t* positions;    // [T]
+  const int64_t* slots;        // [T] (append), NULL otherwise
+  void* q_out;                 // [T, Hq, D]
+  void* k_out;                 // [T, Hkv, D]
+  void* k_cache;               // [num_pages, Hkv, page_size, D] (append)
+  void* v_cache;
+  const void* dq_out;          // [T, Hq, D] (backward)
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float eps;
+  int T, Hq, Hkv, D, R, max_position, interleaved, num_pages, page_size;
+};
+
+// Attention over a paged cache (kda_paged_attention_fwd).
+struct PagedArgs {
+  const void* q;               // [total_T, Hq, D], token stride q_stride elements
+  long long q_stride;
+  const void* k_cache;         // [num_pages, Hkv, page_size, D]
+  const void* v_cache;
+  const int32_t* block_table;  // [N, max_pages]
+  const int32_t* cu_seqlens;   // [N + 1]
+  const int32_t* kv_lens;      // [N]
+  void* out;                   // [total_T, Hq, D]
+  float* lse;                  // [total_T, Hq] or NULL
+  float scale;
+  int N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages, window, sinks;
+};
+
+// KDA_OK, or KDA_ERR_DEVICE when the current device cannot run the library's kernels.
+int check_current_device();
+
 // Launchers (return cudaGetLastError() of their launch).
+cudaError_t launch_step(const StepArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t stream);
+size_t norm_rope_bwd_workspace(int D);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* d_q_weight, float* d_k_weight,
+                                 void* workspace, bool bf16, cudaStream_t stream);
+size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D);
+cudaError_t launch_paged_simt(const PagedArgs& a, bool bf16, void* workspace,
+                              cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 unsigned int decode_read_error(bool reset);
 cudaError_t launch_chunk_simt(const ChunkArgs& a, bool bf16, cudaStream_t stream);

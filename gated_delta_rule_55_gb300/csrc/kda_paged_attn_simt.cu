@@ -1,0 +1,252 @@
+// Attention of new tokens over a paged cache (kda_paged_attention_fwd), the fp32-accurate
+// kernel: fp32 inputs, and bf16 with head dim 32.  bf16 with head dim 64 or 128 runs on the
+// tensor cores (kda_paged_attn.cu).
+//
+// A block takes 16 query rows (tokens x query heads of one kv head) of one sequence and one
+// part of its visible keys, and keeps for every row the running maximum m, the sum l of
+// e^{s - m} and the unnormalised output, so the keys are read once.  Keys are taken 32 at a
+// time into shared memory: a lane scores one key against the warp's four rows, and then owns
+// D / 32 output columns of those rows.  Bound by the FMA pipes for chunks and by HBM latency
+// for single tokens, so a long key range is cut into parts (for few rows) whose (m, l, o) are
+// joined by a second kernel.
+#include "kda_paged.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 16;    // query rows of a block
+constexpr int kRW = 4;       // rows of a warp
+constexpr int kKeys = 32;    // keys of a step
+constexpr int kThreads = 128;
+constexpr int kMaxParts = 32;
+constexpr int kMinPartKeys = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
+                                                              float* part_o, float2* part_ml) {
+  constexpr int PK = D + 4;    // K pitch: 16-byte rows, lanes on different banks
+  constexpr int C = D / 32;    // output columns of a lane
+  __shared__ __align__(16) float sK[kKeys * PK];
+  __shared__ __align__(16) float sV[kKeys * D];
+  __shared__ __align__(16) float sQ[kRows * D];
+  __shared__ int s_find[4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  const int hkv = blockIdx.y, part = blockIdx.z;
+  int n, tile;
+  if (!find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile)) return;
+  const Seq q = load_seq(a, n);
+  const int rows = q.len * G, r0 = tile * kRows;
+  const int nr = min(kRows, rows - r0);
+  const KeyRange kr = key_range(a, q, r0 / G, (r0 + nr - 1) / G);
+  const int total = kr.sinks + kr.hi - kr.lo;
+  int np = min(parts, (total + kMinPartKeys - 1) / kMinPartKeys);
+  np = max(np, 1);
+  const int per = (total + np - 1) / np;
+  const int v0 = min(part * per, total), v1 = part < np ? min(v0 + per, total) : v0;
+
+  for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = i % (D / 4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nr) {
+      const long long tok = q.bos + (r0 + r) / G;
+      const T* p = static_cast<const T*>(a.q) + tok * a.q_stride +
+                   (long long)(hkv * G + (r0 + r) % G) * D + c;
+      x = make_float4(load_as_float(p), load_as_float(p + 1), load_as_float(p + 2),
+                      load_as_float(p + 3));
+    }
+    const float sc = a.scale * 1.4426950408889634f;  // scores in log2 units
+    *reinterpret_cast<float4*>(&sQ[r * D + c]) =
+        make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+  }
+
+  float m[kRW], l[kRW], o[kRW][C];
+  int pos[kRW];
+#pragma unroll
+  for (int r = 0; r < kRW; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+    const int rr = warp * kRW + r;
+    pos[r] = rr < nr ? q.pos0 + (r0 + rr) / G : -1;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+  }
+  const bool busy = warp * kRW < nr;
+  for (int vb = v0; vb < v1; vb += kKeys) {
+    __syncthreads();
+    // 16-byte pieces of the step's K and V rows; places behind the part's end hold zeros
+    constexpr int VE = 16 / sizeof(T), PIECES = D / VE;
+    for (int i = tid; i < kKeys * PIECES; i += kThreads) {
+      const int key_i = i / PIECES, c = i % PIECES * VE;
+      float kx[VE], vx[VE];
+#pragma unroll
+      for (int e = 0; e < VE; ++e) kx[e] = vx[e] = 0.f;
+      if (vb + key_i < v1) {
+        const int key = virtual_key(kr, vb + key_i);
+        const long long off = cache_row(a, n, hkv, key) * D + c;
+        load_piece(static_cast<const T*>(a.k_cache) + off, kx);
+        load_piece(static_cast<const T*>(a.v_cache) + off, vx);
+      }
+#pragma unroll
+      for (int e = 0; e < VE; e += 4) {
+        *reinterpret_cast<float4*>(&sK[key_i * PK + c + e]) =
+            make_float4(kx[e], kx[e + 1], kx[e + 2], kx[e + 3]);
+        *reinterpret_cast<float4*>(&sV[key_i * D + c + e]) =
+            make_float4(vx[e], vx[e + 1], vx[e + 2], vx[e + 3]);
+      }
+    }
+    __syncthreads();
+    if (!busy) continue;
+    float s[kRW];
+#pragma unroll
+    for (int r = 0; r < kRW; ++r) s[r] = 0.f;
+#pragma unroll 8
+    for (int c = 0; c < D; c += 4) {
+      const float4 kx = *reinterpret_cast<const float4*>(&sK[lane * PK + c]);
+#pragma unroll
+      for (int r = 0; r < kRW; ++r) {
+        const float4 qx = *reinterpret_cast<const float4*>(&sQ[(warp * kRW + r) * D + c]);
+        s[r] += qx.x * kx.x + qx.y * kx.y + qx.z * kx.z + qx.w * kx.w;
+      }
+    }
+    const bool in = vb + lane < v1;
+    const int key = in ? virtual_key(kr, vb + lane) : 0;
+    float p[kRW];
+#pragma unroll
+    for (int r = 0; r < kRW; ++r) {
+      const bool see = in && visible(a, pos[r], key);
+      const float x = see ? s[r] : -INFINITY;
+      float mx = x;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, mx, w);
+        mx = (y > mx || y != y) ? y : mx;  // a NaN score stays
+      }
+      const float mn = (mx > m[r] || mx != mx) ? mx : m[r];
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[r] - base);
+      p[r] = see ? exp2f(x - base) : 0.f;
+      m[r] = mn;
+      l[r] = l[r] * f + p[r];  // the lane's own share; joined at the end
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[r][c] *= f;
+    }
+    const int steps = min(kKeys, v1 - vb);
+    for (int j = 0; j < steps; ++j) {
+      float vx[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) vx[c] = sV[j * D + c * 32 + lane];
+#pragma unroll
+      for (int r = 0; r < kRW; ++r) {
+        const float pj = __shfl_sync(0xffffffffu, p[r], j);
+        if (pj != 0.f) {  // a hidden key's value never counts, whatever it holds
+#pragma unroll
+          for (int c = 0; c < C; ++c) o[r][c] += pj * vx[c];
+        }
+      }
+    }
+  }
+  if (!busy) return;
+#pragma unroll
+  for (int r = 0; r < kRW; ++r) {
+    const float lt = warp_sum(l[r]);
+    const int rr = warp * kRW + r;
+    if (rr >= nr) continue;
+    const long long tok = q.bos + (r0 + rr) / G;
+    const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
+    if (parts > 1) {
+      const long long at = (long long)part * a.total_T * a.Hq + row;
+#pragma unroll
+      for (int c = 0; c < C; ++c) part_o[at * D + c * 32 + lane] = o[r][c];
+      if (lane == 0) part_ml[at] = make_float2(m[r], lt);
+    } else {
+      const float inv = lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        store_from_float(static_cast<T*>(a.out) + row * D + c * 32 + lane, o[r][c] * inv);
+      if (lane == 0 && a.lse)
+        a.lse[row] = lt == 0.f ? -INFINITY : (m[r] + log2f(lt)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// One warp per query row: o = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i over the parts.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int parts,
+                                                              const float* part_o,
+                                                              const float2* part_ml) {
+  constexpr int C = D / 32;
+  const long long rows = (long long)a.total_T * a.Hq;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows || !token_owned(a, row / a.Hq)) return;
+  float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const long long at = (long long)i * rows + row;
+    const float2 ml = part_ml[at];
+    if (ml.y == 0.f) continue;  // a part with nothing to see
+    const float mn = (ml.x > m || ml.x != ml.x) ? ml.x : m;
+    const float f = exp2f(m - mn), g = exp2f(ml.x - mn);
+    m = mn;
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = o[c] * f + part_o[at * D + c * 32 + lane] * g;
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    store_from_float(static_cast<T*>(a.out) + row * D + c * 32 + lane, o[c] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Parts of the key range: enough blocks for four on each SM when there are few rows.
+int simt_parts(int N, int total_T, int Hq, int Hkv) {
+  const long long G = Hq / Hkv;
+  long long tiles = (total_T * G + kRows - 1) / kRows;
+  const long long seqs = N < total_T ? N : total_T;
+  if (tiles < seqs) tiles = seqs;
+  if (tiles <= 0) return 1;
+  const long long p = 152 * 4 / (tiles * Hkv);
+  return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
+  const int parts = simt_parts(a.N, a.total_T, a.Hq, a.Hkv);
+  const long long rows = (long long)a.total_T * a.Hq;
+  float* po = static_cast<float*>(workspace);
+  float2* pml = reinterpret_cast<float2*>(po + (parts > 1 ? parts * rows * D : 0));
+  const long long G = a.Hq / a.Hkv;
+  const long long tiles = (a.total_T * G + kRows - 1) / kRows + a.N;  // upper bound
+  const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)parts);
+  paged_simt_kernel<T, D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
+  if (parts > 1)
+    paged_simt_join_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, parts, po, pml);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D) {
+  const int parts = simt_parts(N, total_T, Hq, Hkv);
+  return parts > 1 ? (size_t)parts * total_T * Hq * (D + 2) * sizeof(float) : 0;
+}
+
+cudaError_t launch_paged_simt(const PagedArgs& a, bool bf16, void* workspace, cudaStream_t st) {
+  switch (a.D) {
+    case 32:
+      return bf16 ? launch_t<__nv_bfloat16, 32>(a, workspace, st)
+                  : launch_t<float, 32>(a, workspace, st);
+    case 64:
+      return bf16 ? launch_t<__nv_bfloat16, 64>(a, workspace, st)
+                  : launch_t<float, 64>(a, workspace, st);
+    default:
+      return bf16 ? launch_t<__nv_bfloat16, 128>(a, workspace, st)
+                  : launch_t<float, 128>(a, workspace, st);
+  }
+}
+
+}  // namespace kda

@@ -21,6 +21,7 @@ STATUS_NAMES = {
     -4: "KDA_ERR_CHUNK", -5: "KDA_ERR_LOWER_BOUND", -6: "KDA_ERR_MISALIGNED",
     -7: "KDA_ERR_DTYPE", -8: "KDA_ERR_LAUNCH", -9: "KDA_ERR_DEVICE", -10: "KDA_ERR_SCALE",
     -11: "KDA_ERR_TOO_LARGE", -12: "KDA_ERR_WORKSPACE", -13: "KDA_ERR_FLAGS",
+    -14: "KDA_ERR_PAGE_SIZE", -15: "KDA_ERR_ROTARY", -16: "KDA_ERR_STRIDE",
 }
 # Exported symbols, in declaration order of include/kda.h.
 EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_fwd_workspace_size",
@@ -31,12 +32,16 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_fwd_workspace_siz
            "kda_chunk_fwd_train", "kda_chunk_bwd_saved", "kda_recurrent_attention_fwd", "kda_attention_fwd",
            "kda_attention_fwd_ws", "kda_attention_fwd_workspace_size",
            "kda_recurrent_attention_fwd_ws", "kda_recurrent_attention_fwd_workspace_size",
-           "kda_decode_step",
+           "kda_decode_step", "kda_attention_step", "kda_qk_norm_rope_fwd",
+           "kda_qk_norm_rope_append", "kda_qk_norm_rope_bwd_workspace_size",
+           "kda_qk_norm_rope_bwd", "kda_paged_attention_fwd_workspace_size",
+           "kda_paged_attention_fwd",
            "kda_status_string",
            "kda_version", "kda_device_error", "kda_selftest_bounded_wait")
 KDA_ATTN_NO_QK_L2NORM = 1
 KDA_ATTN_RECURRENT = 2
 KDA_ATTN_ORDER_LITERAL = 4
+KDA_ROPE_INTERLEAVED = 1
 
 
 class KDAError(RuntimeError):
@@ -51,6 +56,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_LL = ctypes.c_longlong
 
 
 def lib(path: str | None = None) -> ctypes.CDLL:
@@ -97,6 +103,17 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.kda_attention_fwd_workspace_size.restype = _Z
     L.kda_decode_step.argtypes = [_P, _P, _P, _P, _P, _P, _P, _F, _F, _P, _P,
                                   _I, _I, _I, _I, _P]
+    L.kda_attention_step.argtypes = ([_P] * 10 + [_F] + [_I] * 7 + [_LL] * 3 + [_I, _I, _P])
+    L.kda_qk_norm_rope_fwd.argtypes = ([_P] * 9 + [_F] + [_I] * 6 + [_LL] * 2 + [_I, _I, _P])
+    L.kda_qk_norm_rope_append.argtypes = ([_P] * 12 + [_F] + [_I] * 8 + [_LL] * 3 +
+                                          [_I, _I, _P])
+    L.kda_qk_norm_rope_bwd_workspace_size.argtypes = [_I] * 4
+    L.kda_qk_norm_rope_bwd_workspace_size.restype = _Z
+    L.kda_qk_norm_rope_bwd.argtypes = ([_P] * 13 + [_F] + [_I] * 6 + [_LL] * 2 +
+                                       [_I, _I, _P, _Z, _P])
+    L.kda_paged_attention_fwd_workspace_size.argtypes = [_I] * 6
+    L.kda_paged_attention_fwd_workspace_size.restype = _Z
+    L.kda_paged_attention_fwd.argtypes = ([_P] * 8 + [_F] + [_I] * 10 + [_LL, _I, _P, _Z, _P])
     L.kda_device_error.argtypes = [_I]
     L.kda_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, _P]
     L.kda_selftest_bounded_wait.restype = _I
@@ -106,7 +123,9 @@ def lib(path: str | None = None) -> ctypes.CDLL:
               "kda_chunk_fwd_train_varlen", "kda_chunk_bwd_saved_varlen",
               "kda_attention_fwd", "kda_attention_fwd_ws", "kda_recurrent_attention_fwd",
               "kda_recurrent_attention_fwd_ws",
-              "kda_decode_step", "kda_version", "kda_device_error"):
+              "kda_decode_step", "kda_attention_step", "kda_qk_norm_rope_fwd",
+              "kda_qk_norm_rope_append", "kda_qk_norm_rope_bwd", "kda_paged_attention_fwd",
+              "kda_version", "kda_device_error"):
         getattr(L, f).restype = _I
     L.kda_status_string.argtypes = [_I]
     L.kda_status_string.restype = ctypes.c_char_p
@@ -421,3 +440,151 @@ def kda_decode_step(q, k, v, g, beta_logits, a_log, dt_bias, scale, lower_bound,
     _check("kda_decode_step", lib().kda_decode_step(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta_logits), _ptr(a_log), _ptr(dt_bias),
         float(scale), float(lower_bound), _ptr(out), _ptr(S), B, H, dk, dv, _stream(stream)))
+
+
+def _dev(x, dtype, what):
+    """Address of a dense tensor of the given type on the current device (None and raw
+    addresses pass as they are)."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} must be a tensor of the current CUDA device")
+    if x.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return x.data_ptr()
+
+
+def _rows(x, dtype, heads, dim, what):
+    """(address, token stride in elements) of a [tokens, heads, dim] argument: a raw address is
+    taken as dense, a tensor may have any distance between its tokens."""
+    if x is None or isinstance(x, int):
+        return x, heads * dim
+    import torch
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} must be a tensor of the current CUDA device")
+    if x.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{what} must have shape [tokens, {heads}, {dim}], not "
+                         f"{list(x.shape)}")
+    st = x.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise ValueError(f"the heads of {what} must be dense")
+    return x.data_ptr(), st[0] if x.shape[0] > 1 else heads * dim
+
+
+def _elem(x, dtype):
+    """(kda dtype, torch dtype) of a call whose first tensor is x."""
+    import torch
+    code = _dtype_code(x, dtype)
+    return code, torch.float32 if code == KDA_F32 else torch.bfloat16
+
+
+def kda_attention_step(query, key, value, beta, decay, state, slots, out, N, T, Hk, Hv, dk, dv,
+                       num_slots, out_slots=None, cu_seqlens=None, softmax_scale=None,
+                       use_qk_l2norm=True, order="decay_first", dtype=None, stream=None):
+    """A few new tokens of N requests against a pool of states (see include/kda.h): T tokens per
+    request, or T packed tokens in all with ``cu_seqlens``."""
+    import torch
+    code, el = _elem(query, dtype)
+    f32, i32 = torch.float32, torch.int32
+    qp, qs = _rows(query, el, Hk, dk, "query")
+    kp, ks = _rows(key, el, Hk, dk, "key")
+    vp, vs = _rows(value, el, Hv, dv, "value")
+    _check("kda_attention_step", lib().kda_attention_step(
+        qp, kp, vp, _dev(beta, f32, "beta"), _dev(decay, f32, "decay"),
+        _dev(state, f32, "state"), _dev(slots, i32, "slots"), _dev(out_slots, i32, "out_slots"),
+        _dev(cu_seqlens, i32, "cu_seqlens"), _dev(out, el, "out"), float(softmax_scale or 0.0),
+        N, T, Hk, Hv, dk, dv, num_slots, qs, ks, vs, _attn_flags(use_qk_l2norm, True, order),
+        code, _stream(stream)))
+
+
+def kda_qk_norm_rope_fwd(query, key, query_weight, key_weight, cos_table, sin_table, positions,
+                         query_out, key_out, T, Hq, Hkv, D, R, max_position, eps=1e-6,
+                         interleaved=False, dtype=None, stream=None):
+    """RMS norm of every query and key head and the position rotation (see include/kda.h)."""
+    import torch
+    code, el = _elem(query, dtype)
+    f32 = torch.float32
+    qp, qs = _rows(query, el, Hq, D, "query")
+    kp, ks = _rows(key, el, Hkv, D, "key")
+    _check("kda_qk_norm_rope_fwd", lib().kda_qk_norm_rope_fwd(
+        qp, kp, _dev(query_weight, f32, "query_weight"), _dev(key_weight, f32, "key_weight"),
+        _dev(cos_table, f32, "cos_table"), _dev(sin_table, f32, "sin_table"),
+        _dev(positions, torch.int32, "positions"), _dev(query_out, el, "query_out"),
+        _dev(key_out, el, "key_out"), float(eps), T, Hq, Hkv, D, R, max_position, qs, ks,
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, _stream(stream)))
+
+
+def kda_qk_norm_rope_append(query, key, value, query_weight, key_weight, cos_table, sin_table,
+                            positions, slots, query_out, k_cache, v_cache, T, Hq, Hkv, D, R,
+                            max_position, num_pages, page_size, eps=1e-6, interleaved=False,
+                            dtype=None, stream=None):
+    """kda_qk_norm_rope_fwd with keys and values written into cache pages (see
+    include/kda.h)."""
+    import torch
+    code, el = _elem(query, dtype)
+    f32 = torch.float32
+    qp, qs = _rows(query, el, Hq, D, "query")
+    kp, ks = _rows(key, el, Hkv, D, "key")
+    vp, vs = _rows(value, el, Hkv, D, "value")
+    _check("kda_qk_norm_rope_append", lib().kda_qk_norm_rope_append(
+        qp, kp, vp, _dev(query_weight, f32, "query_weight"),
+        _dev(key_weight, f32, "key_weight"), _dev(cos_table, f32, "cos_table"),
+        _dev(sin_table, f32, "sin_table"), _dev(positions, torch.int32, "positions"),
+        _dev(slots, torch.int64, "slots"), _dev(query_out, el, "query_out"),
+        _dev(k_cache, el, "k_cache"), _dev(v_cache, el, "v_cache"), float(eps), T, Hq, Hkv, D, R,
+        max_position, num_pages, page_size, qs, ks, vs,
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, _stream(stream)))
+
+
+def kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D) -> int:
+    """Bytes of workspace kda_qk_norm_rope_bwd needs."""
+    return int(lib().kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D))
+
+
+def kda_qk_norm_rope_bwd(query, key, query_weight, key_weight, cos_table, sin_table, positions,
+                         d_query_out, d_key_out, d_query, d_key, d_query_weight, d_key_weight, T,
+                         Hq, Hkv, D, R, max_position, eps=1e-6, interleaved=False, dtype=None,
+                         workspace=None, stream=None):
+    """Gradients of kda_qk_norm_rope_fwd (see include/kda.h)."""
+    import torch
+    code, el = _elem(query, dtype)
+    f32 = torch.float32
+    qp, qs = _rows(query, el, Hq, D, "query")
+    kp, ks = _rows(key, el, Hkv, D, "key")
+    wp, wb = _ws(workspace)
+    _check("kda_qk_norm_rope_bwd", lib().kda_qk_norm_rope_bwd(
+        qp, kp, _dev(query_weight, f32, "query_weight"), _dev(key_weight, f32, "key_weight"),
+        _dev(cos_table, f32, "cos_table"), _dev(sin_table, f32, "sin_table"),
+        _dev(positions, torch.int32, "positions"), _dev(d_query_out, el, "d_query_out"),
+        _dev(d_key_out, el, "d_key_out"), _dev(d_query, el, "d_query"),
+        _dev(d_key, el, "d_key"), _dev(d_query_weight, f32, "d_query_weight"),
+        _dev(d_key_weight, f32, "d_key_weight"), float(eps), T, Hq, Hkv, D, R, max_position, qs,
+        ks, KDA_ROPE_INTERLEAVED if interleaved else 0, code, wp, wb, _stream(stream)))
+
+
+def kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype=KDA_BF16) -> int:
+    """Bytes of workspace kda_paged_attention_fwd needs (0: none; see include/kda.h)."""
+    return int(lib().kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype))
+
+
+def kda_paged_attention_fwd(query, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, N,
+                            total_T, Hq, Hkv, D, num_pages, page_size, max_pages, lse=None,
+                            softmax_scale=None, window=0, sinks=0, dtype=None, workspace=None,
+                            stream=None):
+    """Attention of new tokens over a paged cache (see include/kda.h)."""
+    import torch
+    code, el = _elem(query, dtype)
+    i32 = torch.int32
+    qp, qs = _rows(query, el, Hq, D, "query")
+    wp, wb = _ws(workspace)
+    _check("kda_paged_attention_fwd", lib().kda_paged_attention_fwd(
+        qp, _dev(k_cache, el, "k_cache"), _dev(v_cache, el, "v_cache"),
+        _dev(block_table, i32, "block_table"), _dev(cu_seqlens, i32, "cu_seqlens"),
+        _dev(kv_lens, i32, "kv_lens"), _dev(out, el, "out"), _dev(lse, torch.float32, "lse"),
+        float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
+        window, sinks, qs, code, wp, wb, _stream(stream)))

@@ -66,7 +66,10 @@ enum kda_status {
   KDA_ERR_SCALE = -10,          /* scale is NaN or infinite */
   KDA_ERR_TOO_LARGE = -11,      /* an index would overflow the kernels' 64-bit limits */
   KDA_ERR_WORKSPACE = -12,      /* workspace NULL, too small or not 256-byte aligned */
-  KDA_ERR_FLAGS = -13           /* unknown bits in a flags argument */
+  KDA_ERR_FLAGS = -13,          /* unknown bits in a flags argument */
+  KDA_ERR_PAGE_SIZE = -14,      /* page_size not in {16, 32, 64, 128} */
+  KDA_ERR_ROTARY = -15,         /* rotated part not a multiple of 16 in [0, D] */
+  KDA_ERR_STRIDE = -16          /* token stride below a token's size or not 16-byte aligned */
 };
 
 /*
@@ -443,6 +446,163 @@ int kda_decode_step(const float* q, const float* k, const float* v, const float*
                     const float* beta_logits, const float* a_log, const float* dt_bias,
                     float scale, float lower_bound, float* out, float* S, int B, int H,
                     int dk, int dv, kda_stream_t stream);
+
+/*
+ * kda_attention_step -- the kda_attention_fwd recurrence for serving: a few new tokens for each
+ *   of N requests (one of a decode step, a handful of drafted ones) against a pool of states
+ *   (kernel_delta_attention page, "The core recurrence", initial_state / return_state; the
+ *   page's decode form is the token-generation call of kda_tkg).  With d = e^{decay}:
+ *       k^ = k / sqrt(|k|^2 + 1e-6),  q^ = scale q / sqrt(|q|^2 + 1e-6)
+ *       S' = d S,  u = beta (v - S'^T k^),  S = S' + k^ u^T,  o = S^T q^
+ *
+ *   query, key   [rows, Hk, dk]  dtype (fp32 or bf16); tokens query_stride / key_stride
+ *                                elements apart (views of a projection's rows need no copy)
+ *   value        [rows, Hv, dv]  dtype, value_stride; Hv a multiple of Hk: value head h reads
+ *                                query / key head h / (Hv / Hk)
+ *   beta         [rows, Hv]      fp32, the rate itself
+ *   decay        [rows, Hv]      fp32 log-decay; NULL = no decay
+ *   state        [num_slots, Hv, dk, dv] fp32, the pool
+ *   slots        [N] int32 DEVICE: request n's state.  A request whose slot lies outside
+ *                [0, num_slots) is skipped: its rows of out are left as they were.
+ *   out_slots    [N] int32 DEVICE or NULL: where the advanced state goes (NULL: back in
+ *                place; outside [0, num_slots): nowhere, as when drafts are only verified).  A
+ *                slot that one request writes must not be read or written by another of the
+ *                same call (the result would depend on their order; there is no fault).
+ *   cu_seqlens   [N + 1] int32 DEVICE token offsets, entries clamped into [0, T] (T then is
+ *                the row count; rows behind the last request are left as they were), or NULL
+ *                for T tokens per request.  A request without tokens keeps its state (copied
+ *                when out_slots says so).
+ *   out          [rows, Hv, dv]  dtype, dense
+ *   softmax_scale  multiplies q; <= 0 selects dk^-0.5
+ *   flags        KDA_ATTN_NO_QK_L2NORM and KDA_ATTN_ORDER_LITERAL as in kda_attention_fwd
+ *   dk, dv in {32, 64, 128}.  Strides are in elements: at least a token's size and a multiple
+ *   of 16 bytes (KDA_ERR_STRIDE).  Tokens run one after the other: long prompts belong to
+ *   kda_attention_fwd_ws.
+ */
+int kda_attention_step(const void* query, const void* key, const void* value, const float* beta,
+                       const float* decay, float* state, const int32_t* slots,
+                       const int32_t* out_slots, const int32_t* cu_seqlens, void* out,
+                       float softmax_scale, int N, int T, int Hk, int Hv, int dk, int dv,
+                       int num_slots, long long query_stride, long long key_stride,
+                       long long value_stride, int flags, int dtype, kda_stream_t stream);
+
+/* Options of the kda_qk_norm_rope calls (bitwise OR). */
+enum kda_rope_flags {
+  KDA_ROPE_INTERLEAVED = 1  /* rotate the pairs (2i, 2i + 1); default (i, i + R / 2) */
+};
+
+/*
+ * kda_qk_norm_rope_fwd -- RMS norm of every query and key head and the rotation by the token's
+ *   position, in one pass (what the softmax layers between delta-rule layers, and the recurrent
+ *   page's call with rotated queries and keys, take as input).  Per head row x [D]:
+ *       n = x / sqrt(mean(x^2) + eps) * weight
+ *       (y_a, y_b) = (n_a cos - n_b sin, n_a sin + n_b cos) for the pairs (a, b) of the first R
+ *       elements, y = n behind them.
+ *
+ *   query        [T, Hq, D]  dtype (fp32 or bf16), tokens query_stride elements apart
+ *   key          [T, Hkv, D] dtype, key_stride
+ *   query_weight, key_weight [D] fp32 or NULL (ones)
+ *   cos_table, sin_table     [max_position, R / 2] fp32: row p holds the cosines and sines of
+ *                position p's angles (the caller's frequencies, in the precision it wants);
+ *                may be NULL when R = 0
+ *   positions    [T] int32 DEVICE, clamped into [0, max_position); NULL allowed when R = 0
+ *   query_out    [T, Hq, D], key_out [T, Hkv, D]  dtype, dense.  May be the inputs themselves
+ *                when those are dense.
+ *   R            rotated elements of a head: a multiple of 16 from 0 (no rotation) to D
+ *                (KDA_ERR_ROTARY)
+ *   eps > 0 and finite (KDA_ERR_SCALE).  D in {32, 64, 128}.  Norms are computed in fp32 and
+ *   results rounded once.
+ */
+int kda_qk_norm_rope_fwd(const void* query, const void* key, const float* query_weight,
+                         const float* key_weight, const float* cos_table,
+                         const float* sin_table, const int32_t* positions, void* query_out,
+                         void* key_out, float eps, int T, int Hq, int Hkv, int D, int R,
+                         int max_position, long long query_stride, long long key_stride,
+                         int flags, int dtype, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope_append -- the same for serving: keys go, normed and rotated, and values as
+ *   they are, into the pages that kda_paged_attention_fwd reads.
+ *
+ *   value        [T, Hkv, D] dtype, value_stride
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] dtype; page_size in {16, 32, 64, 128}
+ *   slots        [T] int64 DEVICE: page * page_size + offset of the token.  A token whose slot
+ *                lies outside [0, num_pages * page_size) is not kept (its query is still
+ *                written).  Two tokens of a call must not name the same slot (which of them
+ *                stays would depend on their order; there is no fault).
+ */
+int kda_qk_norm_rope_append(const void* query, const void* key, const void* value,
+                            const float* query_weight, const float* key_weight,
+                            const float* cos_table, const float* sin_table,
+                            const int32_t* positions, const int64_t* slots, void* query_out,
+                            void* k_cache, void* v_cache, float eps, int T, int Hq, int Hkv,
+                            int D, int R, int max_position, int num_pages, int page_size,
+                            long long query_stride, long long key_stride,
+                            long long value_stride, int flags, int dtype, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope_bwd -- gradients of kda_qk_norm_rope_fwd.  With g the output gradient turned
+ *   back and r = 1 / sqrt(mean(x^2) + eps): d_weight = sum over tokens and heads of g x r and
+ *   dx = r (g w - x r^2 mean(g w x)).
+ *
+ *   d_query_out [T, Hq, D], d_key_out [T, Hkv, D]  dtype, dense: the output gradients
+ *   d_query, d_key                                  dtype, dense, written (may be d_query_out /
+ *                                                   d_key_out themselves)
+ *   d_query_weight, d_key_weight [D] fp32, written; NULL when not wanted
+ *   workspace    at least kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D) bytes, 256-byte
+ *                aligned.  Sums are taken in a fixed order: two calls give the same bits.
+ */
+size_t kda_qk_norm_rope_bwd_workspace_size(int T, int Hq, int Hkv, int D);
+int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_weight,
+                         const float* key_weight, const float* cos_table,
+                         const float* sin_table, const int32_t* positions,
+                         const void* d_query_out, const void* d_key_out, void* d_query,
+                         void* d_key, float* d_query_weight, float* d_key_weight, float eps,
+                         int T, int Hq, int Hkv, int D, int R, int max_position,
+                         long long query_stride, long long key_stride, int flags, int dtype,
+                         void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_paged_attention_fwd -- softmax attention of a chunk of new tokens (or one token) of each
+ *   of N sequences over a paged cache that already holds their keys and values (the softmax
+ *   layers of a stack that alternates them with the recurrent ones; ejkernel "attention" page,
+ *   query / key / value, softmax_scale, sliding_window).  Token i of sequence n has position
+ *   kv_lens[n] - (its new tokens) + i and sees the keys up to that position; with window > 0 only
+ *   the last `window` of them and the first `sinks`:
+ *       o = sum_j softmax_j(scale q . k_j) v_j
+ *
+ *   query        [total_T, Hq, D]  dtype (fp32 or bf16), tokens query_stride elements apart
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] dtype; page_size in {16, 32, 64, 128};
+ *                query head h reads kv head h / (Hq / Hkv)
+ *   block_table  [N, max_pages] int32 DEVICE: page of keys [i page_size, (i + 1) page_size).
+ *                Entries behind a sequence's last page are not read; others are clamped into
+ *                the cache.
+ *   cu_seqlens   [N + 1] int32 DEVICE offsets of the new tokens, clamped into [0, total_T].
+ *                Rows of out and lse behind the last sequence are left as they were.
+ *   kv_lens      [N] int32 DEVICE keys of each sequence, the new tokens' included, clamped into
+ *                [0, max_pages page_size]
+ *   out          [total_T, Hq, D]  dtype, dense.  A token that sees nothing gets zeros.
+ *   lse          [total_T, Hq] fp32 or NULL: log of the softmax's denominator (natural,
+ *                maximum included; -inf for a token that sees nothing)
+ *   softmax_scale  <= 0 selects D^-0.5
+ *   window, sinks  0: none
+ *   What lies in the pages outside the visible keys may hold anything, NaN included.  bf16 with
+ *   D = 64 or 128 runs on the tensor cores with bf16 softmax weights (fp32 sums), where a value
+ *   that some token of the call sees must be finite for every token of that sequence; other
+ *   configurations run in fp32.
+ *   workspace    at least kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype)
+ *                bytes (0: none), 256-byte aligned, caller-owned, contents unspecified on
+ *                return; calls that may overlap in time need one each.
+ */
+size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
+                                              int dtype);
+int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, void* out, float* lse, float softmax_scale,
+                            int N, int total_T, int Hq, int Hkv, int D, int num_pages,
+                            int page_size, int max_pages, int window, int sinks,
+                            long long query_stride, int dtype, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
 
 /* Static, human-readable text for a kda_status value (never NULL). */
 const char* kda_status_string(int status);

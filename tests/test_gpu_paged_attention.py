@@ -1,0 +1,275 @@
+"""kda_paged_attention_fwd against the fp64 definition.
+
+Tolerances, per element.  A score is a sum of D products in fp32, scaled: off by at most
+d = (D + 8) 2^-24 Z with Z the largest sum |q k| scale of the row; every softmax weight is then
+off by at most 2 d + (n + 64) 2^-24 relative (numerator and denominator, n keys summed), so the
+output by that times A = sum p |v|.  bf16 weights of the tensor-core path add 2^-8 A (half a
+step on each weight) and the output's own rounding 2^-8 |o|.  lse: d + 2^-22 (|lse| + 1 + n 2^-4)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import gated_delta_rule_55_gb300 as kda  # noqa: E402
+import serving_ref as ref  # noqa: E402
+from gpu_helpers import ensure_built  # noqa: E402
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def host(x):
+    return x.detach().double().cpu().numpy()
+
+
+def make(seqs, Hq, Hkv, D, page, dt, seed=0, spare=3, pad=0, fill=None, std=1.0):
+    """seqs: (new tokens, keys in all).  Keys and pages that no sequence has hold `fill`."""
+    ensure_built()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    cu = np.concatenate([[0], np.cumsum([q for q, _ in seqs])]).astype(np.int32)
+    T = int(cu[-1]) + pad
+    kv = np.array([k for _, k in seqs], np.int32)
+    need = [-(-int(k) // page) for k in kv]
+    pages, maxp = sum(need) + spare, max(need + [1]) + 1
+    table = np.full((len(seqs), maxp), -7 if fill is not None else 0, np.int32)
+    perm = np.random.default_rng(seed).permutation(pages)
+    at = 0
+    for n, m in enumerate(need):
+        table[n, :m] = perm[at:at + m]
+        at += m
+    kc, vc = (torch.randn(pages, Hkv, page, D, generator=g, device="cuda") for _ in range(2))
+    kc *= std
+    if fill is not None:
+        own = torch.zeros(pages, 1, page, 1, dtype=torch.bool, device="cuda")
+        for n, m in enumerate(need):
+            for i in range(m):
+                own[int(table[n, i]), 0, :min(page, int(kv[n]) - i * page)] = True
+        kc, vc = (torch.where(own, x, torch.full_like(x, fill)) for x in (kc, vc))
+    q = torch.randn(T, Hq + 1, D, generator=g, device="cuda").to(DT[dt])[:, :Hq]
+    return dict(q=q, kc=kc.to(DT[dt]), vc=vc.to(DT[dt]), table=torch.from_numpy(table).cuda(),
+                cu=torch.from_numpy(cu).cuda(), kv=torch.from_numpy(kv).cuda(), cu_h=cu, kv_h=kv,
+                table_h=table, page=page, D=D, Hq=Hq, Hkv=Hkv, N=len(seqs), T=T, dt=dt,
+                out=torch.full((T, Hq, D), 7.0, dtype=DT[dt], device="cuda"),
+                lse=torch.full((T, Hq), 7.0, device="cuda"), live=int(cu[-1]))
+
+
+def call(d, ws=None, **kw):
+    n = kda.kda_paged_attention_fwd_workspace_size(
+        d["N"], d["T"], d["Hq"], d["Hkv"], d["D"],
+        dtype=kda.KDA_F32 if d["dt"] == "f32" else kda.KDA_BF16)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    kda.kda_paged_attention_fwd(d["q"], d["kc"], d["vc"], d["table"], d["cu"], d["kv"], d["out"],
+                                d["N"], d["T"], d["Hq"], d["Hkv"], d["D"], d["kc"].shape[0],
+                                d["page"], d["table"].shape[1], lse=d["lse"], workspace=ws, **kw)
+
+
+def check(d, **kw):
+    r = ref.paged_attention(host(d["q"])[:d["live"]], host(d["kc"]), host(d["vc"]), d["table_h"],
+                            d["cu_h"], d["kv_h"], d["page"], **kw)
+    compare(d, r)
+    assert (host(d["out"])[d["live"]:] == 7.0).all()
+    assert (host(d["lse"])[d["live"]:] == 7.0).all()
+
+
+def compare(d, r):
+    out, lse, A, Z = r
+    n = int(max(d["kv_h"], default=0))
+    dl = (d["D"] + 8) * 2.0 ** -24 * Z
+    lim = (2 * dl + (n + 64) * 2.0 ** -24)[..., None] * A
+    if d["dt"] == "bf16":
+        lim = lim + 2.0 ** -8 * (A + np.abs(out))
+    got = host(d["out"])[:d["live"]]
+    bad = ~(np.abs(got - out) <= lim)
+    assert not bad.any(), (np.abs(got - out)[bad].max(), int(bad.sum()), np.argwhere(bad)[:5])
+    gl = host(d["lse"])[:d["live"]]
+    empty = np.isneginf(lse)
+    assert (np.isneginf(gl) == empty).all()
+    ok = ~empty
+    assert (np.abs(gl[ok] - lse[ok]) <= dl[ok] + 2.0 ** -22 * (np.abs(lse[ok]) + 1 + n / 16)).all()
+    assert kda.kda_device_error() == 0
+
+
+KINDS = [("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 32), ("bf16", 64), ("bf16", 128)]
+
+
+@pytest.mark.parametrize("dt,D", KINDS)
+@pytest.mark.parametrize("page", [16, 128])
+def test_mixed_batch(dt, D, page):
+    d = make([(1, 1), (1, 77), (5, 5), (20, 150), (0, 40), (3, 129)], 4, 2, D, page, dt, pad=3)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("dt,D", [("f32", 64), ("bf16", 32), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (40, 0), (40, 4), (128, 300), (7, 2)])
+def test_window_and_sinks(dt, D, window, sinks):
+    d = make([(1, 300), (60, 333), (9, 9), (33, 50)], 6, 2, D, 32, dt, seed=window)
+    call(d, window=window, sinks=sinks)
+    check(d, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dt,D", KINDS)
+@pytest.mark.parametrize("kv", [1, 15, 16, 17, 127, 128, 129, 255, 256, 257])
+def test_single_token_lengths(dt, D, kv):
+    d = make([(1, kv)], 2, 1, D, 16, dt, seed=kv)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q,kv,Hq,Hkv", [(127, 127, 1, 1), (128, 128, 2, 2), (129, 300, 1, 1),
+                                         (256, 256, 1, 1), (257, 257, 1, 1), (31, 500, 8, 1),
+                                         (32, 500, 8, 1), (33, 500, 8, 1), (65, 200, 4, 2),
+                                         (100, 100, 5, 1), (43, 640, 3, 1), (2, 700, 64, 1)])
+def test_chunk_edges(D, q, kv, Hq, Hkv):
+    d = make([(q, kv)], Hq, Hkv, D, 64, "bf16", seed=q)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("dt,D", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
+def test_what_lies_outside_the_keys_never_counts(dt, D, page, fill):
+    d = make([(1, 130), (4, 67), (70, 201), (1, 1)], 4, 2, D, page, dt, fill=fill)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_behind_the_window_may_hold_anything(D):
+    """Single tokens: the pages that left the window are free, whatever they hold by now."""
+    d = make([(1, 500), (1, 90), (1, 700)], 4, 2, D, 32, "bf16", seed=4)
+    w, s = 100, 5
+    r = ref.paged_attention(host(d["q"]), host(d["kc"]), host(d["vc"]), d["table_h"], d["cu_h"],
+                            d["kv_h"], 32, window=w, sinks=s)
+    for n, kv in enumerate(d["kv_h"]):
+        for j in range(s, max(s, int(kv) - w)):
+            p = int(d["table_h"][n, j // 32])
+            d["kc"][p, :, j % 32] = float("nan")
+            d["vc"][p, :, j % 32] = float("nan")
+    call(d, window=w, sinks=s)
+    compare(d, r)
+
+
+def test_more_tokens_than_keys_and_no_keys():
+    for dt, D in (("f32", 64), ("bf16", 128)):
+        d = make([(10, 4), (3, 0), (200, 150)], 2, 2, D, 16, dt, seed=6)
+        call(d)
+        check(d)
+        assert (host(d["out"])[:6] == 0).all()
+
+
+def test_bad_pages_and_lengths_stay_inside_the_cache():
+    """Entries outside the cache are clamped: wrong numbers, no fault, no other row touched."""
+    for dt, D in (("f32", 64), ("bf16", 64), ("bf16", 128)):
+        d = make([(2, 100), (1, 40), (1, 64)], 2, 1, D, 16, dt, pad=2)
+        d["table"][0, 1] = 2 ** 31 - 1
+        d["table"][0, 2] = -2 ** 31
+        d["kv"][1] = 2 ** 31 - 1
+        d["kv"][2] = -5
+        d["cu"][3] = 2 ** 30
+        call(d)
+        torch.cuda.synchronize()
+        assert kda.kda_device_error() == 0
+
+
+def test_scale_and_sharp_softmax():
+    """Large scores of both signs: one key takes all."""
+    for dt, D in (("f32", 128), ("bf16", 64), ("bf16", 128)):
+        d = make([(3, 400), (40, 300)], 4, 4, D, 64, dt, std=30.0, seed=12)
+        call(d, softmax_scale=0.7)
+        check(d, scale=0.7)
+
+
+def test_rising_scores():
+    """Keys whose scores grow along the sequence: the running maximum moves at every tile."""
+    for D in (64, 128):
+        d = make([(1, 1500), (64, 1500)], 2, 1, D, 64, "bf16", seed=13)
+        ramp = {}
+        for n in range(2):
+            for j in range(1500):
+                ramp[int(d["table_h"][n, j // 64]), j % 64] = j / 1500 * 20
+        for (p, o), x in ramp.items():
+            d["kc"][p, :, o] = x / D
+        d["q"].copy_(torch.rand_like(d["q"]) + 0.5)
+        call(d, softmax_scale=1.0)
+        check(d, scale=1.0)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_long_and_many(dt, D):
+    """Few rows over long caches (cut along the keys) beside short ones."""
+    d = make([(1, 5000), (1, 3), (2, 2501), (1, 1)], 4, 2, D, 64, dt, seed=14)
+    call(d)
+    check(d)
+    d = make([(1, int(k)) for k in np.random.default_rng(1).integers(1, 400, 97)], 8, 2, D, 16, dt)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_repeat_stream_and_replay_give_the_same_bits(D):
+    d = make([(1, 3000), (90, 800), (1, 20), (5, 1200)], 8, 2, D, 32, "bf16", seed=15)
+    call(d)
+    a, l = d["out"].clone(), d["lse"].clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    d["out"].fill_(1)
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call(d)
+    s.synchronize()
+    assert torch.equal(a, d["out"]) and torch.equal(l, d["lse"])
+    n = kda.kda_paged_attention_fwd_workspace_size(d["N"], d["T"], 8, 2, D)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call(d, ws=ws)
+    ws.fill_(0xFF)
+    for _ in range(2):
+        d["out"].fill_(1)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, d["out"]) and torch.equal(l, d["lse"])
+    # new lengths under the same graph
+    d["kv"].sub_(torch.tensor([1500, 0, 5, 0], dtype=torch.int32, device="cuda"))
+    d["kv_h"] = host(d["kv"]).astype(np.int32)
+    gr.replay()
+    torch.cuda.synchronize()
+    check(d)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f32", 64)])
+def test_cache_beyond_32_bit_offsets(dt, D):
+    """A cache of more than 2^32 elements whose far pages are the ones in use."""
+    d = make([(1, 600), (40, 300)], 4, 2, D, 64, dt, seed=16)
+    near = d["kc"].shape[0]
+    per = 2 * 64 * D
+    pages = (1 << 32) // per + near
+    shift = pages - near
+    for n in ("kc", "vc"):
+        big = torch.empty(pages, 2, 64, D, dtype=DT[dt], device="cuda")
+        big[shift:] = d[n]
+        d[n + "0"], d[n] = d[n], big
+    d["table"] += shift
+    call(d)
+    d["kc"], d["vc"] = d["kc0"], d["vc0"]
+    check(d)
+
+
+def test_empty_calls():
+    d = make([(1, 5)], 2, 1, 64, 16, "f32")
+    kda.kda_paged_attention_fwd(d["q"], d["kc"], d["vc"], d["table"], d["cu"], d["kv"], d["out"],
+                                0, 0, 2, 1, 64, d["kc"].shape[0], 16, d["table"].shape[1])
+    # a cache without pages: nothing to see
+    for dt, D in (("f32", 64), ("bf16", 128)):
+        d = make([(2, 5)], 2, 1, D, 16, dt)
+        n = kda.kda_paged_attention_fwd_workspace_size(
+            1, 2, 2, 1, D, dtype=kda.KDA_F32 if dt == "f32" else kda.KDA_BF16)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+        kda.kda_paged_attention_fwd(d["q"], None, None, None, d["cu"], d["kv"], d["out"], 1, 2, 2,
+                                    1, D, 0, 16, 0, workspace=ws)
+        torch.cuda.synchronize()
+        assert (d["out"] == 0).all()
