@@ -442,45 +442,71 @@ def kda_decode_step(q, k, v, g, beta_logits, a_log, dt_bias, scale, lower_bound,
         float(scale), float(lower_bound), _ptr(out), _ptr(S), B, H, dk, dv, _stream(stream)))
 
 
-def _dev(x, dtype, what):
+class _Call:
+    """What the serving calls look up once: torch's types, the current device and its stream.
+    A serving step makes many small calls, so their arguments are checked in few Python
+    operations each."""
+    f32 = bf16 = i32 = i64 = None
+    device = raw_stream = None
+
+
+def _setup():
+    import torch
+    _Call.f32, _Call.bf16 = torch.float32, torch.bfloat16
+    _Call.i32, _Call.i64 = torch.int32, torch.int64
+    _Call.device = torch.cuda.current_device
+    # the stream's address without building a stream object, where torch offers it
+    _Call.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _begin(x, dtype, stream):
+    """(kda dtype, torch dtype, device, stream address) of a call whose first tensor is x."""
+    if _Call.f32 is None:
+        _setup()
+    if dtype is None:
+        el = x.dtype
+        if el is _Call.bf16:
+            dtype = KDA_BF16
+        elif el is _Call.f32:
+            dtype = KDA_F32
+        else:
+            raise ValueError(f"unsupported q/k/v dtype {el}")
+    else:
+        el = _Call.f32 if dtype == KDA_F32 else _Call.bf16
+    if x.__class__ is not int and not x.is_cuda:
+        raise ValueError("query must be a tensor of the current CUDA device")
+    dev = _Call.device()
+    if stream is None:
+        stream = _Call.raw_stream(dev)
+    elif stream.__class__ is not int:
+        stream = stream.cuda_stream
+    return dtype, el, dev, stream
+
+
+def _dev(x, dtype, dev, what):
     """Address of a dense tensor of the given type on the current device (None and raw
     addresses pass as they are)."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
-    import torch
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} must be a tensor of the current CUDA device")
-    if x.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
-    if not x.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if x.get_device() != dev or x.dtype is not dtype or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of the current CUDA device")
     return x.data_ptr()
 
 
-def _rows(x, dtype, heads, dim, what):
+def _rows(x, dtype, dev, heads, dim, what):
     """(address, token stride in elements) of a [tokens, heads, dim] argument: a raw address is
     taken as dense, a tensor may have any distance between its tokens."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x, heads * dim
-    import torch
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what} must be a tensor of the current CUDA device")
-    if x.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {x.dtype}")
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise ValueError(f"{what} must have shape [tokens, {heads}, {dim}], not "
-                         f"{list(x.shape)}")
-    st = x.stride()
-    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+    if x.get_device() != dev or x.dtype is not dtype:
+        raise ValueError(f"{what} must be a {dtype} tensor of the current CUDA device")
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what} must have shape [tokens, {heads}, {dim}], not {list(shape)}")
+    if (st[2] != 1 and dim > 1) or (st[1] != dim and heads > 1):
         raise ValueError(f"the heads of {what} must be dense")
-    return x.data_ptr(), st[0] if x.shape[0] > 1 else heads * dim
-
-
-def _elem(x, dtype):
-    """(kda dtype, torch dtype) of a call whose first tensor is x."""
-    import torch
-    code = _dtype_code(x, dtype)
-    return code, torch.float32 if code == KDA_F32 else torch.bfloat16
+    return x.data_ptr(), st[0] if shape[0] > 1 else heads * dim
 
 
 def kda_attention_step(query, key, value, beta, decay, state, slots, out, N, T, Hk, Hv, dk, dv,
@@ -488,35 +514,35 @@ def kda_attention_step(query, key, value, beta, decay, state, slots, out, N, T, 
                        use_qk_l2norm=True, order="decay_first", dtype=None, stream=None):
     """A few new tokens of N requests against a pool of states (see include/kda.h): T tokens per
     request, or T packed tokens in all with ``cu_seqlens``."""
-    import torch
-    code, el = _elem(query, dtype)
-    f32, i32 = torch.float32, torch.int32
-    qp, qs = _rows(query, el, Hk, dk, "query")
-    kp, ks = _rows(key, el, Hk, dk, "key")
-    vp, vs = _rows(value, el, Hv, dv, "value")
+    flags = 0 if use_qk_l2norm and order == "decay_first" else _attn_flags(use_qk_l2norm, True,
+                                                                           order)
+    code, el, dev, st = _begin(query, dtype, stream)
+    f32, i32 = _Call.f32, _Call.i32
+    qp, qs = _rows(query, el, dev, Hk, dk, "query")
+    kp, ks = _rows(key, el, dev, Hk, dk, "key")
+    vp, vs = _rows(value, el, dev, Hv, dv, "value")
     _check("kda_attention_step", lib().kda_attention_step(
-        qp, kp, vp, _dev(beta, f32, "beta"), _dev(decay, f32, "decay"),
-        _dev(state, f32, "state"), _dev(slots, i32, "slots"), _dev(out_slots, i32, "out_slots"),
-        _dev(cu_seqlens, i32, "cu_seqlens"), _dev(out, el, "out"), float(softmax_scale or 0.0),
-        N, T, Hk, Hv, dk, dv, num_slots, qs, ks, vs, _attn_flags(use_qk_l2norm, True, order),
-        code, _stream(stream)))
+        qp, kp, vp, _dev(beta, f32, dev, "beta"), _dev(decay, f32, dev, "decay"),
+        _dev(state, f32, dev, "state"), _dev(slots, i32, dev, "slots"), _dev(out_slots, i32, dev, "out_slots"),
+        _dev(cu_seqlens, i32, dev, "cu_seqlens"), _dev(out, el, dev, "out"), float(softmax_scale or 0.0),
+        N, T, Hk, Hv, dk, dv, num_slots, qs, ks, vs, flags,
+        code, st))
 
 
 def kda_qk_norm_rope_fwd(query, key, query_weight, key_weight, cos_table, sin_table, positions,
                          query_out, key_out, T, Hq, Hkv, D, R, max_position, eps=1e-6,
                          interleaved=False, dtype=None, stream=None):
     """RMS norm of every query and key head and the position rotation (see include/kda.h)."""
-    import torch
-    code, el = _elem(query, dtype)
-    f32 = torch.float32
-    qp, qs = _rows(query, el, Hq, D, "query")
-    kp, ks = _rows(key, el, Hkv, D, "key")
+    code, el, dev, st = _begin(query, dtype, stream)
+    f32 = _Call.f32
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    kp, ks = _rows(key, el, dev, Hkv, D, "key")
     _check("kda_qk_norm_rope_fwd", lib().kda_qk_norm_rope_fwd(
-        qp, kp, _dev(query_weight, f32, "query_weight"), _dev(key_weight, f32, "key_weight"),
-        _dev(cos_table, f32, "cos_table"), _dev(sin_table, f32, "sin_table"),
-        _dev(positions, torch.int32, "positions"), _dev(query_out, el, "query_out"),
-        _dev(key_out, el, "key_out"), float(eps), T, Hq, Hkv, D, R, max_position, qs, ks,
-        KDA_ROPE_INTERLEAVED if interleaved else 0, code, _stream(stream)))
+        qp, kp, _dev(query_weight, f32, dev, "query_weight"), _dev(key_weight, f32, dev, "key_weight"),
+        _dev(cos_table, f32, dev, "cos_table"), _dev(sin_table, f32, dev, "sin_table"),
+        _dev(positions, _Call.i32, dev, "positions"), _dev(query_out, el, dev, "query_out"),
+        _dev(key_out, el, dev, "key_out"), float(eps), T, Hq, Hkv, D, R, max_position, qs, ks,
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
 
 
 def kda_qk_norm_rope_append(query, key, value, query_weight, key_weight, cos_table, sin_table,
@@ -525,20 +551,19 @@ def kda_qk_norm_rope_append(query, key, value, query_weight, key_weight, cos_tab
                             dtype=None, stream=None):
     """kda_qk_norm_rope_fwd with keys and values written into cache pages (see
     include/kda.h)."""
-    import torch
-    code, el = _elem(query, dtype)
-    f32 = torch.float32
-    qp, qs = _rows(query, el, Hq, D, "query")
-    kp, ks = _rows(key, el, Hkv, D, "key")
-    vp, vs = _rows(value, el, Hkv, D, "value")
+    code, el, dev, st = _begin(query, dtype, stream)
+    f32 = _Call.f32
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    kp, ks = _rows(key, el, dev, Hkv, D, "key")
+    vp, vs = _rows(value, el, dev, Hkv, D, "value")
     _check("kda_qk_norm_rope_append", lib().kda_qk_norm_rope_append(
-        qp, kp, vp, _dev(query_weight, f32, "query_weight"),
-        _dev(key_weight, f32, "key_weight"), _dev(cos_table, f32, "cos_table"),
-        _dev(sin_table, f32, "sin_table"), _dev(positions, torch.int32, "positions"),
-        _dev(slots, torch.int64, "slots"), _dev(query_out, el, "query_out"),
-        _dev(k_cache, el, "k_cache"), _dev(v_cache, el, "v_cache"), float(eps), T, Hq, Hkv, D, R,
+        qp, kp, vp, _dev(query_weight, f32, dev, "query_weight"),
+        _dev(key_weight, f32, dev, "key_weight"), _dev(cos_table, f32, dev, "cos_table"),
+        _dev(sin_table, f32, dev, "sin_table"), _dev(positions, _Call.i32, dev, "positions"),
+        _dev(slots, _Call.i64, dev, "slots"), _dev(query_out, el, dev, "query_out"),
+        _dev(k_cache, el, dev, "k_cache"), _dev(v_cache, el, dev, "v_cache"), float(eps), T, Hq, Hkv, D, R,
         max_position, num_pages, page_size, qs, ks, vs,
-        KDA_ROPE_INTERLEAVED if interleaved else 0, code, _stream(stream)))
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
 
 
 def kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D) -> int:
@@ -551,20 +576,19 @@ def kda_qk_norm_rope_bwd(query, key, query_weight, key_weight, cos_table, sin_ta
                          Hq, Hkv, D, R, max_position, eps=1e-6, interleaved=False, dtype=None,
                          workspace=None, stream=None):
     """Gradients of kda_qk_norm_rope_fwd (see include/kda.h)."""
-    import torch
-    code, el = _elem(query, dtype)
-    f32 = torch.float32
-    qp, qs = _rows(query, el, Hq, D, "query")
-    kp, ks = _rows(key, el, Hkv, D, "key")
+    code, el, dev, st = _begin(query, dtype, stream)
+    f32 = _Call.f32
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    kp, ks = _rows(key, el, dev, Hkv, D, "key")
     wp, wb = _ws(workspace)
     _check("kda_qk_norm_rope_bwd", lib().kda_qk_norm_rope_bwd(
-        qp, kp, _dev(query_weight, f32, "query_weight"), _dev(key_weight, f32, "key_weight"),
-        _dev(cos_table, f32, "cos_table"), _dev(sin_table, f32, "sin_table"),
-        _dev(positions, torch.int32, "positions"), _dev(d_query_out, el, "d_query_out"),
-        _dev(d_key_out, el, "d_key_out"), _dev(d_query, el, "d_query"),
-        _dev(d_key, el, "d_key"), _dev(d_query_weight, f32, "d_query_weight"),
-        _dev(d_key_weight, f32, "d_key_weight"), float(eps), T, Hq, Hkv, D, R, max_position, qs,
-        ks, KDA_ROPE_INTERLEAVED if interleaved else 0, code, wp, wb, _stream(stream)))
+        qp, kp, _dev(query_weight, f32, dev, "query_weight"), _dev(key_weight, f32, dev, "key_weight"),
+        _dev(cos_table, f32, dev, "cos_table"), _dev(sin_table, f32, dev, "sin_table"),
+        _dev(positions, _Call.i32, dev, "positions"), _dev(d_query_out, el, dev, "d_query_out"),
+        _dev(d_key_out, el, dev, "d_key_out"), _dev(d_query, el, dev, "d_query"),
+        _dev(d_key, el, dev, "d_key"), _dev(d_query_weight, f32, dev, "d_query_weight"),
+        _dev(d_key_weight, f32, dev, "d_key_weight"), float(eps), T, Hq, Hkv, D, R, max_position, qs,
+        ks, KDA_ROPE_INTERLEAVED if interleaved else 0, code, wp, wb, st))
 
 
 def kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype=KDA_BF16) -> int:
@@ -577,14 +601,13 @@ def kda_paged_attention_fwd(query, k_cache, v_cache, block_table, cu_seqlens, kv
                             softmax_scale=None, window=0, sinks=0, dtype=None, workspace=None,
                             stream=None):
     """Attention of new tokens over a paged cache (see include/kda.h)."""
-    import torch
-    code, el = _elem(query, dtype)
-    i32 = torch.int32
-    qp, qs = _rows(query, el, Hq, D, "query")
+    code, el, dev, st = _begin(query, dtype, stream)
+    i32 = _Call.i32
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
     wp, wb = _ws(workspace)
     _check("kda_paged_attention_fwd", lib().kda_paged_attention_fwd(
-        qp, _dev(k_cache, el, "k_cache"), _dev(v_cache, el, "v_cache"),
-        _dev(block_table, i32, "block_table"), _dev(cu_seqlens, i32, "cu_seqlens"),
-        _dev(kv_lens, i32, "kv_lens"), _dev(out, el, "out"), _dev(lse, torch.float32, "lse"),
+        qp, _dev(k_cache, el, dev, "k_cache"), _dev(v_cache, el, dev, "v_cache"),
+        _dev(block_table, i32, dev, "block_table"), _dev(cu_seqlens, i32, dev, "cu_seqlens"),
+        _dev(kv_lens, i32, dev, "kv_lens"), _dev(out, el, dev, "out"), _dev(lse, _Call.f32, dev, "lse"),
         float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
-        window, sinks, qs, code, wp, wb, _stream(stream)))
+        window, sinks, qs, code, wp, wb, st))
