@@ -703,7 +703,8 @@ int kda_device_error(int reset) {
   if (s != KDA_OK) return s;
   return (int)(kda::chunk_tc_read_error(reset != 0) | kda::chunk_split_read_error(reset != 0) |
                kda::chunk_bwd_read_error(reset != 0) | kda::decode_read_error(reset != 0) |
-               kda::selftest_read_error(reset != 0) | kda::gla_chunk_read_error(reset != 0));
+               kda::selftest_read_error(reset != 0) | kda::gla_chunk_read_error(reset != 0) |
+               kda::paged_read_error(reset != 0));
 }
 
 int kda_selftest_bounded_wait(unsigned long long limit_ns, kda_stream_t stream) {

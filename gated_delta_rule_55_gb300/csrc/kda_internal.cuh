@@ -142,6 +142,11 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t stre
 size_t norm_rope_bwd_workspace(int D);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* d_q_weight, float* d_k_weight,
                                  void* workspace, bool bf16, cudaStream_t stream);
+// Paged attention on the tensor cores: bf16, D = 64 or 128.
+bool paged_tc_supported(int D, bool bf16);
+size_t paged_tc_workspace(int D);
+cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
+unsigned int paged_read_error(bool reset);
 size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D);
 cudaError_t launch_paged_simt(const PagedArgs& a, bool bf16, void* workspace,
                               cudaStream_t stream);

@@ -1,0 +1,801 @@
+// Attention of new tokens over a paged cache (kda_paged_attention_fwd) on the tensor cores:
+// bf16, head dim 64 or 128.
+//
+// Work.  An item is one sequence, one kv head and up to 256 of its query rows (tokens x query
+// heads of that kv head).  Its visible keys come in tiles of 128; the tiles of all items, in
+// order, form one line that is cut into equal stretches, one for each CTA (one CTA per SM).
+// Ragged batches, causal triangles, windows and single tokens over long caches are thus
+// balanced alike, and an item that a cut passes through leaves at most two partial results per
+// CTA, joined by a second kernel.
+//
+// One CTA: two units, each with a score tile S [128 rows x 128 keys] and an output accumulator
+// O [128 x D] in Tensor Memory and a warpgroup for the softmax.  A wide item (more than 128
+// rows) gives each unit 128 rows and every key tile to both; a narrow one (single tokens) gives
+// both units the same rows and every other key tile, and joins their two results at its end.
+// A load warp brings key and value tiles by TMA (one box per page and 64 columns) through a
+// ring of shared-memory stages, a single thread issues the products
+//   S = Q K^T  (both operands in shared memory),  O += P V  (P in Tensor Memory over S's
+//   columns, V read as it lies, keys along the contraction),
+// and the softmax of one unit runs while the tensor cores work for the other.  The product
+// that makes S for the next tile is issued behind the one that reads P, so S complete means O
+// complete: the softmax warps rescale O themselves, and only when a row's maximum has grown by
+// more than 2^8 since the value they subtract (the sums stay far inside fp32).
+//
+// Softmax weights are rounded to bf16 for the product (their sum is taken before, in fp32).
+// Keys that no row of the item sees (behind the last one, outside the window, pages that are
+// not loaded) have weight zero and their values are overwritten with zeros in shared memory,
+// so what the cache holds there never counts.
+#include "chunk_common.cuh"
+#include "kda_paged.cuh"
+
+namespace kda {
+namespace {
+
+using namespace chunk;
+
+__device__ unsigned int g_paged_error;  // bit 6: a bounded wait gave up
+
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kRowsUnit = 128;   // query rows of a unit
+constexpr int kRowsItem = 256;
+constexpr int kThreads = 384;    // two softmax warpgroups; the load and the product warp
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+// Registers: 168 a thread at launch (3 x 128 threads), moved to the softmax warpgroups:
+// 2 x 216 + 72 = 3 x 168.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr float kRescale = 8.0f;  // log2 growth of the maximum that O and l absorb
+
+template <int D> struct Cfg {
+  static constexpr int kStageBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kQBytes = kRowsUnit * D * 2;
+  static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + 1024 + 512;
+};
+
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
+
+struct Header {  // a CTA's part of the line, for the joining kernel
+  int n, h, rt;   // the item its stretch ends in (n < 0: none of its own is cut)
+  int last;       // the last CTA of that item
+  long long total;
+};
+
+// ------------------------------------------------------------------- items of the line
+
+struct Geometry {
+  int row0, rows;  // query rows of the item
+  KeyRange kr;
+  int t_lo, ns, nt;  // first window tile, sink tiles before it, tiles in all
+};
+
+__device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, int G, int rt) {
+  Geometry g;
+  const int rows = s.len * G;
+  g.row0 = rt * kRowsItem;
+  g.rows = min(kRowsItem, rows - g.row0);
+  g.kr = key_range(a, s, g.row0 / G, (g.row0 + g.rows - 1) / G);
+  g.t_lo = g.kr.lo / kKeys;
+  g.ns = min((g.kr.sinks + kKeys - 1) / kKeys, g.t_lo);
+  // an item without keys still has one (empty) tile: its rows get their zeros
+  g.nt = max(g.ns + (g.kr.hi + kKeys - 1) / kKeys - g.t_lo, 1);
+  return g;
+}
+
+__device__ __forceinline__ int tile_start(const Geometry& g, int v) {
+  return (v < g.ns ? v : g.t_lo + v - g.ns) * kKeys;
+}
+
+__device__ __forceinline__ int row_tiles(const Seq& s, int G) {
+  return (int)(((long long)s.len * G + kRowsItem - 1) / kRowsItem);
+}
+
+struct Plan {  // in shared memory
+  long long total, first, end;  // tiles of the line, this CTA's stretch [first, end)
+  int n, h, rt, v;              // where the stretch starts
+};
+
+// Walks the items of a CTA's stretch; every role of the CTA walks on its own.
+struct Walker {
+  int n, h, rt, v0, v1;
+  int nrt, G;
+  long long left;  // tiles of the stretch from v0 on
+  Seq s;
+  Geometry g;
+
+  __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
+    left = p.end - p.first;
+    if (left <= 0) return false;
+    G = a.Hq / a.Hkv;
+    n = p.n; h = p.h; rt = p.rt; v0 = p.v;
+    s = load_seq(a, n);
+    nrt = row_tiles(s, G);
+    g = geometry(a, s, G, rt);
+    v1 = (int)min((long long)g.nt, v0 + left);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const PagedArgs& a) {
+    left -= v1 - v0;
+    if (left <= 0) return false;
+    if (++rt >= nrt) {
+      rt = 0;
+      if (++h >= a.Hkv) {
+        h = 0;
+        do {  // (a token is left somewhere: the line has more tiles)
+          if (++n >= a.N) return false;
+          s = load_seq(a, n);
+        } while (s.len == 0);
+        nrt = row_tiles(s, G);
+      }
+    }
+    g = geometry(a, s, G, rt);
+    v0 = 0;
+    v1 = (int)min((long long)g.nt, left);
+    return true;
+  }
+  __device__ __forceinline__ int tiles() const { return v1 - v0; }
+  __device__ __forceinline__ bool narrow() const { return g.rows <= kRowsUnit; }
+};
+
+// Tiles of all items of sequence n (called by whole warps, one sequence per lane; a lane with
+// many row tiles is helped by its warp).
+__device__ __forceinline__ long long sequence_tiles(const PagedArgs& a, int n, int G) {
+  long long w = 0;
+  int nrt = 0;
+  Seq s{};
+  if (n < a.N) {
+    s = load_seq(a, n);
+    nrt = row_tiles(s, G);
+  }
+  const bool big = nrt > 4;
+  if (!big)
+    for (int rt = 0; rt < nrt; ++rt) w += geometry(a, s, G, rt).nt;
+  unsigned todo = __ballot_sync(0xffffffffu, big);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    Seq t;
+    t.bos = 0;
+    t.len = __shfl_sync(0xffffffffu, s.len, src);
+    t.kv = __shfl_sync(0xffffffffu, s.kv, src);
+    t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
+    const int m = __shfl_sync(0xffffffffu, nrt, src);
+    long long x = 0;
+    for (int rt = threadIdx.x & 31; rt < m; rt += 32) x += geometry(a, t, G, rt).nt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((int)(threadIdx.x & 31) == src) w = x;
+  }
+  return w * a.Hkv;
+}
+
+// The CTA's stretch of the line: all threads call.
+__device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
+  constexpr int W = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
+  const int rounds = (a.N + kThreads - 1) / kThreads;
+  long long mine = 0, sum = 0, total = 0;
+  // total, and (one round: the usual case) the thread's own sequence and the scan at once
+  for (int r = 0; r < rounds; ++r) {
+    mine = sequence_tiles(a, r * kThreads + tid, G);
+    sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < W; ++w) total += s_warp[w];
+    if (rounds > 1) __syncthreads();
+  }
+  const long long P = gridDim.x, c = blockIdx.x;
+  const long long first = c * total / P, end = (c + 1) * total / P;
+  if (tid == 0) {
+    plan.total = total;
+    plan.first = first;
+    plan.end = end;
+  }
+  if (first == end) return;  // (uniform)
+  long long before = 0;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) {
+      mine = sequence_tiles(a, r * kThreads + tid, G);
+      sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_warp[warp] = sum;
+      __syncthreads();
+    }
+    long long pre = before;
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) pre += s_warp[w];
+      before += s_warp[w];
+    }
+    pre += sum - mine;  // tiles before this thread's sequence
+    const bool here = first >= pre && first < pre + mine;
+    const unsigned b = __ballot_sync(0xffffffffu, here);
+    if (b) {  // this warp has the sequence: find head, row tile and tile together
+      const int src = __ffs(b) - 1;
+      const int n = r * kThreads + warp * 32 + src;
+      const long long per = __shfl_sync(0xffffffffu, mine, src) / a.Hkv;
+      long long off = first - __shfl_sync(0xffffffffu, pre, src);
+      const int h = (int)(off / per);
+      off -= h * per;
+      const Seq s = load_seq(a, n);
+      const int nrt = row_tiles(s, G);
+      for (int base = 0; base < nrt; base += 32) {
+        const int rt = base + lane;
+        const int nt = rt < nrt ? geometry(a, s, G, rt).nt : 0;
+        int run = nt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += y;
+        }
+        if (off >= run - nt && off < run) {
+          plan.n = n;
+          plan.h = h;
+          plan.rt = rt;
+          plan.v = (int)(off - (run - nt));
+        }
+        const int all = __shfl_sync(0xffffffffu, run, 31);
+        if (off < all) break;
+        off -= all;
+      }
+    }
+    if (first < before) break;  // (uniform)
+  }
+}
+
+// Ring position of an item's i-th key / value tile (of n), in the order in which the products
+// use them: wide K0 V0 K1 V1 ...; narrow K0 K1 V0 K2 V1 ... (the second unit's scores start
+// before the first unit's values are needed).
+__device__ __forceinline__ uint32_t ring_k(bool narrow, int i) {
+  return narrow ? (i == 0 ? 0u : uint32_t(2 * i - 1)) : uint32_t(2 * i);
+}
+__device__ __forceinline__ uint32_t ring_v(bool narrow, int i, int n) {
+  return narrow ? uint32_t(min(2 * i + 2, 2 * n - 1)) : uint32_t(2 * i + 1);
+}
+
+// ------------------------------------------------------------------------ small pieces
+
+// 128 consecutive columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  float a[32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    tmem_ld32(taddr + 32 * j, a);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[32 * j + i] = a[i];
+  }
+}
+
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+struct Bars {
+  uint64_t kv_full[8], kv_empty[8], q_full[2], s_full[2], p_full[2], o_full[2];
+};
+
+// A wait that gives up marks the thread dead: it then runs through the rest of its work
+// without waiting (its results are void) so that every loop and barrier still ends.
+__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool& dead) {
+  if (!dead && !mbar_wait(bar, parity)) {
+    dead = true;
+    atomicOr(&g_paged_error, 64u);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, Header* headers, float* part_o,
+                float2* part_ml) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages, HALVES = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  uint8_t* sQ = sm;                      // two 128-row tiles
+  uint8_t* sKV = sm + 2 * C::kQBytes;    // the ring
+  float2* s_ml = reinterpret_cast<float2*>(sKV + NS * C::kStageBytes);  // [128], unit 1's m, l
+  __shared__ Bars bars;
+  __shared__ Plan plan;
+  __shared__ long long s_warp[kThreads / 32];
+  __shared__ uint32_t s_tmem;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars.kv_full[i], 1);
+      mbar_init(&bars.kv_empty[i], 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&bars.q_full[u], 4);
+      mbar_init(&bars.s_full[u], 1);
+      mbar_init(&bars.p_full[u], 4);
+      mbar_init(&bars.o_full[u], 1);
+    }
+    fence_mbar_init();
+  }
+  make_plan(a, plan, s_warp);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  bool dead = false;
+  Walker w;
+
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (warp == kLoadWarp) {
+    const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
+    const int pi = lane % ppt, half = lane / ppt;
+    uint32_t pos = 0;  // entries pushed into the ring
+    bool live = w.start(a, plan);
+    while (live) {
+      const int n = w.tiles();
+      const bool narrow = w.narrow();
+      // The page of this lane in the i-th tile of the item, -1 where no key is needed.
+      auto page = [&](int i) -> int {
+        if (half >= HALVES || i >= n) return -1;
+        const int k0 = tile_start(w.g, w.v0 + i) + pi * ps;
+        if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return -1;
+        return page_of(a, w.n, k0);
+      };
+      auto push = [&](const CUtensorMap* map, int pid) {
+        const uint32_t st = pos % NS, ph = (pos / NS) & 1;
+        wait_or_die(&bars.kv_empty[st], ph ^ 1, dead);
+        const unsigned need = __ballot_sync(0xffffffffu, pid >= 0);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&bars.kv_full[st], uint32_t(__popc(need)) * uint32_t(ps) * 128u);
+        __syncwarp();
+        if (pid >= 0 && !dead)
+          tma_load_2d(sKV + st * C::kStageBytes + half * (kKeys * 128) + pi * ps * 128, map,
+                      &bars.kv_full[st], half * 64, (pid * a.Hkv + w.h) * ps);
+        ++pos;
+      };
+      // a tile's pages are looked up one tile ahead of their first use
+      int p0 = page(0), p1 = page(1);
+      push(&kmap, p0);
+      for (int i = 0; i < n; ++i) {
+        const int p2 = page(i + 2);
+        if (narrow && i + 1 < n) push(&kmap, p1);
+        push(&vmap, p0);
+        if (!narrow && i + 1 < n) push(&kmap, p1);
+        p0 = p1;
+        p1 = p2;
+      }
+      live = w.next(a);
+    }
+    // leave no copy in flight behind a give-up
+    if (dead)
+      for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
+        mbar_wait(&bars.kv_full[i % NS], (i / NS) & 1, 100000000ull);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      const uint32_t idesc_s = make_idesc(1, 128, kKeys);
+      const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
+      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
+      uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+      int qtile[2];
+      auto scores = [&](int u, uint32_t at, bool release) {
+        const uint32_t st = at % NS;
+        wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
+        if (!dead) {
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_ss(tm + kColS + 128 * u, sw128_kdesc<2>(q0 + qtile[u] * C::kQBytes, 128, s),
+                   sw128_kdesc<2>(kv0 + st * C::kStageBytes, 128, s), idesc_s, s > 0);
+        }
+        mma_commit(&bars.s_full[u]);
+        if (release) mma_commit(&bars.kv_empty[st]);
+      };
+      auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
+        const uint32_t st = at % NS;
+        wait_or_die(&bars.p_full[u], np[u] & 1, dead);
+        ++np[u];
+        wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
+        if (!dead) {
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            mma_ts(tm + kColO + 128 * u, tm + kColS + 128 * u + 8 * s,
+                   make_sdesc(kv0 + st * C::kStageBytes + uint32_t(s) * 2048u, kKeys * 128u, 1024u,
+                              kSwizzle128),
+                   idesc_o, !(first && s == 0));
+        }
+        if (release) mma_commit(&bars.kv_empty[st]);
+        if (last) mma_commit(&bars.o_full[u]);
+      };
+      bool live = w.start(a, plan);
+      while (live) {
+        const int n = w.tiles();
+        const bool narrow = w.narrow();
+        for (int u = 0; u < (narrow ? 1 : 2); ++u) {
+          wait_or_die(&bars.q_full[u], nq[u] & 1, dead);
+          ++nq[u];
+        }
+        qtile[0] = 0;
+        qtile[1] = narrow ? 0 : 1;
+        if (narrow) {
+          scores(0, pos + ring_k(true, 0), true);
+          if (n > 1) scores(1, pos + ring_k(true, 1), true);
+          for (int i = 0; i < n; ++i) {
+            values(i & 1, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
+            if (i + 2 < n) scores(i & 1, pos + ring_k(true, i + 2), true);
+          }
+        } else {
+          scores(0, pos, false);
+          scores(1, pos, true);
+          for (int i = 0; i < n; ++i)
+            for (int u = 0; u < 2; ++u) {
+              values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
+              if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1);
+            }
+        }
+        pos += 2 * n;
+        live = w.next(a);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int u = warp >> 2, r = tid & 127;  // unit, row within it
+    const uint32_t lanebits = uint32_t(warp & 3) << 21;  // (32 * warp of the group) << 16
+    const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
+    const uint32_t tO1 = tm + kColO + 128 + lanebits;
+    const float sc = a.scale * kLog2E;
+    uint32_t pos = 0, ns = 0, no[2] = {0, 0};
+    bool live = w.start(a, plan);
+    while (live) {
+      const int n = w.tiles();
+      const bool narrow = w.narrow();
+      const int base = narrow ? 0 : u * kRowsUnit;            // first row of the unit's tile
+      const int nr = min(max(w.g.rows - base, 0), kRowsUnit);  // its rows
+      const bool active = (warp & 3) * 32 < nr;               // (warp-uniform)
+      const bool valid = r < nr;
+      const int row = w.g.row0 + base + min(r, max(nr - 1, 0));
+      const long long tok = w.s.bos + min(row / w.G, w.s.len - 1);
+      const int head = w.h * w.G + row % w.G;
+      const int mypos = w.s.pos0 + row / w.G;
+
+      // 1. The unit's query rows into its tile (narrow: unit 0's serve both).
+      if (!narrow || u == 0) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride +
+                                   (long long)head * D;
+        uint8_t* dst = sQ + base / kRowsUnit * C::kQBytes;
+        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
+        if (active)
+#pragma unroll 4
+          for (int i = 0; i < 32; i += RPI) {
+            const int sl = i + lane / CH, ch = lane % CH;
+            const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), sl));
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + ch);
+            *reinterpret_cast<uint4*>(dst + sw128_offset<2>(kRowsUnit, (warp & 3) * 32 + sl,
+                                                            ch * 8)) = x;
+          }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.q_full[u]);
+      }
+
+      // 2. The unit's tiles.
+      float m = -INFINITY, l = 0.f;
+      int mine = 0;
+      // key limits of the unit's rows: all of them see keys below `all_hi` ...
+      const int pos_first = w.s.pos0 + (w.g.row0 + base) / w.G;
+      const int pos_last = w.s.pos0 + (w.g.row0 + base + max(nr - 1, 0)) / w.G;
+      for (int i = narrow ? u : 0; i < n; i += narrow ? 2 : 1) {
+        const int ks = tile_start(w.g, w.v0 + i);
+        wait_or_die(&bars.s_full[u], ns & 1, dead);
+        ++ns;
+        tc_fence_after();
+        // keys of this tile that no row of the item sees, if any: rows of V to clear.
+        // (Behind the wait for the scores: the products before them have used every earlier entry
+        // of the ring, so the value stage's barrier is in the phase that is waited for.)
+        const bool clear = ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks);
+        if (clear) {
+          const uint32_t at = pos + ring_v(narrow, i, n);
+          wait_or_die(&bars.kv_full[at % NS], (at / NS) & 1, dead);
+          const int key = ks + r;
+          if (key >= w.g.kr.hi || (key < w.g.kr.lo && key >= w.g.kr.sinks)) {
+            uint8_t* vrow = sKV + (at % NS) * C::kStageBytes + r * 128;
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch)
+                *reinterpret_cast<uint4*>(vrow + hf * (kKeys * 128) + ch * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        if (active) {
+          float s[128];
+          tmem_ld128(tS, s);
+          // ... and a tile needs masks where some row of the unit does not see all of it
+          const bool whole =
+              ks + kKeys <= pos_first + 1 &&
+              (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
+          if (!whole) {
+            const int hi = mypos - ks;  // keys 0..hi of the tile are not in the future
+            const int lo = a.window ? max(mypos, 0) - a.window - ks : -1;  // <= lo: left the window
+            const int sk = a.sinks - ks;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > hi || (c <= lo && c >= sk)) s[c] = -INFINITY;
+          }
+          float mx = s[0];
+#pragma unroll
+          for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
+          const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mx : m;
+            const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
+            m = mn;
+            l *= f;
+            if (mine > 0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(tO + c, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(tO + c, o);
+              }
+            }
+          }
+          const float nb = m == -INFINITY ? 0.f : -m * sc;
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = fast_exp2(fmaf(s[c + 2 * e], sc, nb));
+              const float y = fast_exp2(fmaf(s[c + 2 * e + 1], sc, nb));
+              sum0 += x;
+              sum1 += y;
+              p[e] = pack_bf16(x, y);
+            }
+            tmem_st16_nowait(tS + c / 2, p);
+          }
+          l += sum0 + sum1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[u]);
+        ++mine;
+      }
+
+      // 3. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
+      // unit 1's accumulator lanes too.
+      if (mine > 0) {
+        wait_or_die(&bars.o_full[u], no[u] & 1, dead);
+        ++no[u];
+      }
+      if (u == 0) {
+        if (narrow && n > 1) wait_or_die(&bars.o_full[1], no[1] & 1, dead);
+        if (!narrow || n > 1) ++no[1];
+      }
+      float f0 = 1.f, f1 = 0.f;
+      bool both = false;
+      if (narrow) {
+        if (u == 1) s_ml[r] = make_float2(m, l);
+        group_sync(1, 256);
+        if (u == 0) {
+          both = n > 1;
+          if (both) {
+            const float2 o = s_ml[r];
+            const float mn = fmaxf(m, o.x);
+            const float b = mn == -INFINITY ? 0.f : mn;
+            f0 = fast_exp2((m - b) * sc);
+            f1 = fast_exp2((o.x - b) * sc);
+            l = l * f0 + o.y * f1;
+            m = mn;
+          }
+        }
+      }
+      tc_fence_after();
+      if ((!narrow || u == 0) && active) {
+        const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
+        const long long orow = tok * a.Hq + head;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const int slot = 2 * blockIdx.x + (cut0 ? 0 : 1);
+        const long long prow = (long long)slot * kRowsItem + base + r;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tO + c, o);
+          if (both) {
+            float o1[32];
+            tmem_ld32(tO1 + c, o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          }
+          if (!valid) continue;
+          if (cut0 || cut1) {
+            float4* dst = reinterpret_cast<float4*>(part_o + prow * D + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D +
+                                                  c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                x[t] = l == 0.f ? 0u
+                                : pack_bf16(o[8 * e + 2 * t] * inv, o[8 * e + 2 * t + 1] * inv);
+              dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        if (valid) {
+          if (cut0 || cut1)
+            part_ml[prow] = make_float2(m * sc, l);
+          else if (a.lse)
+            a.lse[orow] =
+                l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      tc_fence_before();
+      if (narrow) group_sync(1, 256);
+      if (tid == 0) {
+        // (the last item of the stretch leaves its header)
+        if (w.left - (w.v1 - w.v0) <= 0) {
+          Header hd;
+          const bool tail = w.v0 == 0 && w.v1 < w.g.nt;
+          const long long e = plan.end - (w.v1 - w.g.nt);  // the item's end in the line
+          hd.n = tail ? w.n : -1;
+          hd.h = w.h;
+          hd.rt = w.rt;
+          hd.last = (int)((e * gridDim.x + plan.total - 1) / plan.total - 1);
+          hd.total = plan.total;
+          headers[blockIdx.x] = hd;
+        }
+      }
+      pos += 2 * n;
+      live = w.next(a);
+    }
+    if (tid == 0 && plan.first == plan.end) headers[blockIdx.x].n = -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) {
+    tmem_relinquish();
+    tmem_dealloc(tm, kTmemCols);
+  }
+}
+
+// Joins the partial results of an item that was cut: the CTA it starts in has it in its second
+// slot, the following ones (up to the header's last) in their first.  Block (c, i): the item
+// that CTA c's stretch ends in, rows 32 i .. 32 i + 31, one warp per row at a time.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int P,
+                                                         const Header* headers,
+                                                         const float* part_o,
+                                                         const float2* part_ml) {
+  constexpr int E = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const Header hd = headers[c];
+  if (hd.n < 0) return;
+  const Seq s = load_seq(a, hd.n);
+  const int G = a.Hq / a.Hkv;
+  const int row0 = hd.rt * kRowsItem;
+  const int rows = min(kRowsItem, s.len * G - row0);
+  for (int i = 0; i < 4; ++i) {
+    const int r = blockIdx.y * 32 + i * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int k = c; k <= hd.last; ++k) {
+      if (k > c && (long long)k * hd.total / P == (long long)(k + 1) * hd.total / P) continue;
+      const long long at = (long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r;
+      const float2 ml = part_ml[at];
+      if (ml.y == 0.f) continue;  // nothing seen in this part
+      const float mn = (ml.x > m || ml.x != ml.x) ? ml.x : m;
+      const float f = exp2f(m - mn), g = exp2f(ml.x - mn);
+      m = mn;
+      l = l * f + ml.y * g;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f + part_o[at * D + e * 32 + lane] * g;
+    }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const long long row = (s.bos + (row0 + r) / G) * a.Hq + hd.h * G + (row0 + r) % G;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      static_cast<__nv_bfloat16*>(a.out)[row * D + e * 32 + lane] =
+          __float2bfloat16_rn(o[e] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+bool cache_map(CUtensorMap* map, const void* base, const PagedArgs& a) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.D,
+                              (cuuint64_t)a.num_pages * a.Hkv * (cuuint64_t)a.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)a.page_size};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kCtas = 152;  // one per SM
+
+template <int D>
+cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
+  CUtensorMap kmap{}, vmap{};
+  if (a.num_pages > 0 && a.max_pages > 0)
+    if (!cache_map(&kmap, a.k_cache, a) || !cache_map(&vmap, a.v_cache, a))
+      return cudaErrorInvalidValue;
+  Header* headers = static_cast<Header*>(workspace);
+  float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + 8192);
+  float* po = reinterpret_cast<float*>(ml + (size_t)2 * kCtas * kRowsItem);
+  cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, kmap, vmap, headers, po, ml);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  paged_join_kernel<D><<<dim3(kCtas, kRowsItem / 32), 256, 0, st>>>(a, kCtas, headers, po, ml);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+static_assert(sizeof(Header) * kCtas <= 8192, "headers");
+
+bool paged_tc_supported(int D, bool bf16) { return bf16 && (D == 64 || D == 128); }
+
+size_t paged_tc_workspace(int D) {
+  return 8192 + (size_t)2 * kCtas * kRowsItem * (sizeof(float2) + D * sizeof(float));
+}
+
+cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st) {
+  return a.D == 64 ? launch_t<64>(a, workspace, st) : launch_t<128>(a, workspace, st);
+}
+
+unsigned int paged_read_error(bool reset) {
+  unsigned int v = 0;
+  cudaMemcpyFromSymbol(&v, g_paged_error, sizeof(v));
+  if (reset) {
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_paged_error, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace kda

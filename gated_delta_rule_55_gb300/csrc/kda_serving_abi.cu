@@ -199,6 +199,7 @@ size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hk
   if (N <= 0 || total_T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
       !dtype_ok(dtype))
     return 0;
+  if (kda::paged_tc_supported(D, dtype == KDA_BF16)) return kda::paged_tc_workspace(D);
   return kda::paged_simt_workspace(N, total_T, Hq, Hkv, D);
 }
 
@@ -244,7 +245,9 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   a.window = (double)window >= (double)max_pages * page_size ? 0 : window;
   a.sinks = sinks;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(kda::launch_paged_simt(a, dtype == KDA_BF16, workspace, st));
+  return launch_status(kda::paged_tc_supported(D, dtype == KDA_BF16)
+                           ? kda::launch_paged_tc(a, workspace, st)
+                           : kda::launch_paged_simt(a, dtype == KDA_BF16, workspace, st));
 }
 
 }  // extern "C"

@@ -621,7 +621,8 @@ int kda_version(void);
  *   kda_recurrent_attention_fwd_ws or kda_attention_fwd_ws met gates outside its range,
  *   detected per 16-token sub-chunk (a summed key-axis gate or decay totalling outside
  *   [-80, 16] over a sub-chunk, or a value-axis gate outside [-40, 8] over half of one,
- *   which gates in [-5, 1] rule out; that call's results are unspecified).  Synchronises
+ *   which gates in [-5, 1] rule out; that call's results are unspecified); bit 6: a bounded
+ *   wait inside kda_paged_attention_fwd's tensor-core kernel gave up.  Synchronises
  *   the device.  reset != 0
  *   clears the mask.
  *   Returns the mask (>= 0) or KDA_ERR_DEVICE.

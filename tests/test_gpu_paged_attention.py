@@ -210,6 +210,20 @@ def test_long_and_many(dt, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 700])
+def test_many_tiles_of_single_tokens(D, window):
+    """Enough single tokens over long caches that every block walks many tiles and items."""
+    kv = np.random.default_rng(3).integers(300, 3500, 36)
+    d = make([(1, int(k)) for k in kv], 32, 16, D, 64, "bf16", seed=30)
+    call(d, window=window, sinks=3 if window else 0)
+    a = d["out"].clone()
+    check(d, window=window, sinks=3 if window else 0)
+    for _ in range(20):
+        call(d, window=window, sinks=3 if window else 0)
+        assert torch.equal(a, d["out"])
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_repeat_stream_and_replay_give_the_same_bits(D):
     d = make([(1, 3000), (90, 800), (1, 20), (5, 1200)], 8, 2, D, 32, "bf16", seed=15)
     call(d)
