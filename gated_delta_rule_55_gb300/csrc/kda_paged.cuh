@@ -12,17 +12,20 @@ struct Seq {
   int pos0;       // position of its first new token (negative: more new tokens than keys)
 };
 
-__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int n) {
+// From a sequence's raw offsets and key count.
+__device__ __forceinline__ Seq make_seq(const PagedArgs& a, int lo, int hi, int kv) {
   Seq s;
-  int lo = a.cu_seqlens[n], hi = a.cu_seqlens[n + 1];
   lo = min(max(lo, 0), a.total_T);
   hi = min(max(hi, lo), a.total_T);
   s.bos = lo;
   s.len = hi - lo;
   const long long cap = (long long)a.max_pages * a.page_size;
-  s.kv = (int)min((long long)max(a.kv_lens[n], 0), a.num_pages > 0 ? cap : 0ll);
+  s.kv = (int)min((long long)max(kv, 0), a.num_pages > 0 ? cap : 0ll);
   s.pos0 = s.kv - s.len;
   return s;
+}
+__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int n) {
+  return make_seq(a, a.cu_seqlens[n], a.cu_seqlens[n + 1], a.kv_lens[n]);
 }
 
 // Whether a packed token belongs to a sequence (rows behind the last one are left alone).

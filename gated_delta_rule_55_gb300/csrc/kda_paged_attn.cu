@@ -54,13 +54,24 @@ template <int D> struct Cfg {
 
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
 
+// An item counts kOverhead units beside its tiles: what its start and end cost a CTA (the
+// units lie before its tiles, and a cut among them falls to the item's first tile).
+constexpr int kOverhead = 1;
+
 struct Header {  // a CTA's part of the line, for the joining kernel
-  int n, h, rt;   // the item its stretch ends in (n < 0: none of its own is cut)
-  int last;       // the last CTA of that item
-  long long total;
+  int rows;       // rows of the item that starts in its stretch and is cut (0: none)
+  int row0, h;    // its first row and kv head
+  int nt;         // its tiles
+  long long bos;  // its sequence's first token
+  long long start, total;  // its place in the line, the line's length
 };
 
 // ------------------------------------------------------------------- items of the line
+
+// x / (Hq / Hkv) for 0 <= x < 2^31, by the host's multiplier (launch_t).
+__device__ __forceinline__ int div_g(const PagedArgs& a, int x) {
+  return (int)((__umulhi((uint32_t)x, a.g_mul) + (uint32_t)x) >> a.g_shift);
+}
 
 struct Geometry {
   int row0, rows;  // query rows of the item
@@ -73,7 +84,7 @@ __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, i
   const int rows = s.len * G;
   g.row0 = rt * kRowsItem;
   g.rows = min(kRowsItem, rows - g.row0);
-  g.kr = key_range(a, s, g.row0 / G, (g.row0 + g.rows - 1) / G);
+  g.kr = key_range(a, s, div_g(a, g.row0), div_g(a, g.row0 + g.rows - 1));
   g.t_lo = g.kr.lo / kKeys;
   g.ns = min((g.kr.sinks + kKeys - 1) / kKeys, g.t_lo);
   // an item without keys still has one (empty) tile: its rows get their zeros
@@ -90,55 +101,73 @@ __device__ __forceinline__ int row_tiles(const Seq& s, int G) {
 }
 
 struct Plan {  // in shared memory
-  long long total, first, end;  // tiles of the line, this CTA's stretch [first, end)
-  int n, h, rt, v;              // where the stretch starts
+  long long total, first, end;  // units of the line, this CTA's stretch [first, end)
+  int n, h, rt, x;              // where the stretch starts: an item and a unit of it
 };
 
 // Walks the items of a CTA's stretch; every role of the CTA walks on its own.
 struct Walker {
   int n, h, rt, v0, v1;
   int nrt, G;
-  long long left;  // tiles of the stretch from v0 on
+  long long left;  // units of the stretch from the item's first one on
+  int units;       // units of the item in the stretch
   Seq s;
   Geometry g;
+  int c1, c2, kv1;  // the next sequence's offsets and keys, loaded ahead
 
+  __device__ __forceinline__ void ahead(const PagedArgs& a) {
+    c1 = c2 = kv1 = 0;
+    if (n + 1 < a.N) {
+      c1 = a.cu_seqlens[n + 1];
+      c2 = a.cu_seqlens[n + 2];
+      kv1 = a.kv_lens[n + 1];
+    }
+  }
+  // The item's tiles among its units [x, ...); false when the stretch ends before the first (it
+  // is the stretch's last item then, and the next CTA takes it whole).
+  __device__ __forceinline__ bool enter(int x) {
+    const long long last = min((long long)(g.nt + kOverhead), x + left);
+    units = (int)(last - x);
+    v0 = max(x - kOverhead, 0);
+    v1 = max((int)last - kOverhead, 0);
+    return v1 > v0;
+  }
   __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
     left = p.end - p.first;
     if (left <= 0) return false;
     G = a.Hq / a.Hkv;
-    n = p.n; h = p.h; rt = p.rt; v0 = p.v;
+    n = p.n; h = p.h; rt = p.rt;
     s = load_seq(a, n);
+    ahead(a);
     nrt = row_tiles(s, G);
     g = geometry(a, s, G, rt);
-    v1 = (int)min((long long)g.nt, v0 + left);
-    return true;
+    return enter(p.x);
   }
   __device__ __forceinline__ bool next(const PagedArgs& a) {
-    left -= v1 - v0;
+    left -= units;
     if (left <= 0) return false;
     if (++rt >= nrt) {
       rt = 0;
       if (++h >= a.Hkv) {
         h = 0;
-        do {  // (a token is left somewhere: the line has more tiles)
+        do {  // (the line has more units, so a later sequence has tokens)
           if (++n >= a.N) return false;
-          s = load_seq(a, n);
+          s = make_seq(a, c1, c2, kv1);
+          ahead(a);
         } while (s.len == 0);
         nrt = row_tiles(s, G);
       }
     }
     g = geometry(a, s, G, rt);
-    v0 = 0;
-    v1 = (int)min((long long)g.nt, left);
-    return true;
+    return enter(0);
   }
   __device__ __forceinline__ int tiles() const { return v1 - v0; }
   __device__ __forceinline__ bool narrow() const { return g.rows <= kRowsUnit; }
 };
 
-// Tiles of all items of sequence n (called by whole warps, one sequence per lane; a lane with
+// Units of all items of sequence n (called by whole warps, one sequence per lane; a lane with
 // many row tiles is helped by its warp).
-__device__ __forceinline__ long long sequence_tiles(const PagedArgs& a, int n, int G) {
+__device__ __forceinline__ long long sequence_units(const PagedArgs& a, int n, int G) {
   long long w = 0;
   int nrt = 0;
   Seq s{};
@@ -148,7 +177,7 @@ __device__ __forceinline__ long long sequence_tiles(const PagedArgs& a, int n, i
   }
   const bool big = nrt > 4;
   if (!big)
-    for (int rt = 0; rt < nrt; ++rt) w += geometry(a, s, G, rt).nt;
+    for (int rt = 0; rt < nrt; ++rt) w += geometry(a, s, G, rt).nt + kOverhead;
   unsigned todo = __ballot_sync(0xffffffffu, big);
   while (todo) {
     const int src = __ffs(todo) - 1;
@@ -160,7 +189,7 @@ __device__ __forceinline__ long long sequence_tiles(const PagedArgs& a, int n, i
     t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
     const int m = __shfl_sync(0xffffffffu, nrt, src);
     long long x = 0;
-    for (int rt = threadIdx.x & 31; rt < m; rt += 32) x += geometry(a, t, G, rt).nt;
+    for (int rt = threadIdx.x & 31; rt < m; rt += 32) x += geometry(a, t, G, rt).nt + kOverhead;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if ((int)(threadIdx.x & 31) == src) w = x;
@@ -176,7 +205,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
   long long mine = 0, sum = 0, total = 0;
   // total, and (one round: the usual case) the thread's own sequence and the scan at once
   for (int r = 0; r < rounds; ++r) {
-    mine = sequence_tiles(a, r * kThreads + tid, G);
+    mine = sequence_units(a, r * kThreads + tid, G);
     sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -199,7 +228,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
   long long before = 0;
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) {
-      mine = sequence_tiles(a, r * kThreads + tid, G);
+      mine = sequence_units(a, r * kThreads + tid, G);
       sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -218,7 +247,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
     pre += sum - mine;  // tiles before this thread's sequence
     const bool here = first >= pre && first < pre + mine;
     const unsigned b = __ballot_sync(0xffffffffu, here);
-    if (b) {  // this warp has the sequence: find head, row tile and tile together
+    if (b) {  // this warp has the sequence: find head, row tile and unit together
       const int src = __ffs(b) - 1;
       const int n = r * kThreads + warp * 32 + src;
       const long long per = __shfl_sync(0xffffffffu, mine, src) / a.Hkv;
@@ -229,7 +258,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
       const int nrt = row_tiles(s, G);
       for (int base = 0; base < nrt; base += 32) {
         const int rt = base + lane;
-        const int nt = rt < nrt ? geometry(a, s, G, rt).nt : 0;
+        const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
         int run = nt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -240,7 +269,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
           plan.n = n;
           plan.h = h;
           plan.rt = rt;
-          plan.v = (int)(off - (run - nt));
+          plan.x = (int)(off - (run - nt));
         }
         const int all = __shfl_sync(0xffffffffu, run, 31);
         if (off < all) break;
@@ -263,15 +292,60 @@ __device__ __forceinline__ uint32_t ring_v(bool narrow, int i, int n) {
 
 // ------------------------------------------------------------------------ small pieces
 
-// 128 consecutive columns of the thread's lane.
+// 128 consecutive columns of the thread's lane, waited for.
 __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  float a[32];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    tmem_ld32(taddr + 32 * j, a);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[32 * j + i] = a[i];
-  }
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
+      "%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,"
+      "%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,"
+      "%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,"
+      "%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,"
+      "%126,%127"
+      "}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
+        "=f"(v[64]), "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
+        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]),
+        "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]),
+        "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
+        "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]),
+        "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
+        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
+        "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Packed pairs of fp32: a b + c, a + b.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -292,7 +366,7 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
 }
 
 struct Bars {
-  uint64_t kv_full[8], kv_empty[8], q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
 };
 
 // A wait that gives up marks the thread dead: it then runs through the rest of its work
@@ -330,7 +404,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       mbar_init(&bars.kv_empty[i], 1);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&bars.q_full[u], 4);
+      mbar_init(&bars.q_full[u], 1);
+      mbar_init(&bars.q_empty[u], 1);
       mbar_init(&bars.s_full[u], 1);
       mbar_init(&bars.p_full[u], 4);
       mbar_init(&bars.o_full[u], 1);
@@ -347,119 +422,146 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  if (warp == kLoadWarp) {
-    const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
-    const int pi = lane % ppt, half = lane / ppt;
-    uint32_t pos = 0;  // entries pushed into the ring
     bool live = w.start(a, plan);
-    while (live) {
-      const int n = w.tiles();
-      const bool narrow = w.narrow();
-      // The page of this lane in the i-th tile of the item, -1 where no key is needed.
-      auto page = [&](int i) -> int {
-        if (half >= HALVES || i >= n) return -1;
-        const int k0 = tile_start(w.g, w.v0 + i) + pi * ps;
-        if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return -1;
-        return page_of(a, w.n, k0);
-      };
-      auto push = [&](const CUtensorMap* map, int pid) {
-        const uint32_t st = pos % NS, ph = (pos / NS) & 1;
-        wait_or_die(&bars.kv_empty[st], ph ^ 1, dead);
-        const unsigned need = __ballot_sync(0xffffffffu, pid >= 0);
-        if (lane == 0)
-          mbar_arrive_expect_tx(&bars.kv_full[st], uint32_t(__popc(need)) * uint32_t(ps) * 128u);
-        __syncwarp();
-        if (pid >= 0 && !dead)
-          tma_load_2d(sKV + st * C::kStageBytes + half * (kKeys * 128) + pi * ps * 128, map,
-                      &bars.kv_full[st], half * 64, (pid * a.Hkv + w.h) * ps);
-        ++pos;
-      };
-      // a tile's pages are looked up one tile ahead of their first use
-      int p0 = page(0), p1 = page(1);
-      push(&kmap, p0);
-      for (int i = 0; i < n; ++i) {
-        const int p2 = page(i + 2);
-        if (narrow && i + 1 < n) push(&kmap, p1);
-        push(&vmap, p0);
-        if (!narrow && i + 1 < n) push(&kmap, p1);
-        p0 = p1;
-        p1 = p2;
-      }
-      live = w.next(a);
-    }
-    // leave no copy in flight behind a give-up
-    if (dead)
-      for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
-        mbar_wait(&bars.kv_full[i % NS], (i / NS) & 1, 100000000ull);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc_s = make_idesc(1, 128, kKeys);
-      const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
-      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
-      uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      int qtile[2];
-      auto scores = [&](int u, uint32_t at, bool release) {
-        const uint32_t st = at % NS;
-        wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
-        if (!dead) {
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_ss(tm + kColS + 128 * u, sw128_kdesc<2>(q0 + qtile[u] * C::kQBytes, 128, s),
-                   sw128_kdesc<2>(kv0 + st * C::kStageBytes, 128, s), idesc_s, s > 0);
-        }
-        mma_commit(&bars.s_full[u]);
-        if (release) mma_commit(&bars.kv_empty[st]);
-      };
-      auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
-        const uint32_t st = at % NS;
-        wait_or_die(&bars.p_full[u], np[u] & 1, dead);
-        ++np[u];
-        wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
-        if (!dead) {
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_ts(tm + kColO + 128 * u, tm + kColS + 128 * u + 8 * s,
-                   make_sdesc(kv0 + st * C::kStageBytes + uint32_t(s) * 2048u, kKeys * 128u, 1024u,
-                              kSwizzle128),
-                   idesc_o, !(first && s == 0));
-        }
-        if (release) mma_commit(&bars.kv_empty[st]);
-        if (last) mma_commit(&bars.o_full[u]);
-      };
-      bool live = w.start(a, plan);
+    if (warp == kLoadWarp) {
+      const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
+      const int pi = lane % ppt, half = lane / ppt;
+      uint32_t pos = 0;  // entries pushed into the ring
       while (live) {
         const int n = w.tiles();
         const bool narrow = w.narrow();
-        for (int u = 0; u < (narrow ? 1 : 2); ++u) {
-          wait_or_die(&bars.q_full[u], nq[u] & 1, dead);
-          ++nq[u];
+        // The page of this lane in the i-th tile of the item, -1 where no key is needed.
+        auto page = [&](int i) -> int {
+          if (half >= HALVES || i >= n) return -1;
+          const int k0 = tile_start(w.g, w.v0 + i) + pi * ps;
+          if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return -1;
+          return page_of(a, w.n, k0);
+        };
+        auto push = [&](const CUtensorMap* map, int pid) {
+          const uint32_t st = pos % NS, ph = (pos / NS) & 1;
+          wait_or_die(&bars.kv_empty[st], ph ^ 1, dead);
+          const unsigned need = __ballot_sync(0xffffffffu, pid >= 0);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bars.kv_full[st],
+                                  uint32_t(__popc(need)) * uint32_t(ps) * 128u);
+          __syncwarp();
+          if (pid >= 0 && !dead)
+            tma_load_2d(sKV + st * C::kStageBytes + half * (kKeys * 128) + pi * ps * 128, map,
+                        &bars.kv_full[st], half * 64, (pid * a.Hkv + w.h) * ps);
+          ++pos;
+        };
+        // a tile's pages are looked up one tile ahead of their first use
+        int p0 = page(0), p1 = page(1);
+        push(&kmap, p0);
+        for (int i = 0; i < n; ++i) {
+          const int p2 = page(i + 2);
+          if (narrow && i + 1 < n) push(&kmap, p1);
+          push(&vmap, p0);
+          if (!narrow && i + 1 < n) push(&kmap, p1);
+          p0 = p1;
+          p1 = p2;
         }
-        qtile[0] = 0;
-        qtile[1] = narrow ? 0 : 1;
-        if (narrow) {
-          scores(0, pos + ring_k(true, 0), true);
-          if (n > 1) scores(1, pos + ring_k(true, 1), true);
-          for (int i = 0; i < n; ++i) {
-            values(i & 1, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
-            if (i + 2 < n) scores(i & 1, pos + ring_k(true, i + 2), true);
+        live = w.next(a);
+      }
+      // leave no copy in flight behind a give-up
+      if (dead)
+        for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
+          mbar_wait(&bars.kv_full[i % NS], (i / NS) & 1, 100000000ull);
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        const uint32_t idesc_s = make_idesc(1, 128, kKeys);
+        const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
+        const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
+        uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+        int qtile1 = 0;
+        auto scores = [&](int u, uint32_t at, bool release, bool last_q) {
+          const uint32_t st = at % NS;
+          wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
+          if (!dead) {
+            tc_fence_after();
+            const uint32_t q = q0 + (u ? qtile1 : 0) * C::kQBytes;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_ss(tm + kColS + 128 * u, sw128_kdesc<2>(q, 128, s),
+                     sw128_kdesc<2>(kv0 + st * C::kStageBytes, 128, s), idesc_s, s > 0);
           }
-        } else {
-          scores(0, pos, false);
-          scores(1, pos, true);
-          for (int i = 0; i < n; ++i)
-            for (int u = 0; u < 2; ++u) {
-              values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
-              if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1);
+          mma_commit(&bars.s_full[u]);
+          if (release) mma_commit(&bars.kv_empty[st]);
+          if (last_q) mma_commit(&bars.q_empty[u ? qtile1 : 0]);
+        };
+        auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
+          const uint32_t st = at % NS;
+          wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
+          wait_or_die(&bars.p_full[u], np[u] & 1, dead);
+          ++np[u];
+          if (!dead) {
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              mma_ts(tm + kColO + 128 * u, tm + kColS + 128 * u + 8 * s,
+                     make_sdesc(kv0 + st * C::kStageBytes + uint32_t(s) * 2048u, kKeys * 128u,
+                                1024u, kSwizzle128),
+                     idesc_o, !(first && s == 0));
+          }
+          if (release) mma_commit(&bars.kv_empty[st]);
+          if (last) mma_commit(&bars.o_full[u]);
+        };
+        while (live) {
+          const int n = w.tiles();
+          const bool narrow = w.narrow();
+          for (int u = 0; u < (narrow ? 1 : 2); ++u) {
+            wait_or_die(&bars.q_full[u], nq[u] & 1, dead);
+            ++nq[u];
+          }
+          qtile1 = narrow ? 0 : 1;
+          if (narrow) {
+            scores(0, pos + ring_k(true, 0), true, n == 1);
+            if (n > 1) scores(1, pos + ring_k(true, 1), true, n == 2);
+            for (int i = 0; i < n; ++i) {
+              values(i & 1, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
+              if (i + 2 < n) scores(i & 1, pos + ring_k(true, i + 2), true, i + 3 == n);
             }
+          } else {
+            scores(0, pos, false, n == 1);
+            scores(1, pos, true, n == 1);
+            for (int i = 0; i < n; ++i)
+              for (int u = 0; u < 2; ++u) {
+                values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
+                if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1, i + 2 == n);
+              }
+          }
+          pos += 2 * n;
+          live = w.next(a);
         }
-        pos += 2 * n;
+      }
+      __syncwarp();
+    } else {
+      // Query rows of the item's tile t, as soon as the products on the last item's are done.
+      const int t = warp - kMmaWarp - 1;
+      uint32_t nq = 0;
+      while (live) {
+        const int rows = min(w.g.rows - t * kRowsUnit, kRowsUnit);
+        if (rows > 0) {
+          wait_or_die(&bars.q_empty[t], (nq & 1) ^ 1, dead);
+          ++nq;
+          constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
+          const uint32_t dst = smem_u32(sQ + t * C::kQBytes);
+          const int ch = lane % CH, row0 = w.g.row0 + t * kRowsUnit;
+          for (int r = lane / CH; r < rows; r += RPI) {
+            const int tk = div_g(a, row0 + r), hg = row0 + r - tk * w.G;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                       (w.s.bos + tk) * a.q_stride +
+                                       (long long)(w.h * w.G + hg) * D + ch * 8;
+            cp_async16(dst + sw128_offset<2>(kRowsUnit, r, ch * 8), src);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.q_full[t]);
+        }
         live = w.next(a);
       }
     }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int u = warp >> 2, r = tid & 127;  // unit, row within it
@@ -468,56 +570,107 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     const uint32_t tO1 = tm + kColO + 128 + lanebits;
     const float sc = a.scale * kLog2E;
     uint32_t pos = 0, ns = 0, no[2] = {0, 0};
+    Header hd;
+    hd.rows = 0;
     bool live = w.start(a, plan);
     while (live) {
       const int n = w.tiles();
       const bool narrow = w.narrow();
-      const int base = narrow ? 0 : u * kRowsUnit;            // first row of the unit's tile
-      const int nr = min(max(w.g.rows - base, 0), kRowsUnit);  // its rows
-      const bool active = (warp & 3) * 32 < nr;               // (warp-uniform)
-      const bool valid = r < nr;
-      const int row = w.g.row0 + base + min(r, max(nr - 1, 0));
-      const long long tok = w.s.bos + min(row / w.G, w.s.len - 1);
-      const int head = w.h * w.G + row % w.G;
-      const int mypos = w.s.pos0 + row / w.G;
+      const int base = narrow ? 0 : u * kRowsUnit;   // first row of the unit's tile
+      const int nr = min(w.g.rows - base, kRowsUnit);  // its rows (1 at least)
+      const bool active = (warp & 3) * 32 < nr;      // (warp-uniform)
+      const int row = w.g.row0 + base + min(r, nr - 1);
+      const int tk = div_g(a, row);
 
-      // 1. The unit's query rows into its tile (narrow: unit 0's serve both).
-      if (!narrow || u == 0) {
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride +
-                                   (long long)head * D;
-        uint8_t* dst = sQ + base / kRowsUnit * C::kQBytes;
-        constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
-        if (active)
-#pragma unroll 4
-          for (int i = 0; i < 32; i += RPI) {
-            const int sl = i + lane / CH, ch = lane % CH;
-            const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), sl));
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + ch);
-            *reinterpret_cast<uint4*>(dst + sw128_offset<2>(kRowsUnit, (warp & 3) * 32 + sl,
-                                                            ch * 8)) = x;
-          }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_full[u]);
-      }
-
-      // 2. The unit's tiles.
+      // 1. The unit's tiles.
       float m = -INFINITY, l = 0.f;
       int mine = 0;
-      // key limits of the unit's rows: all of them see keys below `all_hi` ...
-      const int pos_first = w.s.pos0 + (w.g.row0 + base) / w.G;
-      const int pos_last = w.s.pos0 + (w.g.row0 + base + max(nr - 1, 0)) / w.G;
+      const int mypos = w.s.pos0 + tk;
+      const int pos_first = w.s.pos0 + div_g(a, w.g.row0 + base);
+      const int pos_last = w.s.pos0 + div_g(a, w.g.row0 + base + nr - 1);
       for (int i = narrow ? u : 0; i < n; i += narrow ? 2 : 1) {
         const int ks = tile_start(w.g, w.v0 + i);
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
         tc_fence_after();
-        // keys of this tile that no row of the item sees, if any: rows of V to clear.
-        // (Behind the wait for the scores: the products before them have used every earlier entry
-        // of the ring, so the value stage's barrier is in the phase that is waited for.)
-        const bool clear = ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks);
-        if (clear) {
+        float s[128];
+        if (active) {
+          tmem_ld128(tS, s);
+          // a tile needs masks where some row of the unit does not see all of it
+          const bool whole =
+              ks + kKeys <= pos_first + 1 &&
+              (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
+          if (!whole) {
+            // bits of the keys that the thread's row sees: not in the future, and in the
+            // window or among the sinks
+            const int hi = min(mypos - ks + 1, kKeys);  // keys [0, hi) of the tile
+            const int lo = a.window ? max(max(mypos, 0) - a.window - ks + 1, 0) : 0;
+            const int sk = a.window ? a.sinks - ks : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              auto below = [&](int x) -> uint32_t {  // bits [0, x - 32 q)
+                const int b = x - 32 * q;
+                return b <= 0 ? 0u : b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+              };
+              const uint32_t bits = below(hi) & (~below(lo) | below(sk));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1)) s[32 * q + c] = -INFINITY;
+            }
+          }
+          float mx4[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mx4[c] = s[c];
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx4[e] = fmaxf(mx4[e], s[c + e]);
+          const float mx = fmaxf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])),
+                                 fmaxf(fmaxf(mx4[4], mx4[5]), fmaxf(mx4[6], mx4[7])));
+          const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mx : m;
+            const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
+            m = mn;
+            l *= f;
+            if (mine > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(tO + c, o);
+                uint32_t x[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
+                tmem_st16(tO + c, x);
+              }
+            }
+          }
+          const float nb = m == -INFINITY ? 0.f : -m * sc;
+          const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(nb, nb);
+          uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x, y;
+              unpack2(fma2(pack2(s[c + 2 * e], s[c + 2 * e + 1]), sc2, nb2), x, y);
+              x = fast_exp2(x);
+              y = fast_exp2(y);
+              sum[e & 3] = add2(sum[e & 3], pack2(x, y));
+              p[e] = pack_bf16(x, y);
+            }
+            tmem_st16_nowait(tS + c / 2, p);
+          }
+          float x, y;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+          l += x + y;
+        }
+        // Keys of this tile that no row of the item sees: their values become zeros (weight
+        // zero times what the cache holds there need not be zero).  Behind the wait for the
+        // scores: the products before them have used every earlier entry of the ring, so the
+        // value stage's barrier is in the phase that is waited for.
+        if (ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks)) {
           const uint32_t at = pos + ring_v(narrow, i, n);
           wait_or_die(&bars.kv_full[at % NS], (at / NS) & 1, dead);
           const int key = ks + r;
@@ -526,72 +679,20 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-              for (int ch = 0; ch < 8; ++ch)
-                *reinterpret_cast<uint4*>(vrow + hf * (kKeys * 128) + ch * 16) =
+              for (int ch = 0; ch < 8; ++ch)  // (from another piece in each lane: all banks)
+                *reinterpret_cast<uint4*>(vrow + hf * (kKeys * 128) + ((ch + lane) & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
         }
-        if (active) {
-          float s[128];
-          tmem_ld128(tS, s);
-          // ... and a tile needs masks where some row of the unit does not see all of it
-          const bool whole =
-              ks + kKeys <= pos_first + 1 &&
-              (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
-          if (!whole) {
-            const int hi = mypos - ks;  // keys 0..hi of the tile are not in the future
-            const int lo = a.window ? max(mypos, 0) - a.window - ks : -1;  // <= lo: left the window
-            const int sk = a.sinks - ks;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > hi || (c <= lo && c >= sk)) s[c] = -INFINITY;
-          }
-          float mx = s[0];
-#pragma unroll
-          for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
-          const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mx : m;
-            const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
-            m = mn;
-            l *= f;
-            if (mine > 0) {
-#pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(tO + c, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(tO + c, o);
-              }
-            }
-          }
-          const float nb = m == -INFINITY ? 0.f : -m * sc;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = fast_exp2(fmaf(s[c + 2 * e], sc, nb));
-              const float y = fast_exp2(fmaf(s[c + 2 * e + 1], sc, nb));
-              sum0 += x;
-              sum1 += y;
-              p[e] = pack_bf16(x, y);
-            }
-            tmem_st16_nowait(tS + c / 2, p);
-          }
-          l += sum0 + sum1;
-          tmem_wait_st();
-        }
+        if (active) tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[u]);
         ++mine;
       }
 
-      // 3. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
+      // 2. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
       // unit 1's accumulator lanes too.
       if (mine > 0) {
         wait_or_die(&bars.o_full[u], no[u] & 1, dead);
@@ -602,31 +703,29 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         if (!narrow || n > 1) ++no[1];
       }
       float f0 = 1.f, f1 = 0.f;
-      bool both = false;
+      const bool both = narrow && n > 1;
       if (narrow) {
         if (u == 1) s_ml[r] = make_float2(m, l);
         group_sync(1, 256);
-        if (u == 0) {
-          both = n > 1;
-          if (both) {
-            const float2 o = s_ml[r];
-            const float mn = fmaxf(m, o.x);
-            const float b = mn == -INFINITY ? 0.f : mn;
-            f0 = fast_exp2((m - b) * sc);
-            f1 = fast_exp2((o.x - b) * sc);
-            l = l * f0 + o.y * f1;
-            m = mn;
-          }
+        if (u == 0 && both) {
+          const float2 o = s_ml[r];
+          const float mn = fmaxf(m, o.x);
+          const float b = mn == -INFINITY ? 0.f : mn;
+          f0 = fast_exp2((m - b) * sc);
+          f1 = fast_exp2((o.x - b) * sc);
+          l = l * f0 + o.y * f1;
+          m = mn;
         }
       }
       tc_fence_after();
+      const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
       if ((!narrow || u == 0) && active) {
-        const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
-        const long long orow = tok * a.Hq + head;
+        const bool valid = r < nr;
+        const long long orow = (w.s.bos + tk) * a.Hq + w.h * w.G + (row - tk * w.G);
         const float inv = l == 0.f ? 0.f : 1.0f / l;
-        const int slot = 2 * blockIdx.x + (cut0 ? 0 : 1);
-        const long long prow = (long long)slot * kRowsItem + base + r;
-#pragma unroll
+        const long long prow =
+            (long long)(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRowsItem + base + r;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(tO + c, o);
@@ -649,9 +748,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             for (int e = 0; e < 4; ++e) {
               uint32_t x[4];
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-                x[t] = l == 0.f ? 0u
-                                : pack_bf16(o[8 * e + 2 * t] * inv, o[8 * e + 2 * t + 1] * inv);
+              for (int q = 0; q < 4; ++q)
+                x[q] = l == 0.f ? 0u
+                                : pack_bf16(o[8 * e + 2 * q] * inv, o[8 * e + 2 * q + 1] * inv);
               dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
@@ -666,24 +765,19 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       }
       tc_fence_before();
       if (narrow) group_sync(1, 256);
-      if (tid == 0) {
-        // (the last item of the stretch leaves its header)
-        if (w.left - (w.v1 - w.v0) <= 0) {
-          Header hd;
-          const bool tail = w.v0 == 0 && w.v1 < w.g.nt;
-          const long long e = plan.end - (w.v1 - w.g.nt);  // the item's end in the line
-          hd.n = tail ? w.n : -1;
-          hd.h = w.h;
-          hd.rt = w.rt;
-          hd.last = (int)((e * gridDim.x + plan.total - 1) / plan.total - 1);
-          hd.total = plan.total;
-          headers[blockIdx.x] = hd;
-        }
+      if (!cut0 && cut1) {  // it starts here and goes on: only the stretch's last item does
+        hd.rows = w.g.rows;
+        hd.row0 = w.g.row0;
+        hd.h = w.h;
+        hd.nt = w.g.nt;
+        hd.bos = w.s.bos;
+        hd.start = plan.end - (kOverhead + w.v1);
+        hd.total = plan.total;
       }
       pos += 2 * n;
       live = w.next(a);
     }
-    if (tid == 0 && plan.first == plan.end) headers[blockIdx.x].n = -1;
+    if (tid == 0) headers[blockIdx.x] = hd;
   }
   tc_fence_before();
   __syncthreads();
@@ -695,8 +789,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 }
 
 // Joins the partial results of an item that was cut: the CTA it starts in has it in its second
-// slot, the following ones (up to the header's last) in their first.  Block (c, i): the item
-// that CTA c's stretch ends in, rows 32 i .. 32 i + 31, one warp per row at a time.
+// slot, the following ones in their first.  Blocks (c, .): the item that starts in CTA c's
+// stretch, one warp per row.  A lane first looks up one part's (m, l), so that the parts'
+// outputs are then independent loads.
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int P,
                                                          const Header* headers,
@@ -705,31 +800,58 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int P,
   constexpr int E = D / 32;
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const Header hd = headers[c];
-  if (hd.n < 0) return;
-  const Seq s = load_seq(a, hd.n);
-  const int G = a.Hq / a.Hkv;
-  const int row0 = hd.rt * kRowsItem;
-  const int rows = min(kRowsItem, s.len * G - row0);
-  for (int i = 0; i < 4; ++i) {
-    const int r = blockIdx.y * 32 + i * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < hd.rows; r += gridDim.y * 8) {
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int k = c; k <= hd.last; ++k) {
-      if (k > c && (long long)k * hd.total / P == (long long)(k + 1) * hd.total / P) continue;
-      const long long at = (long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r;
-      const float2 ml = part_ml[at];
-      if (ml.y == 0.f) continue;  // nothing seen in this part
-      const float mn = (ml.x > m || ml.x != ml.x) ? ml.x : m;
-      const float f = exp2f(m - mn), g = exp2f(ml.x - mn);
-      m = mn;
-      l = l * f + ml.y * g;
+    const long long end = hd.start + kOverhead + hd.nt;  // the item's end in the line
+    for (int k0 = c; k0 < P && (long long)k0 * hd.total / P < end; k0 += 32) {
+      const int k = k0 + lane;
+      // the CTA's tiles of the item, if it has any
+      const long long first = (long long)k * hd.total / P - hd.start - kOverhead;
+      const long long last = min((long long)(k + 1) * hd.total / P - hd.start - kOverhead,
+                                 (long long)hd.nt);
+      const bool has = k < P && last > max(first, 0ll);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (has) ml = part_ml[(long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r];
+      const bool some = ml.y != 0.f;  // (a NaN is something)
+      float mk = some ? ml.x : -INFINITY;
+      float mn = mk;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + part_o[at * D + e * 32 + lane] * g;
+      for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+      mn = fmaxf(mn, m);
+      const float b = mn == -INFINITY ? 0.f : mn;
+      const float g = some ? exp2f(mk - b) : 0.f;  // weight of the lane's part
+      const float f = exp2f(m - b);
+      m = mn;
+      l = l * f + warp_sum(some ? ml.y * g : 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      unsigned parts = __ballot_sync(0xffffffffu, some);
+      while (parts) {
+        constexpr int U = 4;  // parts in flight
+        float x[U][E], gw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int j = parts ? __ffs(parts) - 1 : -1;
+          parts &= parts - 1;
+          gw[i] = __shfl_sync(0xffffffffu, g, max(j, 0));
+          const int kk = k0 + max(j, 0);
+          const float* src =
+              part_o + ((long long)(2 * kk + (kk == c ? 1 : 0)) * kRowsItem + r) * D + lane;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[i][e] = j >= 0 ? src[e * 32] : 0.f;
+          if (j < 0) gw[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += x[i][e] * gw[i];
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const long long row = (s.bos + (row0 + r) / G) * a.Hq + hd.h * G + (row0 + r) % G;
+    const int tk = div_g(a, hd.row0 + r), G = a.Hq / a.Hkv;
+    const long long row = (hd.bos + tk) * a.Hq + hd.h * G + (hd.row0 + r - tk * G);
 #pragma unroll
     for (int e = 0; e < E; ++e)
       static_cast<__nv_bfloat16*>(a.out)[row * D + e * 32 + lane] =
@@ -755,7 +877,12 @@ bool cache_map(CUtensorMap* map, const void* base, const PagedArgs& a) {
 constexpr int kCtas = 152;  // one per SM
 
 template <int D>
-cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
+cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
+  // x / G = (mulhi(x, g_mul) + x) >> g_shift for x < 2^31
+  const uint32_t G = (uint32_t)(a.Hq / a.Hkv);
+  a.g_shift = 0;
+  while ((1u << a.g_shift) < G) ++a.g_shift;
+  a.g_mul = (uint32_t)((((1ull << a.g_shift) - G) << 32) / G + 1);
   CUtensorMap kmap{}, vmap{};
   if (a.num_pages > 0 && a.max_pages > 0)
     if (!cache_map(&kmap, a.k_cache, a) || !cache_map(&vmap, a.v_cache, a))
@@ -770,7 +897,10 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, kmap, vmap, headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_join_kernel<D><<<dim3(kCtas, kRowsItem / 32), 256, 0, st>>>(a, kCtas, headers, po, ml);
+  // a warp per row up to the largest item's rows, few blocks where many sequences share them
+  const long long rows = (long long)a.total_T * G;
+  const unsigned by = (unsigned)((rows < kRowsItem ? rows : kRowsItem) + 7) / 8;
+  paged_join_kernel<D><<<dim3(kCtas, by < 8 ? by : 8), 256, 0, st>>>(a, kCtas, headers, po, ml);
   return cudaGetLastError();
 }
 
