@@ -344,6 +344,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -468,73 +480,91 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
           mbar_wait(&bars.kv_full[i % NS], (i / NS) & 1, 100000000ull);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        const uint32_t idesc_s = make_idesc(1, 128, kKeys);
-        const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
-        const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
-        uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-        int qtile1 = 0;
-        auto scores = [&](int u, uint32_t at, bool release, bool last_q) {
-          const uint32_t st = at % NS;
-          wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
-          if (!dead) {
-            tc_fence_after();
-            const uint32_t q = q0 + (u ? qtile1 : 0) * C::kQBytes;
+      // The whole warp walks and waits, one lane issues.  Addresses are made warp-uniform
+      // before the issuing branch: from values of one lane each product costs conversions
+      // that made eight of them take 800 to 1200 cycles to issue, twice their run time.
+      const uint32_t idesc_s = make_idesc(1, 128, kKeys);
+      const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
+      const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
+      const bool leader = elect_one();
+      uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+      int qtile1 = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        wait_or_die(bar, parity, dead);
+        dead = __any_sync(0xffffffffu, dead);
+      };
+      auto scores = [&](int u, uint32_t at, bool release, bool last_q) {
+        const uint32_t st = at % NS;
+        wait(&bars.kv_full[st], (at / NS) & 1);
+        tc_fence_after();
+        const uint32_t k = __shfl_sync(0xffffffffu, kv0 + st * C::kStageBytes, 0);
+        const uint32_t q = __shfl_sync(0xffffffffu, q0 + (u ? qtile1 : 0) * C::kQBytes, 0);
+        const uint64_t kd = make_sdesc(k, 16, 1024, kSwizzle128);
+        const uint64_t qd = make_sdesc(q, 16, 1024, kSwizzle128);
+        if (leader) {
+          if (!dead)
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              mma_ss(tm + kColS + 128 * u, sw128_kdesc<2>(q, 128, s),
-                     sw128_kdesc<2>(kv0 + st * C::kStageBytes, 128, s), idesc_s, s > 0);
-          }
+            for (int s = 0; s < D / 16; ++s) {
+              // the K step's 32 bytes, in 16-byte units; 64-column blocks are 16 KB apart
+              const uint64_t off = (s / 4) * (kKeys * 128 / 16) + (s % 4) * 2;
+              mma_ss(tmu + kColS + 128 * u, qd + off, kd + off, idesc_s, s > 0);
+            }
           mma_commit(&bars.s_full[u]);
           if (release) mma_commit(&bars.kv_empty[st]);
           if (last_q) mma_commit(&bars.q_empty[u ? qtile1 : 0]);
-        };
-        auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
-          const uint32_t st = at % NS;
-          wait_or_die(&bars.kv_full[st], (at / NS) & 1, dead);
-          wait_or_die(&bars.p_full[u], np[u] & 1, dead);
-          ++np[u];
-          if (!dead) {
-            tc_fence_after();
+        }
+        __syncwarp();
+      };
+      auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
+        const uint32_t st = at % NS;
+        wait(&bars.kv_full[st], (at / NS) & 1);
+        wait(&bars.p_full[u], np[u] & 1);
+        ++np[u];
+        tc_fence_after();
+        const uint32_t v = __shfl_sync(0xffffffffu, kv0 + st * C::kStageBytes, 0);
+        const uint64_t vd = make_sdesc(v, kKeys * 128, 1024, kSwizzle128);
+        if (leader) {
+          if (!dead)
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
-              mma_ts(tm + kColO + 128 * u, tm + kColS + 128 * u + 8 * s,
-                     make_sdesc(kv0 + st * C::kStageBytes + uint32_t(s) * 2048u, kKeys * 128u,
-                                1024u, kSwizzle128),
+              mma_ts(tmu + kColO + 128 * u, tmu + kColS + 128 * u + 8 * s, vd + s * (2048 / 16),
                      idesc_o, !(first && s == 0));
-          }
           if (release) mma_commit(&bars.kv_empty[st]);
           if (last) mma_commit(&bars.o_full[u]);
-        };
-        while (live) {
-          const int n = w.tiles();
-          const bool narrow = w.narrow();
-          for (int u = 0; u < (narrow ? 1 : 2); ++u) {
-            wait_or_die(&bars.q_full[u], nq[u] & 1, dead);
-            ++nq[u];
-          }
-          qtile1 = narrow ? 0 : 1;
-          if (narrow) {
-            scores(0, pos + ring_k(true, 0), true, n == 1);
-            if (n > 1) scores(1, pos + ring_k(true, 1), true, n == 2);
-            for (int i = 0; i < n; ++i) {
-              values(i & 1, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
-              if (i + 2 < n) scores(i & 1, pos + ring_k(true, i + 2), true, i + 3 == n);
-            }
-          } else {
-            scores(0, pos, false, n == 1);
-            scores(1, pos, true, n == 1);
-            for (int i = 0; i < n; ++i)
-              for (int u = 0; u < 2; ++u) {
-                values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
-                if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1, i + 2 == n);
-              }
-          }
-          pos += 2 * n;
-          live = w.next(a);
         }
+        __syncwarp();
+      };
+      while (live) {
+        const int n = w.tiles();
+        const bool narrow = w.narrow();
+        for (int u = 0; u < (narrow ? 1 : 2); ++u) {
+          wait(&bars.q_full[u], nq[u] & 1);
+          ++nq[u];
+        }
+        qtile1 = narrow ? 0 : 1;
+        if (narrow) {
+          scores(0, pos + ring_k(true, 0), true, n == 1);
+          if (n > 1) scores(1, pos + ring_k(true, 1), true, n == 2);
+          for (int i = 0; i < n; ++i) {
+            const int u = i & 1;
+            values(u, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
+            if (i + 2 < n) scores(u, pos + ring_k(true, i + 2), true, i + 3 == n);
+          }
+        } else {
+          scores(0, pos, false, n == 1);
+          scores(1, pos, true, n == 1);
+          for (int i = 0; i < n; ++i) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
+              if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1, i + 2 == n);
+            }
+          }
+        }
+        pos += 2 * n;
+        live = w.next(a);
       }
-      __syncwarp();
     } else {
       // Query rows of the item's tile t, as soon as the products on the last item's are done.
       const int t = warp - kMmaWarp - 1;
@@ -618,15 +648,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                 if (!(bits >> c & 1)) s[32 * q + c] = -INFINITY;
             }
           }
-          float mx4[8];
+          float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) mx4[c] = s[c];
+          for (int c = 4; c < 124; c += 8)
 #pragma unroll
-          for (int c = 8; c < 128; c += 8)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mx4[e] = fmaxf(mx4[e], s[c + e]);
-          const float mx = fmaxf(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])),
-                                 fmaxf(fmaxf(mx4[4], mx4[5]), fmaxf(mx4[6], mx4[7])));
+            for (int e = 0; e < 4; ++e) mx4[e] = max3(mx4[e], s[c + 2 * e], s[c + 2 * e + 1]);
+          const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3],
+                                max3(max3(s[124], s[125], s[126]), s[127], s[127]));
           const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
           if (__any_sync(0xffffffffu, grow)) {
             const float mn = grow ? mx : m;
