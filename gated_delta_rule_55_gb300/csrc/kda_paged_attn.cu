@@ -38,8 +38,8 @@ __device__ unsigned int g_paged_error;  // bit 6: a bounded wait gave up
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kRowsUnit = 128;   // query rows of a unit
 constexpr int kRowsItem = 256;
-constexpr int kThreads = 384;    // two softmax warpgroups; the load and the product warp
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;    // two softmax warpgroups, and one of the warps below
+constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10: one per unit */, kQueryWarp = 11;
 // Registers: 168 a thread at launch (3 x 128 threads), moved to the softmax warpgroups:
 // 2 x 216 + 72 = 3 x 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
@@ -290,39 +290,39 @@ __device__ __forceinline__ uint32_t ring_v(bool narrow, int i, int n) {
   return narrow ? uint32_t(min(2 * i + 2, 2 * n - 1)) : uint32_t(2 * i + 1);
 }
 
+// The unit (0 or 1) whose tile entry e of a narrow item's ring order is.
+__device__ __forceinline__ int ring_owner(int e, int n) {
+  const int i = e == 0 ? 0 : e == 2 * n - 1 ? n - 1 : e & 1 ? (e + 1) / 2 : e / 2 - 1;
+  return i & 1;
+}
+
 // ------------------------------------------------------------------------ small pieces
 
-// 128 consecutive columns of the thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+// 32 consecutive columns of the thread's lane: the load, and the wait after which (and only
+// then) its registers may be read.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
-      "%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,"
-      "%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,"
-      "%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,"
-      "%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,"
-      "%126,%127"
-      "}, [%128];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
-        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
-        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
-        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
-        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
-        "=f"(v[64]), "=f"(v[65]), "=f"(v[66]), "=f"(v[67]), "=f"(v[68]), "=f"(v[69]), "=f"(v[70]), "=f"(v[71]),
-        "=f"(v[72]), "=f"(v[73]), "=f"(v[74]), "=f"(v[75]), "=f"(v[76]), "=f"(v[77]), "=f"(v[78]), "=f"(v[79]),
-        "=f"(v[80]), "=f"(v[81]), "=f"(v[82]), "=f"(v[83]), "=f"(v[84]), "=f"(v[85]), "=f"(v[86]), "=f"(v[87]),
-        "=f"(v[88]), "=f"(v[89]), "=f"(v[90]), "=f"(v[91]), "=f"(v[92]), "=f"(v[93]), "=f"(v[94]), "=f"(v[95]),
-        "=f"(v[96]), "=f"(v[97]), "=f"(v[98]), "=f"(v[99]), "=f"(v[100]), "=f"(v[101]), "=f"(v[102]), "=f"(v[103]),
-        "=f"(v[104]), "=f"(v[105]), "=f"(v[106]), "=f"(v[107]), "=f"(v[108]), "=f"(v[109]), "=f"(v[110]), "=f"(v[111]),
-        "=f"(v[112]), "=f"(v[113]), "=f"(v[114]), "=f"(v[115]), "=f"(v[116]), "=f"(v[117]), "=f"(v[118]), "=f"(v[119]),
-        "=f"(v[120]), "=f"(v[121]), "=f"(v[122]), "=f"(v[123]), "=f"(v[124]), "=f"(v[125]), "=f"(v[126]), "=f"(v[127])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_finish(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
+                 "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // Packed pairs of fp32: a b + c, a + b.
@@ -369,6 +369,18 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
       "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -378,7 +390,7 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
 }
 
 struct Bars {
-  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], turn[2];
 };
 
 // A wait that gives up marks the thread dead: it then runs through the rest of its work
@@ -413,14 +425,15 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars.kv_full[i], 1);
-      mbar_init(&bars.kv_empty[i], 1);
+      mbar_init(&bars.kv_empty[i], 2);  // both units let an entry go
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&bars.q_full[u], 1);
-      mbar_init(&bars.q_empty[u], 1);
+      mbar_init(&bars.q_empty[u], 2);
       mbar_init(&bars.s_full[u], 1);
       mbar_init(&bars.p_full[u], 4);
       mbar_init(&bars.o_full[u], 1);
+      mbar_init(&bars.turn[u], 1);
     }
     fence_mbar_init();
   }
@@ -479,101 +492,125 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       if (dead)
         for (uint32_t i = pos > NS ? pos - NS : 0; i < pos; ++i)
           mbar_wait(&bars.kv_full[i % NS], (i / NS) & 1, 100000000ull);
-    } else if (warp == kMmaWarp) {
-      // The whole warp walks and waits, one lane issues.  Addresses are made warp-uniform
-      // before the issuing branch: from values of one lane each product costs conversions
-      // that made eight of them take 800 to 1200 cycles to issue, twice their run time.
+    } else if (warp < kQueryWarp) {
+      // Products of unit u.  Each unit has a warp, so that one's waits pass while the tensor
+      // cores work for the other.  The whole warp walks and waits, one lane issues.  Addresses
+      // are made warp-uniform before the issuing branch: from values of one lane, eight
+      // products took 800 to 1200 cycles to issue, twice their run time.
+      const int u = warp - kMmaWarp;
       const uint32_t idesc_s = make_idesc(1, 128, kKeys);
       const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
-      const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
+      const uint32_t tmu = __shfl_sync(0xffffffffu, tm + 128 * u, 0);
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
       const bool leader = elect_one();
-      uint32_t pos = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-      int qtile1 = 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        wait_or_die(bar, parity, dead);
-        dead = __any_sync(0xffffffffu, dead);
+      uint32_t pos = 0, seen = 0, np = 0, items = 0, wides = 0, turns = 0;
+      // Ring entries up to `at` have landed.  Every entry is waited for in turn, and the other
+      // unit's are let go at once: a stage is refilled only when both units have passed it, so
+      // no barrier is ever more than the one phase away that a parity can tell.
+      auto ready = [&](uint32_t at, bool narrow, int n) {
+        for (; seen != at + 1; ++seen) {
+          wait_or_die(&bars.kv_full[seen % NS], (seen / NS) & 1, dead);
+          if (narrow && ring_owner((int)(seen - pos), n) != u && leader)
+            mbar_arrive(&bars.kv_empty[seen % NS]);
+        }
       };
-      auto scores = [&](int u, uint32_t at, bool release, bool last_q) {
-        const uint32_t st = at % NS;
-        wait(&bars.kv_full[st], (at / NS) & 1);
-        tc_fence_after();
-        const uint32_t k = __shfl_sync(0xffffffffu, kv0 + st * C::kStageBytes, 0);
-        const uint32_t q = __shfl_sync(0xffffffffu, q0 + (u ? qtile1 : 0) * C::kQBytes, 0);
+      auto stage = [&](uint32_t at) {
+        return __shfl_sync(0xffffffffu, kv0 + at % NS * C::kStageBytes, 0);
+      };
+      auto scores = [&](uint32_t q, uint32_t k) {  // S = Q K^T
         const uint64_t kd = make_sdesc(k, 16, 1024, kSwizzle128);
         const uint64_t qd = make_sdesc(q, 16, 1024, kSwizzle128);
-        if (leader) {
-          if (!dead)
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-              // the K step's 32 bytes, in 16-byte units; 64-column blocks are 16 KB apart
-              const uint64_t off = (s / 4) * (kKeys * 128 / 16) + (s % 4) * 2;
-              mma_ss(tmu + kColS + 128 * u, qd + off, kd + off, idesc_s, s > 0);
-            }
-          mma_commit(&bars.s_full[u]);
-          if (release) mma_commit(&bars.kv_empty[st]);
-          if (last_q) mma_commit(&bars.q_empty[u ? qtile1 : 0]);
+        for (int s = 0; s < D / 16; ++s) {
+          // the K step's 32 bytes, in 16-byte units; 64-column blocks are 16 KB apart
+          const uint64_t off = (s / 4) * (kKeys * 128 / 16) + (s % 4) * 2;
+          mma_ss(tmu + kColS, qd + off, kd + off, idesc_s, s > 0);
         }
-        __syncwarp();
       };
-      auto values = [&](int u, uint32_t at, bool first, bool release, bool last) {
-        const uint32_t st = at % NS;
-        wait(&bars.kv_full[st], (at / NS) & 1);
-        wait(&bars.p_full[u], np[u] & 1);
-        ++np[u];
-        tc_fence_after();
-        const uint32_t v = __shfl_sync(0xffffffffu, kv0 + st * C::kStageBytes, 0);
+      auto values = [&](uint32_t v, bool first) {  // O (+)= P V
         const uint64_t vd = make_sdesc(v, kKeys * 128, 1024, kSwizzle128);
-        if (leader) {
-          if (!dead)
 #pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              mma_ts(tmu + kColO + 128 * u, tmu + kColS + 128 * u + 8 * s, vd + s * (2048 / 16),
-                     idesc_o, !(first && s == 0));
-          if (release) mma_commit(&bars.kv_empty[st]);
-          if (last) mma_commit(&bars.o_full[u]);
-        }
-        __syncwarp();
+        for (int s = 0; s < kKeys / 16; ++s)
+          mma_ts(tmu + kColO, tmu + kColS + 8 * s, vd + s * (2048 / 16), idesc_o,
+                 !(first && s == 0));
       };
       while (live) {
         const int n = w.tiles();
         const bool narrow = w.narrow();
-        for (int u = 0; u < (narrow ? 1 : 2); ++u) {
-          wait(&bars.q_full[u], nq[u] & 1);
-          ++nq[u];
-        }
-        qtile1 = narrow ? 0 : 1;
-        if (narrow) {
-          scores(0, pos + ring_k(true, 0), true, n == 1);
-          if (n > 1) scores(1, pos + ring_k(true, 1), true, n == 2);
-          for (int i = 0; i < n; ++i) {
-            const int u = i & 1;
-            values(u, pos + ring_v(true, i, n), i < 2, true, i + 2 >= n);
-            if (i + 2 < n) scores(u, pos + ring_k(true, i + 2), true, i + 3 == n);
-          }
-        } else {
-          scores(0, pos, false, n == 1);
-          scores(1, pos, true, n == 1);
-          for (int i = 0; i < n; ++i) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              values(u, pos + ring_v(false, i, n), i == 0, u == 1, i + 1 == n);
-              if (i + 1 < n) scores(u, pos + ring_k(false, i + 1), u == 1, i + 2 == n);
+        const int tile = narrow ? 0 : u;  // of the query rows
+        const uint32_t q = __shfl_sync(0xffffffffu, q0 + tile * C::kQBytes, 0);
+        const int first = narrow ? u : 0, by = narrow ? 2 : 1;
+        // (the second tile of a wide item is filled after its first, so neither barrier gets
+        // two phases ahead of a unit that does not wait on it)
+        wait_or_die(&bars.q_full[tile], (tile ? wides : items) & 1, dead);
+        ++items;
+        wides += !narrow;
+        if (first < n) {
+          // the first scores
+          const uint32_t k_at = pos + ring_k(narrow, first);
+          ready(k_at, narrow, n);
+          tc_fence_after();
+          const uint32_t k = stage(k_at);
+          if (leader) {
+            if (!dead) scores(q, k);
+            mma_commit(&bars.s_full[u]);
+            mma_commit(&bars.kv_empty[k_at % NS]);
+            if (first + by >= n) {  // (a wide item's tile has one user, who counts for two)
+              mma_commit(&bars.q_empty[tile]);
+              if (!narrow) mma_commit(&bars.q_empty[tile]);
             }
           }
+          __syncwarp();
+        } else if (leader) {
+          mbar_arrive(&bars.q_empty[tile]);
         }
+        // a tile's values, then the unit's next scores
+        for (int i = first; i < n; i += by) {
+          const bool more = i + by < n;
+          const uint32_t v_at = pos + ring_v(narrow, i, n), k_at = pos + ring_k(narrow, i + by);
+          ready(more ? max(v_at, k_at) : v_at, narrow, n);
+          const uint32_t v = stage(v_at), k = stage(k_at);
+          wait_or_die(&bars.p_full[u], np & 1, dead);
+          ++np;
+          // A wide item's units take turns: interleaved, both would get their scores late and
+          // their softmaxes would fall together; one after the other, one unit's softmax runs
+          // beside the other's products.
+          if (!narrow) {
+            wait_or_die(&bars.turn[u], (turns & 1) ^ (u == 0), dead);
+            ++turns;
+          }
+          tc_fence_after();
+          if (leader) {
+            if (!dead) {
+              values(v, i == first);
+              if (more) scores(q, k);
+            }
+            if (!narrow) mbar_arrive(&bars.turn[u ^ 1]);
+            mma_commit(more ? &bars.s_full[u] : &bars.o_full[u]);
+            mma_commit(&bars.kv_empty[v_at % NS]);
+            if (more) mma_commit(&bars.kv_empty[k_at % NS]);
+            if (more && i + 2 * by >= n) {
+              mma_commit(&bars.q_empty[tile]);
+              if (!narrow) mma_commit(&bars.q_empty[tile]);
+            }
+          }
+          __syncwarp();
+        }
+        ready(pos + 2 * n - 1, narrow, n);
         pos += 2 * n;
         live = w.next(a);
       }
     } else {
-      // Query rows of the item's tile t, as soon as the products on the last item's are done.
-      const int t = warp - kMmaWarp - 1;
-      uint32_t nq = 0;
+      // Query rows of the items, a tile of them as soon as the products on its last rows are
+      // done.
+      uint32_t nq[2] = {0, 0};
       while (live) {
-        const int rows = min(w.g.rows - t * kRowsUnit, kRowsUnit);
-        if (rows > 0) {
-          wait_or_die(&bars.q_empty[t], (nq & 1) ^ 1, dead);
-          ++nq;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int rows = min(w.g.rows - t * kRowsUnit, kRowsUnit);
+          if (rows <= 0) continue;
+          wait_or_die(&bars.q_empty[t], (nq[t] & 1) ^ 1, dead);
+          ++nq[t];
           constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
           const uint32_t dst = smem_u32(sQ + t * C::kQBytes);
           const int ch = lane % CH, row0 = w.g.row0 + t * kRowsUnit;
@@ -599,7 +636,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
     const uint32_t tO1 = tm + kColO + 128 + lanebits;
     const float sc = a.scale * kLog2E;
-    uint32_t pos = 0, ns = 0, no[2] = {0, 0};
+    uint32_t pos = 0, ns = 0, no = 0;
     Header hd;
     hd.rows = 0;
     bool live = w.start(a, plan);
@@ -623,76 +660,126 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
         tc_fence_after();
-        float s[128];
         if (active) {
-          tmem_ld128(tS, s);
           // a tile needs masks where some row of the unit does not see all of it
           const bool whole =
               ks + kKeys <= pos_first + 1 &&
               (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
-          if (!whole) {
-            // bits of the keys that the thread's row sees: not in the future, and in the
-            // window or among the sinks
-            const int hi = min(mypos - ks + 1, kKeys);  // keys [0, hi) of the tile
-            const int lo = a.window ? max(max(mypos, 0) - a.window - ks + 1, 0) : 0;
-            const int sk = a.window ? a.sinks - ks : 0;
+          bool done = false;
+          const uint64_t sc2 = pack2(sc, sc);
+          if (whole && mine > 0) {
+            // Weights against the maximum so far, which almost always stands, while the
+            // tile's own maximum is found beside them; the scores stay until that is known.
+            const float nb = m == -INFINITY ? 0.f : -m * sc;
+            const uint64_t nb2 = pack2(nb, nb);
+            uint64_t sum[4] = {0, 0, 0, 0};
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t p[64], s[2][32];
+            tmem_ld32_start(tS, s[0]);
+            tmem_ld32_finish(s[0]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+              if (q < 3) tmem_ld32_start(tS + 32 * (q + 1), s[(q + 1) & 1]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float s0 = __uint_as_float(s[q & 1][2 * e]);
+                const float s1 = __uint_as_float(s[q & 1][2 * e + 1]);
+                mx[e & 3] = max3(mx[e & 3], s0, s1);
+                float x, y;
+                unpack2(fma2(pack2(s0, s1), sc2, nb2), x, y);
+                x = fast_exp2(x);
+                y = fast_exp2(y);
+                sum[e & 3] = add2(sum[e & 3], pack2(x, y));
+                p[16 * q + e] = pack_bf16(x, y);
+              }
+              if (q < 3) tmem_ld32_finish(s[(q + 1) & 1]);
+            }
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            done = !__any_sync(0xffffffffu, top > m && (top - m) * sc > kRescale);
+            if (done) {
+              tmem_st32_nowait(tS, p);
+              tmem_st32_nowait(tS + 32, p + 32);
+              float x, y;
+              unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+              l += x + y;
+            }
+          }
+          if (!done) {
+            // The first tile, masked ones, and a maximum that has outgrown the range: the
+            // maximum first, then the weights (small code, run by few tiles).
+            // Bits of the keys that the thread's row sees: not in the future, and in the
+            // window or among the sinks.
+            const int hi = whole ? kKeys : mypos - ks + 1;  // keys [0, hi) of the tile
+            const int lo = a.window && !whole ? max(mypos, 0) - a.window - ks + 1 : 0;
+            const int sk = a.window ? a.sinks - ks : 0;
+            auto bits = [&](int q) -> uint32_t {
               auto below = [&](int x) -> uint32_t {  // bits [0, x - 32 q)
                 const int b = x - 32 * q;
                 return b <= 0 ? 0u : b >= 32 ? 0xffffffffu : (1u << b) - 1u;
               };
-              const uint32_t bits = below(hi) & (~below(lo) | below(sk));
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(bits >> c & 1)) s[32 * q + c] = -INFINITY;
-            }
-          }
-          float mx4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int c = 4; c < 124; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx4[e] = max3(mx4[e], s[c + 2 * e], s[c + 2 * e + 1]);
-          const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3],
-                                max3(max3(s[124], s[125], s[126]), s[127], s[127]));
-          const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? mx : m;
-            const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
-            m = mn;
-            l *= f;
-            if (mine > 0) {
+              return below(hi) & (~below(lo) | below(sk));
+            };
+            uint32_t s[32];
+            float mx = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tmem_ld16(tO + c, o);
-                uint32_t x[16];
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld32_start(tS + 32 * q, s);
+              const uint32_t b = bits(q);
+              tmem_ld32_finish(s);
+              float c4[4] = {mx, mx, mx, mx};
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
-                tmem_st16(tO + c, x);
+              for (int c = 0; c < 32; c += 2)
+                c4[c / 2 & 3] = max3(c4[c / 2 & 3],
+                                     b >> c & 1 ? __uint_as_float(s[c]) : -INFINITY,
+                                     b >> (c + 1) & 1 ? __uint_as_float(s[c + 1]) : -INFINITY);
+              mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+            }
+            const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mn = grow ? mx : m;
+              const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
+              m = mn;
+              l *= f;
+              if (mine > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(tO + c, o);
+                  uint32_t x[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
+                  tmem_st16(tO + c, x);
+                }
               }
             }
-          }
-          const float nb = m == -INFINITY ? 0.f : -m * sc;
-          const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(nb, nb);
-          uint64_t sum[4] = {0, 0, 0, 0};
+            const float nb = m == -INFINITY ? 0.f : -m * sc;
+            const uint64_t nb2 = pack2(nb, nb);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              // (weights of 32 keys take 16 columns, behind which every score still to be
+              // read lies)
+              tmem_ld32_start(tS + 32 * q, s);
+              const uint32_t b = bits(q);
+              tmem_ld32_finish(s);
+              uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x, y;
-              unpack2(fma2(pack2(s[c + 2 * e], s[c + 2 * e + 1]), sc2, nb2), x, y);
-              x = fast_exp2(x);
-              y = fast_exp2(y);
-              sum[e & 3] = add2(sum[e & 3], pack2(x, y));
-              p[e] = pack_bf16(x, y);
+              for (int e = 0; e < 16; ++e) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2,
+                             nb2),
+                        x, y);
+                x = b >> (2 * e) & 1 ? fast_exp2(x) : 0.f;
+                y = b >> (2 * e + 1) & 1 ? fast_exp2(y) : 0.f;
+                sum[e & 1] = add2(sum[e & 1], pack2(x, y));
+                p[e] = pack_bf16(x, y);
+              }
+              tmem_st16_nowait(tS + 16 * q, p);
             }
-            tmem_st16_nowait(tS + c / 2, p);
+            float x, y;
+            unpack2(add2(sum[0], sum[1]), x, y);
+            l += x + y;
           }
-          float x, y;
-          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
-          l += x + y;
         }
         // Keys of this tile that no row of the item sees: their values become zeros (weight
         // zero times what the cache holds there need not be zero).  Behind the wait for the
@@ -723,18 +810,17 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       // 2. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
       // unit 1's accumulator lanes too.
       if (mine > 0) {
-        wait_or_die(&bars.o_full[u], no[u] & 1, dead);
-        ++no[u];
+        wait_or_die(&bars.o_full[u], no & 1, dead);
+        ++no;
       }
-      if (u == 0) {
-        if (narrow && n > 1) wait_or_die(&bars.o_full[1], no[1] & 1, dead);
-        if (!narrow || n > 1) ++no[1];
-      }
+      tc_fence_after();
       float f0 = 1.f, f1 = 0.f;
       const bool both = narrow && n > 1;
       if (narrow) {
         if (u == 1) s_ml[r] = make_float2(m, l);
+        tc_fence_before();
         group_sync(1, 256);
+        tc_fence_after();
         if (u == 0 && both) {
           const float2 o = s_ml[r];
           const float mn = fmaxf(m, o.x);
@@ -745,7 +831,6 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           m = mn;
         }
       }
-      tc_fence_after();
       const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
       if ((!narrow || u == 0) && active) {
         const bool valid = r < nr;
