@@ -56,7 +56,7 @@ constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
 
 // An item counts kOverhead units beside its tiles: what its start and end cost a CTA (the
 // units lie before its tiles, and a cut among them falls to the item's first tile).
-constexpr int kOverhead = 1;
+constexpr int kOverhead = 2;
 
 struct Header {  // a CTA's part of the line, for the joining kernel
   int rows;       // rows of the item that starts in its stretch and is cut (0: none)
@@ -165,61 +165,89 @@ struct Walker {
   __device__ __forceinline__ bool narrow() const { return g.rows <= kRowsUnit; }
 };
 
-// Units of all items of sequence n (called by whole warps, one sequence per lane; a lane with
-// many row tiles is helped by its warp).
-__device__ __forceinline__ long long sequence_units(const PagedArgs& a, int n, int G) {
-  long long w = 0;
-  int nrt = 0;
+constexpr int kCtas = 152;      // one per SM
+constexpr int kPlanSeqs = 384;  // sequences whose units are looked at together
+
+// The first unit of CTA c's stretch of a line of `total` units.
+__device__ __forceinline__ long long stretch(long long total, int c) {
+  const long long q = total / kCtas;
+  return q * c + min((long long)c, total - q * kCtas);
+}
+
+// Units of the items n0 .. n0 + count - 1 (all heads) into s_units; all threads call.  A warp
+// takes a sequence and its lanes the row tiles, or, when there are many sequences, a lane takes
+// one and the warp helps the lanes whose sequence has many row tiles.
+__device__ void count_units(const PagedArgs& a, int n0, int count, long long* s_units) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
+  auto together = [&](const Seq& s, int nrt) {
+    long long x = 0;
+    for (int rt = lane; rt < nrt; rt += 32) x += geometry(a, s, G, rt).nt + kOverhead;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x * a.Hkv;
+  };
+  if (count <= 2 * (kThreads / 32)) {
+    for (int i = warp; i < count; i += kThreads / 32) {
+      const Seq s = load_seq(a, n0 + i);
+      const long long x = together(s, row_tiles(s, G));
+      if (lane == 0) s_units[i] = x;
+    }
+    return;
+  }
+  const int i = threadIdx.x;
   Seq s{};
-  if (n < a.N) {
-    s = load_seq(a, n);
+  int nrt = 0;
+  if (i < count) {
+    s = load_seq(a, n0 + i);
     nrt = row_tiles(s, G);
   }
-  const bool big = nrt > 4;
-  if (!big)
-    for (int rt = 0; rt < nrt; ++rt) w += geometry(a, s, G, rt).nt + kOverhead;
-  unsigned todo = __ballot_sync(0xffffffffu, big);
-  while (todo) {
+  long long x = 0;
+  if (nrt <= 4)
+    for (int rt = 0; rt < nrt; ++rt) x += (geometry(a, s, G, rt).nt + kOverhead) * (long long)a.Hkv;
+  for (unsigned todo = __ballot_sync(0xffffffffu, nrt > 4); todo; todo &= todo - 1) {
     const int src = __ffs(todo) - 1;
-    todo &= todo - 1;
     Seq t;
     t.bos = 0;
     t.len = __shfl_sync(0xffffffffu, s.len, src);
     t.kv = __shfl_sync(0xffffffffu, s.kv, src);
     t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
-    const int m = __shfl_sync(0xffffffffu, nrt, src);
-    long long x = 0;
-    for (int rt = threadIdx.x & 31; rt < m; rt += 32) x += geometry(a, t, G, rt).nt + kOverhead;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if ((int)(threadIdx.x & 31) == src) w = x;
+    const long long y = together(t, __shfl_sync(0xffffffffu, nrt, src));
+    if (lane == src) x = y;
   }
-  return w * a.Hkv;
+  if (i < kPlanSeqs) s_units[i] = x;
 }
 
-// The CTA's stretch of the line: all threads call.
-__device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
-  constexpr int W = kThreads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.Hq / a.Hkv;
-  const int rounds = (a.N + kThreads - 1) / kThreads;
-  long long mine = 0, sum = 0, total = 0;
-  // total, and (one round: the usual case) the thread's own sequence and the scan at once
-  for (int r = 0; r < rounds; ++r) {
-    mine = sequence_units(a, r * kThreads + tid, G);
-    sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    if (lane == 31) s_warp[warp] = sum;
+// The CTA's stretch of the line: all threads call.  s_units: kPlanSeqs entries.
+__device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_units) {
+  static_assert(kPlanSeqs == kThreads, "one sequence per thread");
+  constexpr int PER = kPlanSeqs / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rounds = (a.N + kPlanSeqs - 1) / kPlanSeqs;
+  // Every warp sums the whole line, then looks for its first unit in it; with one round (the
+  // usual case) over the same numbers.
+  long long mine[PER], sum = 0, total = 0;
+  auto load = [&](int r) {
+    const int count = min(a.N - r * kPlanSeqs, kPlanSeqs);
     __syncthreads();
-    for (int w = 0; w < W; ++w) total += s_warp[w];
-    if (rounds > 1) __syncthreads();
+    count_units(a, r * kPlanSeqs, count, s_units);
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = lane * PER + k;
+      mine[k] = i < count ? s_units[i] : 0;
+      sum += mine[k];
+    }
+  };
+  for (int r = 0; r < rounds; ++r) {
+    load(r);
+    long long x = sum;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    total += x;
   }
-  const long long P = gridDim.x, c = blockIdx.x;
-  const long long first = c * total / P, end = (c + 1) * total / P;
-  if (tid == 0) {
+  const long long first = stretch(total, blockIdx.x), end = stretch(total, blockIdx.x + 1);
+  if (threadIdx.x == 0) {
     plan.total = total;
     plan.first = first;
     plan.end = end;
@@ -227,56 +255,69 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_warp) {
   if (first == end) return;  // (uniform)
   long long before = 0;
   for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) {
-      mine = sequence_units(a, r * kThreads + tid, G);
-      sum = mine;
+    if (rounds > 1) load(r);
+    long long pre = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    const long long all = __shfl_sync(0xffffffffu, pre, 31);
+    if (first >= before + all) {  // (uniform)
+      before += all;
+      continue;
+    }
+    if (warp != 0) return;
+    pre += before - sum;
+    const unsigned b = __ballot_sync(0xffffffffu, first >= pre && first < pre + sum);
+    const int src = __ffs(b) - 1;
+    int n = 0;
+    long long off = 0, units = 1;
+    if (lane == src) {
+      off = first - pre;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        if (units > 0 && n == k) {  // not found yet
+          if (off < mine[k]) {
+            units = -mine[k];
+          } else {
+            off -= mine[k];
+            ++n;
+          }
+        }
+      }
+      n += r * kPlanSeqs + lane * PER;
+    }
+    n = __shfl_sync(0xffffffffu, n, src);
+    off = __shfl_sync(0xffffffffu, off, src);
+    units = -__shfl_sync(0xffffffffu, units, src);
+    const long long per = units / a.Hkv;  // of one head
+    const int h = (off >> 32) == 0 && (per >> 32) == 0 ? (int)((uint32_t)off / (uint32_t)per)
+                                                       : (int)(off / per);
+    off -= h * per;
+    const int G = a.Hq / a.Hkv;
+    const Seq s = load_seq(a, n);
+    const int nrt = row_tiles(s, G);
+    for (int base = 0; base < nrt; base += 32) {
+      const int rt = base + lane;
+      const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
+      int run = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
+        const int y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
       }
-      __syncthreads();
-      if (lane == 31) s_warp[warp] = sum;
-      __syncthreads();
-    }
-    long long pre = before;
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) pre += s_warp[w];
-      before += s_warp[w];
-    }
-    pre += sum - mine;  // tiles before this thread's sequence
-    const bool here = first >= pre && first < pre + mine;
-    const unsigned b = __ballot_sync(0xffffffffu, here);
-    if (b) {  // this warp has the sequence: find head, row tile and unit together
-      const int src = __ffs(b) - 1;
-      const int n = r * kThreads + warp * 32 + src;
-      const long long per = __shfl_sync(0xffffffffu, mine, src) / a.Hkv;
-      long long off = first - __shfl_sync(0xffffffffu, pre, src);
-      const int h = (int)(off / per);
-      off -= h * per;
-      const Seq s = load_seq(a, n);
-      const int nrt = row_tiles(s, G);
-      for (int base = 0; base < nrt; base += 32) {
-        const int rt = base + lane;
-        const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
-        int run = nt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += y;
-        }
-        if (off >= run - nt && off < run) {
-          plan.n = n;
-          plan.h = h;
-          plan.rt = rt;
-          plan.x = (int)(off - (run - nt));
-        }
-        const int all = __shfl_sync(0xffffffffu, run, 31);
-        if (off < all) break;
-        off -= all;
+      if (off >= run - nt && off < run) {
+        plan.n = n;
+        plan.h = h;
+        plan.rt = rt;
+        plan.x = (int)(off - (run - nt));
       }
+      const int here = __shfl_sync(0xffffffffu, run, 31);
+      if (off < here) break;
+      off -= here;
     }
-    if (first < before) break;  // (uniform)
+    return;
   }
 }
 
@@ -417,7 +458,6 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   float2* s_ml = reinterpret_cast<float2*>(sKV + NS * C::kStageBytes);  // [128], unit 1's m, l
   __shared__ Bars bars;
   __shared__ Plan plan;
-  __shared__ long long s_warp[kThreads / 32];
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -437,10 +477,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     fence_mbar_init();
   }
-  make_plan(a, plan, s_warp);
+  make_plan(a, plan, reinterpret_cast<long long*>(sKV));  // (the ring is not in use yet)
+  fence_async_smem();  // the plan's numbers lay where copies will land
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   const uint32_t tm = s_tmem;
   bool dead = false;
   Walker w;
@@ -449,6 +491,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     bool live = w.start(a, plan);
     if (warp == kLoadWarp) {
+      if (lane == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+      }
       const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
       const int pi = lane % ppt, half = lane / ppt;
       uint32_t pos = 0;  // entries pushed into the ring
@@ -706,7 +752,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           }
           if (!done) {
             // The first tile, masked ones, and a maximum that has outgrown the range: the
-            // maximum first, then the weights (small code, run by few tiles).
+            // maximum first, then the weights.
             // Bits of the keys that the thread's row sees: not in the future, and in the
             // window or among the sinks.
             const int hi = whole ? kKeys : mypos - ks + 1;  // keys [0, hi) of the tile
@@ -719,21 +765,28 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
               };
               return below(hi) & (~below(lo) | below(sk));
             };
-            uint32_t s[32];
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32_start(tS + 32 * q, s);
-              const uint32_t b = bits(q);
-              tmem_ld32_finish(s);
-              float c4[4] = {mx, mx, mx, mx};
+            uint32_t s[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32_start(tS + 32 * q, s[q]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32_finish(s[q]);
+            if (!whole) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t b = bits(q);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(b >> c & 1)) s[q][c] = 0xff800000u;  // -inf: weight zero
+              }
+            }
+            float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int c = 0; c < 32; c += 2)
-                c4[c / 2 & 3] = max3(c4[c / 2 & 3],
-                                     b >> c & 1 ? __uint_as_float(s[c]) : -INFINITY,
-                                     b >> (c + 1) & 1 ? __uint_as_float(s[c + 1]) : -INFINITY);
-              mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
-            }
+                c4[c / 2 & 3] =
+                    max3(c4[c / 2 & 3], __uint_as_float(s[q][c]), __uint_as_float(s[q][c + 1]));
+            const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
             const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx : m;
@@ -755,22 +808,17 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             const float nb = m == -INFINITY ? 0.f : -m * sc;
             const uint64_t nb2 = pack2(nb, nb);
             uint64_t sum[2] = {0, 0};
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
-              // (weights of 32 keys take 16 columns, behind which every score still to be
-              // read lies)
-              tmem_ld32_start(tS + 32 * q, s);
-              const uint32_t b = bits(q);
-              tmem_ld32_finish(s);
               uint32_t p[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x, y;
-                unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2,
-                             nb2),
+                unpack2(fma2(pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1])),
+                             sc2, nb2),
                         x, y);
-                x = b >> (2 * e) & 1 ? fast_exp2(x) : 0.f;
-                y = b >> (2 * e + 1) & 1 ? fast_exp2(y) : 0.f;
+                x = fast_exp2(x);
+                y = fast_exp2(y);
                 sum[e & 1] = add2(sum[e & 1], pack2(x, y));
                 p[e] = pack_bf16(x, y);
               }
@@ -906,25 +954,26 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 // stretch, one warp per row.  A lane first looks up one part's (m, l), so that the parts'
 // outputs are then independent loads.
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, int P,
-                                                         const Header* headers,
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Header* headers,
                                                          const float* part_o,
                                                          const float2* part_ml) {
   constexpr int E = D / 32;
   const int c = blockIdx.x, lane = threadIdx.x & 31;
+  // launched while the first kernel runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Header hd = headers[c];
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < hd.rows; r += gridDim.y * 8) {
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     const long long end = hd.start + kOverhead + hd.nt;  // the item's end in the line
-    for (int k0 = c; k0 < P && (long long)k0 * hd.total / P < end; k0 += 32) {
+    for (int k0 = c; k0 < kCtas && stretch(hd.total, k0) < end; k0 += 32) {
       const int k = k0 + lane;
       // the CTA's tiles of the item, if it has any
-      const long long first = (long long)k * hd.total / P - hd.start - kOverhead;
-      const long long last = min((long long)(k + 1) * hd.total / P - hd.start - kOverhead,
-                                 (long long)hd.nt);
-      const bool has = k < P && last > max(first, 0ll);
+      const long long first = stretch(hd.total, k) - hd.start - kOverhead;
+      const long long last =
+          min(stretch(hd.total, k + 1) - hd.start - kOverhead, (long long)hd.nt);
+      const bool has = k < kCtas && last > max(first, 0ll);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (has) ml = part_ml[(long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r];
       const bool some = ml.y != 0.f;  // (a NaN is something)
@@ -987,8 +1036,6 @@ bool cache_map(CUtensorMap* map, const void* base, const PagedArgs& a) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kCtas = 152;  // one per SM
-
 template <int D>
 cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   // x / G = (mulhi(x, g_mul) + x) >> g_shift for x < 2^31
@@ -1013,8 +1060,17 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   // a warp per row up to the largest item's rows, few blocks where many sequences share them
   const long long rows = (long long)a.total_T * G;
   const unsigned by = (unsigned)((rows < kRowsItem ? rows : kRowsItem) + 7) / 8;
-  paged_join_kernel<D><<<dim3(kCtas, by < 8 ? by : 8), 256, 0, st>>>(a, kCtas, headers, po, ml);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas, by < 8 ? by : 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, (const Header*)headers,
+                            (const float*)po, (const float2*)ml);
 }
 
 }  // namespace
