@@ -115,7 +115,7 @@ struct NormRopeArgs {
   void* dq;
   void* dk;
   float eps;
-  int T, Hq, Hkv, D, R, max_position, interleaved, num_pages, page_size;
+  int T, Hq, Hkv, D, R, max_position, interleaved, num_pages, page_size, page_shift;
 };
 
 // Attention over a paged cache (kda_paged_attention_fwd).

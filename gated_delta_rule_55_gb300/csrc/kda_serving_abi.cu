@@ -52,8 +52,9 @@ int fill_norm_rope(kda::NormRopeArgs& a, const void* query, const void* key,
   int s = check_stride(query_stride, (long long)Hq * D, T, dtype);
   if (s == KDA_OK) s = check_stride(key_stride, (long long)Hkv * D, T, dtype);
   if (s != KDA_OK) return s;
-  // units of the kernels' grids (at most one per token and head) stay inside a grid dimension
-  if ((double)T * ((double)Hq + 2.0 * Hkv) >= 2147483647.0) return KDA_ERR_TOO_LARGE;
+  // tokens and a token's units of work (at most one per head) are grid dimensions
+  if ((double)Hq + 2.0 * Hkv > 65535.0 || (double)T * (Hq + Hkv) * D >= kMaxElems)
+    return KDA_ERR_TOO_LARGE;
   a = kda::NormRopeArgs{};
   a.q = query; a.k = key; a.q_weight = query_weight; a.k_weight = key_weight;
   a.cos_table = cos_table; a.sin_table = sin_table; a.positions = positions; a.eps = eps;
@@ -157,6 +158,7 @@ int kda_qk_norm_rope_append(const void* query, const void* key, const void* valu
   if (T == 0) return KDA_OK;
   a.v = value; a.v_stride = value_stride; a.slots = slots; a.q_out = query_out;
   a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages; a.page_size = page_size;
+  a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   return launch_status(
       kda::launch_norm_rope(a, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
