@@ -145,6 +145,7 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* d_q_weight, float
                                  void* workspace, bool bf16, cudaStream_t stream);
 // Paged attention on the tensor cores: bf16, D = 64 or 128.
 bool paged_tc_supported(int D, bool bf16);
+bool paged_tc_index_ok(const PagedArgs& a);
 size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);

@@ -62,8 +62,8 @@ struct Header {  // a CTA's part of the line, for the joining kernel
   int rows;       // rows of the item that starts in its stretch and is cut (0: none)
   int row0, h;    // its first row and kv head
   int nt;         // its tiles
+  int start, total;  // its place in the line, the line's length
   long long bos;  // its sequence's first token
-  long long start, total;  // its place in the line, the line's length
 };
 
 // ------------------------------------------------------------------- items of the line
@@ -92,6 +92,15 @@ __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, i
   return g;
 }
 
+__device__ __forceinline__ Seq shfl_seq(const Seq& s, int src) {
+  Seq t;
+  t.bos = __shfl_sync(0xffffffffu, s.bos, src);
+  t.len = __shfl_sync(0xffffffffu, s.len, src);
+  t.kv = __shfl_sync(0xffffffffu, s.kv, src);
+  t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
+  return t;
+}
+
 __device__ __forceinline__ int tile_start(const Geometry& g, int v) {
   return (v < g.ns ? v : g.t_lo + v - g.ns) * kKeys;
 }
@@ -101,16 +110,17 @@ __device__ __forceinline__ int row_tiles(const Seq& s, int G) {
 }
 
 struct Plan {  // in shared memory
-  long long total, first, end;  // units of the line, this CTA's stretch [first, end)
-  int n, h, rt, x;              // where the stretch starts: an item and a unit of it
+  int total, first, end;  // units of the line, this CTA's stretch [first, end)
+  int n, h, rt, x;        // where the stretch starts: an item and a unit of it (n < 0: nowhere)
+  Seq s;                  // sequence n
 };
 
 // Walks the items of a CTA's stretch; every role of the CTA walks on its own.
 struct Walker {
   int n, h, rt, v0, v1;
   int nrt, G;
-  long long left;  // units of the stretch from the item's first one on
-  int units;       // units of the item in the stretch
+  int left;   // units of the stretch from the item's first one on
+  int units;  // units of the item in the stretch
   Seq s;
   Geometry g;
   int c1, c2, kv1;  // the next sequence's offsets and keys, loaded ahead
@@ -126,18 +136,18 @@ struct Walker {
   // The item's tiles among its units [x, ...); false when the stretch ends before the first (it
   // is the stretch's last item then, and the next CTA takes it whole).
   __device__ __forceinline__ bool enter(int x) {
-    const long long last = min((long long)(g.nt + kOverhead), x + left);
-    units = (int)(last - x);
+    const int last = min(g.nt + kOverhead, x + left);
+    units = last - x;
     v0 = max(x - kOverhead, 0);
-    v1 = max((int)last - kOverhead, 0);
+    v1 = max(last - kOverhead, 0);
     return v1 > v0;
   }
   __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
     left = p.end - p.first;
-    if (left <= 0) return false;
+    if (left <= 0 || p.n < 0) return false;
     G = a.Hq / a.Hkv;
     n = p.n; h = p.h; rt = p.rt;
-    s = load_seq(a, n);
+    s = p.s;
     ahead(a);
     nrt = row_tiles(s, G);
     g = geometry(a, s, G, rt);
@@ -169,153 +179,143 @@ constexpr int kCtas = 152;      // one per SM
 constexpr int kPlanSeqs = 384;  // sequences whose units are looked at together
 
 // The first unit of CTA c's stretch of a line of `total` units.
-__device__ __forceinline__ long long stretch(long long total, int c) {
-  const long long q = total / kCtas;
-  return q * c + min((long long)c, total - q * kCtas);
+__device__ __forceinline__ int stretch(int total, int c) {
+  const int q = (int)((unsigned)total / kCtas);
+  return q * c + min(c, total - q * kCtas);
 }
 
-// Units of the items n0 .. n0 + count - 1 (all heads) into s_units; all threads call.  A warp
-// takes a sequence and its lanes the row tiles, or, when there are many sequences, a lane takes
-// one and the warp helps the lanes whose sequence has many row tiles.
-__device__ void count_units(const PagedArgs& a, int n0, int count, long long* s_units) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
-  auto together = [&](const Seq& s, int nrt) {
-    long long x = 0;
-    for (int rt = lane; rt < nrt; rt += 32) x += geometry(a, s, G, rt).nt + kOverhead;
+// Units of one head's items of a sequence, its row tiles spread over the warp's lanes.
+__device__ __forceinline__ int head_units(const PagedArgs& a, const Seq& s, int G) {
+  int x = 0;
+  const int nrt = row_tiles(s, G);
+  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) x += geometry(a, s, G, rt).nt + kOverhead;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x * a.Hkv;
-  };
-  if (count <= 2 * (kThreads / 32)) {
-    for (int i = warp; i < count; i += kThreads / 32) {
-      const Seq s = load_seq(a, n0 + i);
-      const long long x = together(s, row_tiles(s, G));
-      if (lane == 0) s_units[i] = x;
-    }
-    return;
-  }
-  const int i = threadIdx.x;
-  Seq s{};
-  int nrt = 0;
-  if (i < count) {
-    s = load_seq(a, n0 + i);
-    nrt = row_tiles(s, G);
-  }
-  long long x = 0;
-  if (nrt <= 4)
-    for (int rt = 0; rt < nrt; ++rt) x += (geometry(a, s, G, rt).nt + kOverhead) * (long long)a.Hkv;
-  for (unsigned todo = __ballot_sync(0xffffffffu, nrt > 4); todo; todo &= todo - 1) {
-    const int src = __ffs(todo) - 1;
-    Seq t;
-    t.bos = 0;
-    t.len = __shfl_sync(0xffffffffu, s.len, src);
-    t.kv = __shfl_sync(0xffffffffu, s.kv, src);
-    t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
-    const long long y = together(t, __shfl_sync(0xffffffffu, nrt, src));
-    if (lane == src) x = y;
-  }
-  if (i < kPlanSeqs) s_units[i] = x;
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
-// The CTA's stretch of the line: all threads call.  s_units: kPlanSeqs entries.
-__device__ void make_plan(const PagedArgs& a, Plan& plan, long long* s_units) {
+// Notes the unit `off` of sequence n's units (`per` of them in each head) as the stretch's
+// start; a whole warp calls.
+__device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const Seq& s, int n,
+                                           int per, int off) {
+  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+  const int h = (int)((unsigned)off / (unsigned)per);
+  off -= h * per;
+  const int nrt = row_tiles(s, G);
+  for (int base = 0; base < nrt; base += 32) {
+    const int rt = base + lane;
+    const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
+    int run = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (off >= run - nt && off < run) {
+      plan.n = n;
+      plan.h = h;
+      plan.rt = rt;
+      plan.x = off - (run - nt);
+      plan.s = s;
+    }
+    const int here = __shfl_sync(0xffffffffu, run, 31);
+    if (off < here) break;
+    off -= here;
+  }
+}
+
+// The CTA's stretch of the line: all threads call.  s_units: kPlanSeqs entries.  The host has
+// made sure that the line's length fits 31 bits; offsets that overlap (against the call's
+// rules) can make it longer and the sums wrong, and then at worst no start is found.
+__device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
   static_assert(kPlanSeqs == kThreads, "one sequence per thread");
-  constexpr int PER = kPlanSeqs / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int W = kThreads / 32, kFew = 2 * W;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
   const int rounds = (a.N + kPlanSeqs - 1) / kPlanSeqs;
-  // Every warp sums the whole line, then looks for its first unit in it; with one round (the
-  // usual case) over the same numbers.
-  long long mine[PER], sum = 0, total = 0;
+  // Sequences r kPlanSeqs + ...: with few of them a warp takes two and its lanes the row tiles,
+  // with many a thread takes one, and its warp helps where there are many row tiles.
+  Seq s[2]{};
+  int per[2], count = 0, sum = 0;
+  if (threadIdx.x == 0) plan.n = -1;
   auto load = [&](int r) {
-    const int count = min(a.N - r * kPlanSeqs, kPlanSeqs);
+    count = min(a.N - r * kPlanSeqs, kPlanSeqs);
     __syncthreads();
-    count_units(a, r * kPlanSeqs, count, s_units);
+    if (count <= kFew) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (warp + k * W < count) s[k] = load_seq(a, r * kPlanSeqs + warp + k * W);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (warp + k * W < count) {
+          per[k] = head_units(a, s[k], G);
+          if (lane == 0) s_units[warp + k * W] = per[k] * a.Hkv;
+        }
+    } else {
+      const int i = threadIdx.x;
+      if (i < count) s[0] = load_seq(a, r * kPlanSeqs + i);
+      const int nrt = i < count ? row_tiles(s[0], G) : 0;
+      per[0] = 0;
+      if (nrt <= 4)
+        for (int rt = 0; rt < nrt; ++rt) per[0] += geometry(a, s[0], G, rt).nt + kOverhead;
+      for (unsigned todo = __ballot_sync(0xffffffffu, nrt > 4); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        const int y = head_units(a, shfl_seq(s[0], src), G);
+        if (lane == src) per[0] = y;
+      }
+      if (i < count) s_units[i] = per[0] * a.Hkv;
+    }
     __syncthreads();
     sum = 0;
+    for (int i = lane; i < count; i += 32) sum += s_units[i];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = lane * PER + k;
-      mine[k] = i < count ? s_units[i] : 0;
-      sum += mine[k];
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   };
+  int total = 0;
   for (int r = 0; r < rounds; ++r) {
     load(r);
-    long long x = sum;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    total += x;
+    total += sum;
   }
-  const long long first = stretch(total, blockIdx.x), end = stretch(total, blockIdx.x + 1);
+  const int first = stretch(total, blockIdx.x), end = stretch(total, blockIdx.x + 1);
   if (threadIdx.x == 0) {
     plan.total = total;
     plan.first = first;
     plan.end = end;
   }
   if (first == end) return;  // (uniform)
-  long long before = 0;
+  int before = 0;
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) load(r);
-    long long pre = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-    }
-    const long long all = __shfl_sync(0xffffffffu, pre, 31);
-    if (first >= before + all) {  // (uniform)
-      before += all;
+    if (first >= before + sum) {  // (uniform)
+      before += sum;
       continue;
     }
-    if (warp != 0) return;
-    pre += before - sum;
-    const unsigned b = __ballot_sync(0xffffffffu, first >= pre && first < pre + sum);
-    const int src = __ffs(b) - 1;
-    int n = 0;
-    long long off = 0, units = 1;
-    if (lane == src) {
-      off = first - pre;
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        if (units > 0 && n == k) {  // not found yet
-          if (off < mine[k]) {
-            units = -mine[k];
-          } else {
-            off -= mine[k];
-            ++n;
-          }
-        }
-      }
-      n += r * kPlanSeqs + lane * PER;
-    }
-    n = __shfl_sync(0xffffffffu, n, src);
-    off = __shfl_sync(0xffffffffu, off, src);
-    units = -__shfl_sync(0xffffffffu, units, src);
-    const long long per = units / a.Hkv;  // of one head
-    const int h = (off >> 32) == 0 && (per >> 32) == 0 ? (int)((uint32_t)off / (uint32_t)per)
-                                                       : (int)(off / per);
-    off -= h * per;
-    const int G = a.Hq / a.Hkv;
-    const Seq s = load_seq(a, n);
-    const int nrt = row_tiles(s, G);
-    for (int base = 0; base < nrt; base += 32) {
-      const int rt = base + lane;
-      const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
-      int run = nt;
+    // the sequence that holds the first unit, and the units before it
+    int n = -1, pre = before;
+    for (int base = 0; base < count; base += 32) {
+      const int mine = base + lane < count ? s_units[base + lane] : 0;
+      int run = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += y;
       }
-      if (off >= run - nt && off < run) {
-        plan.n = n;
-        plan.h = h;
-        plan.rt = rt;
-        plan.x = (int)(off - (run - nt));
+      const unsigned b = __ballot_sync(0xffffffffu, first < pre + run);
+      if (b) {
+        const int src = __ffs(b) - 1;
+        n = base + src;
+        pre += __shfl_sync(0xffffffffu, run - mine, src);
+        break;
       }
-      const int here = __shfl_sync(0xffffffffu, run, 31);
-      if (off < here) break;
-      off -= here;
+      pre += __shfl_sync(0xffffffffu, run, 31);
+    }
+    // its warp has it at hand
+    if (count <= kFew) {
+      if (n % W == warp)
+        note_start(a, plan, n < W ? s[0] : s[1], r * kPlanSeqs + n, n < W ? per[0] : per[1],
+                   first - pre);
+    } else if (n / 32 == warp) {
+      note_start(a, plan, shfl_seq(s[0], n & 31), r * kPlanSeqs + n,
+                 __shfl_sync(0xffffffffu, per[0], n & 31), first - pre);
     }
     return;
   }
@@ -462,6 +462,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
+  if (tid == 32 * kLoadWarp) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars.kv_full[i], 1);
@@ -477,7 +481,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     fence_mbar_init();
   }
-  make_plan(a, plan, reinterpret_cast<long long*>(sKV));  // (the ring is not in use yet)
+  make_plan(a, plan, reinterpret_cast<int*>(sKV));  // (the ring is not in use yet)
   fence_async_smem();  // the plan's numbers lay where copies will land
   tc_fence_before();
   __syncthreads();
@@ -491,10 +495,6 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     bool live = w.start(a, plan);
     if (warp == kLoadWarp) {
-      if (lane == 0) {
-        tma_prefetch_desc(&kmap);
-        tma_prefetch_desc(&vmap);
-      }
       const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
       const int pi = lane % ppt, half = lane / ppt;
       uint32_t pos = 0;  // entries pushed into the ring
@@ -966,14 +966,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Head
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    const long long end = hd.start + kOverhead + hd.nt;  // the item's end in the line
+    const int end = hd.start + kOverhead + hd.nt;  // the item's end in the line
     for (int k0 = c; k0 < kCtas && stretch(hd.total, k0) < end; k0 += 32) {
       const int k = k0 + lane;
       // the CTA's tiles of the item, if it has any
-      const long long first = stretch(hd.total, k) - hd.start - kOverhead;
-      const long long last =
-          min(stretch(hd.total, k + 1) - hd.start - kOverhead, (long long)hd.nt);
-      const bool has = k < kCtas && last > max(first, 0ll);
+      const int first = stretch(hd.total, k) - hd.start - kOverhead;
+      const int last = min(stretch(hd.total, k + 1) - hd.start - kOverhead, hd.nt);
+      const bool has = k < kCtas && last > max(first, 0);
       float2 ml = make_float2(-INFINITY, 0.f);
       if (has) ml = part_ml[(long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r];
       const bool some = ml.y != 0.f;  // (a NaN is something)
@@ -1076,6 +1075,13 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
 }  // namespace
 
 static_assert(sizeof(Header) * kCtas <= 8192, "headers");
+
+// Whether the line of key tiles, at the block table's capacity, fits the kernel's indices.
+bool paged_tc_index_ok(const PagedArgs& a) {
+  const double rows = (double)a.total_T * (a.Hq / a.Hkv) / kRowsItem + a.N;
+  const double tiles = (double)a.max_pages * a.page_size / kKeys + kOverhead + 2;
+  return rows * tiles * a.Hkv < 2147483647.0;
+}
 
 bool paged_tc_supported(int D, bool bf16) { return bf16 && (D == 64 || D == 128); }
 

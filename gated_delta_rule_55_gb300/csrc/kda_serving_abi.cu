@@ -53,7 +53,7 @@ int fill_norm_rope(kda::NormRopeArgs& a, const void* query, const void* key,
   if (s == KDA_OK) s = check_stride(key_stride, (long long)Hkv * D, T, dtype);
   if (s != KDA_OK) return s;
   // tokens and a token's units of work (at most one per head) are grid dimensions
-  if ((double)Hq + 2.0 * Hkv > 65535.0 || (double)T * (Hq + Hkv) * D >= kMaxElems)
+  if ((double)Hq + 2.0 * Hkv > 65535.0 || (double)T * ((double)Hq + 2.0 * Hkv) >= 2147483647.0)
     return KDA_ERR_TOO_LARGE;
   a = kda::NormRopeArgs{};
   a.q = query; a.k = key; a.q_weight = query_weight; a.k_weight = key_weight;
@@ -232,12 +232,6 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
       (double)max_pages * page_size > 2147483647.0 || (double)total_T * Hq > 2147483647.0 ||
       (double)N * max_pages >= kMaxElems || N > 65535 || Hkv > 65535)
     return KDA_ERR_TOO_LARGE;
-  const size_t need = kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype);
-  if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
-    return KDA_ERR_WORKSPACE;
-  const int s = kda::check_current_device();
-  if (s != KDA_OK) return s;
-  if (!work) return KDA_OK;
   kda::PagedArgs a{};
   a.q = query; a.q_stride = query_stride; a.k_cache = k_cache; a.v_cache = v_cache;
   a.block_table = block_table; a.cu_seqlens = cu_seqlens; a.kv_lens = kv_lens; a.out = out;
@@ -246,10 +240,17 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   // a window that no position can leave hides nothing
   a.window = (double)window >= (double)max_pages * page_size ? 0 : window;
   a.sinks = sinks;
+  const bool tensor_cores = kda::paged_tc_supported(D, dtype == KDA_BF16);
+  if (tensor_cores && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
+  const size_t need = kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype);
+  if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
+    return KDA_ERR_WORKSPACE;
+  const int s = kda::check_current_device();
+  if (s != KDA_OK) return s;
+  if (!work) return KDA_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(kda::paged_tc_supported(D, dtype == KDA_BF16)
-                           ? kda::launch_paged_tc(a, workspace, st)
-                           : kda::launch_paged_simt(a, dtype == KDA_BF16, workspace, st));
+  return launch_status(tensor_cores ? kda::launch_paged_tc(a, workspace, st)
+                                    : kda::launch_paged_simt(a, dtype == KDA_BF16, workspace, st));
 }
 
 }  // extern "C"

@@ -590,6 +590,9 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
  *   D = 64 or 128 runs on the tensor cores with bf16 softmax weights (fp32 sums), where a value
  *   that some token of the call sees must be finite for every token of that sequence; other
  *   configurations run in fp32.
+ *   There the kernel counts its work in tiles of 256 query rows by 128 keys, at the block
+ *   table's capacity: Hkv (total_T Hq / Hkv / 256 + N) (max_pages page_size / 128 + 4) must stay
+ *   below 2^31 (KDA_ERR_TOO_LARGE).
  *   workspace    at least kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype)
  *                bytes (0: none), 256-byte aligned, caller-owned, contents unspecified on
  *                return; calls that may overlap in time need one each.

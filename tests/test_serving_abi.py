@@ -101,7 +101,7 @@ def _attn(L, **over):
     (dict(page=256), -14), (dict(scale=float("inf")), -10), (dict(dtype=9), -7),
     (dict(kv=FAKE + 4), -6), (dict(lse=FAKE + 4), -6), (dict(qs=1000), -16),
     (dict(qs=1028), -16), (dict(pages=1 << 26), -11), (dict(maxp=1 << 26), -11),
-    (dict(N=65536), -11), (dict(ws=None), -12), (dict(ws=FAKE + 16), -12), (dict(wb=8), -12),
+    (dict(N=65536), -11), (dict(N=60000, maxp=1 << 20), -11), (dict(ws=None), -12), (dict(ws=FAKE + 16), -12), (dict(wb=8), -12),
 ])
 def test_paged_attention_refuses(L, over, code):
     assert _attn(L, **over) == code
