@@ -49,10 +49,14 @@ template <int D> struct Cfg {
   static constexpr int kStageBytes = kKeys * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kQBytes = kRowsUnit * D * 2;
+  // D = 64 leaves Tensor Memory for weights of their own (D = 128 keeps them over the scores):
+  // the next scores are then made while the softmax of the last is still running.
+  static constexpr bool kOwnP = D == 64;
   static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + 1024 + 512;
 };
 
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
+constexpr uint32_t kColP64 = kColO + 64;                     // weights, D = 64
 
 // An item counts kOverhead units beside its tiles: what its start and end cost a CTA (the
 // units lie before its tiles, and a cut among them falls to the item's first tile).
@@ -182,6 +186,12 @@ constexpr int kPlanSeqs = 384;  // sequences whose units are looked at together
 __device__ __forceinline__ int stretch(int total, int c) {
   const int q = (int)((unsigned)total / kCtas);
   return q * c + min(c, total - q * kCtas);
+}
+
+// The CTA whose stretch holds a unit.
+__device__ __forceinline__ int stretch_of(int total, int unit) {
+  const int q = (int)((unsigned)total / kCtas), more = total - q * kCtas;  // q + 1 units each
+  return unit < more * (q + 1) ? unit / (q + 1) : more + (unit - more * (q + 1)) / max(q, 1);
 }
 
 // Units of one head's items of a sequence, its row tiles spread over the warp's lanes.
@@ -431,7 +441,8 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
 }
 
 struct Bars {
-  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], turn[2];
+  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2],
+      turn[2];
 };
 
 // A wait that gives up marks the thread dead: it then runs through the rest of its work
@@ -475,6 +486,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       mbar_init(&bars.q_full[u], 1);
       mbar_init(&bars.q_empty[u], 2);
       mbar_init(&bars.s_full[u], 1);
+      mbar_init(&bars.s_empty[u], 4);
       mbar_init(&bars.p_full[u], 4);
       mbar_init(&bars.o_full[u], 1);
       mbar_init(&bars.turn[u], 1);
@@ -549,7 +561,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       const uint32_t tmu = __shfl_sync(0xffffffffu, tm + 128 * u, 0);
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
       const bool leader = elect_one();
-      uint32_t pos = 0, seen = 0, np = 0, items = 0, wides = 0, turns = 0;
+      uint32_t pos = 0, seen = 0, np = 0, items = 0, wides = 0, turns = 0, nscores = 0;
       // Ring entries up to `at` have landed.  Every entry is waited for in turn, and the other
       // unit's are let go at once: a stage is refilled only when both units have passed it, so
       // no barrier is ever more than the one phase away that a parity can tell.
@@ -577,8 +589,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         const uint64_t vd = make_sdesc(v, kKeys * 128, 1024, kSwizzle128);
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-          mma_ts(tmu + kColO, tmu + kColS + 8 * s, vd + s * (2048 / 16), idesc_o,
-                 !(first && s == 0));
+          mma_ts(tmu + kColO, tmu + (C::kOwnP ? kColP64 : kColS) + 8 * s, vd + s * (2048 / 16),
+                 idesc_o, !(first && s == 0));
+      };
+      // Weights of their own: scores wait only for the last ones to have been read.
+      auto scores_free = [&]() {
+        if (C::kOwnP) wait_or_die(&bars.s_empty[u], (nscores & 1) ^ 1, dead);
+        ++nscores;
       };
       while (live) {
         const int n = w.tiles();
@@ -595,6 +612,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           // the first scores
           const uint32_t k_at = pos + ring_k(narrow, first);
           ready(k_at, narrow, n);
+          scores_free();
           tc_fence_after();
           const uint32_t k = stage(k_at);
           if (leader) {
@@ -614,33 +632,64 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         for (int i = first; i < n; i += by) {
           const bool more = i + by < n;
           const uint32_t v_at = pos + ring_v(narrow, i, n), k_at = pos + ring_k(narrow, i + by);
-          ready(more ? max(v_at, k_at) : v_at, narrow, n);
-          const uint32_t v = stage(v_at), k = stage(k_at);
-          wait_or_die(&bars.p_full[u], np & 1, dead);
-          ++np;
-          // A wide item's units take turns: interleaved, both would get their scores late and
-          // their softmaxes would fall together; one after the other, one unit's softmax runs
-          // beside the other's products.
-          if (!narrow) {
-            wait_or_die(&bars.turn[u], (turns & 1) ^ (u == 0), dead);
-            ++turns;
-          }
-          tc_fence_after();
-          if (leader) {
-            if (!dead) {
-              values(v, i == first);
-              if (more) scores(q, k);
-            }
-            if (!narrow) mbar_arrive(&bars.turn[u ^ 1]);
-            mma_commit(more ? &bars.s_full[u] : &bars.o_full[u]);
-            mma_commit(&bars.kv_empty[v_at % NS]);
-            if (more) mma_commit(&bars.kv_empty[k_at % NS]);
-            if (more && i + 2 * by >= n) {
+          auto next_scores = [&](uint32_t k) {  // by the leader
+            if (!dead) scores(q, k);
+            mma_commit(&bars.s_full[u]);
+            mma_commit(&bars.kv_empty[k_at % NS]);
+            if (i + 2 * by >= n) {
               mma_commit(&bars.q_empty[tile]);
               if (!narrow) mma_commit(&bars.q_empty[tile]);
             }
+          };
+          if constexpr (C::kOwnP) {
+            if (more) {
+              ready(k_at, narrow, n);
+              scores_free();
+              tc_fence_after();
+              const uint32_t k = stage(k_at);
+              if (leader) next_scores(k);
+              __syncwarp();
+            }
+            if (!more) ready(v_at, narrow, n);  // (lies before k_at otherwise)
+            const uint32_t v = stage(v_at);
+            wait_or_die(&bars.p_full[u], np & 1, dead);
+            ++np;
+            tc_fence_after();
+            if (leader) {
+              if (!dead) values(v, i == first);
+              mma_commit(&bars.o_full[u]);
+              mma_commit(&bars.kv_empty[v_at % NS]);
+            }
+            __syncwarp();
+          } else {
+            ready(more ? k_at : v_at, narrow, n);
+            const uint32_t v = stage(v_at), k = stage(k_at);
+            wait_or_die(&bars.p_full[u], np & 1, dead);
+            ++np;
+            // A wide item's units take turns: interleaved, both would get their scores late and
+            // their softmaxes would fall together; one after the other, one unit's softmax runs
+            // beside the other's products.
+            if (!narrow) {
+              wait_or_die(&bars.turn[u], (turns & 1) ^ (u == 0), dead);
+              ++turns;
+            }
+            tc_fence_after();
+            if (leader) {
+              if (!dead) {
+                values(v, i == first);
+                if (more) scores(q, k);
+              }
+              if (!narrow) mbar_arrive(&bars.turn[u ^ 1]);
+              mma_commit(more ? &bars.s_full[u] : &bars.o_full[u]);
+              mma_commit(&bars.kv_empty[v_at % NS]);
+              if (more) mma_commit(&bars.kv_empty[k_at % NS]);
+              if (more && i + 2 * by >= n) {
+                mma_commit(&bars.q_empty[tile]);
+                if (!narrow) mma_commit(&bars.q_empty[tile]);
+              }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
         ready(pos + 2 * n - 1, narrow, n);
         pos += 2 * n;
@@ -681,6 +730,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     const uint32_t lanebits = uint32_t(warp & 3) << 21;  // (32 * warp of the group) << 16
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
     const uint32_t tO1 = tm + kColO + 128 + lanebits;
+    const uint32_t tP = C::kOwnP ? tm + kColP64 + 128 * u + lanebits : tS;
     const float sc = a.scale * kLog2E;
     uint32_t pos = 0, ns = 0, no = 0;
     Header hd;
@@ -706,6 +756,26 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
         tc_fence_after();
+        // The scores are in the warp's registers (or it has no rows): the next may come.
+        auto scores_read = [&]() {
+          if (C::kOwnP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_empty[u]);
+          }
+        };
+        // The product that reads the last weights and adds to O is done.  Every warp waits for
+        // it, rows or not: none may run ahead and arrive for a tile whose last is still open.
+        auto weights_free = [&]() {
+          if (C::kOwnP) {
+            wait_or_die(&bars.o_full[u], (no & 1) ^ 1, dead);
+            tc_fence_after();
+          }
+        };
+        if (C::kOwnP && !active) {
+          scores_read();
+          weights_free();
+        }
         if (active) {
           // a tile needs masks where some row of the unit does not see all of it
           const bool whole =
@@ -713,7 +783,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
               (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
           bool done = false;
           const uint64_t sc2 = pack2(sc, sc);
-          if (whole && mine > 0) {
+          if (!C::kOwnP && whole && mine > 0) {
             // Weights against the maximum so far, which almost always stands, while the
             // tile's own maximum is found beside them; the scores stay until that is known.
             const float nb = m == -INFINITY ? 0.f : -m * sc;
@@ -743,8 +813,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             done = !__any_sync(0xffffffffu, top > m && (top - m) * sc > kRescale);
             if (done) {
-              tmem_st32_nowait(tS, p);
-              tmem_st32_nowait(tS + 32, p + 32);
+              tmem_st32_nowait(tP, p);
+              tmem_st32_nowait(tP + 32, p + 32);
               float x, y;
               unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
               l += x + y;
@@ -770,6 +840,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             for (int q = 0; q < 4; ++q) tmem_ld32_start(tS + 32 * q, s[q]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32_finish(s[q]);
+            scores_read();
             if (!whole) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -787,6 +858,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                 c4[c / 2 & 3] =
                     max3(c4[c / 2 & 3], __uint_as_float(s[q][c]), __uint_as_float(s[q][c + 1]));
             const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+            weights_free();
             const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
             if (__any_sync(0xffffffffu, grow)) {
               const float mn = grow ? mx : m;
@@ -822,7 +894,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                 sum[e & 1] = add2(sum[e & 1], pack2(x, y));
                 p[e] = pack_bf16(x, y);
               }
-              tmem_st16_nowait(tS + 16 * q, p);
+              tmem_st16_nowait(tP + 16 * q, p);
             }
             float x, y;
             unpack2(add2(sum[0], sum[1]), x, y);
@@ -853,13 +925,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[u]);
         ++mine;
+        if (C::kOwnP) ++no;
       }
 
       // 2. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
       // unit 1's accumulator lanes too.
-      if (mine > 0) {
-        wait_or_die(&bars.o_full[u], no & 1, dead);
-        ++no;
+      if (mine > 0) {  // (kOwnP: a phase for each tile, the last one of which is waited for)
+        if (!C::kOwnP) ++no;
+        wait_or_die(&bars.o_full[u], (no & 1) ^ 1, dead);
       }
       tc_fence_after();
       float f0 = 1.f, f1 = 0.f;
@@ -951,73 +1024,68 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 
 // Joins the partial results of an item that was cut: the CTA it starts in has it in its second
 // slot, the following ones in their first.  Blocks (c, .): the item that starts in CTA c's
-// stretch, one warp per row.  A lane first looks up one part's (m, l), so that the parts'
-// outputs are then independent loads.
+// stretch; a thread has four columns of a row and takes four parts at a time, all their loads in
+// flight together (eight: 39.8 against 37.5 us for a call with 150 items cut in two).
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Header* headers,
                                                          const float* part_o,
                                                          const float2* part_ml) {
-  constexpr int E = D / 32;
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int PIECES = D / 4, U = 4;
+  const int c = blockIdx.x;
   // launched while the first kernel runs: wait for its results
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Header hd = headers[c];
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < hd.rows; r += gridDim.y * 8) {
-    float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    const int end = hd.start + kOverhead + hd.nt;  // the item's end in the line
-    for (int k0 = c; k0 < kCtas && stretch(hd.total, k0) < end; k0 += 32) {
-      const int k = k0 + lane;
-      // the CTA's tiles of the item, if it has any
+  if (hd.rows == 0) return;
+  // CTAs from this one to the one it ends in
+  const int parts = stretch_of(hd.total, hd.start + kOverhead + hd.nt - 1) - c + 1;
+  for (int at = blockIdx.y * 256 + threadIdx.x; at < hd.rows * PIECES; at += gridDim.y * 256) {
+    const int r = at / PIECES, e = at % PIECES;
+    // Row of the i-th part in the partial results, -1 if that CTA has no tile of the item.
+    auto place = [&](int i) -> int {
+      const int k = c + i;
       const int first = stretch(hd.total, k) - hd.start - kOverhead;
       const int last = min(stretch(hd.total, k + 1) - hd.start - kOverhead, hd.nt);
-      const bool has = k < kCtas && last > max(first, 0);
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (has) ml = part_ml[(long long)(2 * k + (k == c ? 1 : 0)) * kRowsItem + r];
-      const bool some = ml.y != 0.f;  // (a NaN is something)
-      float mk = some ? ml.x : -INFINITY;
-      float mn = mk;
+      return i < parts && last > max(first, 0) ? (2 * k + (i == 0)) * kRowsItem + r : -1;
+    };
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += U) {
+      float2 ml[U];
+      float4 x[U];
+      float mn = m;
 #pragma unroll
-      for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-      mn = fmaxf(mn, m);
-      const float b = mn == -INFINITY ? 0.f : mn;
-      const float g = some ? exp2f(mk - b) : 0.f;  // weight of the lane's part
-      const float f = exp2f(m - b);
-      m = mn;
-      l = l * f + warp_sum(some ? ml.y * g : 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= f;
-      unsigned parts = __ballot_sync(0xffffffffu, some);
-      while (parts) {
-        constexpr int U = 4;  // parts in flight
-        float x[U][E], gw[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int j = parts ? __ffs(parts) - 1 : -1;
-          parts &= parts - 1;
-          gw[i] = __shfl_sync(0xffffffffu, g, max(j, 0));
-          const int kk = k0 + max(j, 0);
-          const float* src =
-              part_o + ((long long)(2 * kk + (kk == c ? 1 : 0)) * kRowsItem + r) * D + lane;
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[i][e] = j >= 0 ? src[e * 32] : 0.f;
-          if (j < 0) gw[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += x[i][e] * gw[i];
+      for (int i = 0; i < U; ++i) {
+        const int p = place(i0 + i);
+        ml[i] = p >= 0 ? part_ml[p] : make_float2(-INFINITY, 0.f);
+        x[i] = p >= 0 ? *reinterpret_cast<const float4*>(part_o + (long long)p * D + 4 * e)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (ml[i].y != 0.f) mn = fmaxf(mn, ml[i].x);  // (a part that saw nothing has no say)
+      const float b = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - b);
+      m = mn;
+      l *= f;
+      o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (ml[i].y != 0.f) {
+          const float g = fast_exp2(ml[i].x - b);
+          l += ml[i].y * g;
+          o.x += x[i].x * g;
+          o.y += x[i].y * g;
+          o.z += x[i].z * g;
+          o.w += x[i].w * g;
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const int tk = div_g(a, hd.row0 + r), G = a.Hq / a.Hkv;
     const long long row = (hd.bos + tk) * a.Hq + hd.h * G + (hd.row0 + r - tk * G);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      static_cast<__nv_bfloat16*>(a.out)[row * D + e * 32 + lane] =
-          __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0 && a.lse)
+    uint2 w;
+    w.x = pack_bf16(o.x * inv, o.y * inv);
+    w.y = pack_bf16(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * e) = w;
+    if (e == 0 && a.lse)
       a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
@@ -1056,11 +1124,11 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, kmap, vmap, headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a warp per row up to the largest item's rows, few blocks where many sequences share them
+  // a thread per four columns of the largest item there can be
   const long long rows = (long long)a.total_T * G;
-  const unsigned by = (unsigned)((rows < kRowsItem ? rows : kRowsItem) + 7) / 8;
+  const unsigned by = (unsigned)((rows < kRowsItem ? rows : kRowsItem) * (D / 4) + 255) / 256;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCtas, by < 8 ? by : 8);
+  cfg.gridDim = dim3(kCtas, by);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
