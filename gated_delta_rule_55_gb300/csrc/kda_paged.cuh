@@ -70,12 +70,12 @@ __device__ __forceinline__ long long cache_row(const PagedArgs& a, int n, int hk
   return ((long long)page_of(a, n, key) * a.Hkv + hkv) * a.page_size + key % a.page_size;
 }
 
-__device__ __forceinline__ void load_piece(const float* p, float (&x)[4]) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// 16 bytes of fp32 or bf16 as fp32.
+__device__ __forceinline__ void unpack_piece(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack_piece(uint4 v, float (&x)[8]) {
   const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -19,7 +19,7 @@ constexpr int kRW = 4;       // rows of a warp
 constexpr int kKeys = 32;    // keys of a step
 constexpr int kThreads = 128;
 constexpr int kMaxParts = 32;
-constexpr int kMinPartKeys = 128;
+constexpr int kMinPartKeys = kKeys;  // one step: a step is a round trip to memory
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
@@ -72,21 +72,31 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
     for (int c = 0; c < C; ++c) o[r][c] = 0.f;
   }
   const bool busy = warp * kRW < nr;
+  // 16-byte pieces of a step's K and V rows; places behind the part's end hold zeros.  The next
+  // step's are on their way while this one is computed.
+  constexpr int VE = 16 / sizeof(T), PIECES = D / VE, PT = kKeys * PIECES / kThreads;
+  uint4 kraw[PT], vraw[PT];
+  auto fetch = [&](int vb) {
+#pragma unroll
+    for (int k = 0; k < PT; ++k) {
+      const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
+      kraw[k] = vraw[k] = make_uint4(0, 0, 0, 0);
+      if (vb + key_i < v1) {
+        const long long off = cache_row(a, n, hkv, virtual_key(kr, vb + key_i)) * D + c;
+        kraw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_cache) + off));
+        vraw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_cache) + off));
+      }
+    }
+  };
+  if (v0 < v1) fetch(v0);
   for (int vb = v0; vb < v1; vb += kKeys) {
     __syncthreads();
-    // 16-byte pieces of the step's K and V rows; places behind the part's end hold zeros
-    constexpr int VE = 16 / sizeof(T), PIECES = D / VE;
-    for (int i = tid; i < kKeys * PIECES; i += kThreads) {
-      const int key_i = i / PIECES, c = i % PIECES * VE;
-      float kx[VE], vx[VE];
 #pragma unroll
-      for (int e = 0; e < VE; ++e) kx[e] = vx[e] = 0.f;
-      if (vb + key_i < v1) {
-        const int key = virtual_key(kr, vb + key_i);
-        const long long off = cache_row(a, n, hkv, key) * D + c;
-        load_piece(static_cast<const T*>(a.k_cache) + off, kx);
-        load_piece(static_cast<const T*>(a.v_cache) + off, vx);
-      }
+    for (int k = 0; k < PT; ++k) {
+      const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
+      float kx[VE], vx[VE];
+      unpack_piece(kraw[k], kx);
+      unpack_piece(vraw[k], vx);
 #pragma unroll
       for (int e = 0; e < VE; e += 4) {
         *reinterpret_cast<float4*>(&sK[key_i * PK + c + e]) =
@@ -95,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
             make_float4(vx[e], vx[e + 1], vx[e + 2], vx[e + 3]);
       }
     }
+    if (vb + kKeys < v1) fetch(vb + kKeys);
     __syncthreads();
     if (!busy) continue;
     float s[kRW];
@@ -170,29 +181,52 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
   }
 }
 
-// One warp per query row: o = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i over the parts.
+// One warp per query row: o = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i over the parts.  A
+// lane looks up one part's (m, l), so that the parts' outputs are then independent loads.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int parts,
                                                               const float* part_o,
                                                               const float2* part_ml) {
   constexpr int C = D / 32;
+  static_assert(kMaxParts <= 32, "a part per lane");
   const long long rows = (long long)a.total_T * a.Hq;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  // launched while the first kernel runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows || !token_owned(a, row / a.Hq)) return;
-  float m = -INFINITY, l = 0.f, o[C];
+  const float2 ml = lane < parts ? part_ml[lane * rows + row] : make_float2(0.f, 0.f);
+  const bool some = ml.y != 0.f;  // (a NaN is something)
+  float m = some ? ml.x : -INFINITY;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, m, w);
+    m = (y > m || y != y) ? y : m;
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+  const float g = some ? exp2f(ml.x - base) : 0.f;
+  const float l = warp_sum(some ? ml.y * g : 0.f);
+  float o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const long long at = (long long)i * rows + row;
-    const float2 ml = part_ml[at];
-    if (ml.y == 0.f) continue;  // a part with nothing to see
-    const float mn = (ml.x > m || ml.x != ml.x) ? ml.x : m;
-    const float f = exp2f(m - mn), g = exp2f(ml.x - mn);
-    m = mn;
-    l = l * f + ml.y * g;
+  unsigned todo = __ballot_sync(0xffffffffu, some);
+  while (todo) {
+    constexpr int U = 8;  // parts in flight
+    float x[U][C], gw[U];
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = o[c] * f + part_o[at * D + c * 32 + lane] * g;
+    for (int i = 0; i < U; ++i) {
+      const int j = todo ? __ffs(todo) - 1 : -1;
+      todo &= todo - 1;
+      gw[i] = __shfl_sync(0xffffffffu, g, max(j, 0));
+      const float* src = part_o + (max(j, 0) * rows + row) * D + lane;
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[i][c] = j >= 0 ? src[c * 32] : 0.f;
+      if (j < 0) gw[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] += x[i][c] * gw[i];
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
@@ -223,9 +257,19 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const long long tiles = (a.total_T * G + kRows - 1) / kRows + a.N;  // upper bound
   const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)parts);
   paged_simt_kernel<T, D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
-  if (parts > 1)
-    paged_simt_join_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, parts, po, pml);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || parts == 1) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_simt_join_kernel<T, D>, a, parts, (const float*)po,
+                            (const float2*)pml);
 }
 
 }  // namespace
