@@ -131,7 +131,8 @@ struct PagedArgs {
   float* lse;                  // [total_T, Hq] or NULL
   float scale;
   int N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages, window, sinks;
-  uint32_t g_mul, g_shift;     // division by Hq / Hkv (set by the tensor-core launcher)
+  int G;                       // Hq / Hkv, and division by it (set by the tensor-core launcher)
+  uint32_t g_mul, g_shift;
 };
 
 // KDA_OK, or KDA_ERR_DEVICE when the current device cannot run the library's kernels.

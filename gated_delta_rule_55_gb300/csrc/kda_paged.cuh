@@ -6,10 +6,10 @@
 namespace kda {
 
 struct Seq {
-  long long bos;  // first token of the sequence in the packed token axis
-  int len;        // new tokens
-  int kv;         // keys of the sequence, the new tokens' included
-  int pos0;       // position of its first new token (negative: more new tokens than keys)
+  int bos;   // first token of the sequence in the packed token axis
+  int len;   // new tokens
+  int kv;    // keys of the sequence, the new tokens' included
+  int pos0;  // position of its first new token (negative: more new tokens than keys)
 };
 
 // From a sequence's raw offsets and key count.

@@ -67,12 +67,12 @@ struct Header {  // a CTA's part of the line, for the joining kernel
   int row0, h;    // its first row and kv head
   int nt;         // its tiles
   int start, total;  // its place in the line, the line's length
-  long long bos;  // its sequence's first token
+  int bos;        // its sequence's first token
 };
 
 // ------------------------------------------------------------------- items of the line
 
-// x / (Hq / Hkv) for 0 <= x < 2^31, by the host's multiplier (launch_t).
+// x / G, G = Hq / Hkv, for 0 <= x < 2^31, by the host's multiplier (launch_t).
 __device__ __forceinline__ int div_g(const PagedArgs& a, int x) {
   return (int)((__umulhi((uint32_t)x, a.g_mul) + (uint32_t)x) >> a.g_shift);
 }
@@ -119,15 +119,17 @@ struct Plan {  // in shared memory
   Seq s;                  // sequence n
 };
 
-// Walks the items of a CTA's stretch; every role of the CTA walks on its own.
+// Walks the items of a CTA's stretch; every role of the CTA walks on its own.  AHEAD: the next
+// sequence's numbers are loaded while the current one is worked on (the roles behind them find
+// them in the L1 cache, and have no registers to spare).
+template <bool AHEAD>
 struct Walker {
   int n, h, rt, v0, v1;
-  int nrt, G;
   int left;   // units of the stretch from the item's first one on
   int units;  // units of the item in the stretch
   Seq s;
   Geometry g;
-  int c1, c2, kv1;  // the next sequence's offsets and keys, loaded ahead
+  int c1, c2, kv1;  // the next sequence's offsets and keys
 
   __device__ __forceinline__ void ahead(const PagedArgs& a) {
     c1 = c2 = kv1 = 0;
@@ -139,7 +141,8 @@ struct Walker {
   }
   // The item's tiles among its units [x, ...); false when the stretch ends before the first (it
   // is the stretch's last item then, and the next CTA takes it whole).
-  __device__ __forceinline__ bool enter(int x) {
+  __device__ __forceinline__ bool enter(const PagedArgs& a, int x) {
+    g = geometry(a, s, a.G, rt);
     const int last = min(g.nt + kOverhead, x + left);
     units = last - x;
     v0 = max(x - kOverhead, 0);
@@ -149,31 +152,30 @@ struct Walker {
   __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
     left = p.end - p.first;
     if (left <= 0 || p.n < 0) return false;
-    G = a.Hq / a.Hkv;
     n = p.n; h = p.h; rt = p.rt;
     s = p.s;
-    ahead(a);
-    nrt = row_tiles(s, G);
-    g = geometry(a, s, G, rt);
-    return enter(p.x);
+    if (AHEAD) ahead(a);
+    return enter(a, p.x);
   }
   __device__ __forceinline__ bool next(const PagedArgs& a) {
     left -= units;
     if (left <= 0) return false;
-    if (++rt >= nrt) {
+    if (++rt >= row_tiles(s, a.G)) {
       rt = 0;
       if (++h >= a.Hkv) {
         h = 0;
         do {  // (the line has more units, so a later sequence has tokens)
           if (++n >= a.N) return false;
-          s = make_seq(a, c1, c2, kv1);
-          ahead(a);
+          if (AHEAD) {
+            s = make_seq(a, c1, c2, kv1);
+            ahead(a);
+          } else {
+            s = load_seq(a, n);
+          }
         } while (s.len == 0);
-        nrt = row_tiles(s, G);
       }
     }
-    g = geometry(a, s, G, rt);
-    return enter(0);
+    return enter(a, 0);
   }
   __device__ __forceinline__ int tiles() const { return v1 - v0; }
   __device__ __forceinline__ bool narrow() const { return g.rows <= kRowsUnit; }
@@ -208,7 +210,7 @@ __device__ __forceinline__ int head_units(const PagedArgs& a, const Seq& s, int 
 // start; a whole warp calls.
 __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const Seq& s, int n,
                                            int per, int off) {
-  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+  const int lane = threadIdx.x & 31, G = a.G;
   const int h = (int)((unsigned)off / (unsigned)per);
   off -= h * per;
   const int nrt = row_tiles(s, G);
@@ -240,7 +242,7 @@ __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const
 __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
   static_assert(kPlanSeqs == kThreads, "one sequence per thread");
   constexpr int W = kThreads / 32, kFew = 2 * W;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.G;
   const int rounds = (a.N + kPlanSeqs - 1) / kPlanSeqs;
   // Sequences r kPlanSeqs + ...: with few of them a warp takes two and its lanes the row tiles,
   // with many a thread takes one, and its warp helps where there are many row tiles.
@@ -395,6 +397,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// 32 bytes to a 32-byte boundary: a whole sector, where two 16-byte stores are two partial ones.
+__device__ __forceinline__ void store32(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -456,9 +464,10 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, Header* headers, float* part_o,
-                float2* part_ml) {
+paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, int q_boxes, Header* headers,
+                float* part_o, float2* part_ml) {
   using C = Cfg<D>;
   constexpr int NS = C::kStages, HALVES = D / 64;
   extern __shared__ uint8_t smem_raw[];
@@ -474,6 +483,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
   if (tid == 32 * kLoadWarp) {
+    tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
@@ -501,10 +511,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   const uint32_t tm = s_tmem;
   bool dead = false;
-  Walker w;
 
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    Walker<true> w;
     bool live = w.start(a, plan);
     if (warp == kLoadWarp) {
       const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
@@ -603,9 +613,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         const int tile = narrow ? 0 : u;  // of the query rows
         const uint32_t q = __shfl_sync(0xffffffffu, q0 + tile * C::kQBytes, 0);
         const int first = narrow ? u : 0, by = narrow ? 2 : 1;
-        // (the second tile of a wide item is filled after its first, so neither barrier gets
-        // two phases ahead of a unit that does not wait on it)
-        wait_or_die(&bars.q_full[tile], (tile ? wides : items) & 1, dead);
+        // Every item fills the first tile; both units wait for it and let it go in each, so that
+        // it never gets a phase ahead of either.  The second tile is unit 1's, which counts for
+        // two.
+        wait_or_die(&bars.q_full[0], items & 1, dead);
+        if (tile) {
+          if (leader) mbar_arrive(&bars.q_empty[0]);
+          wait_or_die(&bars.q_full[1], wides & 1, dead);
+        }
         ++items;
         wides += !narrow;
         if (first < n) {
@@ -619,9 +634,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             if (!dead) scores(q, k);
             mma_commit(&bars.s_full[u]);
             mma_commit(&bars.kv_empty[k_at % NS]);
-            if (first + by >= n) {  // (a wide item's tile has one user, who counts for two)
+            if (first + by >= n) {
               mma_commit(&bars.q_empty[tile]);
-              if (!narrow) mma_commit(&bars.q_empty[tile]);
+              if (tile) mma_commit(&bars.q_empty[tile]);
             }
           }
           __syncwarp();
@@ -638,7 +653,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             mma_commit(&bars.kv_empty[k_at % NS]);
             if (i + 2 * by >= n) {
               mma_commit(&bars.q_empty[tile]);
-              if (!narrow) mma_commit(&bars.q_empty[tile]);
+              if (tile) mma_commit(&bars.q_empty[tile]);
             }
           };
           if constexpr (C::kOwnP) {
@@ -685,7 +700,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
               if (more) mma_commit(&bars.kv_empty[k_at % NS]);
               if (more && i + 2 * by >= n) {
                 mma_commit(&bars.q_empty[tile]);
-                if (!narrow) mma_commit(&bars.q_empty[tile]);
+                if (tile) mma_commit(&bars.q_empty[tile]);
               }
             }
             __syncwarp();
@@ -706,14 +721,28 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           if (rows <= 0) continue;
           wait_or_die(&bars.q_empty[t], (nq[t] & 1) ^ 1, dead);
           ++nq[t];
+          const int row0 = w.g.row0 + t * kRowsUnit;
+          if (q_boxes && rows > 32) {
+            // 128 rows are whole tokens: a box of 64 columns, the kv head's query heads and
+            // those tokens (what lies behind the sequence is read and not used)
+            if (lane == 0 && !dead) {
+              mbar_arrive_expect_tx(&bars.q_full[t], C::kQBytes);
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+                tma_load_3d(sQ + t * C::kQBytes + hf * (kRowsUnit * 128), &qmap, &bars.q_full[t],
+                            hf * 64, w.h * a.G, w.s.bos + div_g(a, row0));
+            }
+            __syncwarp();
+            continue;
+          }
           constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
           const uint32_t dst = smem_u32(sQ + t * C::kQBytes);
-          const int ch = lane % CH, row0 = w.g.row0 + t * kRowsUnit;
+          const int ch = lane % CH;
           for (int r = lane / CH; r < rows; r += RPI) {
-            const int tk = div_g(a, row0 + r), hg = row0 + r - tk * w.G;
+            const int tk = div_g(a, row0 + r), hg = row0 + r - tk * a.G;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                       (w.s.bos + tk) * a.q_stride +
-                                       (long long)(w.h * w.G + hg) * D + ch * 8;
+                                       (long long)(w.s.bos + tk) * a.q_stride +
+                                       (long long)(w.h * a.G + hg) * D + ch * 8;
             cp_async16(dst + sw128_offset<2>(kRowsUnit, r, ch * 8), src);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -723,9 +752,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         }
         live = w.next(a);
       }
+      // leave no copy in flight behind a give-up (each tile's last one at most)
+      if (dead)
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) mbar_wait(&bars.q_full[t], (nq[t] - 1) & 1, 100000000ull);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    Walker<false> w;
     const int u = warp >> 2, r = tid & 127;  // unit, row within it
     const uint32_t lanebits = uint32_t(warp & 3) << 21;  // (32 * warp of the group) << 16
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
@@ -955,37 +989,45 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
       if ((!narrow || u == 0) && active) {
         const bool valid = r < nr;
-        const long long orow = (w.s.bos + tk) * a.Hq + w.h * w.G + (row - tk * w.G);
+        const long long orow =
+            (long long)(w.s.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         const long long prow =
             (long long)(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRowsItem + base + r;
+        __nv_bfloat16* orowp = static_cast<__nv_bfloat16*>(a.out) + orow * D;
+        const bool wide_stores = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(tO + c, o);
+          uint32_t o[32], o1[32];
+          tmem_ld32_start(tO + c, o);
+          tmem_ld32_start(both ? tO1 + c : tO + c, o1);
+          tmem_ld32_finish(o);
+          tmem_ld32_finish(o1);
           if (both) {
-            float o1[32];
-            tmem_ld32(tO1 + c, o1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
           }
           if (!valid) continue;
           if (cut0 || cut1) {
-            float4* dst = reinterpret_cast<float4*>(part_o + prow * D + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 32; e += 8) store32(part_o + prow * D + c + e, o + e);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D +
-                                                  c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t x[4];
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t x[8];
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+              for (int q = 0; q < 8; ++q)
                 x[q] = l == 0.f ? 0u
-                                : pack_bf16(o[8 * e + 2 * q] * inv, o[8 * e + 2 * q + 1] * inv);
-              dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
+                                : pack_bf16(__uint_as_float(o[e + 2 * q]) * inv,
+                                            __uint_as_float(o[e + 2 * q + 1]) * inv);
+              if (wide_stores) {
+                store32(orowp + c + e, x);
+              } else {
+                uint4* dst = reinterpret_cast<uint4*>(orowp + c + e);
+                dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+              }
             }
           }
         }
@@ -1079,8 +1121,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Head
         }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    const int tk = div_g(a, hd.row0 + r), G = a.Hq / a.Hkv;
-    const long long row = (hd.bos + tk) * a.Hq + hd.h * G + (hd.row0 + r - tk * G);
+    const int tk = div_g(a, hd.row0 + r);
+    const long long row =
+        (long long)(hd.bos + tk) * a.Hq + hd.h * a.G + (hd.row0 + r - tk * a.G);
     uint2 w;
     w.x = pack_bf16(o.x * inv, o.y * inv);
     w.y = pack_bf16(o.z * inv, o.w * inv);
@@ -1103,14 +1146,32 @@ bool cache_map(CUtensorMap* map, const void* base, const PagedArgs& a) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query rows: 128 rows of a kv head as a box of whole tokens, where its query heads divide 128.
+bool query_map(CUtensorMap* map, const PagedArgs& a) {
+  const auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t G = (cuuint32_t)(a.Hq / a.Hkv);
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.total_T};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t box[3] = {64, G, kRowsUnit / G};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   // x / G = (mulhi(x, g_mul) + x) >> g_shift for x < 2^31
   const uint32_t G = (uint32_t)(a.Hq / a.Hkv);
+  a.G = (int)G;
   a.g_shift = 0;
   while ((1u << a.g_shift) < G) ++a.g_shift;
   a.g_mul = (uint32_t)((((1ull << a.g_shift) - G) << 32) / G + 1);
-  CUtensorMap kmap{}, vmap{};
+  CUtensorMap qmap{}, kmap{}, vmap{};
+  // Rows by TMA where the items are large: a call with one token for each of its sequences has
+  // a few rows in each, which are copied one by one.
+  const int q_boxes = kRowsUnit % G == 0 && (long long)a.total_T * G > 32 && query_map(&qmap, a);
   if (a.num_pages > 0 && a.max_pages > 0)
     if (!cache_map(&kmap, a.k_cache, a) || !cache_map(&vmap, a.v_cache, a))
       return cudaErrorInvalidValue;
@@ -1121,7 +1182,8 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, kmap, vmap, headers, po, ml);
+  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes, headers, po,
+                                                              ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a thread per four columns of the largest item there can be

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
     const int r = i / (D / 4), c = i % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr) {
-      const long long tok = q.bos + (r0 + r) / G;
+      const long long tok = (long long)q.bos + (r0 + r) / G;
       const T* p = static_cast<const T*>(a.q) + tok * a.q_stride +
                    (long long)(hkv * G + (r0 + r) % G) * D + c;
       x = make_float4(load_as_float(p), load_as_float(p + 1), load_as_float(p + 2),
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
     const float lt = warp_sum(l[r]);
     const int rr = warp * kRW + r;
     if (rr >= nr) continue;
-    const long long tok = q.bos + (r0 + rr) / G;
+    const long long tok = (long long)q.bos + (r0 + rr) / G;
     const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
     if (parts > 1) {
       const long long at = (long long)part * a.total_T * a.Hq + row;
