@@ -447,7 +447,7 @@ class _Call:
     A serving step makes many small calls, so their arguments are checked in few Python
     operations each."""
     f32 = bf16 = i32 = i64 = None
-    device = raw_stream = None
+    device = raw_stream = where = dense = address = None
 
 
 def _setup():
@@ -455,6 +455,8 @@ def _setup():
     _Call.f32, _Call.bf16 = torch.float32, torch.bfloat16
     _Call.i32, _Call.i64 = torch.int32, torch.int64
     _Call.device = torch.cuda.current_device
+    _Call.where, _Call.dense = torch.Tensor.get_device, torch.Tensor.is_contiguous
+    _Call.address = torch.Tensor.data_ptr
     # the stream's address without building a stream object, where torch offers it
     _Call.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -494,6 +496,18 @@ def _dev(x, dtype, dev, what):
     return x.data_ptr()
 
 
+def _devs(xs, dtypes, dev, names):
+    """The addresses of several such arguments: whole lists are checked at once, and looked at
+    one by one only when something is not a tensor of its kind."""
+    try:
+        if ([x.dtype for x in xs] == dtypes and all(map(_Call.dense, xs)) and
+                set(map(_Call.where, xs)) == {dev}):
+            return map(_Call.address, xs)
+    except (AttributeError, TypeError):  # an address or None among them
+        pass
+    return [_dev(x, t, dev, n) for x, t, n in zip(xs, dtypes, names.split())]
+
+
 def _rows(x, dtype, dev, heads, dim, what):
     """(address, token stride in elements) of a [tokens, heads, dim] argument: a raw address is
     taken as dense, a tensor may have any distance between its tokens."""
@@ -521,12 +535,20 @@ def kda_attention_step(query, key, value, beta, decay, state, slots, out, N, T, 
     qp, qs = _rows(query, el, dev, Hk, dk, "query")
     kp, ks = _rows(key, el, dev, Hk, dk, "key")
     vp, vs = _rows(value, el, dev, Hv, dv, "value")
+    bp, sp, lp, op = _devs((beta, state, slots, out), [f32, f32, i32, el], dev,
+                           "beta state slots out")
     _check("kda_attention_step", lib().kda_attention_step(
-        qp, kp, vp, _dev(beta, f32, dev, "beta"), _dev(decay, f32, dev, "decay"),
-        _dev(state, f32, dev, "state"), _dev(slots, i32, dev, "slots"), _dev(out_slots, i32, dev, "out_slots"),
-        _dev(cu_seqlens, i32, dev, "cu_seqlens"), _dev(out, el, dev, "out"), float(softmax_scale or 0.0),
-        N, T, Hk, Hv, dk, dv, num_slots, qs, ks, vs, flags,
-        code, st))
+        qp, kp, vp, bp, _dev(decay, f32, dev, "decay"), sp, lp,
+        _dev(out_slots, i32, dev, "out_slots"), _dev(cu_seqlens, i32, dev, "cu_seqlens"), op,
+        float(softmax_scale or 0.0), N, T, Hk, Hv, dk, dv, num_slots, qs, ks, vs, flags, code,
+        st))
+
+
+def _norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev):
+    f32 = _Call.f32
+    return _devs((query_weight, key_weight, cos_table, sin_table, positions),
+                 [f32, f32, f32, f32, _Call.i32], dev,
+                 "query_weight key_weight cos_table sin_table positions")
 
 
 def kda_qk_norm_rope_fwd(query, key, query_weight, key_weight, cos_table, sin_table, positions,
@@ -534,15 +556,12 @@ def kda_qk_norm_rope_fwd(query, key, query_weight, key_weight, cos_table, sin_ta
                          interleaved=False, dtype=None, stream=None):
     """RMS norm of every query and key head and the position rotation (see include/kda.h)."""
     code, el, dev, st = _begin(query, dtype, stream)
-    f32 = _Call.f32
     qp, qs = _rows(query, el, dev, Hq, D, "query")
     kp, ks = _rows(key, el, dev, Hkv, D, "key")
     _check("kda_qk_norm_rope_fwd", lib().kda_qk_norm_rope_fwd(
-        qp, kp, _dev(query_weight, f32, dev, "query_weight"), _dev(key_weight, f32, dev, "key_weight"),
-        _dev(cos_table, f32, dev, "cos_table"), _dev(sin_table, f32, dev, "sin_table"),
-        _dev(positions, _Call.i32, dev, "positions"), _dev(query_out, el, dev, "query_out"),
-        _dev(key_out, el, dev, "key_out"), float(eps), T, Hq, Hkv, D, R, max_position, qs, ks,
-        KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
+        qp, kp, *_norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev),
+        *_devs((query_out, key_out), [el, el], dev, "query_out key_out"), float(eps), T, Hq, Hkv,
+        D, R, max_position, qs, ks, KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
 
 
 def kda_qk_norm_rope_append(query, key, value, query_weight, key_weight, cos_table, sin_table,
@@ -552,18 +571,15 @@ def kda_qk_norm_rope_append(query, key, value, query_weight, key_weight, cos_tab
     """kda_qk_norm_rope_fwd with keys and values written into cache pages (see
     include/kda.h)."""
     code, el, dev, st = _begin(query, dtype, stream)
-    f32 = _Call.f32
     qp, qs = _rows(query, el, dev, Hq, D, "query")
     kp, ks = _rows(key, el, dev, Hkv, D, "key")
     vp, vs = _rows(value, el, dev, Hkv, D, "value")
     _check("kda_qk_norm_rope_append", lib().kda_qk_norm_rope_append(
-        qp, kp, vp, _dev(query_weight, f32, dev, "query_weight"),
-        _dev(key_weight, f32, dev, "key_weight"), _dev(cos_table, f32, dev, "cos_table"),
-        _dev(sin_table, f32, dev, "sin_table"), _dev(positions, _Call.i32, dev, "positions"),
-        _dev(slots, _Call.i64, dev, "slots"), _dev(query_out, el, dev, "query_out"),
-        _dev(k_cache, el, dev, "k_cache"), _dev(v_cache, el, dev, "v_cache"), float(eps), T, Hq, Hkv, D, R,
-        max_position, num_pages, page_size, qs, ks, vs,
-        KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
+        qp, kp, vp,
+        *_norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev),
+        *_devs((slots, query_out, k_cache, v_cache), [_Call.i64, el, el, el], dev,
+               "slots query_out k_cache v_cache"), float(eps), T, Hq, Hkv, D, R, max_position,
+        num_pages, page_size, qs, ks, vs, KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
 
 
 def kda_qk_norm_rope_bwd_workspace_size(T, Hq, Hkv, D) -> int:
@@ -582,13 +598,12 @@ def kda_qk_norm_rope_bwd(query, key, query_weight, key_weight, cos_table, sin_ta
     kp, ks = _rows(key, el, dev, Hkv, D, "key")
     wp, wb = _ws(workspace)
     _check("kda_qk_norm_rope_bwd", lib().kda_qk_norm_rope_bwd(
-        qp, kp, _dev(query_weight, f32, dev, "query_weight"), _dev(key_weight, f32, dev, "key_weight"),
-        _dev(cos_table, f32, dev, "cos_table"), _dev(sin_table, f32, dev, "sin_table"),
-        _dev(positions, _Call.i32, dev, "positions"), _dev(d_query_out, el, dev, "d_query_out"),
-        _dev(d_key_out, el, dev, "d_key_out"), _dev(d_query, el, dev, "d_query"),
-        _dev(d_key, el, dev, "d_key"), _dev(d_query_weight, f32, dev, "d_query_weight"),
-        _dev(d_key_weight, f32, dev, "d_key_weight"), float(eps), T, Hq, Hkv, D, R, max_position, qs,
-        ks, KDA_ROPE_INTERLEAVED if interleaved else 0, code, wp, wb, st))
+        qp, kp, *_norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev),
+        *_devs((d_query_out, d_key_out, d_query, d_key, d_query_weight, d_key_weight),
+               [el, el, el, el, f32, f32], dev,
+               "d_query_out d_key_out d_query d_key d_query_weight d_key_weight"),
+        float(eps), T, Hq, Hkv, D, R, max_position, qs, ks,
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, wp, wb, st))
 
 
 def kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype=KDA_BF16) -> int:
@@ -606,8 +621,8 @@ def kda_paged_attention_fwd(query, k_cache, v_cache, block_table, cu_seqlens, kv
     qp, qs = _rows(query, el, dev, Hq, D, "query")
     wp, wb = _ws(workspace)
     _check("kda_paged_attention_fwd", lib().kda_paged_attention_fwd(
-        qp, _dev(k_cache, el, dev, "k_cache"), _dev(v_cache, el, dev, "v_cache"),
-        _dev(block_table, i32, dev, "block_table"), _dev(cu_seqlens, i32, dev, "cu_seqlens"),
-        _dev(kv_lens, i32, dev, "kv_lens"), _dev(out, el, dev, "out"), _dev(lse, _Call.f32, dev, "lse"),
-        float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
-        window, sinks, qs, code, wp, wb, st))
+        qp, *_devs((k_cache, v_cache, block_table, cu_seqlens, kv_lens, out),
+                   [el, el, i32, i32, i32, el], dev,
+                   "k_cache v_cache block_table cu_seqlens kv_lens out"),
+        _dev(lse, _Call.f32, dev, "lse"), float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D,
+        num_pages, page_size, max_pages, window, sinks, qs, code, wp, wb, st))
