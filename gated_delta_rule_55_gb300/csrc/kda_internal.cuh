@@ -144,15 +144,13 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t stre
 size_t norm_rope_bwd_workspace(int D);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* d_q_weight, float* d_k_weight,
                                  void* workspace, bool bf16, cudaStream_t stream);
-// Paged attention on the tensor cores: bf16, D = 64 or 128.
-bool paged_tc_supported(int D, bool bf16);
+// Paged attention: bf16 on the tensor cores, fp32 on the SIMT kernel.
 bool paged_tc_index_ok(const PagedArgs& a);
 size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
 size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D);
-cudaError_t launch_paged_simt(const PagedArgs& a, bool bf16, void* workspace,
-                              cudaStream_t stream);
+cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 unsigned int decode_read_error(bool reset);
 cudaError_t launch_chunk_simt(const ChunkArgs& a, bool bf16, cudaStream_t stream);

@@ -70,20 +70,6 @@ __device__ __forceinline__ long long cache_row(const PagedArgs& a, int n, int hk
   return ((long long)page_of(a, n, key) * a.Hkv + hkv) * a.page_size + key % a.page_size;
 }
 
-// 16 bytes of fp32 or bf16 as fp32.
-__device__ __forceinline__ void unpack_piece(uint4 v, float (&x)[4]) {
-  x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
-  x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
-}
-__device__ __forceinline__ void unpack_piece(uint4 v, float (&x)[8]) {
-  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(r[i] << 16);
-    x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-  }
-}
-
 // The sequence and row tile behind a block's number, tiles of `rows` query rows counted over
 // the sequences in order.  All NT threads call; false when there is no such tile.
 template <int NT>

@@ -1,5 +1,5 @@
 // Attention of new tokens over a paged cache (kda_paged_attention_fwd) on the tensor cores:
-// bf16, head dim 64 or 128.
+// bf16.
 //
 // Work.  An item is one sequence, one kv head and up to 256 of its query rows (tokens x query
 // heads of that kv head).  Its visible keys come in tiles of 128; the tiles of all items, in
@@ -49,14 +49,17 @@ template <int D> struct Cfg {
   static constexpr int kStageBytes = kKeys * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kQBytes = kRowsUnit * D * 2;
-  // D = 64 leaves Tensor Memory for weights of their own (D = 128 keeps them over the scores):
+  // Rows in shared memory: blocks of up to 64 columns, swizzled over their bytes.
+  static constexpr int kRowBytes = D == 32 ? 64 : 128;
+  static constexpr uint32_t kSwizzle = D == 32 ? 4 : kSwizzle128;  // 64-byte, 128-byte
+  // D <= 64 leaves Tensor Memory for weights of their own (D = 128 keeps them over the scores):
   // the next scores are then made while the softmax of the last is still running.
-  static constexpr bool kOwnP = D == 64;
+  static constexpr bool kOwnP = D <= 64;
   static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + 1024 + 512;
 };
 
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
-constexpr uint32_t kColP64 = kColO + 64;                     // weights, D = 64
+constexpr uint32_t kColP64 = kColO + 64;                     // weights, D <= 64
 
 // An item counts kOverhead units beside its tiles: what its start and end cost a CTA (the
 // units lie before its tiles, and a cut among them falls to the item's first tile).
@@ -448,6 +451,13 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// Byte offset of the 16-byte piece `ch` of row r in a 128-row tile, swizzled as TMA lays it.
+template <int D>
+__device__ __forceinline__ uint32_t piece_offset(int r, int ch) {
+  if (D == 32) return uint32_t(r * 64 + ((ch ^ (r >> 1 & 3)) << 4));
+  return sw128_offset<2>(128, r, ch * 8);
+}
+
 struct Bars {
   uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2],
       turn[2];
@@ -469,7 +479,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap vmap, int q_boxes, Header* headers,
                 float* part_o, float2* part_ml) {
   using C = Cfg<D>;
-  constexpr int NS = C::kStages, HALVES = D / 64;
+  constexpr int NS = C::kStages, RB = C::kRowBytes, HALVES = D * 2 / RB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
@@ -536,10 +546,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           const unsigned need = __ballot_sync(0xffffffffu, pid >= 0);
           if (lane == 0)
             mbar_arrive_expect_tx(&bars.kv_full[st],
-                                  uint32_t(__popc(need)) * uint32_t(ps) * 128u);
+                                  uint32_t(__popc(need)) * uint32_t(ps * RB));
           __syncwarp();
           if (pid >= 0 && !dead)
-            tma_load_2d(sKV + st * C::kStageBytes + half * (kKeys * 128) + pi * ps * 128, map,
+            tma_load_2d(sKV + st * C::kStageBytes + (half * kKeys + pi * ps) * RB, map,
                         &bars.kv_full[st], half * 64, (pid * a.Hkv + w.h) * ps);
           ++pos;
         };
@@ -586,20 +596,20 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         return __shfl_sync(0xffffffffu, kv0 + at % NS * C::kStageBytes, 0);
       };
       auto scores = [&](uint32_t q, uint32_t k) {  // S = Q K^T
-        const uint64_t kd = make_sdesc(k, 16, 1024, kSwizzle128);
-        const uint64_t qd = make_sdesc(q, 16, 1024, kSwizzle128);
+        const uint64_t kd = make_sdesc(k, 16, 8 * RB, C::kSwizzle);
+        const uint64_t qd = make_sdesc(q, 16, 8 * RB, C::kSwizzle);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           // the K step's 32 bytes, in 16-byte units; 64-column blocks are 16 KB apart
-          const uint64_t off = (s / 4) * (kKeys * 128 / 16) + (s % 4) * 2;
+          const uint64_t off = (s / 4) * (kKeys * RB / 16) + (s % 4) * 2;
           mma_ss(tmu + kColS, qd + off, kd + off, idesc_s, s > 0);
         }
       };
       auto values = [&](uint32_t v, bool first) {  // O (+)= P V
-        const uint64_t vd = make_sdesc(v, kKeys * 128, 1024, kSwizzle128);
+        const uint64_t vd = make_sdesc(v, kKeys * RB, 8 * RB, C::kSwizzle);
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-          mma_ts(tmu + kColO, tmu + (C::kOwnP ? kColP64 : kColS) + 8 * s, vd + s * (2048 / 16),
+          mma_ts(tmu + kColO, tmu + (C::kOwnP ? kColP64 : kColS) + 8 * s, vd + s * (16 * RB / 16),
                  idesc_o, !(first && s == 0));
       };
       // Weights of their own: scores wait only for the last ones to have been read.
@@ -729,7 +739,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               mbar_arrive_expect_tx(&bars.q_full[t], C::kQBytes);
 #pragma unroll
               for (int hf = 0; hf < HALVES; ++hf)
-                tma_load_3d(sQ + t * C::kQBytes + hf * (kRowsUnit * 128), &qmap, &bars.q_full[t],
+                tma_load_3d(sQ + t * C::kQBytes + hf * (kRowsUnit * RB), &qmap, &bars.q_full[t],
                             hf * 64, w.h * a.G, w.s.bos + div_g(a, row0));
             }
             __syncwarp();
@@ -743,7 +753,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
                                        (long long)(w.s.bos + tk) * a.q_stride +
                                        (long long)(w.h * a.G + hg) * D + ch * 8;
-            cp_async16(dst + sw128_offset<2>(kRowsUnit, r, ch * 8), src);
+            cp_async16(dst + piece_offset<D>(r, ch), src);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_async_smem();
@@ -944,12 +954,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           wait_or_die(&bars.kv_full[at % NS], (at / NS) & 1, dead);
           const int key = ks + r;
           if (key >= w.g.kr.hi || (key < w.g.kr.lo && key >= w.g.kr.sinks)) {
-            uint8_t* vrow = sKV + (at % NS) * C::kStageBytes + r * 128;
+            uint8_t* vrow = sKV + (at % NS) * C::kStageBytes + r * RB;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-              for (int ch = 0; ch < 8; ++ch)  // (from another piece in each lane: all banks)
-                *reinterpret_cast<uint4*>(vrow + hf * (kKeys * 128) + ((ch + lane) & 7) * 16) =
+              for (int ch = 0; ch < RB / 16; ++ch)  // (from another piece in each lane: all banks)
+                *reinterpret_cast<uint4*>(vrow + hf * (kKeys * RB) +
+                                          ((ch + lane) & (RB / 16 - 1)) * 16) =
                     make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
@@ -1139,10 +1150,11 @@ bool cache_map(CUtensorMap* map, const void* base, const PagedArgs& a) {
   const cuuint64_t dims[2] = {(cuuint64_t)a.D,
                               (cuuint64_t)a.num_pages * a.Hkv * (cuuint64_t)a.page_size};
   const cuuint64_t strides[1] = {(cuuint64_t)a.D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)a.page_size};
+  const cuuint32_t box[2] = {a.D == 32 ? 32u : 64u, (cuuint32_t)a.page_size};
   const cuuint32_t es[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             a.D == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1153,10 +1165,11 @@ bool query_map(CUtensorMap* map, const PagedArgs& a) {
   const cuuint32_t G = (cuuint32_t)(a.Hq / a.Hkv);
   const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.total_T};
   const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.q_stride * 2};
-  const cuuint32_t box[3] = {64, G, kRowsUnit / G};
+  const cuuint32_t box[3] = {a.D == 32 ? 32u : 64u, G, kRowsUnit / G};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             a.D == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1213,14 +1226,14 @@ bool paged_tc_index_ok(const PagedArgs& a) {
   return rows * tiles * a.Hkv < 2147483647.0;
 }
 
-bool paged_tc_supported(int D, bool bf16) { return bf16 && (D == 64 || D == 128); }
-
 size_t paged_tc_workspace(int D) {
   return 8192 + (size_t)2 * kCtas * kRowsItem * (sizeof(float2) + D * sizeof(float));
 }
 
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st) {
-  return a.D == 64 ? launch_t<64>(a, workspace, st) : launch_t<128>(a, workspace, st);
+  return a.D == 32   ? launch_t<32>(a, workspace, st)
+         : a.D == 64 ? launch_t<64>(a, workspace, st)
+                     : launch_t<128>(a, workspace, st);
 }
 
 unsigned int paged_read_error(bool reset) {

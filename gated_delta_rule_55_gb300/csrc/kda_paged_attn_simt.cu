@@ -1,6 +1,5 @@
-// Attention of new tokens over a paged cache (kda_paged_attention_fwd), the fp32-accurate
-// kernel: fp32 inputs, and bf16 with head dim 32.  bf16 with head dim 64 or 128 runs on the
-// tensor cores (kda_paged_attn.cu).
+// Attention of new tokens over a paged cache (kda_paged_attention_fwd) in fp32.  (bf16 runs on
+// the tensor cores: kda_paged_attn.cu.)
 //
 // A block takes 16 query rows (tokens x query heads of one kv head) of one sequence and one
 // part of its visible keys, and keeps for every row the running maximum m, the sum l of
@@ -21,7 +20,7 @@ constexpr int kThreads = 128;
 constexpr int kMaxParts = 32;
 constexpr int kMinPartKeys = kKeys;  // one step: a step is a round trip to memory
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
                                                               float* part_o, float2* part_ml) {
   constexpr int PK = D + 4;    // K pitch: 16-byte rows, lanes on different banks
@@ -50,10 +49,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr) {
       const long long tok = (long long)q.bos + (r0 + r) / G;
-      const T* p = static_cast<const T*>(a.q) + tok * a.q_stride +
+      const float* p = static_cast<const float*>(a.q) + tok * a.q_stride +
                    (long long)(hkv * G + (r0 + r) % G) * D + c;
-      x = make_float4(load_as_float(p), load_as_float(p + 1), load_as_float(p + 2),
-                      load_as_float(p + 3));
+      x = *reinterpret_cast<const float4*>(p);
     }
     const float sc = a.scale * 1.4426950408889634f;  // scores in log2 units
     *reinterpret_cast<float4*>(&sQ[r * D + c]) =
@@ -74,17 +72,17 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
   const bool busy = warp * kRW < nr;
   // 16-byte pieces of a step's K and V rows; places behind the part's end hold zeros.  The next
   // step's are on their way while this one is computed.
-  constexpr int VE = 16 / sizeof(T), PIECES = D / VE, PT = kKeys * PIECES / kThreads;
-  uint4 kraw[PT], vraw[PT];
+  constexpr int VE = 4, PIECES = D / VE, PT = kKeys * PIECES / kThreads;
+  float4 kraw[PT], vraw[PT];
   auto fetch = [&](int vb) {
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
       const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
-      kraw[k] = vraw[k] = make_uint4(0, 0, 0, 0);
+      kraw[k] = vraw[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (vb + key_i < v1) {
         const long long off = cache_row(a, n, hkv, virtual_key(kr, vb + key_i)) * D + c;
-        kraw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_cache) + off));
-        vraw[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_cache) + off));
+        kraw[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + off));
+        vraw[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + off));
       }
     }
   };
@@ -94,16 +92,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
 #pragma unroll
     for (int k = 0; k < PT; ++k) {
       const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
-      float kx[VE], vx[VE];
-      unpack_piece(kraw[k], kx);
-      unpack_piece(vraw[k], vx);
-#pragma unroll
-      for (int e = 0; e < VE; e += 4) {
-        *reinterpret_cast<float4*>(&sK[key_i * PK + c + e]) =
-            make_float4(kx[e], kx[e + 1], kx[e + 2], kx[e + 3]);
-        *reinterpret_cast<float4*>(&sV[key_i * D + c + e]) =
-            make_float4(vx[e], vx[e + 1], vx[e + 2], vx[e + 3]);
-      }
+      *reinterpret_cast<float4*>(&sK[key_i * PK + c]) = kraw[k];
+      *reinterpret_cast<float4*>(&sV[key_i * D + c]) = vraw[k];
     }
     if (vb + kKeys < v1) fetch(vb + kKeys);
     __syncthreads();
@@ -174,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
       const float inv = lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        store_from_float(static_cast<T*>(a.out) + row * D + c * 32 + lane, o[r][c] * inv);
+        static_cast<float*>(a.out)[row * D + c * 32 + lane] = o[r][c] * inv;
       if (lane == 0 && a.lse)
         a.lse[row] = lt == 0.f ? -INFINITY : (m[r] + log2f(lt)) * 0.6931471805599453f;
     }
@@ -183,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
 
 // One warp per query row: o = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i over the parts.  A
 // lane looks up one part's (m, l), so that the parts' outputs are then independent loads.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int parts,
                                                               const float* part_o,
                                                               const float2* part_ml) {
@@ -231,7 +221,7 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
   const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
   for (int c = 0; c < C; ++c)
-    store_from_float(static_cast<T*>(a.out) + row * D + c * 32 + lane, o[c] * inv);
+    static_cast<float*>(a.out)[row * D + c * 32 + lane] = o[c] * inv;
   if (lane == 0 && a.lse)
     a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
@@ -247,7 +237,7 @@ int simt_parts(int N, int total_T, int Hq, int Hkv) {
   return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const int parts = simt_parts(a.N, a.total_T, a.Hq, a.Hkv);
   const long long rows = (long long)a.total_T * a.Hq;
@@ -256,7 +246,7 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const long long G = a.Hq / a.Hkv;
   const long long tiles = (a.total_T * G + kRows - 1) / kRows + a.N;  // upper bound
   const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)parts);
-  paged_simt_kernel<T, D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
+  paged_simt_kernel<D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || parts == 1) return e;
   cudaLaunchConfig_t cfg{};
@@ -268,7 +258,7 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_simt_join_kernel<T, D>, a, parts, (const float*)po,
+  return cudaLaunchKernelEx(&cfg, paged_simt_join_kernel<D>, a, parts, (const float*)po,
                             (const float2*)pml);
 }
 
@@ -279,17 +269,11 @@ size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D) {
   return parts > 1 ? (size_t)parts * total_T * Hq * (D + 2) * sizeof(float) : 0;
 }
 
-cudaError_t launch_paged_simt(const PagedArgs& a, bool bf16, void* workspace, cudaStream_t st) {
+cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t st) {
   switch (a.D) {
-    case 32:
-      return bf16 ? launch_t<__nv_bfloat16, 32>(a, workspace, st)
-                  : launch_t<float, 32>(a, workspace, st);
-    case 64:
-      return bf16 ? launch_t<__nv_bfloat16, 64>(a, workspace, st)
-                  : launch_t<float, 64>(a, workspace, st);
-    default:
-      return bf16 ? launch_t<__nv_bfloat16, 128>(a, workspace, st)
-                  : launch_t<float, 128>(a, workspace, st);
+    case 32: return launch_t<32>(a, workspace, st);
+    case 64: return launch_t<64>(a, workspace, st);
+    default: return launch_t<128>(a, workspace, st);
   }
 }
 

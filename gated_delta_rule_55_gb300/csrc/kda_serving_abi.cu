@@ -201,8 +201,8 @@ size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hk
   if (N <= 0 || total_T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
       !dtype_ok(dtype))
     return 0;
-  if (kda::paged_tc_supported(D, dtype == KDA_BF16)) return kda::paged_tc_workspace(D);
-  return kda::paged_simt_workspace(N, total_T, Hq, Hkv, D);
+  return dtype == KDA_BF16 ? kda::paged_tc_workspace(D)
+                           : kda::paged_simt_workspace(N, total_T, Hq, Hkv, D);
 }
 
 int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
@@ -240,8 +240,7 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   // a window that no position can leave hides nothing
   a.window = (double)window >= (double)max_pages * page_size ? 0 : window;
   a.sinks = sinks;
-  const bool tensor_cores = kda::paged_tc_supported(D, dtype == KDA_BF16);
-  if (tensor_cores && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
+  if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
   const size_t need = kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype);
   if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
     return KDA_ERR_WORKSPACE;
@@ -249,8 +248,8 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   if (s != KDA_OK) return s;
   if (!work) return KDA_OK;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(tensor_cores ? kda::launch_paged_tc(a, workspace, st)
-                                    : kda::launch_paged_simt(a, dtype == KDA_BF16, workspace, st));
+  return launch_status(dtype == KDA_BF16 ? kda::launch_paged_tc(a, workspace, st)
+                                         : kda::launch_paged_simt(a, workspace, st));
 }
 
 }  // extern "C"

@@ -586,11 +586,11 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
  *                maximum included; -inf for a token that sees nothing)
  *   softmax_scale  <= 0 selects D^-0.5
  *   window, sinks  0: none
- *   What lies in the pages outside the visible keys may hold anything, NaN included.  bf16 with
- *   D = 64 or 128 runs on the tensor cores with bf16 softmax weights (fp32 sums), where a value
- *   that some token of the call sees must be finite for every token of that sequence; other
- *   configurations run in fp32.
- *   There the kernel counts its work in tiles of 256 query rows by 128 keys, at the block
+ *   What lies in the pages outside the visible keys may hold anything, NaN included.  bf16 runs
+ *   on the tensor cores with bf16 softmax weights (fp32 scores and sums); there a value that
+ *   some token of a sequence's call sees must be finite for the other tokens of that sequence,
+ *   which do not see it (a weight of zero times it is not zero).  fp32 runs in fp32.
+ *   The bf16 kernel counts its work in tiles of 256 query rows by 128 keys, at the block
  *   table's capacity: Hkv (total_T Hq / Hkv / 256 + N) (max_pages page_size / 128 + 4) must stay
  *   below 2^31 (KDA_ERR_TOO_LARGE).
  *   workspace    at least kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype)

@@ -273,6 +273,40 @@ def test_cache_beyond_32_bit_offsets(dt, D):
     check(d)
 
 
+@pytest.mark.parametrize("dt,D", KINDS)
+def test_more_sequences_than_threads(dt, D):
+    """1000 sequences of 0 to 3 tokens: several rounds of the kernels' search for their rows."""
+    rng = np.random.default_rng(7)
+    d = make([(int(q), int(q + k)) for q, k in zip(rng.integers(0, 4, 1000),
+                                                   rng.integers(0, 40, 1000))], 2, 1, D, 16, dt)
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (10, 2), (64, 1), (128, 1), (160, 1), (7, 7)])
+def test_head_groups(Hq, Hkv):
+    for dt, D in (("bf16", 64), ("bf16", 128), ("f32", 32)):
+        d = make([(1, 70), (40, 140), (3, 3)], Hq, Hkv, D, 32, dt, seed=Hq)
+        call(d)
+        check(d)
+
+
+@pytest.mark.parametrize("dt,D", KINDS)
+def test_sixteen_byte_alignment(dt, D):
+    """Buffers on 16-byte boundaries that are no 32-byte ones."""
+    d = make([(1, 200), (50, 180)], 4, 2, D, 16, dt, seed=40)
+    for n in ("q", "kc", "vc", "out", "lse", "table", "cu", "kv"):
+        x = d[n]
+        pad = 16 // x.element_size()
+        flat = torch.empty(x.numel() + pad, dtype=x.dtype, device="cuda")
+        y = flat[pad:].view(x.shape)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        d[n] = y
+    call(d)
+    check(d)
+
+
 def test_empty_calls():
     d = make([(1, 5)], 2, 1, 64, 16, "f32")
     kda.kda_paged_attention_fwd(d["q"], d["kc"], d["vc"], d["table"], d["cu"], d["kv"], d["out"],
