@@ -458,9 +458,34 @@ __device__ __forceinline__ uint32_t piece_offset(int r, int ch) {
   return sw128_offset<2>(128, r, ch * 8);
 }
 
+// Softmax weights of 32 scores: p = 2^(s sc + nb), packed to bf16; their sum (in fp32, before the
+// rounding) and the largest score, started or carried on.
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float sc, float nb, uint32_t* p,
+                                          float& sum, float& top, bool start) {
+  const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(nb, nb);
+  uint64_t acc[4] = {0, 0, 0, 0};
+  float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float s0 = __uint_as_float(s[2 * e]), s1 = __uint_as_float(s[2 * e + 1]);
+    c4[e & 3] = max3(c4[e & 3], s0, s1);
+    float x, y;
+    unpack2(fma2(pack2(s0, s1), sc2, nb2), x, y);
+    x = fast_exp2(x);
+    y = fast_exp2(y);
+    acc[e & 3] = add2(acc[e & 3], pack2(x, y));
+    p[e] = pack_bf16(x, y);
+  }
+  float x, y;
+  unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), x, y);
+  sum = start ? x + y : sum + (x + y);
+  const float t = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+  top = start ? t : fmaxf(top, t);
+}
+
 struct Bars {
   uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2],
-      turn[2];
+      turn[2], ph_full[2], oh_full[2];
 };
 
 // A wait that gives up marks the thread dead: it then runs through the rest of its work
@@ -510,6 +535,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       mbar_init(&bars.p_full[u], 4);
       mbar_init(&bars.o_full[u], 1);
       mbar_init(&bars.turn[u], 1);
+      mbar_init(&bars.ph_full[u], 4);
+      mbar_init(&bars.oh_full[u], 1);
     }
     fence_mbar_init();
   }
@@ -605,10 +632,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           mma_ss(tmu + kColS, qd + off, kd + off, idesc_s, s > 0);
         }
       };
-      auto values = [&](uint32_t v, bool first) {  // O (+)= P V
+      // O (+)= P V over a part of the keys: halves of the tile, or all of it.
+      constexpr int kHalf = kKeys / 32;
+      auto values = [&](uint32_t v, bool first, bool lower, bool upper) {
         const uint64_t vd = make_sdesc(v, kKeys * RB, 8 * RB, C::kSwizzle);
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s)
+        for (int s = 0; s < 2 * kHalf; ++s)
+          if (s < kHalf ? lower : upper)
           mma_ts(tmu + kColO, tmu + (C::kOwnP ? kColP64 : kColS) + 8 * s, vd + s * (16 * RB / 16),
                  idesc_o, !(first && s == 0));
       };
@@ -681,7 +711,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             ++np;
             tc_fence_after();
             if (leader) {
-              if (!dead) values(v, i == first);
+              if (!dead) values(v, i == first, true, true);
               mma_commit(&bars.o_full[u]);
               mma_commit(&bars.kv_empty[v_at % NS]);
             }
@@ -689,8 +719,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           } else {
             ready(more ? k_at : v_at, narrow, n);
             const uint32_t v = stage(v_at), k = stage(k_at);
-            wait_or_die(&bars.p_full[u], np & 1, dead);
-            ++np;
+            // the lower half of the keys' weights comes first
+            wait_or_die(&bars.ph_full[u], np & 1, dead);
             // A wide item's units take turns: interleaved, both would get their scores late and
             // their softmaxes would fall together; one after the other, one unit's softmax runs
             // beside the other's products.
@@ -700,8 +730,16 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             }
             tc_fence_after();
             if (leader) {
+              if (!dead) values(v, i == first, true, false);
+              mma_commit(&bars.oh_full[u]);
+            }
+            __syncwarp();
+            wait_or_die(&bars.p_full[u], np & 1, dead);
+            ++np;
+            tc_fence_after();
+            if (leader) {
               if (!dead) {
-                values(v, i == first);
+                values(v, false, false, true);
                 if (more) scores(q, k);
               }
               if (!narrow) mbar_arrive(&bars.turn[u ^ 1]);
@@ -800,6 +838,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
         tc_fence_after();
+        bool halves = false;  // the lower half of the weights has been handed over
         // The scores are in the warp's registers (or it has no rows): the next may come.
         auto scores_read = [&]() {
           if (C::kOwnP) {
@@ -826,42 +865,68 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               ks + kKeys <= pos_first + 1 &&
               (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
           bool done = false;
-          const uint64_t sc2 = pack2(sc, sc);
+          // O and l to another maximum (mine > 0, or O is not there yet).
+          auto rescale = [&](float mn) {
+            const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
+            m = mn;
+            l *= f;
+            if (mine > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(tO + c, o);
+                uint32_t x[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
+                tmem_st16(tO + c, x);
+              }
+            }
+          };
           if (!C::kOwnP && whole && mine > 0) {
             // Weights against the maximum so far, which almost always stands, while the
             // tile's own maximum is found beside them; the scores stay until that is known.
+            // The lower half of the keys is handed over while the upper is computed.
             const float nb = m == -INFINITY ? 0.f : -m * sc;
-            const uint64_t nb2 = pack2(nb, nb);
-            uint64_t sum[4] = {0, 0, 0, 0};
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t p[64], s[2][32];
+            uint32_t p[32], s[2][32];
+            float sum, top;
+            auto outgrown = [&]() { return top > m && (top - m) * sc > kRescale; };
             tmem_ld32_start(tS, s[0]);
             tmem_ld32_finish(s[0]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q < 3) tmem_ld32_start(tS + 32 * (q + 1), s[(q + 1) & 1]);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float s0 = __uint_as_float(s[q & 1][2 * e]);
-                const float s1 = __uint_as_float(s[q & 1][2 * e + 1]);
-                mx[e & 3] = max3(mx[e & 3], s0, s1);
-                float x, y;
-                unpack2(fma2(pack2(s0, s1), sc2, nb2), x, y);
-                x = fast_exp2(x);
-                y = fast_exp2(y);
-                sum[e & 3] = add2(sum[e & 3], pack2(x, y));
-                p[16 * q + e] = pack_bf16(x, y);
-              }
-              if (q < 3) tmem_ld32_finish(s[(q + 1) & 1]);
-            }
-            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-            done = !__any_sync(0xffffffffu, top > m && (top - m) * sc > kRescale);
+            tmem_ld32_start(tS + 32, s[1]);
+            weights32(s[0], sc, nb, p, sum, top, true);
+            tmem_ld32_finish(s[1]);
+            tmem_ld32_start(tS + 64, s[0]);
+            weights32(s[1], sc, nb, p + 16, sum, top, false);
+            done = !__any_sync(0xffffffffu, outgrown());
             if (done) {
               tmem_st32_nowait(tP, p);
-              tmem_st32_nowait(tP + 32, p + 32);
-              float x, y;
-              unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
-              l += x + y;
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.ph_full[u]);
+              l += sum;
+            }
+            tmem_ld32_finish(s[0]);
+            if (done) {
+              tmem_ld32_start(tS + 96, s[1]);
+              weights32(s[0], sc, nb, p, sum, top, true);
+              tmem_ld32_finish(s[1]);
+              weights32(s[1], sc, nb, p + 16, sum, top, false);
+              if (__any_sync(0xffffffffu, outgrown())) {
+                // The upper half has outgrown the range: once the lower half's product is in O,
+                // O and l are scaled down and the upper half's weights made again.
+                wait_or_die(&bars.oh_full[u], (ns - 1) & 1, dead);
+                tc_fence_after();
+                rescale(outgrown() ? top : m);
+                const float nb2 = m == -INFINITY ? 0.f : -m * sc;
+                tmem_ld32_start(tS + 64, s[0]);
+                tmem_ld32_finish(s[0]);
+                weights32(s[0], sc, nb2, p, sum, top, true);
+                weights32(s[1], sc, nb2, p + 16, sum, top, false);
+              }
+              tmem_st32_nowait(tP + 32, p);
+              l += sum;
+              halves = true;
             }
           }
           if (!done) {
@@ -904,45 +969,16 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
             weights_free();
             const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
-            if (__any_sync(0xffffffffu, grow)) {
-              const float mn = grow ? mx : m;
-              const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
-              m = mn;
-              l *= f;
-              if (mine > 0) {
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  float o[16];
-                  tmem_ld16(tO + c, o);
-                  uint32_t x[16];
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * f);
-                  tmem_st16(tO + c, x);
-                }
-              }
-            }
+            if (__any_sync(0xffffffffu, grow)) rescale(grow ? mx : m);
             const float nb = m == -INFINITY ? 0.f : -m * sc;
-            const uint64_t nb2 = pack2(nb, nb);
-            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x, y;
-                unpack2(fma2(pack2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1])),
-                             sc2, nb2),
-                        x, y);
-                x = fast_exp2(x);
-                y = fast_exp2(y);
-                sum[e & 1] = add2(sum[e & 1], pack2(x, y));
-                p[e] = pack_bf16(x, y);
-              }
+              float sum, top;
+              weights32(s[q], sc, nb, p, sum, top, true);
+              l += sum;
               tmem_st16_nowait(tP + 16 * q, p);
             }
-            float x, y;
-            unpack2(add2(sum[0], sum[1]), x, y);
-            l += x + y;
           }
         }
         // Keys of this tile that no row of the item sees: their values become zeros (weight
@@ -968,7 +1004,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         if (active) tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[u]);
+        if (lane == 0) {
+          if (!C::kOwnP && !halves) mbar_arrive(&bars.ph_full[u]);
+          mbar_arrive(&bars.p_full[u]);
+        }
         ++mine;
         if (C::kOwnP) ++no;
       }
