@@ -73,7 +73,7 @@ __device__ __forceinline__ long long cache_row(const PagedArgs& a, int n, int hk
 // The sequence and row tile behind a block's number, tiles of `rows` query rows counted over
 // the sequences in order.  All NT threads call; false when there is no such tile.
 template <int NT>
-__device__ bool find_row_tile(const PagedArgs& a, int rows, int number, int* s4, int& seq,
+__device__ bool find_row_tile(const PagedArgs& a, int rows, int number, int* s2, int& seq,
                               int& tile) {
   __shared__ int s_warp[NT / 32];
   const int G = a.Hq / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -93,7 +93,7 @@ __device__ bool find_row_tile(const PagedArgs& a, int rows, int number, int* s4,
       if (lane >= o) sum += y;
     }
     if (lane == 31) s_warp[warp] = sum;
-    if (tid == 0) s4[0] = -1;
+    if (tid == 0) s2[0] = -1;
     __syncthreads();
     int all = 0, pre = before;
 #pragma unroll
@@ -103,13 +103,13 @@ __device__ bool find_row_tile(const PagedArgs& a, int rows, int number, int* s4,
     }
     pre += sum - t;
     if (number >= pre && number < pre + t) {
-      s4[0] = n;
-      s4[1] = number - pre;
+      s2[0] = n;
+      s2[1] = number - pre;
     }
     __syncthreads();
-    if (s4[0] >= 0) {
-      seq = s4[0];
-      tile = s4[1];
+    if (s2[0] >= 0) {
+      seq = s2[0];
+      tile = s2[1];
       return true;
     }
     before += all;

@@ -20,20 +20,18 @@ constexpr int kThreads = 128;
 constexpr int kMaxParts = 32;
 constexpr int kMinPartKeys = kKeys;  // one step: a step is a round trip to memory
 
+// One row tile of sequence n; all threads of the block call.
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
-                                                              float* part_o, float2* part_ml) {
+__device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* part_o,
+                         float2* part_ml) {
   constexpr int PK = D + 4;    // K pitch: 16-byte rows, lanes on different banks
   constexpr int C = D / 32;    // output columns of a lane
   __shared__ __align__(16) float sK[kKeys * PK];
   __shared__ __align__(16) float sV[kKeys * D];
   __shared__ __align__(16) float sQ[kRows * D];
-  __shared__ int s_find[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
   const int hkv = blockIdx.y, part = blockIdx.z;
-  int n, tile;
-  if (!find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile)) return;
   const Seq q = load_seq(a, n);
   const int rows = q.len * G, r0 = tile * kRows;
   const int nr = min(kRows, rows - r0);
@@ -171,6 +169,28 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
   }
 }
 
+// Blocks are numbered over the sequences' row tiles; with many sequences, where the search for a
+// block's tile would cost more than the tile, over the sequences.
+constexpr int kSearch = 1024;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
+                                                              float* part_o, float2* part_ml) {
+  __shared__ int s_find[2];
+  if (a.N > kSearch) {
+    const int n = blockIdx.x, G = a.Hq / a.Hkv;
+    const int tiles = (int)(((long long)load_seq(a, n).len * G + kRows - 1) / kRows);
+    for (int tile = 0; tile < tiles; ++tile) {
+      __syncthreads();  // the last tile's shared memory is free
+      row_tile<D>(a, n, tile, parts, part_o, part_ml);
+    }
+  } else {
+    int n, tile;
+    if (find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile))
+      row_tile<D>(a, n, tile, parts, part_o, part_ml);
+  }
+}
+
 // One warp per query row: o = sum_i e^{m_i - m} o_i / sum_i e^{m_i - m} l_i over the parts.  A
 // lane looks up one part's (m, l), so that the parts' outputs are then independent loads.
 template <int D>
@@ -245,7 +265,7 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   float2* pml = reinterpret_cast<float2*>(po + (parts > 1 ? parts * rows * D : 0));
   const long long G = a.Hq / a.Hkv;
   const long long tiles = (a.total_T * G + kRows - 1) / kRows + a.N;  // upper bound
-  const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)parts);
+  const dim3 grid((unsigned)(a.N > kSearch ? a.N : tiles), (unsigned)a.Hkv, (unsigned)parts);
   paged_simt_kernel<D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || parts == 1) return e;

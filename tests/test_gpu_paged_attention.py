@@ -275,12 +275,14 @@ def test_cache_beyond_32_bit_offsets(dt, D):
 
 @pytest.mark.parametrize("dt,D", KINDS)
 def test_more_sequences_than_threads(dt, D):
-    """1000 sequences of 0 to 3 tokens: several rounds of the kernels' search for their rows."""
+    """1000 and 1500 sequences of 0 to 20 tokens: several rounds of the kernels' search for their
+    rows, and no search."""
     rng = np.random.default_rng(7)
-    d = make([(int(q), int(q + k)) for q, k in zip(rng.integers(0, 4, 1000),
-                                                   rng.integers(0, 40, 1000))], 2, 1, D, 16, dt)
-    call(d)
-    check(d)
+    for N, most in ((1000, 4), (1500, 21)):
+        d = make([(int(q), int(q + k)) for q, k in zip(rng.integers(0, most, N),
+                                                       rng.integers(0, 40, N))], 2, 1, D, 16, dt)
+        call(d)
+        check(d)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(3, 1), (10, 2), (64, 1), (128, 1), (160, 1), (7, 7)])
