@@ -14,14 +14,21 @@
 // piece holds the partners of the first (R / 2 elements on), so that a rotation needs no other
 // lane and a lane needs one cosine and sine per pair; the mean is a few shuffles.  A warp takes
 // a token's queries, keys or copied values: the lane's cosines, sines and weights are loaded
-// once for all of them, and kUnroll row groups are in flight together.
+// once for all of them, and kUnroll row groups are in flight together.  16384 tokens of 32 + 8
+// heads of 128, bf16: 53 us, 6.5 TB/s of the 6.8 of a copy (55.5 with 8 warps a block instead
+// of 4); 80 when the rotation exchanged partners between lanes.  Of 4095 tokens of 16 + 2 + 2
+// heads into the pages: 10.2 us, a third of it the start and end of the one wave of blocks.
 #include "kda_internal.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kUnroll = 4;   // row groups in flight
-constexpr int kWarps = 8;    // warps of a block
+constexpr int kUnroll = 4;    // row groups in flight
+constexpr int kWarps = 4;     // warps of a block, forward
+constexpr int kBwdWarps = 16;  // and backward
+constexpr int kBwdUnroll = 2;  // row groups of a backward part
+constexpr int kParts = 2;      // parts of a unit, at most
+constexpr int kRing = 3;       // parts in a warp's ring
 
 // Lane pieces of T as fp32: 8 bytes each.
 template <typename T> struct Piece;
@@ -240,16 +247,49 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
   }
 }
 
+// Two fp32 numbers in one register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Backward: a fixed grid of warps walks the tokens, the first q_blocks blocks their queries and
 // the others their keys, so that a warp sums its share of dw in registers; the block's sums go to
-// partial[blockIdx.x][D].
+// partial[blockIdx.x][D].  A unit is up to kParts parts of kBwdUnroll row groups of a token; the
+// grid sweeps the units in order, so that all warps read one neighbourhood of memory.  What a
+// warp reads comes through a ring of its own in shared memory, kRing - 1 parts ahead, each lane
+// copying what it will use itself: no register waits for memory, so that 16 warps of 118
+// registers fit.
+// 16384 tokens of 32 + 8 heads of 128: 84 us, 6.0 TB/s of the 6.8 of a copy; the instructions
+// take 60% of the issue slots beside it.  91.5 with the loads in registers, 87 with single
+// instead of packed fp32 arithmetic or 20 warps, 94 with 18, 108 with a ring of 6 (which leaves
+// the tables no L1), 96 with one row group a part.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_bwd_kernel(NormRopeArgs a,
-                                                                    int q_blocks,
-                                                                    float* partial) {
+__global__ void __launch_bounds__(32 * kBwdWarps) norm_rope_bwd_kernel(NormRopeArgs a,
+                                                                       int q_blocks,
+                                                                       float* partial) {
   using Ln = Lane<T, D>;
-  constexpr int PE = Ln::PE, VE = Ln::VE, L = Ln::L, RPW = Ln::RPW, U = 2;
-  __shared__ float s_dw[kWarps][D];
+  constexpr int PE = Ln::PE, VE = Ln::VE, L = Ln::L, RPW = Ln::RPW, U = kBwdUnroll;
+  __shared__ float s_dw[kBwdWarps][D];
+  extern __shared__ __align__(16) uint2 s_ring[];  // [warp][kRing][U][4][lane]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % L, rw = lane / L;
   const bool isk = (int)blockIdx.x >= q_blocks;
   const int first = isk ? blockIdx.x - q_blocks : blockIdx.x;
@@ -257,104 +297,155 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_bwd_kernel(NormRopeArgs
   const int H = isk ? a.Hkv : a.Hq;
   Ln l;
   l.place(a, li, IL);
-  float wa[PE], wb[PE], dw[VE];
-  l.load_weight(isk ? a.k_weight : a.q_weight, wa, wb);
+  // A lane's values of a row as pairs of pairs: v[j] the lower elements of its pairs 2j and
+  // 2j + 1, v[NP + j] the upper ones.
+  constexpr int NP = PE / 2;
+  auto arrange = [](const float (&x)[VE], uint64_t (&v)[2 * NP]) {
 #pragma unroll
-  for (int e = 0; e < VE; ++e) dw[e] = 0.f;
-  // A unit is a token's kParts * U row groups; the grid sweeps the units in order, so that all
-  // warps read one neighbourhood of memory (92.4 us at 16384 tokens of 32 + 8 heads of 128; 95.1
-  // with a stretch of tokens for each warp, 99.9 with whole tokens as units), and
-  // a warp's next loads, the next unit's among them, run while it computes.
-  constexpr int kParts = 2;
-  const int per = (H + kParts * U * RPW - 1) / (kParts * U * RPW);  // units of a token
-  const long long units = (long long)a.T * per, W = (long long)blocks * kWarps;
+    for (int j = 0; j < NP; ++j) {
+      v[j] = pair(x[Ln::template lo<IL>(2 * j)], x[Ln::template lo<IL>(2 * j + 1)]);
+      v[NP + j] = pair(x[Ln::template hi<IL>(2 * j)], x[Ln::template hi<IL>(2 * j + 1)]);
+    }
+  };
+  auto restore = [](const uint64_t (&v)[2 * NP], float (&x)[VE]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      split(v[j], x[Ln::template lo<IL>(2 * j)], x[Ln::template lo<IL>(2 * j + 1)]);
+      split(v[NP + j], x[Ln::template hi<IL>(2 * j)], x[Ln::template hi<IL>(2 * j + 1)]);
+    }
+  };
+  uint64_t w[2 * NP], dw[2 * NP];
+  {
+    float wa[PE], wb[PE], both[VE];
+    l.load_weight(isk ? a.k_weight : a.q_weight, wa, wb);
+#pragma unroll
+    for (int e = 0; e < PE; ++e) {
+      both[e] = wa[e];
+      both[PE + e] = wb[e];
+    }
+    arrange(both, w);
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j) dw[j] = pair(0.f, 0.f);
+  const int parts = min(kParts, (H + U * RPW - 1) / (U * RPW));
+  const int per = (H + parts * U * RPW - 1) / (parts * U * RPW);  // units of a token
+  const int W = blocks * kBwdWarps, step_tok = W / per, step_unit = W % per;
   const T* src = static_cast<const T*>(isk ? a.k : a.q);
   const T* gsrc = static_cast<const T*>(isk ? a.dk_out : a.dq_out);
   T* dst = static_cast<T*>(isk ? a.dk : a.dq);
   const long long stride = isk ? a.k_stride : a.q_stride;
-  uint2 xa[U], xb[U], ga[U], gb[U];
-  auto fetch = [&](int tk, int gr) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = min((gr * U + i) * RPW + rw, H - 1);
-      const T* x = src + tk * stride + h * D;
-      const T* g = gsrc + ((long long)tk * H + h) * D;
-      xa[i] = load_piece(x + l.a);
-      xb[i] = load_piece(x + l.b);
-      ga[i] = load_piece(g + l.a);
-      gb[i] = load_piece(g + l.b);
+  const uint2* ring = s_ring + warp * (kRing * U * 4 * 32) + lane;
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  // token and unit in it, of the loads and of the sums
+  int ltok = (warp * blocks + first) / per, lunit = (warp * blocks + first) % per, lpart = 0;
+  int tok = ltok, unit = lunit, lslot = 0, slot = 0;
+  auto next = [&](int& tk, int& un) {
+    tk += step_tok;
+    un += step_unit;
+    if (un >= per) {
+      un -= per;
+      ++tk;
     }
   };
-  long long u = (long long)first * kWarps + warp;
-  int tok = (int)(u / per), grp = (int)(u - (long long)tok * per) * kParts;
-  if (u < units) {
-    fetch(tok, grp);
-    l.load_turn(a, tok, li);
-  }
-  while (u < units) {
-    u += W;
-    const int tok2 = (int)(u / per), grp2 = (int)(u - (long long)tok2 * per) * kParts;
-    Ln nx = l;
-    if (u < units) nx.load_turn(a, tok2, li);
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) {
-      float x[U][VE], g[U][VE];
+  auto load = [&] {
+    if (ltok < a.T) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        unpack_row<T, D>(xa[i], xb[i], x[i]);
-        unpack_row<T, D>(ga[i], gb[i], g[i]);
+        const int h = min(((lunit * parts + lpart) * U + i) * RPW + rw, H - 1);
+        const T* x = src + ltok * stride + h * D;
+        const T* g = gsrc + ((long long)ltok * H + h) * D;
+        const uint32_t at = ring_at + (lslot * U + i) * (4 * 32 * 8);
+        copy8(at, x + l.a);
+        copy8(at + 256, x + l.b);
+        copy8(at + 512, g + l.a);
+        copy8(at + 768, g + l.b);
       }
-      if (part + 1 < kParts)
-        fetch(tok, grp + part + 1);
-      else if (u < units)
-        fetch(tok2, grp2);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    lslot = lslot + 1 == kRing ? 0 : lslot + 1;
+    if (++lpart == parts || (lunit * parts + lpart) * (U * RPW) >= H) {
+      lpart = 0;
+      next(ltok, lunit);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load();
+  if (tok < a.T) l.load_turn(a, tok, li);
+  while (tok < a.T) {
+    int tok2 = tok, unit2 = unit;
+    next(tok2, unit2);
+    Ln nx = l;
+    if (tok2 < a.T) nx.load_turn(a, tok2, li);
+    for (int part = 0; part < parts && (unit * parts + part) * (U * RPW) < H; ++part) {
+      uint64_t x[U][2 * NP], g[U][2 * NP];
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int row = ((grp + part) * U + i) * RPW + rw;
-        float ss = 0.f, sd = 0.f, gw[VE];
+        const uint2* at = ring + (slot * U + i) * (4 * 32);
+        float raw[VE];
+        unpack_row<T, D>(at[0], at[32], raw);
+        arrange(raw, x[i]);
+        unpack_row<T, D>(at[64], at[96], raw);
+        arrange(raw, g[i]);
+      }
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+      load();  // into the part used before this one
 #pragma unroll
-        for (int k = 0; k < PE; ++k) {
-          const int e0 = Ln::template lo<IL>(k), e1 = Ln::template hi<IL>(k);
-          const float d0 = g[i][e0], d1 = g[i][e1];
-          g[i][e0] = d0 * l.c[k] + d1 * l.s[k];
-          g[i][e1] = d1 * l.c[k] - d0 * l.s[k];
+      for (int i = 0; i < U; ++i) {
+        const int row = ((unit * parts + part) * U + i) * RPW + rw;
+        uint64_t gw[2 * NP], ss2 = pair(0.f, 0.f), sd2 = ss2;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const uint64_t c = pair(l.c[2 * j], l.c[2 * j + 1]);
+          const uint64_t s = pair(l.s[2 * j], l.s[2 * j + 1]);
+          const uint64_t ns = pair(-l.s[2 * j], -l.s[2 * j + 1]);
+          const uint64_t d0 = g[i][j], d1 = g[i][NP + j];
+          g[i][j] = fma2(d0, c, mul2(d1, s));
+          g[i][NP + j] = fma2(d1, c, mul2(d0, ns));
         }
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          gw[e] = g[i][e] * (e < PE ? wa[e % PE] : wb[e % PE]);
-          ss += x[i][e] * x[i][e];
-          sd += gw[e] * x[i][e];
+        for (int j = 0; j < 2 * NP; ++j) {
+          gw[j] = mul2(g[i][j], w[j]);
+          ss2 = fma2(x[i][j], x[i][j], ss2);
+          sd2 = fma2(gw[j], x[i][j], sd2);
         }
-        const float r = rsqrtf(row_sum<L>(ss) * (1.0f / D) + a.eps);
-        const float c = row_sum<L>(sd) * (1.0f / D) * r * r;
+        float ss, sd, hs, hd;
+        split(ss2, ss, hs);
+        split(sd2, sd, hd);
+        const float r = rsqrtf(row_sum<L>(ss + hs) * (1.0f / D) + a.eps);
+        const float c = row_sum<L>(sd + hd) * (-1.0f / D) * r * r;
         const bool in = row < H;
-        // a lane behind the last head has read that head and adds it times zero (loads under a
-        // condition took 101 us for 92, a condition here 96)
+        // a lane behind the last head has read that head and adds it times zero
         const float rd = in ? r : 0.f;
+        const uint64_t r2 = pair(r, r), c2 = pair(c, c), rd2 = pair(rd, rd);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          dw[e] += g[i][e] * (x[i][e] * rd);
-          gw[e] = r * (gw[e] - x[i][e] * c);
+        for (int j = 0; j < 2 * NP; ++j) {
+          dw[j] = fma2(g[i][j], mul2(x[i][j], rd2), dw[j]);
+          gw[j] = mul2(r2, fma2(x[i][j], c2, gw[j]));
         }
-        if (in) store_row<T, D>(dst + ((long long)tok * H + row) * D, l, gw);
+        float y[VE];
+        restore(gw, y);
+        if (in) store_row<T, D>(dst + ((long long)tok * H + row) * D, l, y);
       }
     }
     l = nx;
     tok = tok2;
-    grp = grp2;
+    unit = unit2;
   }
+  float sums[VE];
+  restore(dw, sums);
 #pragma unroll
   for (int e = 0; e < VE; ++e) {
-    float v = dw[e];
+    float v = sums[e];
 #pragma unroll
     for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (rw == 0) s_dw[warp][e < PE ? l.a + e : l.b + e - PE] = v;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < D; i += 32 * kBwdWarps) {
     float v = 0.f;
 #pragma unroll
-    for (int wp = 0; wp < kWarps; ++wp) v += s_dw[wp][i];
+    for (int wp = 0; wp < kBwdWarps; ++wp) v += s_dw[wp][i];
     partial[(long long)blockIdx.x * D + i] = v;
   }
 }
@@ -381,14 +472,16 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* partial,
   if (lane == 0 && out) out[e] = (float)v;
 }
 
-// The walking grid: as many blocks as the SMs hold at once.
-constexpr int kBwdBlocks = 152 * 2;
+// The walking grid: one block an SM.
+constexpr int kBwdBlocks = 152;
+constexpr int kRingBytes = kBwdWarps * kRing * kBwdUnroll * 4 * 32 * (int)sizeof(uint2);
 
 template <typename T, int D>
 cudaError_t launch_fwd_t(const NormRopeArgs& a, cudaStream_t st) {
   constexpr int step = Lane<T, D>::RPW * kUnroll;
-  // A warp takes all heads of a kind, or, with few tokens, as many as it has in flight.
-  const bool whole = a.T >= 152 * 32;
+  // A warp takes all heads of a kind, or, with few tokens, as many as it has in flight (32 + 8
+  // heads of 128: 9.1 us for 10.8 with 2048 tokens, 7.1 for 6.9 with 1024).
+  const bool whole = a.T >= 152 * 8;
   const int per = whole ? (a.Hq > a.Hkv ? a.Hq : a.Hkv) : step;
   const int qu = (a.Hq + per - 1) / per, ku = (a.Hkv + per - 1) / per;
   const dim3 grid((a.T + kWarps - 1) / kWarps, qu + ku + (a.slots ? ku : 0));
@@ -402,19 +495,25 @@ cudaError_t launch_fwd_t(const NormRopeArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_bwd_t(const NormRopeArgs& a, float* dqw, float* dkw, float* partial,
                          cudaStream_t st) {
-  // blocks in proportion to the heads, and no more than there are tokens for
-  const int need = (a.T + kWarps - 1) / kWarps;
-  int qb = (int)((long long)kBwdBlocks * a.Hq / (a.Hq + a.Hkv));
+  // Blocks in proportion to the parts, and no more than there are units for.  (In proportion to
+  // the heads, 16 + 2 heads of 64, whose two keys fill a quarter of a part, took 85 us for 30.)
+  constexpr int rows = kBwdUnroll * Lane<T, D>::RPW;
+  const int qp = (a.Hq + rows - 1) / rows, kp = (a.Hkv + rows - 1) / rows;
+  const long long units = (long long)a.T * (((qp < kp ? kp : qp) + kParts - 1) / kParts);
+  const int need = (int)min((units + kBwdWarps - 1) / kBwdWarps, (long long)kBwdBlocks);
+  int qb = (int)((long long)kBwdBlocks * qp / (qp + kp));
   qb = qb < 1 ? 1 : qb > kBwdBlocks - 1 ? kBwdBlocks - 1 : qb;
   int kb = kBwdBlocks - qb;
   if (qb > need) qb = need;
   if (kb > need) kb = need;
   const int blocks = qb + kb;
   if (blocks > 0) {
-    if (a.interleaved)
-      norm_rope_bwd_kernel<T, D, true><<<blocks, 32 * kWarps, 0, st>>>(a, qb, partial);
-    else
-      norm_rope_bwd_kernel<T, D, false><<<blocks, 32 * kWarps, 0, st>>>(a, qb, partial);
+    auto kernel =
+        a.interleaved ? norm_rope_bwd_kernel<T, D, true> : norm_rope_bwd_kernel<T, D, false>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, 32 * kBwdWarps, kRingBytes, st>>>(a, qb, partial);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(dqw || dkw)) return e;
