@@ -7,7 +7,8 @@
 // time into shared memory: a lane scores one key against the warp's four rows, and then owns
 // D / 32 output columns of those rows.  Bound by the FMA pipes for chunks and by HBM latency
 // for single tokens, so a long key range is cut into parts (for few rows) whose (m, l, o) are
-// joined by a second kernel.
+// joined by a second kernel.  5 sequences of 1..17 tokens over up to 700 keys, 4 + 4 heads of 64:
+// 11.4 us, one round trip to memory after another.
 #include "kda_paged.cuh"
 
 namespace kda {
