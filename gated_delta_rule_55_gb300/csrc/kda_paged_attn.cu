@@ -64,6 +64,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10: one per unit */, kQueryWarp
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr float kRescale = 8.0f;  // log2 growth of the maximum that O and l absorb
 
+// What lies before the tiles: m and l of both units' rows (2 KB), barriers, the plan.
+constexpr int kFront = 3072;
+
 template <int D> struct Cfg {
   static constexpr int kStageBytes = kKeys * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
@@ -74,7 +77,7 @@ template <int D> struct Cfg {
   // D <= 64 leaves Tensor Memory for weights of their own (D = 128 keeps them over the scores):
   // the next scores are then made while the softmax of the last is still running.
   static constexpr bool kOwnP = D <= 64;
-  static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + 1024 + 512;
+  static constexpr int kSmem = kFront + 2 * kQBytes + kStages * kStageBytes;
 };
 
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
@@ -524,15 +527,22 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 float* part_o, float2* part_ml) {
   using C = Cfg<D>;
   constexpr int NS = C::kStages, RB = C::kRowBytes, HALVES = D * 2 / RB;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~uintptr_t(1023));
-  uint8_t* sQ = sm;                      // two 128-row tiles
-  uint8_t* sKV = sm + 2 * C::kQBytes;    // the ring
-  float2* s_ml = reinterpret_cast<float2*>(sKV + NS * C::kStageBytes);  // [128], unit 1's m, l
-  __shared__ Bars bars;
-  __shared__ Plan plan;
-  __shared__ uint32_t s_tmem;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  float2* s_ml = reinterpret_cast<float2*>(smem_raw);  // [2][128]: m, l of the units' rows
+  struct Small {
+    Bars bars;
+    Plan plan;
+    uint32_t tmem;
+  };
+  // (the dynamic memory starts at a multiple of 1024: there is no other)
+  static_assert(2048 + sizeof(Small) <= kFront - 640, "front");
+  Small& small = *reinterpret_cast<Small*>(smem_raw + 2048);
+  Bars& bars = small.bars;
+  Plan& plan = small.plan;
+  uint32_t& s_tmem = small.tmem;
+  uint8_t* sQ = reinterpret_cast<uint8_t*>(  // two 128-row tiles
+      (reinterpret_cast<uintptr_t>(smem_raw) + 2048 + sizeof(Small) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = sQ + 2 * C::kQBytes;        // the ring
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
@@ -830,7 +840,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     const int u = warp >> 2, r = tid & 127;  // unit, row within it
     const uint32_t lanebits = uint32_t(warp & 3) << 21;  // (32 * warp of the group) << 16
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
-    const uint32_t tO1 = tm + kColO + 128 + lanebits;
+    const uint32_t tO0 = tm + kColO + lanebits, tO1 = tO0 + 128;
     const uint32_t tP = C::kOwnP ? tm + kColP64 + 128 * u + lanebits : tS;
     const float sc = a.scale * kLog2E;
     uint32_t pos = 0, ns = 0, no = 0;
@@ -1031,32 +1041,33 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         if (C::kOwnP) ++no;
       }
 
-      // 2. The unit's result; a narrow item's two are joined by unit 0's threads, which reach
-      // unit 1's accumulator lanes too.
+      // 2. The unit's result.  A narrow item's two are joined, half of the columns by each unit:
+      // a warp reaches both accumulators' lanes.
       if (mine > 0) {  // (kOwnP: a phase for each tile, the last one of which is waited for)
         if (!C::kOwnP) ++no;
         wait_or_die(&bars.o_full[u], (no & 1) ^ 1, dead);
       }
-      tc_fence_after();
-      float f0 = 1.f, f1 = 0.f;
+      float f0 = 1.f, f1 = 0.f;  // of units 0 and 1 (wide: f0 is the unit's own)
       const bool both = narrow && n > 1;
+      constexpr int kShare = D == 32 ? 32 : D / 2;  // columns of unit 0
       if (narrow) {
-        if (u == 1) s_ml[r] = make_float2(m, l);
+        s_ml[128 * u + r] = make_float2(m, l);
         tc_fence_before();
         group_sync(1, 256);
-        tc_fence_after();
-        if (u == 0 && both) {
-          const float2 o = s_ml[r];
-          const float mn = fmaxf(m, o.x);
-          const float b = mn == -INFINITY ? 0.f : mn;
-          f0 = fast_exp2((m - b) * sc);
-          f1 = fast_exp2((o.x - b) * sc);
-          l = l * f0 + o.y * f1;
-          m = mn;
+        const float2 x = s_ml[r], y = s_ml[128 + r];
+        m = x.x;
+        l = x.y;
+        if (both) {
+          m = fmaxf(x.x, y.x);
+          const float b = m == -INFINITY ? 0.f : m;
+          f0 = fast_exp2((x.x - b) * sc);
+          f1 = fast_exp2((y.x - b) * sc);
+          l = x.y * f0 + y.y * f1;
         }
       }
+      tc_fence_after();
       const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
-      if ((!narrow || u == 0) && active) {
+      if (active) {
         const bool valid = r < nr;
         const long long orow =
             (long long)(w.s.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
@@ -1066,10 +1077,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         __nv_bfloat16* orowp = static_cast<__nv_bfloat16*>(a.out) + orow * D;
         const bool wide_stores = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = narrow ? u * kShare : 0; c < (narrow && u == 0 ? kShare : D); c += 32) {
           uint32_t o[32], o1[32];
-          tmem_ld32_start(tO + c, o);
-          tmem_ld32_start(both ? tO1 + c : tO + c, o1);
+          tmem_ld32_start((narrow ? tO0 : tO) + c, o);
+          tmem_ld32_start((both ? tO1 : narrow ? tO0 : tO) + c, o1);
           tmem_ld32_finish(o);
           tmem_ld32_finish(o1);
           if (both) {
@@ -1100,7 +1111,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
-        if (valid) {
+        if (valid && (!narrow || u == 0)) {
           if (cut0 || cut1)
             part_ml[prow] = make_float2(m * sc, l);
           else if (a.lse)
