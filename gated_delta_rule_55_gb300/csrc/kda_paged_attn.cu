@@ -9,15 +9,23 @@
 // CTA, joined by a second kernel.
 //
 // One CTA: two units, each with a score tile S [128 rows x 128 keys] and an output accumulator
-// O [128 x D] in Tensor Memory and a warpgroup for the softmax.  A wide item (more than 128
-// rows) gives each unit 128 rows and every key tile to both; a narrow one (single tokens) gives
-// both units the same rows and every other key tile, and joins their two results at its end.
+// O [128 x D] in Tensor Memory and a warpgroup for the softmax.  They work in steps.  A wide item
+// (more than 128 rows) gives each unit 128 rows and every key tile to both.  Two narrow ones
+// (single tokens) of about the same length are taken side by side, one by each unit, so that one
+// item's start and end pass beside the other's tiles (256 sequences of 100 to 1000 keys: 113 us
+// for 156); any other narrow item gives both units the same rows and every other key tile, and
+// their two results are joined at its end.
 // A load warp brings key and value tiles by TMA (one box per page and 64 columns) through a
-// ring of shared-memory stages, another the query rows (a box where 128 rows are whole tokens),
-// and a warp of each unit issues the products
+// ring of shared-memory stages; a warp of each unit issues the products
 //   S = Q K^T  (both operands in shared memory),  O += P V  (P in Tensor Memory, V read as it
 //   lies, keys along the contraction),
-// so that the softmax of one unit runs while the tensor cores work for the other.
+// so that the softmax of one unit runs while the tensor cores work for the other; another warp
+// walks the items, puts the steps down for all roles a few ahead, and brings the query rows (a box
+// where 128 rows are whole tokens).
+//
+// The code is kept small where it does not cost: each role's instructions push the others' out of
+// the instruction cache.  Loops in place of unrolled copies in the cut, the load warp and the
+// masked tiles' softmax took 30% of its length and 10 to 20% of the time of short items.
 //
 // The softmax subtracts a standing maximum: weights are made against the maximum so far while
 // the tile's own is found beside them, and only where a row's has grown by more than 2^8 do the
@@ -144,10 +152,8 @@ struct Plan {  // in shared memory
   Seq s;                  // sequence n
 };
 
-// Walks the items of a CTA's stretch; every role of the CTA walks on its own.  AHEAD: the next
-// sequence's numbers are loaded while the current one is worked on (the roles behind them find
-// them in the L1 cache, and have no registers to spare).
-template <bool AHEAD>
+// Walks the items of a CTA's stretch.  The next sequence's numbers are loaded while the current
+// one is worked on.
 struct Walker {
   int n, h, rt, v0, v1;
   int left;   // units of the stretch from the item's first one on
@@ -179,7 +185,7 @@ struct Walker {
     if (left <= 0 || p.n < 0) return false;
     n = p.n; h = p.h; rt = p.rt;
     s = p.s;
-    if (AHEAD) ahead(a);
+    ahead(a);
     return enter(a, p.x);
   }
   __device__ __forceinline__ bool next(const PagedArgs& a) {
@@ -191,12 +197,8 @@ struct Walker {
         h = 0;
         do {  // (the line has more units, so a later sequence has tokens)
           if (++n >= a.N) return false;
-          if (AHEAD) {
-            s = make_seq(a, c1, c2, kv1);
-            ahead(a);
-          } else {
-            s = load_seq(a, n);
-          }
+          s = make_seq(a, c1, c2, kv1);
+          ahead(a);
         } while (s.len == 0);
       }
     }
@@ -225,6 +227,7 @@ __device__ __forceinline__ int stretch_of(int total, int unit) {
 __device__ __forceinline__ int head_units(const PagedArgs& a, const Seq& s, int G) {
   int x = 0;
   const int nrt = row_tiles(s, G);
+#pragma unroll 1
   for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) x += geometry(a, s, G, rt).nt + kOverhead;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -239,6 +242,7 @@ __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const
   const int h = (int)((unsigned)off / (unsigned)per);
   off -= h * per;
   const int nrt = row_tiles(s, G);
+#pragma unroll 1
   for (int base = 0; base < nrt; base += 32) {
     const int rt = base + lane;
     const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
@@ -281,11 +285,12 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (warp + k * W < count) s[k] = load_seq(a, r * kPlanSeqs + warp + k * W);
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 2; ++k)
         if (warp + k * W < count) {
-          per[k] = head_units(a, s[k], G);
-          if (lane == 0) s_units[warp + k * W] = per[k] * a.Hkv;
+          const int y = head_units(a, k == 0 ? s[0] : s[1], G);
+          if (lane == 0) s_units[warp + k * W] = y * a.Hkv;
+          (k == 0 ? per[0] : per[1]) = y;
         }
     } else {
       const int i = threadIdx.x;
@@ -293,7 +298,9 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
       const int nrt = i < count ? row_tiles(s[0], G) : 0;
       per[0] = 0;
       if (nrt <= 4)
+#pragma unroll 1
         for (int rt = 0; rt < nrt; ++rt) per[0] += geometry(a, s[0], G, rt).nt + kOverhead;
+#pragma unroll 1
       for (unsigned todo = __ballot_sync(0xffffffffu, nrt > 4); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
         const int y = head_units(a, shfl_seq(s[0], src), G);
@@ -303,31 +310,37 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
     }
     __syncthreads();
     sum = 0;
+#pragma unroll 1
     for (int i = lane; i < count; i += 32) sum += s_units[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   };
-  int total = 0;
-  for (int r = 0; r < rounds; ++r) {
-    load(r);
-    total += sum;
-  }
-  const int first = stretch(total, blockIdx.x), end = stretch(total, blockIdx.x + 1);
-  if (threadIdx.x == 0) {
-    plan.total = total;
-    plan.first = first;
-    plan.end = end;
-  }
-  if (first == end) return;  // (uniform)
-  int before = 0;
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) load(r);
+  // (one loop for the sum and the search: little code, which a call has to fetch first)
+  int total = 0, before = 0, first = 0;
+#pragma unroll 1
+  for (int x = 0; x < 2 * rounds; ++x) {
+    const int r = x < rounds ? x : x - rounds;
+    if (x < rounds || rounds > 1) load(r);
+    if (x < rounds) {
+      total += sum;
+      if (x + 1 < rounds) continue;
+      first = stretch(total, blockIdx.x);
+      const int end = stretch(total, blockIdx.x + 1);
+      if (threadIdx.x == 0) {
+        plan.total = total;
+        plan.first = first;
+        plan.end = end;
+      }
+      if (first == end) return;  // (uniform)
+      continue;
+    }
     if (first >= before + sum) {  // (uniform)
       before += sum;
       continue;
     }
     // the sequence that holds the first unit, and the units before it
     int n = -1, pre = before;
+#pragma unroll 1
     for (int base = 0; base < count; base += 32) {
       const int mine = base + lane < count ? s_units[base + lane] : 0;
       int run = mine;
@@ -346,33 +359,76 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
       pre += __shfl_sync(0xffffffffu, run, 31);
     }
     // its warp has it at hand
-    if (count <= kFew) {
-      if (n % W == warp)
-        note_start(a, plan, n < W ? s[0] : s[1], r * kPlanSeqs + n, n < W ? per[0] : per[1],
-                   first - pre);
-    } else if (n / 32 == warp) {
-      note_start(a, plan, shfl_seq(s[0], n & 31), r * kPlanSeqs + n,
-                 __shfl_sync(0xffffffffu, per[0], n & 31), first - pre);
-    }
+    const bool few = count <= kFew;
+    if ((few ? n % W : n / 32) != warp) return;
+    const int src = n & 31;
+    note_start(a, plan, few ? (n < W ? s[0] : s[1]) : shfl_seq(s[0], src), r * kPlanSeqs + n,
+               few ? (n < W ? per[0] : per[1]) : __shfl_sync(0xffffffffu, per[0], src),
+               first - pre);
     return;
   }
 }
 
-// Ring position of an item's i-th key / value tile (of n), in the order in which the products
-// use them: wide K0 V0 K1 V1 ...; narrow K0 K1 V0 K2 V1 ... (the second unit's scores start
-// before the first unit's values are needed).
-__device__ __forceinline__ uint32_t ring_k(bool narrow, int i) {
-  return narrow ? (i == 0 ? 0u : uint32_t(2 * i - 1)) : uint32_t(2 * i);
-}
-__device__ __forceinline__ uint32_t ring_v(bool narrow, int i, int n) {
-  return narrow ? uint32_t(min(2 * i + 2, 2 * n - 1)) : uint32_t(2 * i + 1);
-}
+// What a CTA's units work on together; made by the query warp, kSteps of them ahead at most.
+enum Kind : int {
+  kEnd,    // nothing more
+  kWide,   // one item, 128 rows for each unit, every tile for both
+  kSplit,  // one narrow item, the same rows for both units, every other tile for each
+  kPair,   // two narrow items, one for each unit
+};
+struct Item {
+  int n, h, bos, pos0;  // sequence, kv head, first token and its position
+  int v0, v1;           // its tiles in the stretch
+  Geometry g;
+};
+struct Step {
+  int kind;
+  Item it[2];
+  __device__ __forceinline__ int tiles(int i) const { return it[i].v1 - it[i].v0; }
+};
+constexpr int kSteps = 4;
+// Two narrow items next to each other are worked on side by side when neither has more than
+// kSkew tiles more than the other: their starts and ends then pass beside the other's tiles.  What
+// is left of a longer one would go through one unit alone.
+constexpr int kSkew = 3;
 
-// The unit (0 or 1) whose tile entry e of a narrow item's ring order is.
-__device__ __forceinline__ int ring_owner(int e, int n) {
-  const int i = e == 0 ? 0 : e == 2 * n - 1 ? n - 1 : e & 1 ? (e + 1) / 2 : e / 2 - 1;
-  return i & 1;
-}
+// A step's order of key and value tiles in the ring, that in which the products use them:
+// wide K0 V0 K1 V1 ...; otherwise K0 K1 V0 K2 V1 ... (the second unit's scores start before the
+// first unit's values are needed), where tiles go to the units in turn, a pair's last ones to the
+// unit of the longer item.
+struct Order {
+  int kind, n;  // tiles in all
+  int turns;    // tiles that the units take in turn
+  int longer;   // the unit that takes the others
+  __device__ __forceinline__ explicit Order(const Step& s) {
+    kind = s.kind;
+    const int n0 = s.tiles(0), n1 = kind == kPair ? s.tiles(1) : 0;
+    n = n0 + n1;
+    turns = kind == kPair ? 2 * min(n0, n1) : n;
+    longer = n1 > n0;
+  }
+  // Number of unit u's i-th tile (split: the item's i-th).
+  __device__ __forceinline__ int tile(int u, int i) const {
+    return kind == kPair ? (2 * i < turns ? 2 * i + u : turns / 2 + i) : i;
+  }
+  // Unit and place in its item of tile t of a pair.
+  __device__ __forceinline__ int unit(int t) const { return t < turns ? t & 1 : longer; }
+  __device__ __forceinline__ int place(int t) const { return t < turns ? t / 2 : t - turns / 2; }
+  // Entry of tile t's keys, values.
+  __device__ __forceinline__ uint32_t key(int t) const {
+    return kind == kWide ? uint32_t(2 * t) : t == 0 ? 0u : uint32_t(2 * t - 1);
+  }
+  __device__ __forceinline__ uint32_t value(int t) const {
+    return kind == kWide ? uint32_t(2 * t + 1) : uint32_t(min(2 * t + 2, 2 * n - 1));
+  }
+  // The tile of entry e.
+  __device__ __forceinline__ int tile_of(int e) const {
+    if (kind == kWide) return e / 2;
+    return e == 0 ? 0 : e == 2 * n - 1 ? n - 1 : e & 1 ? (e + 1) / 2 : e / 2 - 1;
+  }
+  // The unit that uses entry e (not wide: both do).
+  __device__ __forceinline__ int owner(int e) const { return unit(tile_of(e)); }
+};
 
 // ------------------------------------------------------------------------ small pieces
 
@@ -469,10 +525,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void group_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Byte offset of the 16-byte piece `ch` of row r in a 128-row tile, swizzled as TMA lays it.
 template <int D>
 __device__ __forceinline__ uint32_t piece_offset(int r, int ch) {
@@ -506,17 +558,36 @@ __device__ __forceinline__ void weights32(const uint32_t (&s)[32], float sc, flo
 }
 
 struct Bars {
-  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], o_full[2],
-      turn[2], ph_full[2], oh_full[2];
+  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2],
+      o_full[2], turn[2], ph_full[2], oh_full[2], join, step_full[kSteps], step_empty[kSteps];
 };
 
-// A wait that gives up marks the thread dead: it then runs through the rest of its work
-// without waiting (its results are void) so that every loop and barrier still ends.
+// One try of a wait, of a microsecond at most.
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A wait that gives up (after a second or two) marks the thread dead: it then runs through the
+// rest of its step without waiting (its results are void) and leaves, so that every loop ends.
+// Tries are counted, not timed: there are many of these loops, and their instructions push those
+// of the softmax out of the cache.
 __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool& dead) {
-  if (!dead && !mbar_wait(bar, parity)) {
-    dead = true;
-    atomicOr(&g_paged_error, 64u);
-  }
+  if (dead) return;
+#pragma unroll 1
+  for (int i = 0; !try_wait(bar, parity); ++i)
+    if (i == 2000000) {
+      dead = true;
+      atomicOr(&g_paged_error, 64u);
+      break;
+    }
 }
 
 template <int D>
@@ -527,21 +598,20 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 float* part_o, float2* part_ml) {
   using C = Cfg<D>;
   constexpr int NS = C::kStages, RB = C::kRowBytes, HALVES = D * 2 / RB;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   float2* s_ml = reinterpret_cast<float2*>(smem_raw);  // [2][128]: m, l of the units' rows
   struct Small {
     Bars bars;
     Plan plan;
+    Step steps[kSteps];
     uint32_t tmem;
   };
-  // (the dynamic memory starts at a multiple of 1024: there is no other)
-  static_assert(2048 + sizeof(Small) <= kFront - 640, "front");
+  static_assert(2048 + sizeof(Small) <= kFront, "front");
   Small& small = *reinterpret_cast<Small*>(smem_raw + 2048);
   Bars& bars = small.bars;
   Plan& plan = small.plan;
   uint32_t& s_tmem = small.tmem;
-  uint8_t* sQ = reinterpret_cast<uint8_t*>(  // two 128-row tiles
-      (reinterpret_cast<uintptr_t>(smem_raw) + 2048 + sizeof(Small) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem_raw + kFront;           // two 128-row tiles
   uint8_t* sKV = sQ + 2 * C::kQBytes;        // the ring
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -567,6 +637,11 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       mbar_init(&bars.ph_full[u], 4);
       mbar_init(&bars.oh_full[u], 1);
     }
+    mbar_init(&bars.join, 8);
+    for (int i = 0; i < kSteps; ++i) {
+      mbar_init(&bars.step_full[i], 1);
+      mbar_init(&bars.step_empty[i], 11);  // load, products, softmaxes: one for each warp
+    }
     fence_mbar_init();
   }
   make_plan(a, plan, reinterpret_cast<int*>(sKV));  // (the ring is not in use yet)
@@ -577,50 +652,89 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
   const uint32_t tm = s_tmem;
   bool dead = false;
+  // The CTA's j-th step (null: none, or the warp has given up), and that the warp is done with it.
+  auto step = [&](uint32_t j) -> const Step* {
+    wait_or_die(&bars.step_full[j % kSteps], (j / kSteps) & 1, dead);
+    dead = __any_sync(0xffffffffu, dead);
+    const Step* s = &small.steps[j % kSteps];
+    return dead || s->kind == kEnd ? nullptr : s;
+  };
+  auto step_done = [&](uint32_t j) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.step_empty[j % kSteps]);
+  };
 
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    Walker<true> w;
-    bool live = w.start(a, plan);
     if (warp == kLoadWarp) {
       const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
-      const int pi = lane % ppt, half = lane / ppt;
-      uint32_t pos = 0;  // entries pushed into the ring
-      while (live) {
-        const int n = w.tiles();
-        const bool narrow = w.narrow();
-        // The page of this lane in the i-th tile of the item, -1 where no key is needed.
-        auto page = [&](int i) -> int {
-          if (half >= HALVES || i >= n) return -1;
-          const int k0 = tile_start(w.g, w.v0 + i) + pi * ps;
-          if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return -1;
-          return page_of(a, w.n, k0);
+      // Lane 8 x + p looks up and copies page p of the tiles x, x + 4, ..., four tiles ahead.
+      const int quarter = lane >> 3, pi = lane & 7;
+      uint32_t pos = 0, sg = 0, ph = 0;  // entries pushed into the ring; the next one's stage, phase
+      for (uint32_t j = 0;; ++j) {
+        const Step* st = step(j);
+        if (!st) break;
+        const Order o(*st);
+        const bool pair = o.kind == kPair;
+        int x = pair ? quarter & 1 : 0;  // the item of the lane's tiles
+        Item w = st->it[x];
+        int row = -1;       // of the page in the caches, for the lane's tile; -1: not needed
+        bool fresh = true;  // a look-up that has not been made a row yet
+        int page = 0, head = -1;
+        auto look_up = [&](int t) {
+          head = -1;
+          fresh = true;
+          if (pi >= ppt || t >= o.n) return;
+          if (pair && o.unit(t) != x) {
+            x = o.unit(t);
+            w = st->it[x];
+          }
+          const int k0 = tile_start(w.g, w.v0 + (pair ? o.place(t) : t)) + pi * ps;
+          if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return;
+          head = w.h;
+          page = __ldg(a.block_table + (long long)w.n * a.max_pages + k0 / kKeys * ppt + pi);
         };
-        auto push = [&](const CUtensorMap* map, int pid) {
-          const uint32_t st = pos % NS, ph = (pos / NS) & 1;
-          wait_or_die(&bars.kv_empty[st], ph ^ 1, dead);
-          const unsigned need = __ballot_sync(0xffffffffu, pid >= 0);
-          if (lane == 0)
-            mbar_arrive_expect_tx(&bars.kv_full[st],
-                                  uint32_t(__popc(need)) * uint32_t(ps * RB));
-          __syncwarp();
-          if (pid >= 0 && !dead)
-            tma_load_2d(sKV + st * C::kStageBytes + (half * kKeys + pi * ps) * RB, map,
-                        &bars.kv_full[st], half * 64, (pid * a.Hkv + w.h) * ps);
-          ++pos;
+        auto settle = [&]() {  // (touches the loaded number: a tile later)
+          if (fresh) row = head < 0 ? -1 : (min(max(page, 0), a.num_pages - 1) * a.Hkv + head) * ps;
+          fresh = false;
         };
-        // a tile's pages are looked up one tile ahead of their first use
-        int p0 = page(0), p1 = page(1);
-        push(&kmap, p0);
-        for (int i = 0; i < n; ++i) {
-          const int p2 = page(i + 2);
-          if (narrow && i + 1 < n) push(&kmap, p1);
-          push(&vmap, p0);
-          if (!narrow && i + 1 < n) push(&kmap, p1);
-          p0 = p1;
-          p1 = p2;
+        look_up(quarter);
+        settle();
+        const bool wide = o.kind == kWide;
+#pragma unroll 1
+        for (int t = -1; t < o.n; ++t) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const bool keys = (z == 0) != wide;  // the next tile's; or this tile's values
+            const int y = keys ? t + 1 : t;
+            if (y < 0 || y >= o.n) continue;
+            wait_or_die(&bars.kv_empty[sg], ph ^ 1, dead);
+            const bool mine = (y & 3) == quarter && row >= 0;
+            const unsigned need = __ballot_sync(0xffffffffu, mine);
+            uint64_t* bar = &bars.kv_full[sg];
+            if (lane == 0)
+              mbar_arrive_expect_tx(bar, uint32_t(__popc(need)) * uint32_t(HALVES * ps * RB));
+            __syncwarp();
+            if (mine && !dead) {
+              uint8_t* dst = sKV + sg * C::kStageBytes + pi * ps * RB;
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+                tma_load_2d(dst + hf * (kKeys * RB), keys ? &kmap : &vmap, bar, hf * 64, row);
+            }
+            __syncwarp();
+            if (++sg == NS) {
+              sg = 0;
+              ph ^= 1;
+            }
+            ++pos;
+          }
+          if (t >= 0) {
+            settle();
+            if ((t & 3) == quarter) look_up(t + 4);
+            __syncwarp();
+          }
         }
-        live = w.next(a);
+        step_done(j);
       }
       // leave no copy in flight behind a give-up
       if (dead)
@@ -641,10 +755,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       // Ring entries up to `at` have landed.  Every entry is waited for in turn, and the other
       // unit's are let go at once: a stage is refilled only when both units have passed it, so
       // no barrier is ever more than the one phase away that a parity can tell.
-      auto ready = [&](uint32_t at, bool narrow, int n) {
-        for (; seen != at + 1; ++seen) {
+      auto ready = [&](uint32_t at, const Order& o) {
+        for (; (int)(at - seen) >= 0; ++seen) {
           wait_or_die(&bars.kv_full[seen % NS], (seen / NS) & 1, dead);
-          if (narrow && ring_owner((int)(seen - pos), n) != u && leader)
+          if (o.kind != kWide && o.owner((int)(seen - pos)) != u && leader)
             mbar_arrive(&bars.kv_empty[seen % NS]);
         }
       };
@@ -676,13 +790,16 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         if (C::kOwnP) wait_or_die(&bars.s_empty[u], (nscores & 1) ^ 1, dead);
         ++nscores;
       };
-      while (live) {
-        const int n = w.tiles();
-        const bool narrow = w.narrow();
-        const int tile = narrow ? 0 : u;  // of the query rows
+      for (uint32_t j = 0;; ++j) {
+        const Step* st = step(j);
+        if (!st) break;
+        const Order o(*st);
+        const int kind = o.kind, n = kind == kPair ? st->tiles(u) : o.n;
+        const bool split = kind == kSplit;
+        const int tile = split ? 0 : u;  // of the query rows
         const uint32_t q = __shfl_sync(0xffffffffu, q0 + tile * C::kQBytes, 0);
-        const int first = narrow ? u : 0, by = narrow ? 2 : 1;
-        // Every item fills the first tile; both units wait for it and let it go in each, so that
+        const int first = split ? u : 0, by = split ? 2 : 1;
+        // Every step fills the first tile; both units wait for it and let it go in each, so that
         // it never gets a phase ahead of either.  The second tile is unit 1's, which counts for
         // two.
         wait_or_die(&bars.q_full[0], items & 1, dead);
@@ -691,11 +808,11 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           wait_or_die(&bars.q_full[1], wides & 1, dead);
         }
         ++items;
-        wides += !narrow;
+        wides += !split;
         if (first < n) {
           // the first scores
-          const uint32_t k_at = pos + ring_k(narrow, first);
-          ready(k_at, narrow, n);
+          const uint32_t k_at = pos + o.key(o.tile(u, first));
+          ready(k_at, o);
           scores_free();
           tc_fence_after();
           const uint32_t k = stage(k_at);
@@ -715,7 +832,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         // a tile's values, then the unit's next scores
         for (int i = first; i < n; i += by) {
           const bool more = i + by < n;
-          const uint32_t v_at = pos + ring_v(narrow, i, n), k_at = pos + ring_k(narrow, i + by);
+          const uint32_t v_at = pos + o.value(o.tile(u, i));
+          const uint32_t k_at = pos + o.key(o.tile(u, i + by));
           auto next_scores = [&](uint32_t k) {  // by the leader
             if (!dead) scores(q, k);
             mma_commit(&bars.s_full[u]);
@@ -727,14 +845,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           };
           if constexpr (C::kOwnP) {
             if (more) {
-              ready(k_at, narrow, n);
+              ready(k_at, o);
               scores_free();
               tc_fence_after();
               const uint32_t k = stage(k_at);
               if (leader) next_scores(k);
               __syncwarp();
             }
-            if (!more) ready(v_at, narrow, n);  // (lies before k_at otherwise)
+            ready(v_at, o);
             const uint32_t v = stage(v_at);
             wait_or_die(&bars.p_full[u], np & 1, dead);
             ++np;
@@ -746,14 +864,15 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             }
             __syncwarp();
           } else {
-            ready(more ? k_at : v_at, narrow, n);
+            ready(v_at, o);
+            if (more) ready(k_at, o);
             const uint32_t v = stage(v_at), k = stage(k_at);
             // the lower half of the keys' weights comes first
             wait_or_die(&bars.ph_full[u], np & 1, dead);
             // A wide item's units take turns: interleaved, both would get their scores late and
             // their softmaxes would fall together; one after the other, one unit's softmax runs
             // beside the other's products.
-            if (!narrow) {
+            if (kind == kWide) {
               wait_or_die(&bars.turn[u], (turns & 1) ^ (u == 0), dead);
               ++turns;
             }
@@ -771,7 +890,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 values(v, false, false, true);
                 if (more) scores(q, k);
               }
-              if (!narrow) mbar_arrive(&bars.turn[u ^ 1]);
+              if (kind == kWide) mbar_arrive(&bars.turn[u ^ 1]);
               mma_commit(more ? &bars.s_full[u] : &bars.o_full[u]);
               mma_commit(&bars.kv_empty[v_at % NS]);
               if (more) mma_commit(&bars.kv_empty[k_at % NS]);
@@ -783,22 +902,69 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             __syncwarp();
           }
         }
-        ready(pos + 2 * n - 1, narrow, n);
-        pos += 2 * n;
-        live = w.next(a);
+        ready(pos + 2 * o.n - 1, o);
+        pos += 2 * o.n;
+        step_done(j);
       }
     } else {
-      // Query rows of the items, a tile of them as soon as the products on its last rows are
-      // done.
-      uint32_t nq[2] = {0, 0};
-      while (live) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int rows = min(w.g.rows - t * kRowsUnit, kRowsUnit);
-          if (rows <= 0) continue;
-          wait_or_die(&bars.q_empty[t], (nq[t] & 1) ^ 1, dead);
-          ++nq[t];
-          const int row0 = w.g.row0 + t * kRowsUnit;
+      // The steps, one ahead of the query rows of each; a tile of rows as soon as the products on
+      // its last rows are done.
+      Walker w;
+      bool live = w.start(a, plan);
+      Header hd;
+      hd.rows = 0;
+      uint32_t nq0 = 0, nq1 = 0;
+      for (uint32_t j = 0;; ++j) {
+        wait_or_die(&bars.step_empty[j % kSteps], ((j / kSteps) & 1) ^ 1, dead);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
+        Step& next = small.steps[j % kSteps];
+        int kind = kEnd;
+#pragma unroll 1
+        for (int x = 0, n = 0; x < 2 && live; ++x) {
+          if (x == 0) {
+            kind = w.narrow() ? kSplit : kWide;
+            n = w.tiles();
+          } else {
+            if (kind != kSplit || !w.narrow() || abs(w.tiles() - n) > kSkew) break;
+            kind = kPair;
+          }
+          if (lane == 0) {
+            Item& it = next.it[x];
+            it.n = w.n; it.h = w.h; it.bos = w.s.bos; it.pos0 = w.s.pos0;
+            it.v0 = w.v0; it.v1 = w.v1;
+            it.g = w.g;
+          }
+          if (w.v0 == 0 && w.v1 < w.g.nt) {  // starts here and goes on: only the last item does
+            hd.rows = w.g.rows;
+            hd.row0 = w.g.row0;
+            hd.h = w.h;
+            hd.nt = w.g.nt;
+            hd.bos = w.s.bos;
+            hd.start = plan.end - (kOverhead + w.v1);
+            hd.total = plan.total;
+          }
+          live = w.next(a);
+        }
+        if (lane == 0) {
+          next.kind = kind;
+          mbar_arrive(&bars.step_full[j % kSteps]);
+        }
+        __syncwarp();
+        // the rows of the step before
+        const Step& st = small.steps[(j + kSteps - 1) % kSteps];
+        const int before = j == 0 ? kEnd : st.kind;
+#pragma unroll 1
+        for (int t = 0; t < (before == kEnd ? 0 : before == kSplit ? 1 : 2); ++t) {
+          const Item& it = st.it[before == kPair ? t : 0];
+          const int skip = before == kWide ? t * kRowsUnit : 0;
+          const int rows = min(it.g.rows - skip, kRowsUnit), row0 = it.g.row0 + skip;
+          const int bos = it.bos, h = it.h;
+          wait_or_die(&bars.q_empty[t], ((t ? nq1 : nq0) & 1) ^ 1, dead);
+          if (t)
+            ++nq1;
+          else
+            ++nq0;
           if (q_boxes && rows > 32) {
             // 128 rows are whole tokens: a box of 64 columns, the kv head's query heads and
             // those tokens (what lies behind the sequence is read and not used)
@@ -807,7 +973,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
               for (int hf = 0; hf < HALVES; ++hf)
                 tma_load_3d(sQ + t * C::kQBytes + hf * (kRowsUnit * RB), &qmap, &bars.q_full[t],
-                            hf * 64, w.h * a.G, w.s.bos + div_g(a, row0));
+                            hf * 64, h * a.G, bos + div_g(a, row0));
             }
             __syncwarp();
             continue;
@@ -818,8 +984,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           for (int r = lane / CH; r < rows; r += RPI) {
             const int tk = div_g(a, row0 + r), hg = row0 + r - tk * a.G;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                       (long long)(w.s.bos + tk) * a.q_stride +
-                                       (long long)(w.h * a.G + hg) * D + ch * 8;
+                                       (long long)(bos + tk) * a.q_stride +
+                                       (long long)(h * a.G + hg) * D + ch * 8;
             cp_async16(dst + piece_offset<D>(r, ch), src);
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -827,30 +993,38 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.q_full[t]);
         }
-        live = w.next(a);
+        if (kind == kEnd) break;
       }
+      if (lane == 0) headers[blockIdx.x] = hd;
       // leave no copy in flight behind a give-up (each tile's last one at most)
       if (dead)
         for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) mbar_wait(&bars.q_full[t], (nq[t] - 1) & 1, 100000000ull);
+          if ((t ? nq1 : nq0) > 0)
+            mbar_wait(&bars.q_full[t], ((t ? nq1 : nq0) - 1) & 1, 100000000ull);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    Walker<false> w;
     const int u = warp >> 2, r = tid & 127;  // unit, row within it
     const uint32_t lanebits = uint32_t(warp & 3) << 21;  // (32 * warp of the group) << 16
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
     const uint32_t tO0 = tm + kColO + lanebits, tO1 = tO0 + 128;
     const uint32_t tP = C::kOwnP ? tm + kColP64 + 128 * u + lanebits : tS;
     const float sc = a.scale * kLog2E;
-    uint32_t pos = 0, ns = 0, no = 0;
-    Header hd;
-    hd.rows = 0;
-    bool live = w.start(a, plan);
-    while (live) {
-      const int n = w.tiles();
-      const bool narrow = w.narrow();
-      const int base = narrow ? 0 : u * kRowsUnit;   // first row of the unit's tile
+    uint32_t pos = 0, ns = 0, no = 0, joins = 0;
+    auto join = [&]() {  // all softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.join);
+      wait_or_die(&bars.join, joins & 1, dead);
+      ++joins;
+    };
+    for (uint32_t j = 0;; ++j) {
+      const Step* st = step(j);
+      if (!st) break;
+      const Order order(*st);
+      const bool split = order.kind == kSplit;
+      const Item w = st->it[order.kind == kPair ? u : 0];
+      const int n = w.v1 - w.v0;
+      const int base = order.kind == kWide ? u * kRowsUnit : 0;  // first row of the unit's tile
       const int nr = min(w.g.rows - base, kRowsUnit);  // its rows (1 at least)
       const bool active = (warp & 3) * 32 < nr;      // (warp-uniform)
       const int row = w.g.row0 + base + min(r, nr - 1);
@@ -859,10 +1033,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       // 1. The unit's tiles.
       float m = -INFINITY, l = 0.f;
       int mine = 0;
-      const int mypos = w.s.pos0 + tk;
-      const int pos_first = w.s.pos0 + div_g(a, w.g.row0 + base);
-      const int pos_last = w.s.pos0 + div_g(a, w.g.row0 + base + nr - 1);
-      for (int i = narrow ? u : 0; i < n; i += narrow ? 2 : 1) {
+      const int mypos = w.pos0 + tk;
+      const int pos_first = w.pos0 + div_g(a, w.g.row0 + base);
+      const int pos_last = w.pos0 + div_g(a, w.g.row0 + base + nr - 1);
+      for (int i = split ? u : 0; i < n; i += split ? 2 : 1) {
         const int ks = tile_start(w.g, w.v0 + i);
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
@@ -973,40 +1147,70 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               };
               return below(hi) & (~below(lo) | below(sk));
             };
-            uint32_t s[4][32];
+            auto mask = [&](uint32_t(&s)[32], int q) {
+              const uint32_t b = bits(q);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32_start(tS + 32 * q, s[q]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32_finish(s[q]);
-            scores_read();
-            if (!whole) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t b = bits(q);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!(b >> c & 1)) s[q][c] = 0xff800000u;  // -inf: weight zero
-              }
-            }
+              for (int c = 0; c < 32; ++c)
+                if (!(b >> c & 1)) s[c] = 0xff800000u;  // -inf: weight zero
+            };
             float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
+            auto largest = [&](const uint32_t(&s)[32]) {
 #pragma unroll
               for (int c = 0; c < 32; c += 2)
                 c4[c / 2 & 3] =
-                    max3(c4[c / 2 & 3], __uint_as_float(s[q][c]), __uint_as_float(s[q][c + 1]));
-            const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
-            weights_free();
-            const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
-            if (__any_sync(0xffffffffu, grow)) rescale(grow ? mx : m);
-            const float nb = m == -INFINITY ? 0.f : -m * sc;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+                    max3(c4[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            };
+            float nb = 0.f;
+            auto standing = [&]() {
+              const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+              weights_free();
+              const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
+              if (__any_sync(0xffffffffu, grow)) rescale(grow ? mx : m);
+              nb = m == -INFINITY ? 0.f : -m * sc;
+            };
+            auto weigh = [&](const uint32_t(&s)[32], int q) {
               uint32_t p[16];
               float sum, top;
-              weights32(s[q], sc, nb, p, sum, top, true);
+              weights32(s, sc, nb, p, sum, top, true);
               l += sum;
               tmem_st16_nowait(tP + 16 * q, p);
+            };
+            if constexpr (C::kOwnP) {
+              // the scores are read at once, so that the next can be made
+              uint32_t s[4][32];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) tmem_ld32_start(tS + 32 * q, s[q]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) tmem_ld32_finish(s[q]);
+              scores_read();
+              if (!whole) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mask(s[q], q);
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) largest(s[q]);
+              standing();
+#pragma unroll
+              for (int q = 0; q < 4; ++q) weigh(s[q], q);
+            } else {
+              // twice, in loops: their instructions do not push the other roles' out of the cache
+              // (weights go over scores that have been read)
+              uint32_t s[32];
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                tmem_ld32_start(tS + 32 * q, s);
+                tmem_ld32_finish(s);
+                if (!whole) mask(s, q);
+                largest(s);
+              }
+              standing();
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                tmem_ld32_start(tS + 32 * q, s);
+                tmem_ld32_finish(s);
+                if (!whole) mask(s, q);
+                weigh(s, q);
+              }
             }
           }
         }
@@ -1015,7 +1219,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         // scores: the products before them have used every earlier entry of the ring, so the
         // value stage's barrier is in the phase that is waited for.
         if (ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks)) {
-          const uint32_t at = pos + ring_v(narrow, i, n);
+          const uint32_t at = pos + order.value(order.tile(u, i));
           wait_or_die(&bars.kv_full[at % NS], (at / NS) & 1, dead);
           const int key = ks + r;
           if (key >= w.g.kr.hi || (key < w.g.kr.lo && key >= w.g.kr.sinks)) {
@@ -1048,12 +1252,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         wait_or_die(&bars.o_full[u], (no & 1) ^ 1, dead);
       }
       float f0 = 1.f, f1 = 0.f;  // of units 0 and 1 (wide: f0 is the unit's own)
-      const bool both = narrow && n > 1;
+      const bool both = split && n > 1;
       constexpr int kShare = D == 32 ? 32 : D / 2;  // columns of unit 0
-      if (narrow) {
+      if (split) {
         s_ml[128 * u + r] = make_float2(m, l);
         tc_fence_before();
-        group_sync(1, 256);
+        join();
         const float2 x = s_ml[r], y = s_ml[128 + r];
         m = x.x;
         l = x.y;
@@ -1070,17 +1274,17 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       if (active) {
         const bool valid = r < nr;
         const long long orow =
-            (long long)(w.s.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
+            (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         const long long prow =
             (long long)(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRowsItem + base + r;
         __nv_bfloat16* orowp = static_cast<__nv_bfloat16*>(a.out) + orow * D;
         const bool wide_stores = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
-        for (int c = narrow ? u * kShare : 0; c < (narrow && u == 0 ? kShare : D); c += 32) {
+        for (int c = split ? u * kShare : 0; c < (split && u == 0 ? kShare : D); c += 32) {
           uint32_t o[32], o1[32];
-          tmem_ld32_start((narrow ? tO0 : tO) + c, o);
-          tmem_ld32_start((both ? tO1 : narrow ? tO0 : tO) + c, o1);
+          tmem_ld32_start((split ? tO0 : tO) + c, o);
+          tmem_ld32_start((both ? tO1 : split ? tO0 : tO) + c, o1);
           tmem_ld32_finish(o);
           tmem_ld32_finish(o1);
           if (both) {
@@ -1111,7 +1315,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
-        if (valid && (!narrow || u == 0)) {
+        if (valid && (!split || u == 0)) {
           if (cut0 || cut1)
             part_ml[prow] = make_float2(m * sc, l);
           else if (a.lse)
@@ -1120,20 +1324,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         }
       }
       tc_fence_before();
-      if (narrow) group_sync(1, 256);
-      if (!cut0 && cut1) {  // it starts here and goes on: only the stretch's last item does
-        hd.rows = w.g.rows;
-        hd.row0 = w.g.row0;
-        hd.h = w.h;
-        hd.nt = w.g.nt;
-        hd.bos = w.s.bos;
-        hd.start = plan.end - (kOverhead + w.v1);
-        hd.total = plan.total;
-      }
-      pos += 2 * n;
-      live = w.next(a);
+      if (split) join();  // (neither overwrites what the other reads)
+      pos += 2 * order.n;
+      step_done(j);
     }
-    if (tid == 0) headers[blockIdx.x] = hd;
   }
   tc_fence_before();
   __syncthreads();
@@ -1264,8 +1458,8 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes, headers, po,
-                                                              ml);
+  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes,
+                                                             headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a thread per four columns of the largest item there can be
