@@ -1069,11 +1069,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
           bool done = false;
           // O and l to another maximum (mine > 0, or O is not there yet).
+          bool lower = false;  // the product of the tile's lower half is in O
           auto rescale = [&](float mn) {
             const float f = mn == -INFINITY ? 1.f : fast_exp2((m - mn) * sc);
             m = mn;
             l *= f;
-            if (mine > 0) {
+            if (mine > 0 || lower) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 float o[16];
@@ -1085,7 +1086,19 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               }
             }
           };
-          if (!C::kOwnP && whole && mine > 0) {
+          if (!C::kOwnP && whole && mine == 0) {
+            // no maximum yet: that of the first 32 keys
+            uint32_t s[32];
+            tmem_ld32_start(tS, s);
+            tmem_ld32_finish(s);
+            float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              c4[c / 2 & 3] =
+                  max3(c4[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            m = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+          }
+          if (!C::kOwnP && whole) {
             // Weights against the maximum so far, which almost always stands, while the
             // tile's own maximum is found beside them; the scores stay until that is known.
             // The lower half of the keys is handed over while the upper is computed.
@@ -1120,6 +1133,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 // O and l are scaled down and the upper half's weights made again.
                 wait_or_die(&bars.oh_full[u], (ns - 1) & 1, dead);
                 tc_fence_after();
+                lower = true;
                 rescale(outgrown() ? top : m);
                 const float nb2 = m == -INFINITY ? 0.f : -m * sc;
                 tmem_ld32_start(tS + 64, s[0]);
