@@ -1105,7 +1105,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             const float nb = m == -INFINITY ? 0.f : -m * sc;
             uint32_t p[32], s[2][32];
             float sum, top;
-            auto outgrown = [&]() { return top > m && (top - m) * sc > kRescale; };
+            // (rows behind the item's last hold anything, and must not choose the way: the two
+            // ways sum in different orders)
+            auto outgrown = [&]() { return r < nr && top > m && (top - m) * sc > kRescale; };
             tmem_ld32_start(tS, s[0]);
             tmem_ld32_finish(s[0]);
             tmem_ld32_start(tS + 32, s[1]);
@@ -1178,7 +1180,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             auto standing = [&]() {
               const float mx = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
               weights_free();
-              const bool grow = mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any score)
+              const bool grow = r < nr && mx > m && (mx - m) * sc > kRescale;  // (m = -inf: any)
               if (__any_sync(0xffffffffu, grow)) rescale(grow ? mx : m);
               nb = m == -INFINITY ? 0.f : -m * sc;
             };

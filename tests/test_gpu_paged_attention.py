@@ -323,3 +323,64 @@ def test_empty_calls():
                                     1, D, 0, 16, 0, workspace=ws)
         torch.cuda.synchronize()
         assert (d["out"] == 0).all()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("window", [0, 300])
+def test_neighbours_of_any_length(D, window):
+    """Single tokens and short chunks whose neighbours have fewer, as many or more key tiles, so
+    that every block meets each of these pairs."""
+    rng = np.random.default_rng(11)
+    kv = np.concatenate([rng.integers(1, 400, 350), rng.integers(1, 1600, 350)])
+    rng.shuffle(kv)
+    d = make([(int(min(k, rng.integers(1, 4))), int(k)) for k in kv], 4, 1, D, 32, "bf16", seed=50)
+    call(d, window=window, sinks=2 if window else 0)
+    a = d["out"].clone()
+    check(d, window=window, sinks=2 if window else 0)
+    for _ in range(10):
+        call(d, window=window, sinks=2 if window else 0)
+        assert torch.equal(a, d["out"])
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (70, 5), (64, 200)])
+def test_chunks_in_fp32(D, window, sinks):
+    for Hq, Hkv, page in ((4, 2, 64), (5, 1, 16)):
+        d = make([(100, 100), (1, 700), (16, 16), (0, 9), (17, 300), (64, 64), (65, 900)], Hq, Hkv,
+                 D, page, "f32", seed=window, pad=2, fill=float("nan"))
+        call(d, window=window, sinks=sinks)
+        d["kc"], d["vc"] = torch.nan_to_num(d["kc"]), torch.nan_to_num(d["vc"])
+        check(d, window=window, sinks=sinks)
+
+
+def test_one_fp32_chunk_over_a_long_cache():
+    d = make([(40, 6000)], 2, 1, 128, 128, "f32", seed=60)  # its keys in parts
+    call(d)
+    check(d)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_fp32_values_that_only_the_last_token_sees(bad):
+    d = make([(70, 200)], 2, 1, 64, 32, "f32", seed=61)
+    p = int(d["table_h"][0, 199 // 32])
+    d["vc"][p, :, 199 % 32] = bad
+    call(d)
+    got = d["out"].clone()
+    d["vc"][p, :, 199 % 32] = 0
+    d["out"].copy_(torch.where(torch.isfinite(got), got, torch.zeros_like(got)))
+    assert not torch.isfinite(got[69]).any() and torch.isfinite(got[:69]).all()
+    r = ref.paged_attention(host(d["q"])[:69], host(d["kc"]), host(d["vc"]), d["table_h"],
+                            np.array([0, 69], np.int32), np.array([199], np.int32), 32)
+    lim = (2 * (64 + 8) * 2.0 ** -24 * r[3] + 264 * 2.0 ** -24)[..., None] * r[2]
+    assert (np.abs(host(got[:69]) - r[0]) <= lim).all()
+
+
+def test_more_fp32_chunks_than_blocks_search():
+    rng = np.random.default_rng(8)
+    q = rng.integers(0, 9, 1100)
+    q[::7] += 4
+    d = make([(int(x), int(x + k)) for x, k in zip(q, rng.integers(0, 90, 1100))], 8, 1, 32, 16,
+             "f32", seed=62)
+    assert d["T"] * 8 >= 32 * 1100
+    call(d)
+    check(d)
