@@ -170,6 +170,254 @@ __device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* 
   }
 }
 
+// ------------------------------------------------------------------------- tall row tiles
+//
+// The same for chunks: 64 rows against 64 keys at a time.  A thread of a block of 8 x 16 scores
+// the rows ty + 8 i against the keys tx + 16 j (NI x 4 products, in pairs along D), and then owns
+// D / 16 output columns of those rows; the weights pass through shared memory, over the keys.
+// Bound by the FMA pipes: a thread reads 12 (scores) and 8 + 8 (outputs) 16-byte pieces of shared
+// memory for 128 and 256 multiply-adds.  Two blocks share an SM, and one computes while the other
+// waits for its keys.  NI: the rows of a thread that the tile needs.
+
+constexpr int kTallRows = 64, kTallKeys = 64;
+
+template <int D> struct Tall {
+  static constexpr int PQ = D + 4;           // pitches: 16-byte rows, neighbours on other banks
+  static constexpr int PP = kTallKeys + 4;
+  static constexpr int KP = PQ > PP ? PQ : PP;  // keys, then weights
+  static constexpr int CW = D < 64 ? 2 : 4;  // neighbouring columns of a thread
+  static constexpr int CG = D / (16 * CW);   // groups of them
+  static constexpr int kSmem = (kTallRows * PQ + kTallKeys * KP + kTallKeys * D) * 4;
+};
+
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// 16 bytes, or zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+
+template <int D, int NI>
+__device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
+                          float* smem, float* part_o, float2* part_ml) {
+  using T = Tall<D>;
+  constexpr int PQ = T::PQ, PP = T::PP, CW = T::CW, CG = T::CG, NC = CW / 2 * CG;
+  float* sQ = smem;
+  float* sK = sQ + kTallRows * PQ;
+  float* sP = sK;
+  float* sV = sK + kTallKeys * T::KP;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int G = a.Hq / a.Hkv, hkv = blockIdx.y, part = blockIdx.z;
+  const KeyRange kr = key_range(a, q, r0 / G, (r0 + nr - 1) / G);
+  const int total = kr.sinks + kr.hi - kr.lo;
+  const int np = max(min(parts, (total + kTallKeys - 1) / kTallKeys), 1);
+  const int per = (total + np - 1) / np;
+  const int v0 = min(part * per, total), v1 = part < np ? min(v0 + per, total) : v0;
+  const int shift = __ffs(a.page_size) - 1;
+
+  auto fetch = [&](int vb) {
+    constexpr int PIECES = D / 4;
+#pragma unroll 4
+    for (int i = tid; i < kTallKeys * PIECES; i += kThreads) {
+      const int key_i = i / PIECES, c = i % PIECES * 4;
+      const bool there = vb + key_i < v1;
+      const int key = there ? virtual_key(kr, vb + key_i) : 0;
+      const int p = there ? __ldg(a.block_table + (long long)n * a.max_pages + (key >> shift)) : 0;
+      const long long row =
+          (((long long)min(max(p, 0), a.num_pages - 1) * a.Hkv + hkv) << shift) +
+          (key & (a.page_size - 1));
+      copy16(&sK[key_i * PQ + c], static_cast<const float*>(a.k_cache) + row * D + c, there);
+      copy16(&sV[key_i * D + c], static_cast<const float*>(a.v_cache) + row * D + c, there);
+    }
+  };
+  if (v0 < v1) fetch(v0);
+  for (int i = tid; i < NI * 8 * (D / 4); i += kThreads) {
+    const int row = i / (D / 4), c = i % (D / 4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < nr) {
+      const long long tok = (long long)q.bos + (r0 + row) / G;
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + tok * a.q_stride +
+                                           (long long)(hkv * G + (r0 + row) % G) * D + c);
+    }
+    const float sc = a.scale * 1.4426950408889634f;  // scores in log2 units
+    *reinterpret_cast<float4*>(&sQ[row * PQ + c]) =
+        make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+  }
+  float m[NI], l[NI];
+  int pos[NI];
+  uint64_t o[NI][NC];  // pairs of columns
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    pos[i] = ty + 8 * i < nr ? q.pos0 + (r0 + ty + 8 * i) / G : -1;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) o[i][c] = 0;
+  }
+  const int pos_first = q.pos0 + r0 / G, pos_last = q.pos0 + (r0 + nr - 1) / G;
+  for (int vb = v0; vb < v1; vb += kTallKeys) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // Values that are not finite: then hidden keys are left out one by one (zero times them
+    // would not be zero).
+    float odd = 0.f;
+#pragma unroll 4
+    for (int i = tid; i < kTallKeys * (D / 4); i += kThreads) {
+      const float4 x = *reinterpret_cast<const float4*>(&sV[i * 4]);
+      odd += x.x * 0.f + x.y * 0.f + x.z * 0.f + x.w * 0.f;
+    }
+    const bool careful = __syncthreads_or(odd != 0.f);  // (each thread has read its own pieces)
+    uint64_t s2[NI][4];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+#pragma unroll 2
+    for (int c = 0; c < D; c += 4) {
+      ulonglong2 k[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k[j] = *reinterpret_cast<const ulonglong2*>(&sK[(tx + 16 * j) * PQ + c]);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sQ[(ty + 8 * i) * PQ + c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2[i][j] = fma2(x.y, k[j].y, fma2(x.x, k[j].x, s2[i][j]));
+      }
+    }
+    const int first = virtual_key(kr, vb);
+    const bool whole = vb + kTallKeys <= v1 && virtual_key(kr, vb + kTallKeys - 1) <= pos_first &&
+                       (a.window == 0 || first > pos_last - a.window);
+    __syncthreads();  // the keys are done with
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float s[4], mx = -INFINITY;
+      bool see[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 h = split(s2[i][j]);
+        const int v = vb + tx + 16 * j;
+        see[j] = whole || (v < v1 && visible(a, pos[i], virtual_key(kr, v)));
+        s[j] = see[j] ? h.x + h.y : -INFINITY;
+        mx = (s[j] > mx || s[j] != s[j]) ? s[j] : mx;  // a NaN score stays
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, mx, w);
+        mx = (y > mx || y != y) ? y : mx;
+      }
+      const float mn = (mx > m[i] || mx != mx) ? mx : m[i];
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - base);
+      m[i] = mn;
+      l[i] *= f;  // the thread's own share; joined at the end
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = see[j] ? exp2f(s[j] - base) : 0.f;
+        l[i] += p;
+        sP[(ty + 8 * i) * PP + tx + 16 * j] = p;
+      }
+      const uint64_t f2 = pair(f, f);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[i][c] = mul2(o[i][c], f2);
+    }
+    __syncthreads();
+    // columns CW tx + 16 CW g + ...
+    auto values = [&](int k, uint64_t(&v)[NC]) {
+#pragma unroll
+      for (int g = 0; g < CG; ++g) {
+        const float* src = &sV[k * D + CW * (tx + 16 * g)];
+        if constexpr (CW == 4) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(src);
+          v[2 * g] = x.x;
+          v[2 * g + 1] = x.y;
+        } else {
+          v[g] = *reinterpret_cast<const uint64_t*>(src);
+        }
+      }
+    };
+    if (!careful) {
+#pragma unroll 2
+      for (int k = 0; k < kTallKeys; k += 4) {
+        uint64_t v[4][NC];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) values(k + e, v[e]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float4 p = *reinterpret_cast<const float4*>(&sP[(ty + 8 * i) * PP + k]);
+          const uint64_t p2[4] = {pair(p.x, p.x), pair(p.y, p.y), pair(p.z, p.z), pair(p.w, p.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] = fma2(p2[e], v[e][c], o[i][c]);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kTallKeys; ++k) {
+        uint64_t v[NC];
+        values(k, v);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float p = sP[(ty + 8 * i) * PP + k];
+          if (p != 0.f)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] = fma2(pair(p, p), v[c], o[i][c]);
+        }
+      }
+    }
+    __syncthreads();
+    if (vb + kTallKeys < v1) fetch(vb + kTallKeys);
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    float lt = l[i];
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+    const int rr = ty + 8 * i;
+    if (rr >= nr) continue;
+    const long long tok = (long long)q.bos + (r0 + rr) / G;
+    const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
+    const long long at = (long long)part * a.total_T * a.Hq + row;
+    const float inv = parts > 1 ? 1.f : lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
+    float* dst = parts > 1 ? part_o + at * D : static_cast<float*>(a.out) + row * D;
+#pragma unroll
+    for (int g = 0; g < CG; ++g)
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) {
+        const float2 x = split(o[i][CW / 2 * g + c]);
+        *reinterpret_cast<float2*>(dst + CW * (tx + 16 * g) + 2 * c) =
+            make_float2(x.x * inv, x.y * inv);
+      }
+    if (tx == 0) {
+      if (parts > 1)
+        part_ml[at] = make_float2(m[i], lt);
+      else if (a.lse)
+        a.lse[row] = lt == 0.f ? -INFINITY : (m[i] + log2f(lt)) * 0.6931471805599453f;
+    }
+  }
+}
+
 // Blocks are numbered over the sequences' row tiles; with many sequences, where the search for a
 // block's tile would cost more than the tile, over the sequences.
 constexpr int kSearch = 1024;
@@ -189,6 +437,33 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int p
     int n, tile;
     if (find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile))
       row_tile<D>(a, n, tile, parts, part_o, part_ml);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) paged_tall_kernel(PagedArgs a, int parts,
+                                                                 float* part_o, float2* part_ml) {
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int s_find[2];
+  auto tile_of = [&](int n, int tile) {
+    const Seq q = load_seq(a, n);
+    const int rows = q.len * (a.Hq / a.Hkv), r0 = tile * kTallRows;
+    const int nr = min(kTallRows, rows - r0);
+    if (nr <= 16)
+      tall_tile<D, 2>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+    else
+      tall_tile<D, 8>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+  };
+  if (a.N > kSearch) {
+    const int n = blockIdx.x, G = a.Hq / a.Hkv;
+    const int tiles = (int)(((long long)load_seq(a, n).len * G + kTallRows - 1) / kTallRows);
+    for (int tile = 0; tile < tiles; ++tile) {
+      __syncthreads();  // the last tile's shared memory is free
+      tile_of(n, tile);
+    }
+  } else {
+    int n, tile;
+    if (find_row_tile<kThreads>(a, kTallRows, (int)blockIdx.x, s_find, n, tile)) tile_of(n, tile);
   }
 }
 
@@ -247,14 +522,20 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
     a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Parts of the key range: enough blocks for four on each SM when there are few rows.
+// Tall tiles where a sequence has 32 rows or more on average.
+bool tall(int N, int total_T, int Hq, int Hkv) {
+  return (long long)total_T * (Hq / Hkv) >= 32ll * N;
+}
+
+// Parts of the key range: enough blocks for four (tall: two) on each SM when there are few rows.
 int simt_parts(int N, int total_T, int Hq, int Hkv) {
-  const long long G = Hq / Hkv;
-  long long tiles = (total_T * G + kRows - 1) / kRows;
+  const bool big = tall(N, total_T, Hq, Hkv);
+  const long long G = Hq / Hkv, height = big ? kTallRows : kRows;
+  long long tiles = (total_T * G + height - 1) / height;
   const long long seqs = N < total_T ? N : total_T;
   if (tiles < seqs) tiles = seqs;
   if (tiles <= 0) return 1;
-  const long long p = 152 * 4 / (tiles * Hkv);
+  const long long p = 152 * (big ? 2 : 4) / (tiles * Hkv);
   return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
@@ -265,9 +546,18 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   float* po = static_cast<float*>(workspace);
   float2* pml = reinterpret_cast<float2*>(po + (parts > 1 ? parts * rows * D : 0));
   const long long G = a.Hq / a.Hkv;
-  const long long tiles = (a.total_T * G + kRows - 1) / kRows + a.N;  // upper bound
+  const bool big = tall(a.N, a.total_T, a.Hq, a.Hkv);
+  const int height = big ? kTallRows : kRows;
+  const long long tiles = (a.total_T * G + height - 1) / height + a.N;  // upper bound
   const dim3 grid((unsigned)(a.N > kSearch ? a.N : tiles), (unsigned)a.Hkv, (unsigned)parts);
-  paged_simt_kernel<D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
+  if (big) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        paged_tall_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tall<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    paged_tall_kernel<D><<<grid, kThreads, Tall<D>::kSmem, st>>>(a, parts, po, pml);
+  } else {
+    paged_simt_kernel<D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || parts == 1) return e;
   cudaLaunchConfig_t cfg{};
