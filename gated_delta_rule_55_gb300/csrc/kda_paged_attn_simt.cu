@@ -172,21 +172,22 @@ __device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* 
 
 // ------------------------------------------------------------------------- tall row tiles
 //
-// The same for chunks: 64 rows against 64 keys at a time.  A thread of a block of 8 x 16 scores
-// the rows ty + 8 i against the keys tx + 16 j (NI x 4 products, in pairs along D), and then owns
-// D / 16 output columns of those rows; the weights pass through shared memory, over the keys.
-// Bound by the FMA pipes: a thread reads 12 (scores) and 8 + 8 (outputs) 16-byte pieces of shared
-// memory for 128 and 256 multiply-adds.  Two blocks share an SM, and one computes while the other
-// waits for its keys.  NI: the rows of a thread that the tile needs.
+// The same for chunks: 64 rows against 64 keys at a time.  A thread of a block of 16 x 8 scores
+// the rows ty + 16 i against the keys tx + 8 j (NI x 8 products, in pairs along D), and then owns
+// D / 8 output columns of those rows; the weights pass through shared memory, over the keys.
+// Bound by the FMA pipes, closely followed by shared memory: a warp's 16-byte load takes a cycle
+// for each half of it, however many lanes share an address, so 12 loads for 128 multiply-adds of
+// a thread are three quarters of what the FMA pipes take (16 x 16 threads: 24 cycles of loads for
+// 16).  Two blocks share an SM, and one computes while the other waits for its keys.
+// NI: the rows of a thread that the tile needs.
 
 constexpr int kTallRows = 64, kTallKeys = 64;
 
 template <int D> struct Tall {
-  static constexpr int PQ = D + 4;           // pitches: 16-byte rows, neighbours on other banks
-  static constexpr int PP = kTallKeys + 4;
+  static constexpr int PQ = D + 4;             // pitches: 16-byte rows, neighbours on other banks
+  static constexpr int PP = kTallKeys + 8;
   static constexpr int KP = PQ > PP ? PQ : PP;  // keys, then weights
-  static constexpr int CW = D < 64 ? 2 : 4;  // neighbouring columns of a thread
-  static constexpr int CG = D / (16 * CW);   // groups of them
+  static constexpr int CG = D / 32;            // groups of 4 neighbouring columns of a thread
   static constexpr int kSmem = (kTallRows * PQ + kTallKeys * KP + kTallKeys * D) * 4;
 };
 
@@ -222,12 +223,12 @@ template <int D, int NI>
 __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
                           float* smem, float* part_o, float2* part_ml) {
   using T = Tall<D>;
-  constexpr int PQ = T::PQ, PP = T::PP, CW = T::CW, CG = T::CG, NC = CW / 2 * CG;
+  constexpr int PQ = T::PQ, PP = T::PP, CG = T::CG, NC = 2 * CG, NJ = kTallKeys / 8;
   float* sQ = smem;
   float* sK = sQ + kTallRows * PQ;
   float* sP = sK;
   float* sV = sK + kTallKeys * T::KP;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
   const int G = a.Hq / a.Hkv, hkv = blockIdx.y, part = blockIdx.z;
   const KeyRange kr = key_range(a, q, r0 / G, (r0 + nr - 1) / G);
   const int total = kr.sinks + kr.hi - kr.lo;
@@ -252,7 +253,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
     }
   };
   if (v0 < v1) fetch(v0);
-  for (int i = tid; i < NI * 8 * (D / 4); i += kThreads) {
+  for (int i = tid; i < NI * 16 * (D / 4); i += kThreads) {
     const int row = i / (D / 4), c = i % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < nr) {
@@ -271,7 +272,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
   for (int i = 0; i < NI; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-    pos[i] = ty + 8 * i < nr ? q.pos0 + (r0 + ty + 8 * i) / G : -1;
+    pos[i] = ty + 16 * i < nr ? q.pos0 + (r0 + ty + 16 * i) / G : -1;
 #pragma unroll
     for (int c = 0; c < NC; ++c) o[i][c] = 0;
   }
@@ -287,22 +288,22 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
       odd += x.x * 0.f + x.y * 0.f + x.z * 0.f + x.w * 0.f;
     }
     const bool careful = __syncthreads_or(odd != 0.f);  // (each thread has read its own pieces)
-    uint64_t s2[NI][4];
+    uint64_t s2[NI][NJ];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s2[i][j] = 0;
+      for (int j = 0; j < NJ; ++j) s2[i][j] = 0;
 #pragma unroll 2
     for (int c = 0; c < D; c += 4) {
-      ulonglong2 k[4];
+      ulonglong2 k[NJ];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        k[j] = *reinterpret_cast<const ulonglong2*>(&sK[(tx + 16 * j) * PQ + c]);
+      for (int j = 0; j < NJ; ++j)
+        k[j] = *reinterpret_cast<const ulonglong2*>(&sK[(tx + 8 * j) * PQ + c]);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sQ[(ty + 8 * i) * PQ + c]);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sQ[(ty + 16 * i) * PQ + c]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s2[i][j] = fma2(x.y, k[j].y, fma2(x.x, k[j].x, s2[i][j]));
+        for (int j = 0; j < NJ; ++j) s2[i][j] = fma2(x.y, k[j].y, fma2(x.x, k[j].x, s2[i][j]));
       }
     }
     const int first = virtual_key(kr, vb);
@@ -311,18 +312,18 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
     __syncthreads();  // the keys are done with
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      float s[4], mx = -INFINITY;
-      bool see[4];
+      float s[NJ], mx = -INFINITY;
+      bool see[NJ];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         const float2 h = split(s2[i][j]);
-        const int v = vb + tx + 16 * j;
+        const int v = vb + tx + 8 * j;
         see[j] = whole || (v < v1 && visible(a, pos[i], virtual_key(kr, v)));
         s[j] = see[j] ? h.x + h.y : -INFINITY;
         mx = (s[j] > mx || s[j] != s[j]) ? s[j] : mx;  // a NaN score stays
       }
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) {
+      for (int w = 4; w > 0; w >>= 1) {
         const float y = __shfl_xor_sync(0xffffffffu, mx, w);
         mx = (y > mx || y != y) ? y : mx;
       }
@@ -332,28 +333,22 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
       m[i] = mn;
       l[i] *= f;  // the thread's own share; joined at the end
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         const float p = see[j] ? exp2f(s[j] - base) : 0.f;
         l[i] += p;
-        sP[(ty + 8 * i) * PP + tx + 16 * j] = p;
+        sP[(ty + 16 * i) * PP + tx + 8 * j] = p;
       }
       const uint64_t f2 = pair(f, f);
 #pragma unroll
       for (int c = 0; c < NC; ++c) o[i][c] = mul2(o[i][c], f2);
     }
     __syncthreads();
-    // columns CW tx + 16 CW g + ...
-    auto values = [&](int k, uint64_t(&v)[NC]) {
+    auto values = [&](int k, uint64_t(&v)[NC]) {  // columns 4 tx + 32 g + ...
 #pragma unroll
       for (int g = 0; g < CG; ++g) {
-        const float* src = &sV[k * D + CW * (tx + 16 * g)];
-        if constexpr (CW == 4) {
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(src);
-          v[2 * g] = x.x;
-          v[2 * g + 1] = x.y;
-        } else {
-          v[g] = *reinterpret_cast<const uint64_t*>(src);
-        }
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&sV[k * D + 4 * tx + 32 * g]);
+        v[2 * g] = x.x;
+        v[2 * g + 1] = x.y;
       }
     };
     if (!careful) {
@@ -364,7 +359,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
         for (int e = 0; e < 4; ++e) values(k + e, v[e]);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const float4 p = *reinterpret_cast<const float4*>(&sP[(ty + 8 * i) * PP + k]);
+          const float4 p = *reinterpret_cast<const float4*>(&sP[(ty + 16 * i) * PP + k]);
           const uint64_t p2[4] = {pair(p.x, p.x), pair(p.y, p.y), pair(p.z, p.z), pair(p.w, p.w)};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -379,7 +374,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
         values(k, v);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const float p = sP[(ty + 8 * i) * PP + k];
+          const float p = sP[(ty + 16 * i) * PP + k];
           if (p != 0.f)
 #pragma unroll
             for (int c = 0; c < NC; ++c) o[i][c] = fma2(pair(p, p), v[c], o[i][c]);
@@ -393,8 +388,8 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
   for (int i = 0; i < NI; ++i) {
     float lt = l[i];
 #pragma unroll
-    for (int w = 8; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
-    const int rr = ty + 8 * i;
+    for (int w = 4; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+    const int rr = ty + 16 * i;
     if (rr >= nr) continue;
     const long long tok = (long long)q.bos + (r0 + rr) / G;
     const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
@@ -402,13 +397,11 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
     const float inv = parts > 1 ? 1.f : lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
     float* dst = parts > 1 ? part_o + at * D : static_cast<float*>(a.out) + row * D;
 #pragma unroll
-    for (int g = 0; g < CG; ++g)
-#pragma unroll
-      for (int c = 0; c < CW / 2; ++c) {
-        const float2 x = split(o[i][CW / 2 * g + c]);
-        *reinterpret_cast<float2*>(dst + CW * (tx + 16 * g) + 2 * c) =
-            make_float2(x.x * inv, x.y * inv);
-      }
+    for (int g = 0; g < CG; ++g) {
+      const float2 x = split(o[i][2 * g]), y = split(o[i][2 * g + 1]);
+      *reinterpret_cast<float4*>(dst + 4 * tx + 32 * g) =
+          make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+    }
     if (tx == 0) {
       if (parts > 1)
         part_ml[at] = make_float2(m[i], lt);
@@ -450,9 +443,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tall_kernel(PagedArgs a, in
     const int rows = q.len * (a.Hq / a.Hkv), r0 = tile * kTallRows;
     const int nr = min(kTallRows, rows - r0);
     if (nr <= 16)
+      tall_tile<D, 1>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+    else if (nr <= 32)
       tall_tile<D, 2>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
     else
-      tall_tile<D, 8>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+      tall_tile<D, 4>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
   };
   if (a.N > kSearch) {
     const int n = blockIdx.x, G = a.Hq / a.Hkv;
