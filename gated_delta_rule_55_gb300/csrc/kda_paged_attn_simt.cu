@@ -4,38 +4,46 @@
 // A block takes 16 query rows (tokens x query heads of one kv head) of one sequence and one
 // part of its visible keys, and keeps for every row the running maximum m, the sum l of
 // e^{s - m} and the unnormalised output, so the keys are read once.  Keys are taken 32 at a
-// time into shared memory: a lane scores one key against the warp's four rows, and then owns
-// D / 32 output columns of those rows.  Bound by the FMA pipes for chunks and by HBM latency
-// for single tokens, so a long key range is cut into parts (for few rows) whose (m, l, o) are
-// joined by a second kernel.  5 sequences of 1..17 tokens over up to 700 keys, 4 + 4 heads of 64:
-// 11.4 us, one round trip to memory after another.
+// time into shared memory: a lane scores one key against the warp's rows, and then owns D / 32
+// output columns of those rows.  Bound by latency (a step of keys is a round trip to memory), so
+// a long key range is cut into parts (for few rows) whose (m, l, o) are joined by a second
+// kernel, and blocks share an SM.  5 sequences of 1..17 tokens over up to 700 keys, 4 + 4 heads
+// of 64: 11.5 us.  Chunks take taller tiles (below), which the FMA pipes bound.
 #include "kda_paged.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kRows = 16;    // query rows of a block
-constexpr int kRW = 4;       // rows of a warp
+constexpr int kWarps = 4;    // of a block
 constexpr int kKeys = 32;    // keys of a step
 constexpr int kThreads = 128;
 constexpr int kMaxParts = 32;
 constexpr int kMinPartKeys = kKeys;  // one step: a step is a round trip to memory
 
-// One row tile of sequence n; all threads of the block call.
-template <int D>
-__device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* part_o,
-                         float2* part_ml) {
-  constexpr int PK = D + 4;    // K pitch: 16-byte rows, lanes on different banks
-  constexpr int C = D / 32;    // output columns of a lane
-  __shared__ __align__(16) float sK[kKeys * PK];
-  __shared__ __align__(16) float sV[kKeys * D];
-  __shared__ __align__(16) float sQ[kRows * D];
+// 16 bytes, or zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+
+template <int D> struct Short {
+  static constexpr int PK = D + 4;  // K pitch: 16-byte rows, lanes on different banks
+  float k[kKeys * PK], v[kKeys * D], q[kRows * D];
+};
+
+// One row tile of sequence n, RW rows for each warp; all threads of the block call.
+template <int D, int RW>
+__device__ void row_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
+                         Short<D>& sm, float* part_o, float2* part_ml) {
+  constexpr int PK = Short<D>::PK;
+  constexpr int C = D / 32;  // output columns of a lane
+  float *sK = sm.k, *sV = sm.v, *sQ = sm.q;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
   const int hkv = blockIdx.y, part = blockIdx.z;
-  const Seq q = load_seq(a, n);
-  const int rows = q.len * G, r0 = tile * kRows;
-  const int nr = min(kRows, rows - r0);
   const KeyRange kr = key_range(a, q, r0 / G, (r0 + nr - 1) / G);
   const int total = kr.sinks + kr.hi - kr.lo;
   int np = min(parts, (total + kMinPartKeys - 1) / kMinPartKeys);
@@ -57,63 +65,58 @@ __device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* 
         make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
   }
 
-  float m[kRW], l[kRW], o[kRW][C];
-  int pos[kRW];
+  float m[RW], l[RW], o[RW][C];
+  int pos[RW];
 #pragma unroll
-  for (int r = 0; r < kRW; ++r) {
+  for (int r = 0; r < RW; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
-    const int rr = warp * kRW + r;
+    const int rr = warp * RW + r;
     pos[r] = rr < nr ? q.pos0 + (r0 + rr) / G : -1;
 #pragma unroll
     for (int c = 0; c < C; ++c) o[r][c] = 0.f;
   }
-  const bool busy = warp * kRW < nr;
-  // 16-byte pieces of a step's K and V rows; places behind the part's end hold zeros.  The next
-  // step's are on their way while this one is computed.
-  constexpr int VE = 4, PIECES = D / VE, PT = kKeys * PIECES / kThreads;
-  float4 kraw[PT], vraw[PT];
+  const bool busy = warp * RW < nr;
+  // A step's K and V rows; places behind the part's end hold zeros.
+  constexpr int PIECES = D / 4;
   auto fetch = [&](int vb) {
 #pragma unroll
-    for (int k = 0; k < PT; ++k) {
-      const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
-      kraw[k] = vraw[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (vb + key_i < v1) {
-        const long long off = cache_row(a, n, hkv, virtual_key(kr, vb + key_i)) * D + c;
-        kraw[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.k_cache) + off));
-        vraw[k] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.v_cache) + off));
-      }
+    for (int k = 0; k < kKeys * PIECES / kThreads; ++k) {
+      const int i = tid + k * kThreads;
+      const int key_i = i / PIECES, c = i % PIECES * 4;
+      const bool there = vb + key_i < v1;
+      const long long off =
+          there ? cache_row(a, n, hkv, virtual_key(kr, vb + key_i)) * D + c : 0;
+      copy16(&sK[key_i * PK + c], static_cast<const float*>(a.k_cache) + off, there);
+      copy16(&sV[key_i * D + c], static_cast<const float*>(a.v_cache) + off, there);
     }
   };
   if (v0 < v1) fetch(v0);
   for (int vb = v0; vb < v1; vb += kKeys) {
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < PT; ++k) {
-      const int i = tid + k * kThreads, key_i = i / PIECES, c = i % PIECES * VE;
-      *reinterpret_cast<float4*>(&sK[key_i * PK + c]) = kraw[k];
-      *reinterpret_cast<float4*>(&sV[key_i * D + c]) = vraw[k];
+    if (vb > v0) {
+      __syncthreads();  // the last step's are done with
+      fetch(vb);
     }
-    if (vb + kKeys < v1) fetch(vb + kKeys);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!busy) continue;
-    float s[kRW];
+    float s[RW];
 #pragma unroll
-    for (int r = 0; r < kRW; ++r) s[r] = 0.f;
+    for (int r = 0; r < RW; ++r) s[r] = 0.f;
 #pragma unroll 8
     for (int c = 0; c < D; c += 4) {
       const float4 kx = *reinterpret_cast<const float4*>(&sK[lane * PK + c]);
 #pragma unroll
-      for (int r = 0; r < kRW; ++r) {
-        const float4 qx = *reinterpret_cast<const float4*>(&sQ[(warp * kRW + r) * D + c]);
+      for (int r = 0; r < RW; ++r) {
+        const float4 qx = *reinterpret_cast<const float4*>(&sQ[(warp * RW + r) * D + c]);
         s[r] += qx.x * kx.x + qx.y * kx.y + qx.z * kx.z + qx.w * kx.w;
       }
     }
     const bool in = vb + lane < v1;
     const int key = in ? virtual_key(kr, vb + lane) : 0;
-    float p[kRW];
+    float p[RW];
 #pragma unroll
-    for (int r = 0; r < kRW; ++r) {
+    for (int r = 0; r < RW; ++r) {
       const bool see = in && visible(a, pos[r], key);
       const float x = see ? s[r] : -INFINITY;
       float mx = x;
@@ -137,7 +140,7 @@ __device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* 
 #pragma unroll
       for (int c = 0; c < C; ++c) vx[c] = sV[j * D + c * 32 + lane];
 #pragma unroll
-      for (int r = 0; r < kRW; ++r) {
+      for (int r = 0; r < RW; ++r) {
         const float pj = __shfl_sync(0xffffffffu, p[r], j);
         if (pj != 0.f) {  // a hidden key's value never counts, whatever it holds
 #pragma unroll
@@ -148,9 +151,9 @@ __device__ void row_tile(const PagedArgs& a, int n, int tile, int parts, float* 
   }
   if (!busy) return;
 #pragma unroll
-  for (int r = 0; r < kRW; ++r) {
+  for (int r = 0; r < RW; ++r) {
     const float lt = warp_sum(l[r]);
-    const int rr = warp * kRW + r;
+    const int rr = warp * RW + r;
     if (rr >= nr) continue;
     const long long tok = (long long)q.bos + (r0 + rr) / G;
     const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
@@ -211,14 +214,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-// 16 bytes, or zeros.
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-
 template <int D, int NI>
 __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
                           float* smem, float* part_o, float2* part_ml) {
@@ -416,20 +411,31 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
 constexpr int kSearch = 1024;
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(PagedArgs a, int parts,
+__global__ void __launch_bounds__(kThreads, 4) paged_simt_kernel(PagedArgs a, int parts,
                                                               float* part_o, float2* part_ml) {
   __shared__ int s_find[2];
+  __shared__ __align__(16) Short<D> sm;
+  // Few rows are spread over the warps (16 single tokens over 4096 keys, 32 + 8 heads of 128:
+  // 159 us; 350 when one warp had all of them).
+  auto tile_of = [&](int n, int tile) {
+    const Seq q = load_seq(a, n);
+    const int rows = q.len * (a.Hq / a.Hkv), r0 = tile * kRows;
+    const int nr = min(kRows, rows - r0);
+    if (nr <= kWarps)
+      row_tile<D, 1>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
+    else
+      row_tile<D, 4>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
+  };
   if (a.N > kSearch) {
     const int n = blockIdx.x, G = a.Hq / a.Hkv;
     const int tiles = (int)(((long long)load_seq(a, n).len * G + kRows - 1) / kRows);
     for (int tile = 0; tile < tiles; ++tile) {
       __syncthreads();  // the last tile's shared memory is free
-      row_tile<D>(a, n, tile, parts, part_o, part_ml);
+      tile_of(n, tile);
     }
   } else {
     int n, tile;
-    if (find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile))
-      row_tile<D>(a, n, tile, parts, part_o, part_ml);
+    if (find_row_tile<kThreads>(a, kRows, (int)blockIdx.x, s_find, n, tile)) tile_of(n, tile);
   }
 }
 
@@ -517,31 +523,40 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
     a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Tall tiles where a sequence has 32 rows or more on average.
-bool tall(int N, int total_T, int Hq, int Hkv) {
-  return (long long)total_T * (Hq / Hkv) >= 32ll * N;
+// Row tiles of a call, about.
+long long row_tiles(bool big, int N, int total_T, int Hq, int Hkv) {
+  const long long height = big ? kTallRows : kRows;
+  const long long tiles = ((long long)total_T * (Hq / Hkv) + height - 1) / height;
+  const long long seqs = N < total_T ? N : total_T;
+  return tiles < seqs ? seqs : tiles;
 }
 
-// Parts of the key range: enough blocks for four (tall: two) on each SM when there are few rows.
-int simt_parts(int N, int total_T, int Hq, int Hkv) {
-  const bool big = tall(N, total_T, Hq, Hkv);
-  const long long G = Hq / Hkv, height = big ? kTallRows : kRows;
-  long long tiles = (total_T * G + height - 1) / height;
-  const long long seqs = N < total_T ? N : total_T;
-  if (tiles < seqs) tiles = seqs;
+// Tall tiles where a sequence has 32 rows or more on average and the caches (at the block table's
+// capacity) make a step of 64 keys for every place on the SMs.  16 sequences of 8 new tokens and
+// 500 cached keys, 16 + 4 heads of 64: 24 us for 29; of 32 and 1000, 8 + 8 heads of 128: 118 for
+// 223; but 200 tokens alone, 8 + 8 heads of 64: 19 for 14.
+bool tall(const PagedArgs& a) {
+  if ((long long)a.total_T * (a.Hq / a.Hkv) < 32ll * a.N) return false;
+  const double steps = (double)a.max_pages * a.page_size / kTallKeys + 1;
+  return row_tiles(true, a.N, a.total_T, a.Hq, a.Hkv) * steps * a.Hkv >= 2 * 152;
+}
+
+// Parts of the key range: enough blocks for eight (tall: two) on each SM when there are few rows.
+int simt_parts(bool big, int N, int total_T, int Hq, int Hkv) {
+  const long long tiles = row_tiles(big, N, total_T, Hq, Hkv);
   if (tiles <= 0) return 1;
-  const long long p = 152 * (big ? 2 : 4) / (tiles * Hkv);
+  const long long p = 152 * (big ? 2 : 8) / (tiles * Hkv);
   return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
 template <int D>
 cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
-  const int parts = simt_parts(a.N, a.total_T, a.Hq, a.Hkv);
+  const bool big = tall(a);
+  const int parts = simt_parts(big, a.N, a.total_T, a.Hq, a.Hkv);
   const long long rows = (long long)a.total_T * a.Hq;
   float* po = static_cast<float*>(workspace);
   float2* pml = reinterpret_cast<float2*>(po + (parts > 1 ? parts * rows * D : 0));
   const long long G = a.Hq / a.Hkv;
-  const bool big = tall(a.N, a.total_T, a.Hq, a.Hkv);
   const int height = big ? kTallRows : kRows;
   const long long tiles = (a.total_T * G + height - 1) / height + a.N;  // upper bound
   const dim3 grid((unsigned)(a.N > kSearch ? a.N : tiles), (unsigned)a.Hkv, (unsigned)parts);
@@ -571,7 +586,8 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
 }  // namespace
 
 size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D) {
-  const int parts = simt_parts(N, total_T, Hq, Hkv);
+  const int p = simt_parts(false, N, total_T, Hq, Hkv), q = simt_parts(true, N, total_T, Hq, Hkv);
+  const int parts = p < q ? q : p;
   return parts > 1 ? (size_t)parts * total_T * Hq * (D + 2) * sizeof(float) : 0;
 }
 

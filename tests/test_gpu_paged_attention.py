@@ -384,3 +384,29 @@ def test_more_fp32_chunks_than_blocks_search():
     assert d["T"] * 8 >= 32 * 1100
     call(d)
     check(d)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_fp32_chunks_over_long_caches(D):
+    """Tall tiles with their keys in parts, and values that only the last tokens see."""
+    d = make([(40, 6000), (3, 2000)], 4, 2, D, 128, "f32", seed=63)
+    call(d)
+    check(d)
+    for at in (5999, 5998):
+        d["vc"][int(d["table_h"][0, at // 128]), :, at % 128] = float("inf")
+    call(d)
+    got = d["out"][:38].clone()
+    assert torch.isfinite(got).all() and not torch.isfinite(d["out"][38:40]).any()
+    for at in (5999, 5998):
+        d["vc"][int(d["table_h"][0, at // 128]), :, at % 128] = 0
+    r = ref.paged_attention(host(d["q"])[:38], host(d["kc"]), host(d["vc"]), d["table_h"],
+                            np.array([0, 38], np.int32), np.array([5998], np.int32), 128)
+    lim = (2 * (D + 8) * 2.0 ** -24 * r[3] + 6064 * 2.0 ** -24)[..., None] * r[2]
+    assert (np.abs(host(got) - r[0]) <= lim).all()
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8, 9, 16])
+def test_few_rows_in_fp32(G):
+    d = make([(1, 90), (1, 1), (2, 300), (0, 4)], 2 * G, 2, 64, 16, "f32", seed=G)
+    call(d)
+    check(d)
