@@ -38,15 +38,15 @@
 //   still runs (43.5 us for 45.6 on the mixed batch below).
 //
 // What bounds it, and measured (alone on the GPU):
-//   64 single tokens over 512..8192 keys, 32 + 8 heads of 128: HBM; 179 us, 6.0 TB/s of the 6.8
+//   64 single tokens over 512..8192 keys, 32 + 8 heads of 128: HBM; 167 us, 6.4 TB/s of the 6.8
 //   of a copy.
-//   2 chunks of 4096 tokens behind 12288 keys, the same heads: the softmax's chain beside the
-//   tensor cores; 1.23 ms, 1.57 PFLOP/s of the 1.92 of a library product.
+//   2 chunks of 4096 tokens behind 12288 keys, the same heads: the tensor cores; 1.13 ms, 1.70
+//   PFLOP/s of the 1.92 of a library product.
 //   9 sequences of 1..700 tokens, window 1024, 16 + 2 heads of 64: 35 us, of which the start (the
-//   cut, barriers, first loads) takes 4 and an item's start and end 8 thousand cycles each.
-//   One token over 1000 keys: 11.8 us of latencies in a row.
-// Two units of line for an item's start and end: 39.0 us on the mixed batch when it was chosen,
-// 41.4 with one, 38.5 with three (single tokens and chunks did not change).
+//   cut, barriers, first loads) takes 4; then items' starts and ends.
+//   One token over 1000 keys: 12 us of latencies in a row.
+// Two units of line for an item's start and end: 1000 tokens and single ones mixed take 142 us
+// for 151 with one, and 137 with three, single tokens 57.4 for 59.0 and 58.1.
 //
 // Softmax weights are rounded to bf16 for the product (their sum is taken before, in fp32).
 // Keys that no row of the item sees (behind the last one, outside the window, pages that are
@@ -670,7 +670,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const int ps = a.page_size, ppt = kKeys / ps;  // pages of a tile: 8, 4, 2 or 1
       // Lane 8 x + p looks up and copies page p of the tiles x, x + 4, ..., four tiles ahead.
       const int quarter = lane >> 3, pi = lane & 7;
-      uint32_t pos = 0, sg = 0, ph = 0;  // entries pushed into the ring; the next one's stage, phase
+      uint32_t pos = 0, sg = 0, ph = 0;  // entries pushed, the next one's stage and phase
       for (uint32_t j = 0;; ++j) {
         const Step* st = step(j);
         if (!st) break;
