@@ -45,8 +45,6 @@
 //   9 sequences of 1..700 tokens, window 1024, 16 + 2 heads of 64: 35 us, of which the start (the
 //   cut, barriers, first loads) takes 4; then items' starts and ends.
 //   One token over 1000 keys: 12 us of latencies in a row.
-// Two units of line for an item's start and end: 1000 tokens and single ones mixed take 142 us
-// for 151 with one, and 137 with three, single tokens 57.4 for 59.0 and 58.1.
 //
 // Softmax weights are rounded to bf16 for the product (their sum is taken before, in fp32).
 // Keys that no row of the item sees (behind the last one, outside the window, pages that are
@@ -91,15 +89,18 @@ template <int D> struct Cfg {
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
 constexpr uint32_t kColP64 = kColO + 64;                     // weights, D <= 64
 
-// An item counts kOverhead units beside its tiles: what its start and end cost a CTA (the
-// units lie before its tiles, and a cut among them falls to the item's first tile).
-constexpr int kOverhead = 2;
+// An item counts some units beside its tiles: what its start and end cost a CTA (the units lie
+// before its tiles, and a cut among them falls to the item's first tile).  A wide one of D = 128
+// counts 3: 12 sequences of 1 to 600 tokens, 32 + 8 heads, take 125 us for 132 with 2 and 145
+// with 1; 256 single tokens 111 us with 2, 114 with 3; the mixed batch above 35.0 with 2, 35.7
+// with 3.
+constexpr int kOverhead = 2, kOverheadMost = 3;
 
 struct Header {  // a CTA's part of the line, for the joining kernel
   int rows;       // rows of the item that starts in its stretch and is cut (0: none)
   int row0, h;    // its first row and kv head
   int nt;         // its tiles
-  int start, total;  // its place in the line, the line's length
+  int start, total;  // place of its first tile in the line, the line's length
   int bos;        // its sequence's first token
 };
 
@@ -114,6 +115,8 @@ struct Geometry {
   int row0, rows;  // query rows of the item
   KeyRange kr;
   int t_lo, ns, nt;  // first window tile, sink tiles before it, tiles in all
+  int extra;         // units of the line before its tiles
+  __device__ __forceinline__ int units() const { return nt + extra; }
 };
 
 __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, int G, int rt) {
@@ -121,6 +124,7 @@ __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, i
   const int rows = s.len * G;
   g.row0 = rt * kRowsItem;
   g.rows = min(kRowsItem, rows - g.row0);
+  g.extra = a.D == 128 && g.rows > kRowsUnit ? kOverheadMost : kOverhead;
   g.kr = key_range(a, s, div_g(a, g.row0), div_g(a, g.row0 + g.rows - 1));
   g.t_lo = g.kr.lo / kKeys;
   g.ns = min((g.kr.sinks + kKeys - 1) / kKeys, g.t_lo);
@@ -174,10 +178,10 @@ struct Walker {
   // is the stretch's last item then, and the next CTA takes it whole).
   __device__ __forceinline__ bool enter(const PagedArgs& a, int x) {
     g = geometry(a, s, a.G, rt);
-    const int last = min(g.nt + kOverhead, x + left);
+    const int last = min(g.nt + g.extra, x + left);
     units = last - x;
-    v0 = max(x - kOverhead, 0);
-    v1 = max(last - kOverhead, 0);
+    v0 = max(x - g.extra, 0);
+    v1 = max(last - g.extra, 0);
     return v1 > v0;
   }
   __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
@@ -228,7 +232,7 @@ __device__ __forceinline__ int head_units(const PagedArgs& a, const Seq& s, int 
   int x = 0;
   const int nrt = row_tiles(s, G);
 #pragma unroll 1
-  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) x += geometry(a, s, G, rt).nt + kOverhead;
+  for (int rt = threadIdx.x & 31; rt < nrt; rt += 32) x += geometry(a, s, G, rt).units();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -245,7 +249,7 @@ __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const
 #pragma unroll 1
   for (int base = 0; base < nrt; base += 32) {
     const int rt = base + lane;
-    const int nt = rt < nrt ? geometry(a, s, G, rt).nt + kOverhead : 0;
+    const int nt = rt < nrt ? geometry(a, s, G, rt).units() : 0;
     int run = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -299,7 +303,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
       per[0] = 0;
       if (nrt <= 4)
 #pragma unroll 1
-        for (int rt = 0; rt < nrt; ++rt) per[0] += geometry(a, s[0], G, rt).nt + kOverhead;
+        for (int rt = 0; rt < nrt; ++rt) per[0] += geometry(a, s[0], G, rt).units();
 #pragma unroll 1
       for (unsigned todo = __ballot_sync(0xffffffffu, nrt > 4); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
@@ -941,7 +945,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             hd.h = w.h;
             hd.nt = w.g.nt;
             hd.bos = w.s.bos;
-            hd.start = plan.end - (kOverhead + w.v1);
+            hd.start = plan.end - w.v1;
             hd.total = plan.total;
           }
           live = w.next(a);
@@ -1369,14 +1373,14 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Head
   const Header hd = headers[c];
   if (hd.rows == 0) return;
   // CTAs from this one to the one it ends in
-  const int parts = stretch_of(hd.total, hd.start + kOverhead + hd.nt - 1) - c + 1;
+  const int parts = stretch_of(hd.total, hd.start + hd.nt - 1) - c + 1;
   for (int at = blockIdx.y * 256 + threadIdx.x; at < hd.rows * PIECES; at += gridDim.y * 256) {
     const int r = at / PIECES, e = at % PIECES;
     // Row of the i-th part in the partial results, -1 if that CTA has no tile of the item.
     auto place = [&](int i) -> int {
       const int k = c + i;
-      const int first = stretch(hd.total, k) - hd.start - kOverhead;
-      const int last = min(stretch(hd.total, k + 1) - hd.start - kOverhead, hd.nt);
+      const int first = stretch(hd.total, k) - hd.start;
+      const int last = min(stretch(hd.total, k + 1) - hd.start, hd.nt);
       return i < parts && last > max(first, 0) ? (2 * k + (i == 0)) * kRowsItem + r : -1;
     };
     float m = -INFINITY, l = 0.f;
@@ -1501,7 +1505,7 @@ static_assert(sizeof(Header) * kCtas <= 8192, "headers");
 // Whether the line of key tiles, at the block table's capacity, fits the kernel's indices.
 bool paged_tc_index_ok(const PagedArgs& a) {
   const double rows = (double)a.total_T * (a.Hq / a.Hkv) / kRowsItem + a.N;
-  const double tiles = (double)a.max_pages * a.page_size / kKeys + kOverhead + 2;
+  const double tiles = (double)a.max_pages * a.page_size / kKeys + kOverheadMost + 2;
   return rows * tiles * a.Hkv < 2147483647.0;
 }
 
