@@ -244,6 +244,7 @@ __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const
                                            int per, int off) {
   const int lane = threadIdx.x & 31, G = a.G;
   const int h = (int)((unsigned)off / (unsigned)per);
+  if (h >= a.Hkv) return;
   off -= h * per;
   const int nrt = row_tiles(s, G);
 #pragma unroll 1
@@ -364,7 +365,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
     }
     // its warp has it at hand
     const bool few = count <= kFew;
-    if ((few ? n % W : n / 32) != warp) return;
+    if (n < 0 || (few ? n % W : n / 32) != warp) return;
     const int src = n & 31;
     note_start(a, plan, few ? (n < W ? s[0] : s[1]) : shfl_seq(s[0], src), r * kPlanSeqs + n,
                few ? (n < W ? per[0] : per[1]) : __shfl_sync(0xffffffffu, per[0], src),
