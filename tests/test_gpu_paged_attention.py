@@ -410,3 +410,29 @@ def test_few_rows_in_fp32(G):
     d = make([(1, 90), (1, 1), (2, 300), (0, 4)], 2 * G, 2, 64, 16, "f32", seed=G)
     call(d)
     check(d)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_calls_at_once(dt):
+    """Calls with workspaces of their own on two streams give what they give alone."""
+    ds = [make([(1, 700), (130, 900), (1, 64), (7, 2000)], 8, 2, 128, 64, dt, seed=70),
+          make([(1, int(k)) for k in range(40, 1500, 23)], 8, 2, 64, 32, dt, seed=71)]
+    want, ws = [], []
+    for d in ds:
+        call(d)
+        want.append(d["out"].clone())
+        n = kda.kda_paged_attention_fwd_workspace_size(
+            d["N"], d["T"], 8, 2, d["D"], dtype=kda.KDA_F32 if dt == "f32" else kda.KDA_BF16)
+        ws.append(torch.empty(max(n, 1), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(30):
+        for d in ds:
+            d["out"].fill_(5)
+        torch.cuda.synchronize()
+        for d, w, s in zip(ds, ws, streams):
+            with torch.cuda.stream(s):
+                call(d, ws=w)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, d["out"]) for x, d in zip(want, ds))
+    assert kda.kda_device_error() == 0
