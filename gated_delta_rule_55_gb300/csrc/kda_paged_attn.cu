@@ -35,7 +35,8 @@
 //   weights is handed over while the upper half is computed (1283 -> 1244 us for the long chunks
 //   below), and a wide item's units take turns at the tensor cores.
 //   D <= 64: P has columns of its own, and the next scores are made while the last tile's softmax
-//   still runs (43.5 us for 45.6 on the mixed batch below).
+//   still runs (43.5 us for 45.6 on the mixed batch below); without a window, where few tiles are
+//   masked, whole tiles are made in one pass as above.
 //
 // What bounds it, and measured (alone on the GPU):
 //   64 single tokens over 512..8192 keys, 32 + 8 heads of 128: HBM; 167 us, 6.4 TB/s of the 6.8
@@ -595,7 +596,8 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool
     }
 }
 
-template <int D>
+// ONE: whole tiles with weights of their own in one pass (D <= 64 without a window).
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap kmap,
@@ -1091,7 +1093,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               }
             }
           };
-          if (!C::kOwnP && whole && mine == 0) {
+          constexpr bool kOnePass = !C::kOwnP || ONE;
+          if (kOnePass && whole && mine == 0) {
             // no maximum yet: that of the first 32 keys
             uint32_t s[32];
             tmem_ld32_start(tS, s);
@@ -1153,6 +1156,32 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               halves = true;
             }
           }
+          if (C::kOwnP && kOnePass && whole) {
+            // The same in one piece; the scores stay until the tile's own maximum is known.
+            const float nb = m == -INFINITY ? 0.f : -m * sc;
+            uint32_t p[2][32], s[2][32];
+            float sum, top;
+            tmem_ld32_start(tS, s[0]);
+            tmem_ld32_finish(s[0]);
+            tmem_ld32_start(tS + 32, s[1]);
+            weights32(s[0], sc, nb, p[0], sum, top, true);
+            tmem_ld32_finish(s[1]);
+            tmem_ld32_start(tS + 64, s[0]);
+            weights32(s[1], sc, nb, p[0] + 16, sum, top, false);
+            tmem_ld32_finish(s[0]);
+            tmem_ld32_start(tS + 96, s[1]);
+            weights32(s[0], sc, nb, p[1], sum, top, false);
+            tmem_ld32_finish(s[1]);
+            weights32(s[1], sc, nb, p[1] + 16, sum, top, false);
+            done = !__any_sync(0xffffffffu, r < nr && top > m && (top - m) * sc > kRescale);
+            if (done) {
+              scores_read();
+              weights_free();
+              tmem_st32_nowait(tP, p[0]);
+              tmem_st32_nowait(tP + 32, p[1]);
+              l += sum;
+            }
+          }
           if (!done) {
             // The first tile, masked ones, and a maximum that has outgrown the range: the
             // maximum first, then the weights.
@@ -1196,7 +1225,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               l += sum;
               tmem_st16_nowait(tP + 16 * q, p);
             };
-            if constexpr (C::kOwnP) {
+            if constexpr (!kOnePass) {
               // the scores are read at once, so that the next can be made
               uint32_t s[4][32];
 #pragma unroll
@@ -1229,6 +1258,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               for (int q = 0; q < 4; ++q) {
                 tmem_ld32_start(tS + 32 * q, s);
                 tmem_ld32_finish(s);
+                if (q == 3) scores_read();
                 if (!whole) mask(s, q);
                 weigh(s, q);
               }
@@ -1475,12 +1505,17 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   Header* headers = static_cast<Header*>(workspace);
   float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + 8192);
   float* po = reinterpret_cast<float*>(ml + (size_t)2 * kCtas * kRowsItem);
-  cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // D <= 64: with a window a third of the tiles is masked, and those are faster unrolled, which
+  // the one pass over whole tiles does not go with.  Chunks of 2048 behind 8192 keys, 32 + 4 heads
+  // of 64: 320 us for 352 with one pass, 148 for 162 with D = 32; the windowed batch above 36.2
+  // for 35.1.
+  auto kernel = paged_tc_kernel<D, false>;
+  if constexpr (Cfg<D>::kOwnP)
+    if (a.window == 0) kernel = paged_tc_kernel<D, true>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes,
-                                                             headers, po, ml);
+  kernel<<<kCtas, kThreads, Cfg<D>::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes, headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // a thread per four columns of the largest item there can be
