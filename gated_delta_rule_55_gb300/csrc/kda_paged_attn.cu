@@ -72,7 +72,7 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr float kRescale = 8.0f;  // log2 growth of the maximum that O and l absorb
 
 // What lies before the tiles: m and l of both units' rows (2 KB), barriers, the plan.
-constexpr int kFront = 3072;
+constexpr int kFront = 3 * 1024;
 
 template <int D> struct Cfg {
   static constexpr int kStageBytes = kKeys * D * 2;
