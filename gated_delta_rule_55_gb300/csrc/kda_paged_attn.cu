@@ -41,8 +41,8 @@
 // What bounds it, and measured (alone on the GPU):
 //   64 single tokens over 512..8192 keys, 32 + 8 heads of 128: HBM; 167 us, 6.4 TB/s of the 6.8
 //   of a copy.
-//   2 chunks of 4096 tokens behind 12288 keys, the same heads: the tensor cores; 1.13 ms, 1.70
-//   PFLOP/s of the 1.92 of a library product.
+//   2 chunks of 4096 tokens behind 12288 keys, the same heads: the tensor cores; 1.13 to
+//   1.18 ms, 1.63 to 1.70 PFLOP/s of the 1.92 of a library product.
 //   9 sequences of 1..700 tokens, window 1024, 16 + 2 heads of 64: 35 us, of which the start (the
 //   cut, barriers, first loads) takes 4; then items' starts and ends.
 //   One token over 1000 keys: 12 us of latencies in a row.
