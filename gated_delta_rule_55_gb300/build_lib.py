@@ -19,7 +19,7 @@ SOURCES = ["kda_abi.cu", "kda_decode.cu", "kda_chunk_simt.cu", "kda_chunk_tc.cu"
            "kda_gla.cu", "kda_gla_chunk.cu", "kda_chunk_bwd.cu", "kda_selftest.cu", "kda_step.cu",
            "kda_norm_rope.cu", "kda_paged_attn.cu", "kda_paged_attn_simt.cu", "kda_serving_abi.cu"]
 HEADERS = ["kda_internal.cuh", "tc_prims.cuh", "chunk_common.cuh", "chunk_records.cuh",
-           "kda_paged.cuh"]
+           "kda_paged.cuh", "kda_paged_line.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

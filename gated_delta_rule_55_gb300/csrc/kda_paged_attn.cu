@@ -53,6 +53,7 @@
 // so what the cache holds there never counts.
 #include "chunk_common.cuh"
 #include "kda_paged.cuh"
+#include "kda_paged_line.h"
 
 namespace kda {
 namespace {
@@ -213,20 +214,7 @@ struct Walker {
   __device__ __forceinline__ bool narrow() const { return g.rows <= kRowsUnit; }
 };
 
-constexpr int kCtas = 152;      // one per SM
 constexpr int kPlanSeqs = 384;  // sequences whose units are looked at together
-
-// The first unit of CTA c's stretch of a line of `total` units.
-__device__ __forceinline__ int stretch(int total, int c) {
-  const int q = (int)((unsigned)total / kCtas);
-  return q * c + min(c, total - q * kCtas);
-}
-
-// The CTA whose stretch holds a unit.
-__device__ __forceinline__ int stretch_of(int total, int unit) {
-  const int q = (int)((unsigned)total / kCtas), more = total - q * kCtas;  // q + 1 units each
-  return unit < more * (q + 1) ? unit / (q + 1) : more + (unit - more * (q + 1)) / max(q, 1);
-}
 
 // Units of one head's items of a sequence, its row tiles spread over the warp's lanes.
 __device__ __forceinline__ int head_units(const PagedArgs& a, const Seq& s, int G) {
@@ -271,9 +259,9 @@ __device__ __forceinline__ void note_start(const PagedArgs& a, Plan& plan, const
   }
 }
 
-// The CTA's stretch of the line: all threads call.  s_units: kPlanSeqs entries.  The host has
-// made sure that the line's length fits 31 bits; offsets that overlap (against the call's
-// rules) can make it longer and the sums wrong, and then at worst no start is found.
+// The CTA's stretch of the line: all threads call.  s_units: kPlanSeqs entries, each of which
+// fits 31 bits (paged_tc_index_ok).  So does the line when the offsets are in order; when they
+// overlap, against the call's rules, it may not, and then every CTA's stretch is empty.
 __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
   static_assert(kPlanSeqs == kThreads, "one sequence per thread");
   constexpr int W = kThreads / 32, kFew = 2 * W;
@@ -317,9 +305,9 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
     __syncthreads();
     sum = 0;
 #pragma unroll 1
-    for (int i = lane; i < count; i += 32) sum += s_units[i];
+    for (int i = lane; i < count; i += 32) sum = line_add(sum, s_units[i]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) sum = line_add(sum, __shfl_xor_sync(0xffffffffu, sum, o));
   };
   // (one loop for the sum and the search: little code, which a call has to fetch first)
   int total = 0, before = 0, first = 0;
@@ -328,8 +316,9 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
     const int r = x < rounds ? x : x - rounds;
     if (x < rounds || rounds > 1) load(r);
     if (x < rounds) {
-      total += sum;
+      total = line_add(total, sum);
       if (x + 1 < rounds) continue;
+      if (total == kLineTooLong) total = 0;
       first = stretch(total, blockIdx.x);
       const int end = stretch(total, blockIdx.x + 1);
       if (threadIdx.x == 0) {

@@ -577,8 +577,10 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
  *   block_table  [N, max_pages] int32 DEVICE: page of keys [i page_size, (i + 1) page_size).
  *                Entries behind a sequence's last page are not read; others are clamped into
  *                the cache.
- *   cu_seqlens   [N + 1] int32 DEVICE offsets of the new tokens, clamped into [0, total_T].
- *                Rows of out and lse behind the last sequence are left as they were.
+ *   cu_seqlens   [N + 1] int32 DEVICE offsets of the new tokens, clamped into [0, total_T]; they
+ *                must not decrease (sequences that overlap leave their rows unspecified; there
+ *                is no fault).  Rows of out and lse behind the last sequence are left as they
+ *                were.
  *   kv_lens      [N] int32 DEVICE keys of each sequence, the new tokens' included, clamped into
  *                [0, max_pages page_size]
  *   out          [total_T, Hq, D]  dtype, dense.  A token that sees nothing gets zeros.

@@ -436,3 +436,29 @@ def test_two_calls_at_once(dt):
         torch.cuda.synchronize()
         assert all(torch.equal(x, d["out"]) for x, d in zip(want, ds))
     assert kda.kda_device_error() == 0
+
+
+def test_overlapping_sequences_longer_than_the_line():
+    """Offsets against the rules, whose tiles in all pass 2^32: no access leaves the buffers (rows
+    behind them keep what they held), nothing is reported, and the next call is right."""
+    ensure_built()
+    N, T, Hkv, D, page = 8192, 4096, 3500, 32, 128
+    maxp = T // page
+    cache = torch.zeros(1, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T + 1, Hkv, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 1, Hkv), 7.0, device="cuda")
+    table = torch.zeros(N, maxp, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    kv = torch.full((N,), T, dtype=torch.int32, device="cuda")
+    n = kda.kda_paged_attention_fwd_workspace_size(N, T, Hkv, Hkv, D)
+    ws = torch.zeros(n + 1024, dtype=torch.uint8, device="cuda")
+    kda.kda_paged_attention_fwd(q, cache, cache, table, cu, kv, out[:T], N, T, Hkv, Hkv, D, 1, page,
+                                maxp, lse=lse[:T], workspace=(ws.data_ptr(), n))
+    torch.cuda.synchronize()
+    assert (out[T] == 7.0).all() and (lse[T] == 7.0).all() and (ws[n:] == 0).all()
+    assert kda.kda_device_error() == 0
+    d = make([(1, 70), (40, 140)], 4, 2, D, 32, "bf16", seed=80)
+    call(d)
+    check(d)
