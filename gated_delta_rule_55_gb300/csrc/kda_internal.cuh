@@ -149,7 +149,8 @@ bool paged_tc_index_ok(const PagedArgs& a);
 size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
-size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D);
+size_t paged_simt_workspace(int total_T, int Hq, int D);  // of any call of up to total_T tokens
+size_t paged_simt_need(const PagedArgs& a);               // of this one
 cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 unsigned int decode_read_error(bool reset);

@@ -549,6 +549,9 @@ int simt_parts(bool big, int N, int total_T, int Hq, int Hkv) {
   return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
 }
 
+// Partial results of `rows` query rows (tokens x heads), counted for each part.
+size_t simt_bytes(long long rows, int D) { return (size_t)rows * (D + 2) * sizeof(float); }
+
 template <int D>
 cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const bool big = tall(a);
@@ -585,10 +588,18 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
 
 }  // namespace
 
-size_t paged_simt_workspace(int N, int total_T, int Hq, int Hkv, int D) {
-  const int p = simt_parts(false, N, total_T, Hq, Hkv), q = simt_parts(true, N, total_T, Hq, Hkv);
-  const int parts = p < q ? q : p;
-  return parts > 1 ? (size_t)parts * total_T * Hq * (D + 2) * sizeof(float) : 0;
+size_t paged_simt_need(const PagedArgs& a) {
+  const int parts = simt_parts(tall(a), a.N, a.total_T, a.Hq, a.Hkv);
+  return parts > 1 ? simt_bytes((long long)parts * a.total_T * a.Hq, a.D) : 0;
+}
+
+// The most that a call of up to total_T tokens can need, so that a buffer for a program's largest
+// batch serves every smaller one: simt_parts' parts times row tiles are at most its blocks.
+size_t paged_simt_workspace(int total_T, int Hq, int D) {
+  constexpr long long kMost = 152ll * 8 * kRows;
+  static_assert(kMost == 152ll * 2 * kTallRows, "rows in flight, short and tall tiles");
+  const long long rows = (long long)kMaxParts * total_T * Hq;
+  return simt_bytes(rows < kMost ? rows : kMost, D);
 }
 
 cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t st) {

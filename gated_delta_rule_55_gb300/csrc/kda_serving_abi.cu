@@ -202,7 +202,7 @@ size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hk
       !dtype_ok(dtype))
     return 0;
   return dtype == KDA_BF16 ? kda::paged_tc_workspace(D)
-                           : kda::paged_simt_workspace(N, total_T, Hq, Hkv, D);
+                           : kda::paged_simt_workspace(total_T, Hq, D);
 }
 
 int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
@@ -241,7 +241,9 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   a.window = (double)window >= (double)max_pages * page_size ? 0 : window;
   a.sinks = sinks;
   if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
-  const size_t need = kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype);
+  const size_t need = !work                 ? 0
+                      : dtype == KDA_BF16 ? kda::paged_tc_workspace(D)
+                                          : kda::paged_simt_need(a);
   if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
     return KDA_ERR_WORKSPACE;
   const int s = kda::check_current_device();

@@ -597,7 +597,9 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
  *   below 2^31 (KDA_ERR_TOO_LARGE).
  *   workspace    at least kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype)
  *                bytes (0: none), 256-byte aligned, caller-owned, contents unspecified on
- *                return; calls that may overlap in time need one each.
+ *                return; calls that may overlap in time need one each.  The size never
+ *                decreases as N or total_T grows: a buffer for the largest batch serves all
+ *                smaller ones.
  */
 size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
                                               int dtype);

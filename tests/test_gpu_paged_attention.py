@@ -462,3 +462,18 @@ def test_overlapping_sequences_longer_than_the_line():
     d = make([(1, 70), (40, 140)], 4, 2, D, 32, "bf16", seed=80)
     call(d)
     check(d)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_one_workspace_for_all_batches(dt):
+    """A buffer of the size for the largest batch, with bytes behind it that stay."""
+    Hq, Hkv, D = 16, 8, 128
+    n = kda.kda_paged_attention_fwd_workspace_size(
+        16, 4096, Hq, Hkv, D, dtype=kda.KDA_F32 if dt == "f32" else kda.KDA_BF16)
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    for seqs in ([(1, 900)] * 16, [(1, 3000)], [(64, 64)], [(64, 700)], [(3, 40), (100, 300)],
+                 [(7, 7 + 60 * i) for i in range(16)]):
+        d = make(seqs, Hq, Hkv, D, 64, dt, seed=len(seqs))
+        call(d, ws=(ws.data_ptr(), n))
+        check(d)
+        assert (ws[n:] == 0x5A).all()

@@ -124,3 +124,29 @@ def test_binding_refuses_tensors_of_another_kind():
         kda.kda_paged_attention_fwd(x, x, x, x, x, x, x, 1, 2, 4, 4, 64, 1, 16, 1)
     with pytest.raises(ValueError, match="dtype"):
         kda.kda_attention_step(x.half(), x, x, x, x, x, x, x, 2, 1, 4, 4, 64, 64, 4)
+
+
+@pytest.mark.parametrize("dtype", [kda.KDA_F32, kda.KDA_BF16])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (32, 8, 128), (4, 4, 64), (10, 2, 32), (1, 1, 64)])
+def test_paged_attention_workspace_of_the_largest_batch_serves_smaller_ones(L, dtype, Hq, Hkv, D):
+    """The size never decreases in the number of sequences or of tokens, and no smaller call is
+    refused with it, at any capacity of the block table."""
+    import torch
+    size = lambda N, T: kda.kda_paged_attention_fwd_workspace_size(N, T, Hq, Hkv, D, dtype)  # noqa: E731
+    Ns, Ts = [1, 2, 5, 16, 64, 300, 2000], [1, 2, 15, 16, 17, 64, 100, 256, 1024, 4096, 70000]
+    for i, N in enumerate(Ns):
+        for j, T in enumerate(Ts):
+            for n in Ns[max(i - 1, 0):i + 1]:
+                for t in Ts[max(j - 1, 0):j + 1]:
+                    assert size(n, t) <= size(N, T), (n, t, N, T)
+    if torch.cuda.is_available():
+        return  # (the addresses below are never to reach a device)
+    for N in Ns:
+        for T in Ts:
+            for maxp in (1, 4, 64, 4096):
+                code = _attn(L, N=N, T=T, Hq=Hq, Hkv=Hkv, D=D, maxp=maxp, qs=Hq * D, dtype=dtype,
+                             ws=FAKE, wb=size(Ns[-1], Ts[-1]))
+                assert code == -9, (code, N, T, maxp)
+                # and what the call's own size gives is enough for it
+                assert _attn(L, N=N, T=T, Hq=Hq, Hkv=Hkv, D=D, maxp=maxp, qs=Hq * D, dtype=dtype,
+                             ws=FAKE, wb=size(N, T)) == -9
