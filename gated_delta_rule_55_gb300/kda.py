@@ -452,14 +452,14 @@ class _Call:
 
 def _setup():
     import torch
-    _Call.f32, _Call.bf16 = torch.float32, torch.bfloat16
-    _Call.i32, _Call.i64 = torch.int32, torch.int64
+    _Call.bf16, _Call.i32, _Call.i64 = torch.bfloat16, torch.int32, torch.int64
     _Call.device = torch.cuda.current_device
     _Call.where, _Call.dense = torch.Tensor.get_device, torch.Tensor.is_contiguous
     _Call.address = torch.Tensor.data_ptr
     # the stream's address without building a stream object, where torch offers it
     _Call.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _Call.f32 = torch.float32  # last: what _begin looks at, perhaps in another thread
 
 
 def _begin(x, dtype, stream):

@@ -150,3 +150,45 @@ def test_paged_attention_workspace_of_the_largest_batch_serves_smaller_ones(L, d
                 # and what the call's own size gives is enough for it
                 assert _attn(L, N=N, T=T, Hq=Hq, Hkv=Hkv, D=D, maxp=maxp, qs=Hq * D, dtype=dtype,
                              ws=FAKE, wb=size(N, T)) == -9
+
+
+def test_first_calls_from_two_threads(monkeypatch):
+    """A call that begins while another one's first look-up is at any of its lines finds all of it
+    (or looks up for itself)."""
+    import sys
+    import threading
+    torch = pytest.importorskip("torch")
+    from gated_delta_rule_55_gb300 import kda as binding
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 77, raising=False)
+    for n in ("f32", "bf16", "i32", "i64", "device", "raw_stream", "where", "dense", "address"):
+        monkeypatch.setattr(binding._Call, n, None)
+    lines, got = [], []
+
+    def other():
+        try:
+            got.append(binding._begin(FAKE, kda.KDA_F32, None))
+        except Exception as e:  # noqa: BLE001
+            got.append(e)
+
+    names = [n for n in vars(binding._Call) if not n.startswith("_")]
+
+    def trace(frame, event, arg):
+        if frame.f_code is binding._setup.__code__ and event == "line":
+            lines.append(frame.f_lineno)
+            before = {n: getattr(binding._Call, n) for n in names}
+            t = threading.Thread(target=other)
+            t.start()
+            t.join()
+            for n in names:
+                setattr(binding._Call, n, before[n])
+        return trace
+
+    old = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        binding._setup()
+    finally:
+        sys.settrace(old)
+    assert len(lines) >= 4 and len(got) == len(lines)
+    assert all(g == (kda.KDA_F32, torch.float32, 0, 77) for g in got), got
