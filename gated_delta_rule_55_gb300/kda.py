@@ -523,6 +523,14 @@ def _rows(x, dtype, dev, heads, dim, what):
     return x.data_ptr(), st[0] if shape[0] > 1 else heads * dim
 
 
+def _scratch(workspace, dev):
+    """_ws, for scratch that has to lie on the call's device."""
+    p, n = _ws(workspace)
+    if workspace is not None and workspace.__class__ is not tuple and workspace.get_device() != dev:
+        raise ValueError("workspace must be a tensor of the current CUDA device")
+    return p, n
+
+
 def kda_attention_step(query, key, value, beta, decay, state, slots, out, N, T, Hk, Hv, dk, dv,
                        num_slots, out_slots=None, cu_seqlens=None, softmax_scale=None,
                        use_qk_l2norm=True, order="decay_first", dtype=None, stream=None):
@@ -596,7 +604,7 @@ def kda_qk_norm_rope_bwd(query, key, query_weight, key_weight, cos_table, sin_ta
     f32 = _Call.f32
     qp, qs = _rows(query, el, dev, Hq, D, "query")
     kp, ks = _rows(key, el, dev, Hkv, D, "key")
-    wp, wb = _ws(workspace)
+    wp, wb = _scratch(workspace, dev)
     _check("kda_qk_norm_rope_bwd", lib().kda_qk_norm_rope_bwd(
         qp, kp, *_norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev),
         *_devs((d_query_out, d_key_out, d_query, d_key, d_query_weight, d_key_weight),
@@ -619,7 +627,7 @@ def kda_paged_attention_fwd(query, k_cache, v_cache, block_table, cu_seqlens, kv
     code, el, dev, st = _begin(query, dtype, stream)
     i32 = _Call.i32
     qp, qs = _rows(query, el, dev, Hq, D, "query")
-    wp, wb = _ws(workspace)
+    wp, wb = _scratch(workspace, dev)
     _check("kda_paged_attention_fwd", lib().kda_paged_attention_fwd(
         qp, *_devs((k_cache, v_cache, block_table, cu_seqlens, kv_lens, out),
                    [el, el, i32, i32, i32, el], dev,

@@ -192,3 +192,29 @@ def test_first_calls_from_two_threads(monkeypatch):
         sys.settrace(old)
     assert len(lines) >= 4 and len(got) == len(lines)
     assert all(g == (kda.KDA_F32, torch.float32, 0, 77) for g in got), got
+
+
+def test_binding_refuses_a_workspace_on_another_device(monkeypatch):
+    torch = pytest.importorskip("torch")
+    from gated_delta_rule_55_gb300 import kda as binding
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(binding._Call, "f32", None)  # look up anew, and again afterwards
+    monkeypatch.setattr(binding._Call, "raw_stream", None)
+    monkeypatch.setattr(binding._Call, "device", None)
+
+    class Scratch:  # a tensor of the second device
+        is_cuda = True
+        is_contiguous = staticmethod(lambda: True)
+        get_device = staticmethod(lambda: 1)
+        data_ptr = staticmethod(lambda: FAKE)
+        numel = staticmethod(lambda: 1 << 30)
+        element_size = staticmethod(lambda: 1)
+
+    with pytest.raises(ValueError, match="workspace"):
+        kda.kda_paged_attention_fwd(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1, 0, 4, 4, 64, 1,
+                                    16, 1, dtype=kda.KDA_BF16, workspace=Scratch())
+    with pytest.raises(ValueError, match="workspace"):
+        kda.kda_qk_norm_rope_bwd(FAKE, FAKE, None, None, None, None, None, FAKE, FAKE, FAKE, FAKE,
+                                 None, None, 0, 4, 4, 64, 0, 0, dtype=kda.KDA_BF16,
+                                 workspace=Scratch())
