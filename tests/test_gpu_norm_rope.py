@@ -240,3 +240,56 @@ def test_capture_and_replay():
     gr.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, got))
+
+
+# From 1216 tokens on a warp takes all heads of a kind, several groups of them in turn.
+LONG = [("bf16", 128, 128, 17, 1, False), ("bf16", 128, 64, 33, 9, True),
+        ("bf16", 32, 32, 65, 33, False),
+        ("f32", 128, 128, 9, 5, False), ("f32", 128, 48, 17, 1, True),
+        ("f32", 32, 16, 33, 17, True)]
+
+
+@pytest.mark.parametrize("T", [1215, 1216, 1217, 2049])
+@pytest.mark.parametrize("dt,D,R,Hq,Hkv,il", LONG)
+def test_forward_of_many_tokens(dt, D, R, Hq, Hkv, il, T):
+    d = make(T, Hq, Hkv, D, R, dt, seed=T + D)
+    q, k = fwd(d, il)
+    check_rows(host(q), want_fwd(d, "q", il), d)
+    check_rows(host(k), want_fwd(d, "k", il), d)
+
+
+@pytest.mark.parametrize("dt,D,R,Hq,Hkv,il", LONG)
+def test_forward_of_many_tokens_in_place(dt, D, R, Hq, Hkv, il):
+    for T in (1215, 1217):
+        d = make(T, Hq, Hkv, D, R, dt, seed=T)
+        d["q"], d["k"] = d["q"].contiguous(), d["k"].contiguous()
+        wq, wk = want_fwd(d, "q", il), want_fwd(d, "k", il)
+        fwd(d, il, d["q"], d["k"])
+        check_rows(host(d["q"]), wq, d)
+        check_rows(host(d["k"]), wk, d)
+
+
+@pytest.mark.parametrize("T", [1215, 1216, 2049])
+@pytest.mark.parametrize("dt,D,R,Hq,Hkv,il", LONG)
+def test_append_of_many_tokens(dt, D, R, Hq, Hkv, il, T):
+    """Some tokens without a place; what no token names keeps what it held."""
+    page = 16 if il else 128
+    d = make(T, Hq, Hkv, D, R, dt, seed=T + R)
+    pages = T // page + 3
+    kc = torch.randn(pages, Hkv, page, D, device="cuda").to(DT[dt])
+    vc = torch.randn(pages, Hkv, page, D, device="cuda").to(DT[dt])
+    slots = torch.randperm(pages * page, device="cuda")[:T].clone()
+    slots[5::97] = -1
+    slots[7::101] = pages * page + 3
+    s = slots.cpu().numpy()
+    kept = (s >= 0) & (s < pages * page)
+    wk = want_fwd(d, "k", il)[kept]
+    k0, v0 = (host(x).transpose(0, 2, 1, 3).reshape(-1, Hkv, D) for x in (kc, vc))
+    q = torch.empty(T, Hq, D, dtype=DT[dt], device="cuda")
+    append(d, il, kc, vc, slots, q)
+    check_rows(host(q), want_fwd(d, "q", il), d)
+    gk, gv = (host(x).transpose(0, 2, 1, 3).reshape(-1, Hkv, D) for x in (kc, vc))
+    check_rows(gk[s[kept]], wk, d)
+    v0[s[kept]] = host(d["v"])[kept]
+    k0[s[kept]] = gk[s[kept]]
+    assert (gv == v0).all() and (gk == k0).all()
