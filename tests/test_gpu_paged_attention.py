@@ -477,3 +477,56 @@ def test_one_workspace_for_all_batches(dt):
         call(d, ws=(ws.data_ptr(), n))
         check(d)
         assert (ws[n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5), (1000, 140)])
+def test_chunks_of_several_items_over_long_caches(D, window, sinks):
+    """Chunks of 256-row items behind more keys than a stretch has, with and without a window."""
+    for Hq, Hkv, page in ((2, 1, 64), (5, 1, 16), (2, 2, 128)):
+        d = make([(300, 2100), (1, 900), (411, 1300), (140, 140)], Hq, Hkv, D, page, "bf16",
+                 seed=D + Hq, pad=1)
+        call(d, window=window, sinks=sinks)
+        check(d, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("slope", [20.0, 150.0, 300.0, 600.0, -300.0])
+@pytest.mark.parametrize("jump", [0, 48])
+def test_rising_scores_of_chunks(D, slope, jump):
+    """Scores that grow along the keys (per 1500 of them): the running maximum moves at every tile,
+    in either half of it, by less or more than what is taken without scaling anew.  With `jump`
+    they grow in steps at other places than the tiles' ends."""
+    d = make([(200, 1500), (130, 130), (1, 1500)], 2, 1, D, 64, "bf16", seed=13)
+    for n in range(3):
+        for j in range(int(d["kv_h"][n])):
+            at = (j + jump) // 64 * 64 if jump else j
+            d["kc"][int(d["table_h"][n, j // 64]), :, j % 64] = slope * at / 1500 / D
+    d["q"].copy_(torch.rand_like(d["q"]) + 0.5)
+    call(d, softmax_scale=1.0)
+    check(d, scale=1.0)
+
+
+@pytest.mark.parametrize("dt,D", KINDS)
+@pytest.mark.parametrize("over", [False, True])
+def test_bad_pages_and_lengths_are_clamped(dt, D, over):
+    """Entries outside the cache, lengths outside the table and a last offset behind the rows count
+    as the nearest ones inside; no row behind the sequences or the buffers is touched."""
+    d = make([(2, 100), (1, 40), (1, 64)], 2, 1, D, 16, dt, pad=2, seed=90)
+    T, maxp = d["T"], d["table"].shape[1]
+    big = torch.full((T + 8, 2, D), 7.0, dtype=DT[dt], device="cuda")
+    ends = torch.full((T + 8, 2), 7.0, device="cuda")
+    d["out"], d["lse"] = big[4:4 + T], ends[4:4 + T]
+    d["table"][0, 1], d["table"][0, 2] = 2 ** 31 - 1, -2 ** 31
+    d["kv"][1], d["kv"][2] = 2 ** 31 - 1, -5
+    d["table_h"] = np.clip(d["table"].cpu().numpy().astype(np.int64), 0, d["kc"].shape[0] - 1)
+    d["kv_h"] = np.array([100, 16 * maxp, 0])
+    if over:
+        d["cu"][3] = 2 ** 30
+        d["cu_h"] = np.array([0, 2, 3, T], np.int32)
+        d["live"] = T
+    call(d)
+    check(d)
+    assert (d["out"][3:d["live"]] == 0).all() and torch.isneginf(d["lse"][3:d["live"]]).all()
+    for x in (big, ends):
+        assert (x[:4] == 7.0).all() and (x[4 + T:] == 7.0).all()
