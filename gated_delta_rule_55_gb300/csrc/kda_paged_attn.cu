@@ -558,27 +558,14 @@ struct Bars {
       o_full[2], turn[2], ph_full[2], oh_full[2], join, step_full[kSteps], step_empty[kSteps];
 };
 
-// One try of a wait, of a microsecond at most.
-__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// A wait that gives up (after a second or two) marks the thread dead: it then runs through the
+// A wait that gives up (after 2 to 8 seconds) marks the thread dead: it then runs through the
 // rest of its step without waiting (its results are void) and leaves, so that every loop ends.
 // Tries are counted, not timed: there are many of these loops, and their instructions push those
 // of the softmax out of the cache.
 __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool& dead) {
   if (dead) return;
 #pragma unroll 1
-  for (int i = 0; !try_wait(bar, parity); ++i)
+  for (int i = 0; !mbar_try_wait_short(bar, parity); ++i)
     if (i == 2000000) {
       dead = true;
       atomicOr(&g_paged_error, 64u);

@@ -184,7 +184,7 @@ def kda_device_error(reset: bool = True) -> int:
 
 
 def kda_selftest_bounded_wait(limit_ns: int, stream=None) -> None:
-    """Launch one bounded wait that runs out (sets bit 3 of kda_device_error)."""
+    """Launch a bounded wait of each kind that runs out (sets bit 3 of kda_device_error)."""
     _check("kda_selftest_bounded_wait", lib().kda_selftest_bounded_wait(int(limit_ns),
                                                                          _stream(stream)))
 

@@ -623,7 +623,7 @@ int kda_version(void);
  *   Bit 0: a bounded wait inside the single-pass tensor-core chunk kernel gave up; bit 1:
  *   one inside the two-launch (workspace) chunk kernels did; bit 2: one inside the
  *   chunked backward's kernels did (the outputs of that launch are incomplete); bit 3: the
- *   wait of kda_selftest_bounded_wait gave up (which is what it is for); bit 4: one inside
+ *   waits of kda_selftest_bounded_wait gave up (which is what it is for); bit 4: one inside
  *   the chunked recurrent-attention kernels did; bit 5: a tensor-core kernel of
  *   kda_recurrent_attention_fwd_ws or kda_attention_fwd_ws met gates outside its range,
  *   detected per 16-token sub-chunk (a summed key-axis gate or decay totalling outside
@@ -637,10 +637,12 @@ int kda_version(void);
 int kda_device_error(int reset);
 
 /*
- * kda_selftest_bounded_wait -- launches one kernel whose single wait, on an mbarrier that
- *   nothing arrives on, runs out after limit_ns nanoseconds (1 .. 1e9) and records bit 3 of
- *   kda_device_error: the give-up path every tensor-core kernel takes instead of hanging
- *   the device.  No paper counterpart.  Returns KDA_OK once enqueued; limit_ns outside
+ * kda_selftest_bounded_wait -- launches one kernel with a wait of each kind that the tensor-core
+ *   kernels have, one by the clock and one of counted tries, on an mbarrier that nothing arrives
+ *   on.  The first runs out after limit_ns nanoseconds (1 .. 1e9), the second after
+ *   limit_ns / 1000 tries of a few microseconds at most; both together record bit 3 of
+ *   kda_device_error: the give-up path every tensor-core kernel takes instead of hanging the
+ *   device.  No paper counterpart.  Returns KDA_OK once enqueued; limit_ns outside
  *   (0, 1e9] gives KDA_ERR_BAD_SHAPE.
  */
 int kda_selftest_bounded_wait(unsigned long long limit_ns, kda_stream_t stream);

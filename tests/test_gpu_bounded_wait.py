@@ -45,3 +45,18 @@ def test_wait_runs_out_and_reports():
     assert rel_err(out, ref_out) <= BF16_REL
     assert rel_err(S, ref_S) <= BF16_REL
     assert kda.kda_device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("limit_ns", [1, 1_000, 50_000_000, 400_000_000])
+def test_both_kinds_of_wait_end_near_the_limit(limit_ns):
+    """By the clock and by counted tries, one for each microsecond of the limit, which the hardware
+    ends after 1 to 4 of them: the launch ends with the longer of the two."""
+    kda.kda_device_error(reset=True)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    a.record()
+    kda.kda_selftest_bounded_wait(limit_ns)
+    b.record()
+    torch.cuda.synchronize()
+    assert limit_ns * 1e-6 <= a.elapsed_time(b) <= 5 * limit_ns * 1e-6 + 5.0
+    assert kda.kda_device_error(reset=True) == 8
