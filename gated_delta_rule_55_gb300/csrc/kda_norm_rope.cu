@@ -17,7 +17,9 @@
 // once for all of them, and kUnroll row groups are in flight together.  16384 tokens of 32 + 8
 // heads of 128, bf16: 53 us, 6.5 TB/s of the 6.8 of a copy (55.5 with 8 warps a block instead
 // of 4); 80 when the rotation exchanged partners between lanes.  Of 4095 tokens of 16 + 2 + 2
-// heads into the pages: 10.2 us, a third of it the start and end of the one wave of blocks.
+// heads into the pages: 10.1 us for 6.3 of bytes, in almost three waves of blocks; the two thirds
+// of them that have the keys or values find one row group, of two heads, and load it kUnroll
+// times over.
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -278,7 +280,7 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
 // warp reads comes through a ring of its own in shared memory, kRing - 1 parts ahead, each lane
 // copying what it will use itself: no register waits for memory, so that 16 warps of 118
 // registers fit.
-// 16384 tokens of 32 + 8 heads of 128: 84 us, 6.0 TB/s of the 6.8 of a copy; the instructions
+// 16384 tokens of 32 + 8 heads of 128: 84 to 86 us, 6.0 TB/s of the 6.8 of a copy; the instructions
 // take 60% of the issue slots beside it.  91.5 with the loads in registers, 87 with single
 // instead of packed fp32 arithmetic or 20 warps, 94 with 18, 108 with a ring of 6 (which leaves
 // the tables no L1), 96 with one row group a part.

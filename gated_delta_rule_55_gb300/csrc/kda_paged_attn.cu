@@ -42,7 +42,7 @@
 //   64 single tokens over 512..8192 keys, 32 + 8 heads of 128: HBM; 167 us, 6.4 TB/s of the 6.8
 //   of a copy.
 //   2 chunks of 4096 tokens behind 12288 keys, the same heads: the tensor cores; 1.13 to
-//   1.18 ms, 1.63 to 1.70 PFLOP/s of the 1.92 of a library product.
+//   1.19 ms, 1.61 to 1.70 PFLOP/s of the 1.92 of a library product.
 //   9 sequences of 1..700 tokens, window 1024, 16 + 2 heads of 64: 35 us, of which the start (the
 //   cut, barriers, first loads) takes 4; then items' starts and ends.
 //   One token over 1000 keys: 12 us of latencies in a row.
@@ -70,7 +70,9 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10: one per unit */, kQueryWarp
 // Registers: 168 a thread at launch (3 x 128 threads), moved to the softmax warpgroups:
 // 2 x 216 + 72 = 3 x 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-constexpr float kRescale = 8.0f;  // log2 growth of the maximum that O and l absorb
+// log2 growth of the maximum that O and l absorb.  (Rescaling only from some growth on, and two
+// softmax warpgroups beside two score tiles, are published ways for attention on this hardware.)
+constexpr float kRescale = 8.0f;
 
 // What lies before the tiles: m and l of both units' rows (2 KB), barriers, the plan.
 constexpr int kFront = 3 * 1024;
@@ -1482,10 +1484,11 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   Header* headers = static_cast<Header*>(workspace);
   float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + 8192);
   float* po = reinterpret_cast<float*>(ml + (size_t)2 * kCtas * kRowsItem);
-  // D <= 64: with a window a third of the tiles is masked, and those are faster unrolled, which
-  // the one pass over whole tiles does not go with.  Chunks of 2048 behind 8192 keys, 32 + 4 heads
-  // of 64: 320 us for 352 with one pass, 148 for 162 with D = 32; the windowed batch above 36.2
-  // for 35.1.
+  // D <= 64: chunks of 2048 behind 8192 keys, 32 + 4 heads of 64: 320 us for 352 with one pass over
+  // whole tiles, 148 for 162 with D = 32.  Masked tiles are faster unrolled, which the one pass does
+  // not go with; under a window they can be many (a third in the windowed batch above: 36.2 us for
+  // 35.1).  How many there are lies in device memory, so any window counts as narrow: a chunk under
+  // a wide one forgoes the gain.
   auto kernel = paged_tc_kernel<D, false>;
   if constexpr (Cfg<D>::kOwnP)
     if (a.window == 0) kernel = paged_tc_kernel<D, true>;

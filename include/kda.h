@@ -594,7 +594,7 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
  *   which do not see it (a weight of zero times it is not zero).  fp32 runs in fp32.
  *   The bf16 kernel counts its work in tiles of 256 query rows by 128 keys, at the block
  *   table's capacity: Hkv (total_T Hq / Hkv / 256 + N) (max_pages page_size / 128 + 5) must stay
- *   below 2^31 (KDA_ERR_TOO_LARGE).
+ *   below 2^31 (KDA_ERR_TOO_LARGE); N and Hkv at most 65535.
  *   workspace    at least kda_paged_attention_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype)
  *                bytes (0: none), 256-byte aligned, caller-owned, contents unspecified on
  *                return; calls that may overlap in time need one each.  The size never
