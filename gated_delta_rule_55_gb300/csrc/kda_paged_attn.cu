@@ -1485,8 +1485,8 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
   float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + 8192);
   float* po = reinterpret_cast<float*>(ml + (size_t)2 * kCtas * kRowsItem);
   // D <= 64: chunks of 2048 behind 8192 keys, 32 + 4 heads of 64: 320 us for 352 with one pass over
-  // whole tiles, 148 for 162 with D = 32.  Masked tiles are faster unrolled, which the one pass does
-  // not go with; under a window they can be many (a third in the windowed batch above: 36.2 us for
+  // whole tiles, 148 for 162 with D = 32.  Masked tiles are faster unrolled, which the one pass
+  // does not go with; under a window they can be many (a third in the windowed batch above: 36.2 us for
   // 35.1).  How many there are lies in device memory, so any window counts as narrow: a chunk under
   // a wide one forgoes the gain.
   auto kernel = paged_tc_kernel<D, false>;

@@ -35,13 +35,15 @@ def line(tmp_path_factory):
                     str(d / "main.cpp"), "-o", str(d / "line")], check=True)
 
     def ask(queries):
-        r = subprocess.run([str(d / "line")], input="\n".join(f"{o} {a} {b}" for o, a, b in queries),
-                           capture_output=True, text=True, check=True)
+        text = "\n".join(f"{o} {a} {b}" for o, a, b in queries)
+        r = subprocess.run([str(d / "line")], input=text, capture_output=True, text=True,
+                           check=True)
         return [int(x) for x in r.stdout.split()]
     return ask
 
 
-@pytest.mark.parametrize("total", [0, 1, 3, 151, 152, 153, 303, 304, 305, 100_001, 2 ** 30, MOST - 1])
+@pytest.mark.parametrize("total", [0, 1, 3, 151, 152, 153, 303, 304, 305, 100_001, 2 ** 30,
+                                   MOST - 1])
 def test_stretches_and_their_units(line, total):
     at = line([("s", total, c) for c in range(CTAS + 1)])
     assert at[0] == 0 and at[-1] == total

@@ -127,12 +127,16 @@ def test_binding_refuses_tensors_of_another_kind():
 
 
 @pytest.mark.parametrize("dtype", [kda.KDA_F32, kda.KDA_BF16])
-@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (32, 8, 128), (4, 4, 64), (10, 2, 32), (1, 1, 64)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (32, 8, 128), (4, 4, 64), (10, 2, 32),
+                                      (1, 1, 64)])
 def test_paged_attention_workspace_of_the_largest_batch_serves_smaller_ones(L, dtype, Hq, Hkv, D):
     """The size never decreases in the number of sequences or of tokens, and no smaller call is
     refused with it, at any capacity of the block table."""
     import torch
-    size = lambda N, T: kda.kda_paged_attention_fwd_workspace_size(N, T, Hq, Hkv, D, dtype)  # noqa: E731
+
+    def size(N, T):
+        return kda.kda_paged_attention_fwd_workspace_size(N, T, Hq, Hkv, D, dtype)
+
     Ns, Ts = [1, 2, 5, 16, 64, 300, 2000], [1, 2, 15, 16, 17, 64, 100, 256, 1024, 4096, 70000]
     for i, N in enumerate(Ns):
         for j, T in enumerate(Ts):
