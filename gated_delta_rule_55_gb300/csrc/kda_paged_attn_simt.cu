@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
   const long long rows = (long long)a.total_T * a.Hq;
   const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  // launched while the first kernel runs: wait for its results
+  // a programmatic launch behind the first kernel, which gives no early trigger: it may begin once
+  // that one's blocks have left, so wait for what they wrote
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows || !token_owned(a, row / a.Hq)) return;
   const float2 ml = lane < parts ? part_ml[lane * rows + row] : make_float2(0.f, 0.f);
@@ -573,6 +574,8 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || parts == 1) return e;
+  // Programmatic: 14.3 us for 16.4 in the small case above, called from the host (in a graph the
+  // same).
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
   cfg.blockDim = dim3(128);
