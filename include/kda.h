@@ -470,8 +470,9 @@ int kda_decode_step(const float* q, const float* k, const float* v, const float*
  *                same call (the result would depend on their order; there is no fault).
  *   cu_seqlens   [N + 1] int32 DEVICE token offsets, entries clamped into [0, T] (T then is
  *                the row count; rows behind the last request are left as they were), or NULL
- *                for T tokens per request.  A request without tokens keeps its state (copied
- *                when out_slots says so).
+ *                for T tokens per request.  They must not decrease (of rows that two requests
+ *                share either's output may stay; there is no fault).  A request without tokens
+ *                keeps its state (copied when out_slots says so).
  *   out          [rows, Hv, dv]  dtype, dense
  *   softmax_scale  multiplies q; <= 0 selects dk^-0.5
  *   flags        KDA_ATTN_NO_QK_L2NORM and KDA_ATTN_ORDER_LITERAL as in kda_attention_fwd
@@ -511,7 +512,8 @@ enum kda_rope_flags {
  *   R            rotated elements of a head: a multiple of 16 from 0 (no rotation) to D
  *                (KDA_ERR_ROTARY)
  *   eps > 0 and finite (KDA_ERR_SCALE).  D in {32, 64, 128}.  Norms are computed in fp32 and
- *   results rounded once.
+ *   results rounded once.  An infinity or a NaN in a head's row may make any of that row's
+ *   results NaN (and, in the gradients, those of the weight); other rows are not touched by it.
  */
 int kda_qk_norm_rope_fwd(const void* query, const void* key, const float* query_weight,
                          const float* key_weight, const float* cos_table,
