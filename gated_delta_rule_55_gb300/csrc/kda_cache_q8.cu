@@ -1,0 +1,79 @@
+// Reading tokens back from a cache in 8 bits (kda_paged_cache_read_q8): keys and values of given
+// slots as dense rows of fp32 or bf16, which both hold them exactly.
+//
+// Bound by HBM: D + 1 bytes in and 2 D or 4 D out per row.  A thread has 16 numbers of a token's
+// key and value of one head, so that its loads are 16 bytes and its four loads of the two rows
+// (numbers and scales) are in flight together behind the slot's.
+#include "kda_q8.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void put(float* dst, const uint4& w, float s) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = q8::unpack2(x[i]), b = q8::unpack2(x[i] >> 16);
+    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
+  }
+}
+__device__ __forceinline__ void put(__nv_bfloat16* dst, const uint4& w, float s) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = q8::unpack2(x[i + j / 2] >> (j % 2 * 16));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x * s, a.y * s);
+      y[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    __stcs(reinterpret_cast<uint4*>(dst) + i / 2, make_uint4(y[0], y[1], y[2], y[3]));
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadArgs a) {
+  constexpr int PIECES = D / 16;
+  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long row = i / PIECES;  // token * Hkv + head
+  if (row >= (long long)a.T * a.Hkv) return;
+  const int tok = (int)(row / a.Hkv), h = (int)(row - (long long)tok * a.Hkv);
+  const int c = (int)(i % PIECES) * 16;
+  const long long slot = __ldg(a.slots + tok);
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  uint32_t ks = q8::kBias, vs = q8::kBias;
+  if (slot >= 0 && slot < (long long)a.num_pages * a.page_size) {
+    const long long page = slot / a.page_size;
+    const long long at = (page * a.Hkv + h) * a.page_size + (slot - page * a.page_size);
+    k = __ldcs(reinterpret_cast<const uint4*>(a.k_cache + at * D + c));
+    v = __ldcs(reinterpret_cast<const uint4*>(a.v_cache + at * D + c));
+    ks = a.k_scale[at];
+    vs = a.v_scale[at];
+  }
+  put(static_cast<T*>(a.k_out) + row * D + c, k, q8::scale(ks));
+  put(static_cast<T*>(a.v_out) + row * D + c, v, q8::scale(vs));
+}
+
+template <int D>
+cudaError_t launch_t(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
+  const long long n = (long long)a.T * a.Hkv * (D / 16);
+  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+  if (bf16)
+    cache_read_kernel<__nv_bfloat16, D><<<grid, kThreads, 0, st>>>(a);
+  else
+    cache_read_kernel<float, D><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_read(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
+  return a.D == 32   ? launch_t<32>(a, bf16, st)
+         : a.D == 64 ? launch_t<64>(a, bf16, st)
+                     : launch_t<128>(a, bf16, st);
+}
+
+}  // namespace kda

@@ -110,6 +110,8 @@ struct NormRopeArgs {
   void* k_out;                 // [T, Hkv, D]
   void* k_cache;               // [num_pages, Hkv, page_size, D] (append)
   void* v_cache;
+  uint8_t* k_scale;            // [num_pages, Hkv, page_size]: rows in 8 bits; NULL otherwise
+  uint8_t* v_scale;
   const void* dq_out;          // [T, Hq, D] (backward)
   const void* dk_out;
   void* dq;
@@ -118,7 +120,19 @@ struct NormRopeArgs {
   int T, Hq, Hkv, D, R, max_position, interleaved, num_pages, page_size, page_shift;
 };
 
-// Attention over a paged cache (kda_paged_attention_fwd).
+// Reading rows of an 8-bit cache back (kda_paged_cache_read_q8).
+struct CacheReadArgs {
+  const uint8_t* k_cache;      // [num_pages, Hkv, page_size, D] e4m3
+  const uint8_t* v_cache;
+  const uint8_t* k_scale;      // [num_pages, Hkv, page_size]
+  const uint8_t* v_scale;
+  const int64_t* slots;        // [T]
+  void* k_out;                 // [T, Hkv, D]
+  void* v_out;
+  int T, Hkv, D, num_pages, page_size;
+};
+
+// Attention over a paged cache (kda_paged_attention_fwd, _q8_fwd, kda_paged_prefix_attention_fwd).
 struct PagedArgs {
   const void* q;               // [total_T, Hq, D], token stride q_stride elements
   long long q_stride;
@@ -131,6 +145,13 @@ struct PagedArgs {
   float* lse;                  // [total_T, Hq] or NULL
   float scale;
   int N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages, window, sinks;
+  const uint8_t* k_scale;      // [num_pages, Hkv, page_size]: caches in 8 bits; NULL otherwise
+  const uint8_t* v_scale;
+  // Shared prefixes: lists of keys in front of the sequences' own (groups = 0: none)
+  const int32_t* prefix_table; // [groups, max_prefix_pages]
+  const int32_t* prefix_lens;  // [groups]
+  const int32_t* cu_groups;    // [groups + 1]
+  int groups, max_prefix_pages;
   int G;                       // Hq / Hkv, and division by it (set by the tensor-core launcher)
   uint32_t g_mul, g_shift;
 };
@@ -144,12 +165,21 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t stre
 size_t norm_rope_bwd_workspace(int D);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* d_q_weight, float* d_k_weight,
                                  void* workspace, bool bf16, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadArgs& a, bool bf16, cudaStream_t stream);
 // Paged attention: bf16 on the tensor cores, fp32 on the SIMT kernel.
 bool paged_tc_index_ok(const PagedArgs& a);
 size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
+size_t paged_prefix_tc_workspace(int total_T, int Hq, int D);
+cudaError_t launch_paged_tc_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_tc_prefix(const PagedArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_tc_prefix_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
-size_t paged_simt_workspace(int total_T, int Hq, int D);  // of any call of up to total_T tokens
+unsigned int paged_q8_read_error(bool reset);
+unsigned int paged_prefix_read_error(bool reset);
+unsigned int paged_prefix_q8_read_error(bool reset);
+// Of any call of up to total_T tokens.
+size_t paged_simt_workspace(int total_T, int Hq, int D, bool prefix);
 size_t paged_simt_need(const PagedArgs& a);               // of this one
 cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);

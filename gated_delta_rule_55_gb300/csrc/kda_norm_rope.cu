@@ -1,5 +1,5 @@
 // RMS norm of every query and key head with the position rotation in the same pass
-// (kda_qk_norm_rope_fwd / _append / _bwd).
+// (kda_qk_norm_rope_fwd / _append / _append_q8 / _bwd).
 //
 // Per head row x [D] of a token at position p, with weight w [D]:
 //   r = 1 / sqrt(mean(x^2) + eps),   n = x r w,   y = Rot(p) n
@@ -21,6 +21,7 @@
 // of them that have the keys or values find one row group, of two heads, and load it kUnroll
 // times over.
 #include "kda_internal.cuh"
+#include "kda_q8.cuh"
 
 namespace kda {
 namespace {
@@ -142,14 +143,46 @@ __device__ __forceinline__ void store_row(T* row, const Lane<T, D>& l,
   *reinterpret_cast<uint2*>(row + l.a) = Piece<T>::pack(u);
   *reinterpret_cast<uint2*>(row + l.b) = Piece<T>::pack(v);
 }
+// A row in 8 bits: the lane's two pieces, and the scale's byte by the row's first lane.  The whole
+// warp calls; `keep`: the row is one.
+template <typename T, int D>
+__device__ __forceinline__ void store_row_q8(uint8_t* row, uint8_t* scale, const Lane<T, D>& l,
+                                             const float (&x)[Lane<T, D>::VE], int li, bool keep) {
+  constexpr int PE = Lane<T, D>::PE, L = Lane<T, D>::L;
+  uint32_t top = 0;  // magnitudes as integers: infinities above numbers, NaNs above those
+#pragma unroll
+  for (int e = 0; e < 2 * PE; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool odd = top >= 0x7f800000u;
+  const int e = q8::exponent(top);
+  const float f = odd ? 0.f : q8::power(-e);
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    uint32_t b[PE / 2];
+#pragma unroll
+    for (int i = 0; i < PE; i += 2) {
+      const float u = odd ? 0.f : x[part * PE + i], v = odd ? 0.f : x[part * PE + i + 1];
+      b[i / 2] = q8::pack2(u * f, v * f);
+    }
+    uint8_t* dst = row + (part ? l.b : l.a);
+    if (!keep) continue;
+    if constexpr (PE == 4)
+      *reinterpret_cast<uint32_t*>(dst) = b[0] | b[PE / 2 - 1] << 16;
+    else
+      *reinterpret_cast<uint16_t*>(dst) = (uint16_t)b[0];
+  }
+  if (keep && li == 0) *scale = (uint8_t)(odd ? q8::kNaN : e + q8::kBias);
+}
 template <typename T>
 __device__ __forceinline__ uint2 load_piece(const T* p) {
   return __ldcs(reinterpret_cast<const uint2*>(p));
 }
 
 // Forward: queries to query_out; keys to key_out, or (append) keys and values to their place
-// in the pages.  blockIdx.y numbers a token's units of `per` heads of one kind.
-template <typename T, int D, bool IL>
+// in the pages, as they are or (Q8) in 8 bits.  blockIdx.y numbers a token's units of `per` heads
+// of one kind.
+template <typename T, int D, bool IL, bool Q8>
 __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, int per, int qu,
                                                                 int ku) {
   using Ln = Lane<T, D>;
@@ -178,6 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
   fetch(h0);
   // Where head h of this token goes: dst + h * dst_head.
   T* dst;
+  uint8_t *dst8 = nullptr, *scale8 = nullptr;  // (Q8)
   long long dst_head = D;
   if (kind == 0) {
     dst = static_cast<T*>(a.q_out) + tok * a.Hq * D;
@@ -188,15 +222,28 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
     if (slot < 0 || slot >= (long long)a.num_pages * a.page_size) return;  // not kept
     const long long page = slot >> a.page_shift;
     dst_head = (long long)a.page_size * D;
-    dst = static_cast<T*>(kind == 1 ? a.k_cache : a.v_cache) + page * a.Hkv * dst_head +
-          (slot - (page << a.page_shift)) * D;
+    const long long in_page = slot - (page << a.page_shift);
+    if constexpr (Q8) {
+      dst = nullptr;
+      dst8 = static_cast<uint8_t*>(kind == 1 ? a.k_cache : a.v_cache) + page * a.Hkv * dst_head +
+             in_page * D;
+      scale8 = (kind == 1 ? a.k_scale : a.v_scale) + page * a.Hkv * a.page_size + in_page;
+    } else {
+      dst = static_cast<T*>(kind == 1 ? a.k_cache : a.v_cache) + page * a.Hkv * dst_head +
+            in_page * D;
+    }
   }
   if (kind == 2) {
     for (int h = h0;;) {
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int r = h + i * RPW + rw;
-        if (r < h1) {
+        if constexpr (Q8) {
+          float x[VE];
+          unpack_row<T, D>(ra[i], rb[i], x);
+          store_row_q8<T, D>(dst8 + r * dst_head, scale8 + (long long)r * a.page_size, l, x, li,
+                             r < h1);
+        } else if (r < h1) {
           T* row = dst + r * dst_head;
           *reinterpret_cast<uint2*>(row + l.a) = ra[i];
           *reinterpret_cast<uint2*>(row + l.b) = rb[i];
@@ -243,7 +290,11 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
         y[e0] = x0 * p0[k] - x1 * p1[k];
         y[e1] = x0 * p2[k] + x1 * p3[k];
       }
-      if (row < h1) store_row<T, D>(dst + row * dst_head, l, y);
+      if (Q8 && kind == 1)  // (warp-uniform)
+        store_row_q8<T, D>(dst8 + row * dst_head, scale8 + (long long)row * a.page_size, l, y, li,
+                           row < h1);
+      else if (row < h1)
+        store_row<T, D>(dst + row * dst_head, l, y);
     }
     if (h >= h1) break;
   }
@@ -479,7 +530,7 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(const float* partial,
 constexpr int kBwdBlocks = 152;
 constexpr int kRingBytes = kBwdWarps * kRing * kBwdUnroll * 4 * 32 * (int)sizeof(uint2);
 
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 cudaError_t launch_fwd_t(const NormRopeArgs& a, cudaStream_t st) {
   constexpr int step = Lane<T, D>::RPW * kUnroll;
   // A warp takes all heads of a kind, or, with few tokens, as many as it has in flight (32 + 8
@@ -489,9 +540,9 @@ cudaError_t launch_fwd_t(const NormRopeArgs& a, cudaStream_t st) {
   const int qu = (a.Hq + per - 1) / per, ku = (a.Hkv + per - 1) / per;
   const dim3 grid((a.T + kWarps - 1) / kWarps, qu + ku + (a.slots ? ku : 0));
   if (a.interleaved)
-    norm_rope_kernel<T, D, true><<<grid, 32 * kWarps, 0, st>>>(a, per, qu, ku);
+    norm_rope_kernel<T, D, true, Q8><<<grid, 32 * kWarps, 0, st>>>(a, per, qu, ku);
   else
-    norm_rope_kernel<T, D, false><<<grid, 32 * kWarps, 0, st>>>(a, per, qu, ku);
+    norm_rope_kernel<T, D, false, Q8><<<grid, 32 * kWarps, 0, st>>>(a, per, qu, ku);
   return cudaGetLastError();
 }
 
@@ -538,13 +589,19 @@ cudaError_t launch_bwd_t(const NormRopeArgs& a, float* dqw, float* dkw, float* p
 
 size_t norm_rope_bwd_workspace(int D) { return (size_t)kBwdBlocks * D * sizeof(float); }
 
+namespace {
+template <int D>
+cudaError_t launch_fwd_d(const NormRopeArgs& a, bool bf16, cudaStream_t st) {
+  if (a.k_scale)
+    return bf16 ? launch_fwd_t<__nv_bfloat16, D, true>(a, st) : launch_fwd_t<float, D, true>(a, st);
+  return bf16 ? launch_fwd_t<__nv_bfloat16, D, false>(a, st) : launch_fwd_t<float, D, false>(a, st);
+}
+}  // namespace
+
 cudaError_t launch_norm_rope(const NormRopeArgs& a, bool bf16, cudaStream_t st) {
-  switch (a.D) {
-    case 32: return bf16 ? launch_fwd_t<__nv_bfloat16, 32>(a, st) : launch_fwd_t<float, 32>(a, st);
-    case 64: return bf16 ? launch_fwd_t<__nv_bfloat16, 64>(a, st) : launch_fwd_t<float, 64>(a, st);
-    default:
-      return bf16 ? launch_fwd_t<__nv_bfloat16, 128>(a, st) : launch_fwd_t<float, 128>(a, st);
-  }
+  return a.D == 32   ? launch_fwd_d<32>(a, bf16, st)
+         : a.D == 64 ? launch_fwd_d<64>(a, bf16, st)
+                     : launch_fwd_d<128>(a, bf16, st);
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* dqw, float* dkw, void* workspace,

@@ -12,25 +12,54 @@ struct Seq {
   int pos0;  // position of its first new token (negative: more new tokens than keys)
 };
 
-// From a sequence's raw offsets and key count.
-__device__ __forceinline__ Seq make_seq(const PagedArgs& a, int lo, int hi, int kv) {
+// Lists of keys: those of the shared prefixes, which all tokens of a group of sequences see, and
+// behind them the sequences' own.  List i < groups is a prefix, list groups + n is sequence n's.
+__device__ __forceinline__ int lists(const PagedArgs& a) { return a.groups + a.N; }
+// Block table row of a list.
+__device__ __forceinline__ const int32_t* table_of(const PagedArgs& a, int i) {
+  return i < a.groups ? a.prefix_table + (long long)i * a.max_prefix_pages
+                      : a.block_table + (long long)(i - a.groups) * a.max_pages;
+}
+// Raw offsets and key count of a list.
+__device__ __forceinline__ void raw_seq(const PagedArgs& a, int i, int& lo, int& hi, int& kv) {
+  if (i < a.groups) {
+    lo = a.cu_seqlens[min(max(a.cu_groups[i], 0), a.N)];
+    hi = a.cu_seqlens[min(max(a.cu_groups[i + 1], 0), a.N)];
+    kv = a.prefix_lens[i];
+  } else {
+    lo = a.cu_seqlens[i - a.groups];
+    hi = a.cu_seqlens[i - a.groups + 1];
+    kv = a.kv_lens[i - a.groups];
+  }
+}
+
+// From a list's raw offsets and key count.  All of a prefix is in its tokens' past: they are given
+// the position of its last key (positions behind it are clamped to it where they count).
+__device__ __forceinline__ Seq make_seq(const PagedArgs& a, int lo, int hi, int kv, bool prefix) {
   Seq s;
   lo = min(max(lo, 0), a.total_T);
   hi = min(max(hi, lo), a.total_T);
   s.bos = lo;
   s.len = hi - lo;
-  const long long cap = (long long)a.max_pages * a.page_size;
+  const long long cap = (long long)(prefix ? a.max_prefix_pages : a.max_pages) * a.page_size;
   s.kv = (int)min((long long)max(kv, 0), a.num_pages > 0 ? cap : 0ll);
-  s.pos0 = s.kv - s.len;
+  s.pos0 = s.kv - (prefix ? 1 : s.len);
   return s;
 }
-__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int n) {
-  return make_seq(a, a.cu_seqlens[n], a.cu_seqlens[n + 1], a.kv_lens[n]);
+__device__ __forceinline__ Seq load_seq(const PagedArgs& a, int i) {
+  int lo, hi, kv;
+  raw_seq(a, i, lo, hi, kv);
+  return make_seq(a, lo, hi, kv, i < a.groups);
 }
 
 // Whether a packed token belongs to a sequence (rows behind the last one are left alone).
 __device__ __forceinline__ bool token_owned(const PagedArgs& a, long long tok) {
   return tok >= a.cu_seqlens[0] && tok < a.cu_seqlens[a.N];
+}
+// Whether it belongs to a group (of a call with groups).
+__device__ __forceinline__ bool token_grouped(const PagedArgs& a, long long tok) {
+  const int g0 = min(max(a.cu_groups[0], 0), a.N), g1 = min(max(a.cu_groups[a.groups], 0), a.N);
+  return tok >= a.cu_seqlens[g0] && tok < a.cu_seqlens[g1];
 }
 
 // The query at position `pos` sees `key`: causal, and with a window the last `window` keys
@@ -61,7 +90,7 @@ __device__ __forceinline__ int virtual_key(const KeyRange& r, int v) {
 // The page that holds `key`, clamped into the cache: a bad table entry gives wrong numbers
 // but no access outside it.
 __device__ __forceinline__ int page_of(const PagedArgs& a, int n, int key) {
-  const int p = __ldg(a.block_table + (long long)n * a.max_pages + key / a.page_size);
+  const int p = __ldg(table_of(a, n) + key / a.page_size);
   return min(max(p, 0), a.num_pages - 1);
 }
 
@@ -70,20 +99,22 @@ __device__ __forceinline__ long long cache_row(const PagedArgs& a, int n, int hk
   return ((long long)page_of(a, n, key) * a.Hkv + hkv) * a.page_size + key % a.page_size;
 }
 
-// The sequence and row tile behind a block's number, tiles of `rows` query rows counted over
-// the sequences in order.  All NT threads call; false when there is no such tile.
+// The list and row tile behind a block's number, tiles of `rows` query rows counted over
+// the lists in order.  All NT threads call; false when there is no such tile.
 template <int NT>
 __device__ bool find_row_tile(const PagedArgs& a, int rows, int number, int* s2, int& seq,
                               int& tile) {
   __shared__ int s_warp[NT / 32];
   const int G = a.Hq / a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int before = 0;  // tiles of the sequences before this round
-  for (int base = 0; base < a.N; base += NT) {
+  for (int base = 0; base < lists(a); base += NT) {
     const int n = base + tid;
     int t = 0;
-    if (n < a.N) {
-      const int lo = min(max(a.cu_seqlens[n], 0), a.total_T);
-      const int hi = min(max(a.cu_seqlens[n + 1], lo), a.total_T);
+    if (n < lists(a)) {
+      int lo, hi, kv;
+      raw_seq(a, n, lo, hi, kv);
+      lo = min(max(lo, 0), a.total_T);
+      hi = min(max(hi, lo), a.total_T);
       t = (int)(((long long)(hi - lo) * G + rows - 1) / rows);
     }
     int sum = t;

@@ -1,0 +1,13 @@
+// Attention behind shared prefixes, caches in 8 bits, on the tensor cores
+// (kda_paged_prefix_attention_fwd).
+#include "kda_paged_tc.cuh"
+
+namespace kda {
+
+cudaError_t launch_paged_tc_prefix_q8(const PagedArgs& a, void* workspace, cudaStream_t st) {
+  return launch_any<true, true>(a, workspace, st);
+}
+
+unsigned int paged_prefix_q8_read_error(bool reset) { return read_error(reset); }
+
+}  // namespace kda

@@ -1,5 +1,5 @@
-// Attention of new tokens over a paged cache (kda_paged_attention_fwd) in fp32.  (bf16 runs on
-// the tensor cores: kda_paged_attn.cu.)
+// Attention of new tokens over a paged cache (kda_paged_attention_fwd, _q8_fwd,
+// kda_paged_prefix_attention_fwd) in fp32.  (bf16 runs on the tensor cores: kda_paged_tc.cuh.)
 //
 // A block takes 16 query rows (tokens x query heads of one kv head) of one sequence and one
 // part of its visible keys, and keeps for every row the running maximum m, the sum l of
@@ -10,6 +10,7 @@
 // kernel, and blocks share an SM.  5 sequences of 1..17 tokens over up to 700 keys, 4 + 4 heads
 // of 64: 11.5 us.  Chunks take taller tiles (below), which the FMA pipes bound.
 #include "kda_paged.cuh"
+#include "kda_q8.cuh"
 
 namespace kda {
 namespace {
@@ -29,13 +30,38 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
                : "memory");
 }
 
+// 16 numbers of an 8-bit row, from column c on, as fp32 (or zeros).  Their rounding to 8 bits is
+// undone exactly, so the arithmetic behind it is that of an fp32 cache.
+__device__ __forceinline__ void expand16(float* dst, const void* cache, const uint8_t* scales,
+                                         long long row, int D, int c, bool there) {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  float s = 1.f;
+  if (there) {
+    w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + row * D + c));
+    s = q8::scale(__ldg(scales + row));
+  }
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = q8::unpack2(x[i]), b = q8::unpack2(x[i] >> 16);
+    *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+  }
+}
+
+// Place of a row's part in the partial results: those of prefixes come first.
+__device__ __forceinline__ long long part_row(const PagedArgs& a, int n, int part, int parts,
+                                              long long row) {
+  const int side = a.groups > 0 && n >= a.groups;
+  return ((long long)side * parts + part) * a.total_T * a.Hq + row;
+}
+
 template <int D> struct Short {
   static constexpr int PK = D + 4;  // K pitch: 16-byte rows, lanes on different banks
   float k[kKeys * PK], v[kKeys * D], q[kRows * D];
 };
 
-// One row tile of sequence n, RW rows for each warp; all threads of the block call.
-template <int D, int RW>
+// One row tile of list n, RW rows for each warp; all threads of the block call.
+template <int D, int RW, bool Q8>
 __device__ void row_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
                          Short<D>& sm, float* part_o, float2* part_ml) {
   constexpr int PK = Short<D>::PK;
@@ -80,6 +106,18 @@ __device__ void row_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr
   // A step's K and V rows; places behind the part's end hold zeros.
   constexpr int PIECES = D / 4;
   auto fetch = [&](int vb) {
+    if constexpr (Q8) {
+      constexpr int P16 = D / 16;
+#pragma unroll
+      for (int i = tid; i < kKeys * P16; i += kThreads) {
+        const int key_i = i / P16, c = i % P16 * 16;
+        const bool there = vb + key_i < v1;
+        const long long row = there ? cache_row(a, n, hkv, virtual_key(kr, vb + key_i)) : 0;
+        expand16(&sK[key_i * PK + c], a.k_cache, a.k_scale, row, D, c, there);
+        expand16(&sV[key_i * D + c], a.v_cache, a.v_scale, row, D, c, there);
+      }
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < kKeys * PIECES / kThreads; ++k) {
       const int i = tid + k * kThreads;
@@ -157,8 +195,8 @@ __device__ void row_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr
     if (rr >= nr) continue;
     const long long tok = (long long)q.bos + (r0 + rr) / G;
     const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
-    if (parts > 1) {
-      const long long at = (long long)part * a.total_T * a.Hq + row;
+    if (parts > 1 || a.groups > 0) {
+      const long long at = part_row(a, n, part, parts, row);
 #pragma unroll
       for (int c = 0; c < C; ++c) part_o[at * D + c * 32 + lane] = o[r][c];
       if (lane == 0) part_ml[at] = make_float2(m[r], lt);
@@ -214,7 +252,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-template <int D, int NI>
+template <int D, int NI, bool Q8>
 __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int nr, int parts,
                           float* smem, float* part_o, float2* part_ml) {
   using T = Tall<D>;
@@ -232,17 +270,23 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
   const int v0 = min(part * per, total), v1 = part < np ? min(v0 + per, total) : v0;
   const int shift = __ffs(a.page_size) - 1;
 
+  const int32_t* table = table_of(a, n);
   auto fetch = [&](int vb) {
-    constexpr int PIECES = D / 4;
+    constexpr int PIECES = Q8 ? D / 16 : D / 4;
 #pragma unroll 4
     for (int i = tid; i < kTallKeys * PIECES; i += kThreads) {
-      const int key_i = i / PIECES, c = i % PIECES * 4;
+      const int key_i = i / PIECES, c = i % PIECES * (D / PIECES);
       const bool there = vb + key_i < v1;
       const int key = there ? virtual_key(kr, vb + key_i) : 0;
-      const int p = there ? __ldg(a.block_table + (long long)n * a.max_pages + (key >> shift)) : 0;
+      const int p = there ? __ldg(table + (key >> shift)) : 0;
       const long long row =
           (((long long)min(max(p, 0), a.num_pages - 1) * a.Hkv + hkv) << shift) +
           (key & (a.page_size - 1));
+      if constexpr (Q8) {
+        expand16(&sK[key_i * PQ + c], a.k_cache, a.k_scale, row, D, c, there);
+        expand16(&sV[key_i * D + c], a.v_cache, a.v_scale, row, D, c, there);
+        continue;
+      }
       copy16(&sK[key_i * PQ + c], static_cast<const float*>(a.k_cache) + row * D + c, there);
       copy16(&sV[key_i * D + c], static_cast<const float*>(a.v_cache) + row * D + c, there);
     }
@@ -276,6 +320,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
     asm volatile("cp.async.wait_all;" ::: "memory");
     // Values that are not finite: then hidden keys are left out one by one (zero times them
     // would not be zero).
+    if (Q8) __syncthreads();  // (the pieces below are others' here)
     float odd = 0.f;
 #pragma unroll 4
     for (int i = tid; i < kTallKeys * (D / 4); i += kThreads) {
@@ -388,9 +433,10 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
     if (rr >= nr) continue;
     const long long tok = (long long)q.bos + (r0 + rr) / G;
     const long long row = tok * a.Hq + hkv * G + (r0 + rr) % G;
-    const long long at = (long long)part * a.total_T * a.Hq + row;
-    const float inv = parts > 1 ? 1.f : lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
-    float* dst = parts > 1 ? part_o + at * D : static_cast<float*>(a.out) + row * D;
+    const bool partial = parts > 1 || a.groups > 0;
+    const long long at = part_row(a, n, part, parts, row);
+    const float inv = partial ? 1.f : lt == 0.f ? 0.f : 1.0f / lt;  // (NaN stays NaN)
+    float* dst = partial ? part_o + at * D : static_cast<float*>(a.out) + row * D;
 #pragma unroll
     for (int g = 0; g < CG; ++g) {
       const float2 x = split(o[i][2 * g]), y = split(o[i][2 * g + 1]);
@@ -398,7 +444,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
           make_float4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
     }
     if (tx == 0) {
-      if (parts > 1)
+      if (partial)
         part_ml[at] = make_float2(m[i], lt);
       else if (a.lse)
         a.lse[row] = lt == 0.f ? -INFINITY : (m[i] + log2f(lt)) * 0.6931471805599453f;
@@ -410,7 +456,7 @@ __device__ void tall_tile(const PagedArgs& a, const Seq& q, int n, int r0, int n
 // block's tile would cost more than the tile, over the sequences.
 constexpr int kSearch = 1024;
 
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 4) paged_simt_kernel(PagedArgs a, int parts,
                                                               float* part_o, float2* part_ml) {
   __shared__ int s_find[2];
@@ -422,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 4) paged_simt_kernel(PagedArgs a, in
     const int rows = q.len * (a.Hq / a.Hkv), r0 = tile * kRows;
     const int nr = min(kRows, rows - r0);
     if (nr <= kWarps)
-      row_tile<D, 1>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
+      row_tile<D, 1, Q8>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
     else
-      row_tile<D, 4>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
+      row_tile<D, 4, Q8>(a, q, n, r0, nr, parts, sm, part_o, part_ml);
   };
-  if (a.N > kSearch) {
+  if (lists(a) > kSearch) {
     const int n = blockIdx.x, G = a.Hq / a.Hkv;
     const int tiles = (int)(((long long)load_seq(a, n).len * G + kRows - 1) / kRows);
     for (int tile = 0; tile < tiles; ++tile) {
@@ -439,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_simt_kernel(PagedArgs a, in
   }
 }
 
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 2) paged_tall_kernel(PagedArgs a, int parts,
                                                                  float* part_o, float2* part_ml) {
   extern __shared__ __align__(16) float smem[];
@@ -449,13 +495,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tall_kernel(PagedArgs a, in
     const int rows = q.len * (a.Hq / a.Hkv), r0 = tile * kTallRows;
     const int nr = min(kTallRows, rows - r0);
     if (nr <= 16)
-      tall_tile<D, 1>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+      tall_tile<D, 1, Q8>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
     else if (nr <= 32)
-      tall_tile<D, 2>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+      tall_tile<D, 2, Q8>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
     else
-      tall_tile<D, 4>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
+      tall_tile<D, 4, Q8>(a, q, n, r0, nr, parts, smem, part_o, part_ml);
   };
-  if (a.N > kSearch) {
+  if (lists(a) > kSearch) {
     const int n = blockIdx.x, G = a.Hq / a.Hkv;
     const int tiles = (int)(((long long)load_seq(a, n).len * G + kTallRows - 1) / kTallRows);
     for (int tile = 0; tile < tiles; ++tile) {
@@ -483,7 +529,10 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
   // that one's blocks have left, so wait for what they wrote
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= rows || !token_owned(a, row / a.Hq)) return;
-  const float2 ml = lane < parts ? part_ml[lane * rows + row] : make_float2(0.f, 0.f);
+  // with prefixes, twice as many parts, the first half for the tokens that have one
+  const int all = a.groups > 0 ? 2 * parts : parts;
+  const int none = a.groups > 0 && !token_grouped(a, row / a.Hq) ? parts : 0;
+  const float2 ml = lane >= none && lane < all ? part_ml[lane * rows + row] : make_float2(0.f, 0.f);
   const bool some = ml.y != 0.f;  // (a NaN is something)
   float m = some ? ml.x : -INFINITY;
 #pragma unroll
@@ -524,56 +573,71 @@ __global__ void __launch_bounds__(128) paged_simt_join_kernel(PagedArgs a, int p
     a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Row tiles of a call, about.
-long long row_tiles(bool big, int N, int total_T, int Hq, int Hkv) {
+// Row tiles of a call, about (with prefixes, of the two lists that every row has).
+long long row_tiles(bool big, const PagedArgs& a) {
   const long long height = big ? kTallRows : kRows;
-  const long long tiles = ((long long)total_T * (Hq / Hkv) + height - 1) / height;
-  const long long seqs = N < total_T ? N : total_T;
-  return tiles < seqs ? seqs : tiles;
+  const long long tiles = ((long long)a.total_T * (a.Hq / a.Hkv) + height - 1) / height;
+  auto side = [&](int n) {
+    const long long seqs = n < a.total_T ? n : a.total_T;
+    return tiles < seqs ? seqs : tiles;
+  };
+  return side(a.N) + (a.groups > 0 ? side(a.groups) : 0);
 }
 
 // Tall tiles where a sequence has 32 rows or more on average and the caches (at the block table's
 // capacity) make a step of 64 keys for every place on the SMs.  16 sequences of 8 new tokens and
 // 500 cached keys, 16 + 4 heads of 64: 24 us for 29; of 32 and 1000, 8 + 8 heads of 128: 118 for
-// 223; but 200 tokens alone, 8 + 8 heads of 64: 19 for 14.
+// 223; but 200 tokens alone, 8 + 8 heads of 64: 19 for 14.  With prefixes the lists count as
+// sequences, and the larger capacity.
 bool tall(const PagedArgs& a) {
-  if ((long long)a.total_T * (a.Hq / a.Hkv) < 32ll * a.N) return false;
-  const double steps = (double)a.max_pages * a.page_size / kTallKeys + 1;
-  return row_tiles(true, a.N, a.total_T, a.Hq, a.Hkv) * steps * a.Hkv >= 2 * 152;
+  const long long sides = a.groups > 0 ? 2 : 1;
+  if (sides * a.total_T * (a.Hq / a.Hkv) < 32ll * (a.N + a.groups)) return false;
+  const int pages = a.max_pages > a.max_prefix_pages ? a.max_pages : a.max_prefix_pages;
+  const double steps = (double)pages * a.page_size / kTallKeys + 1;
+  return row_tiles(true, a) * steps * a.Hkv >= 2 * 152;
 }
 
 // Parts of the key range: enough blocks for eight (tall: two) on each SM when there are few rows.
-int simt_parts(bool big, int N, int total_T, int Hq, int Hkv) {
-  const long long tiles = row_tiles(big, N, total_T, Hq, Hkv);
+int simt_parts(bool big, const PagedArgs& a) {
+  const long long tiles = row_tiles(big, a);
   if (tiles <= 0) return 1;
-  const long long p = 152 * (big ? 2 : 8) / (tiles * Hkv);
-  return (int)(p < 1 ? 1 : p > kMaxParts ? kMaxParts : p);
+  const int most = a.groups > 0 ? kMaxParts / 2 : kMaxParts;  // (of each side)
+  const long long p = 152 * (big ? 2 : 8) / (tiles * a.Hkv);
+  return (int)(p < 1 ? 1 : p > most ? most : p);
 }
 
 // Partial results of `rows` query rows (tokens x heads), counted for each part.
 size_t simt_bytes(long long rows, int D) { return (size_t)rows * (D + 2) * sizeof(float); }
 
-template <int D>
+// Rows of partial results of a call (0: it writes its output at once).
+long long part_rows(const PagedArgs& a, int parts) {
+  const long long rows = (long long)a.total_T * a.Hq;
+  return a.groups > 0 ? 2 * parts * rows : parts > 1 ? parts * rows : 0;
+}
+
+template <int D, bool Q8>
 cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const bool big = tall(a);
-  const int parts = simt_parts(big, a.N, a.total_T, a.Hq, a.Hkv);
+  const int parts = simt_parts(big, a);
   const long long rows = (long long)a.total_T * a.Hq;
   float* po = static_cast<float*>(workspace);
-  float2* pml = reinterpret_cast<float2*>(po + (parts > 1 ? parts * rows * D : 0));
+  float2* pml = reinterpret_cast<float2*>(po + part_rows(a, parts) * D);
   const long long G = a.Hq / a.Hkv;
   const int height = big ? kTallRows : kRows;
-  const long long tiles = (a.total_T * G + height - 1) / height + a.N;  // upper bound
-  const dim3 grid((unsigned)(a.N > kSearch ? a.N : tiles), (unsigned)a.Hkv, (unsigned)parts);
+  const int n = a.N + a.groups;
+  const long long tiles =
+      (a.groups > 0 ? 2 : 1) * ((a.total_T * G + height - 1) / height) + n;  // upper bound
+  const dim3 grid((unsigned)(n > kSearch ? n : tiles), (unsigned)a.Hkv, (unsigned)parts);
   if (big) {
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_tall_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tall<D>::kSmem);
+        paged_tall_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tall<D>::kSmem);
     if (e != cudaSuccess) return e;
-    paged_tall_kernel<D><<<grid, kThreads, Tall<D>::kSmem, st>>>(a, parts, po, pml);
+    paged_tall_kernel<D, Q8><<<grid, kThreads, Tall<D>::kSmem, st>>>(a, parts, po, pml);
   } else {
-    paged_simt_kernel<D><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
+    paged_simt_kernel<D, Q8><<<grid, kThreads, 0, st>>>(a, parts, po, pml);
   }
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || parts == 1) return e;
+  if (e != cudaSuccess || part_rows(a, parts) == 0) return e;
   // Programmatic: 14.3 us for 16.4 in the small case above, called from the host (in a graph the
   // same).
   cudaLaunchConfig_t cfg{};
@@ -592,24 +656,27 @@ cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
 }  // namespace
 
 size_t paged_simt_need(const PagedArgs& a) {
-  const int parts = simt_parts(tall(a), a.N, a.total_T, a.Hq, a.Hkv);
-  return parts > 1 ? simt_bytes((long long)parts * a.total_T * a.Hq, a.D) : 0;
+  return simt_bytes(part_rows(a, simt_parts(tall(a), a)), a.D);
 }
 
 // The most that a call of up to total_T tokens can need, so that a buffer for a program's largest
-// batch serves every smaller one: simt_parts' parts times row tiles are at most its blocks.
-size_t paged_simt_workspace(int total_T, int Hq, int D) {
+// batch serves every smaller one: simt_parts' parts times row tiles are at most its blocks.  With
+// prefixes one part of each side at least.
+size_t paged_simt_workspace(int total_T, int Hq, int D, bool prefix) {
   constexpr long long kMost = 152ll * 8 * kRows;
   static_assert(kMost == 152ll * 2 * kTallRows, "rows in flight, short and tall tiles");
-  const long long rows = (long long)kMaxParts * total_T * Hq;
-  return simt_bytes(rows < kMost ? rows : kMost, D);
+  const long long tokens = (long long)total_T * Hq, all = kMaxParts * tokens;
+  const long long rows = all < kMost ? all : kMost;
+  return simt_bytes(prefix && rows < 2 * tokens ? 2 * tokens : rows, D);
 }
 
 cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t st) {
+  const bool q8 = a.k_scale != nullptr;
   switch (a.D) {
-    case 32: return launch_t<32>(a, workspace, st);
-    case 64: return launch_t<64>(a, workspace, st);
-    default: return launch_t<128>(a, workspace, st);
+    case 32: return q8 ? launch_t<32, true>(a, workspace, st) : launch_t<32, false>(a, workspace, st);
+    case 64: return q8 ? launch_t<64, true>(a, workspace, st) : launch_t<64, false>(a, workspace, st);
+    default:
+      return q8 ? launch_t<128, true>(a, workspace, st) : launch_t<128, false>(a, workspace, st);
   }
 }
 

@@ -64,6 +64,103 @@ int fill_norm_rope(kda::NormRopeArgs& a, const void* query, const void* key,
   return KDA_OK;
 }
 
+// Those of the calls that write into pages.
+int fill_append(kda::NormRopeArgs& a, const void* query, const void* key, const void* value,
+                const float* query_weight, const float* key_weight, const float* cos_table,
+                const float* sin_table, const int32_t* positions, const int64_t* slots,
+                void* query_out, void* k_cache, void* v_cache, float eps, int T, int Hq, int Hkv,
+                int D, int R, int max_position, int num_pages, int page_size,
+                long long query_stride, long long key_stride, long long value_stride, int flags,
+                int dtype) {
+  int s = fill_norm_rope(a, query, key, query_weight, key_weight, cos_table, sin_table, positions,
+                         eps, T, Hq, Hkv, D, R, max_position, query_stride, key_stride, flags,
+                         dtype);
+  if (s != KDA_OK) return s;
+  if (num_pages < 0) return KDA_ERR_BAD_SHAPE;
+  if (!page_size_ok(page_size)) return KDA_ERR_PAGE_SIZE;
+  if (T > 0 && (!value || !slots || !query_out || (num_pages > 0 && (!k_cache || !v_cache))))
+    return KDA_ERR_NULL_POINTER;
+  const void* const ptrs[] = {value, slots, query_out, k_cache, v_cache};
+  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
+  s = check_stride(value_stride, (long long)Hkv * D, T, dtype);
+  if (s != KDA_OK) return s;
+  if ((double)num_pages * Hkv * page_size * D >= kMaxElems) return KDA_ERR_TOO_LARGE;
+  a.v = value; a.v_stride = value_stride; a.slots = slots; a.q_out = query_out;
+  a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages; a.page_size = page_size;
+  a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  return KDA_OK;
+}
+
+// Checks of the attention calls (a holds the arguments as they came, the scale and window too),
+// and the call itself.
+int run_paged(kda::PagedArgs a, int dtype, void* workspace, size_t workspace_bytes,
+              kda_stream_t stream) {
+  if (a.N < 0 || a.total_T < 0 || a.Hq <= 0 || a.Hkv <= 0 || a.Hq % a.Hkv != 0 ||
+      a.num_pages < 0 || a.max_pages < 0 || a.window < 0 || a.sinks < 0 || a.groups < 0 ||
+      a.max_prefix_pages < 0)
+    return KDA_ERR_BAD_SHAPE;
+  if (!head_dim_ok(a.D)) return KDA_ERR_HEAD_DIM;
+  if (!page_size_ok(a.page_size)) return KDA_ERR_PAGE_SIZE;
+  if (!isfinite(a.scale)) return KDA_ERR_SCALE;
+  if (a.scale <= 0.f) a.scale = 1.0f / sqrtf((float)a.D);
+  if (!dtype_ok(dtype)) return KDA_ERR_DTYPE;
+  if (a.groups == 0) a.max_prefix_pages = 0;
+  const bool work = a.N > 0 && a.total_T > 0;
+  const bool own = a.max_pages > 0, shared = a.max_prefix_pages > 0;
+  if (work && (!a.q || !a.out || !a.cu_seqlens || !a.kv_lens ||
+               (a.groups > 0 && (!a.cu_groups || !a.prefix_lens)) ||
+               (a.num_pages > 0 &&
+                ((own && !a.block_table) || (shared && !a.prefix_table) ||
+                 ((own || shared) && (!a.k_cache || !a.v_cache))))))
+    return KDA_ERR_NULL_POINTER;
+  const void* const ptrs[] = {a.q,       a.k_cache, a.v_cache, a.block_table,
+                              a.cu_seqlens, a.kv_lens, a.out,     a.lse,
+                              a.k_scale, a.v_scale, a.prefix_table, a.prefix_lens, a.cu_groups};
+  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
+  const int s0 = check_stride(a.q_stride, (long long)a.Hq * a.D, a.total_T, dtype);
+  if (s0 != KDA_OK) return s0;
+  if ((double)a.num_pages * a.Hkv * a.page_size > 2147483647.0 ||
+      (double)a.max_pages * a.page_size > 2147483647.0 ||
+      (double)a.max_prefix_pages * a.page_size > 2147483647.0 ||
+      (double)a.total_T * a.Hq > 2147483647.0 || (double)a.N * a.max_pages >= kMaxElems ||
+      (double)a.groups * a.max_prefix_pages >= kMaxElems || a.N > 65535 || a.groups > 65535 ||
+      a.Hkv > 65535)
+    return KDA_ERR_TOO_LARGE;
+  // a window that no position can leave hides nothing
+  if ((double)a.window >= (double)a.max_pages * a.page_size) a.window = 0;
+  if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
+  const size_t need = !work                ? 0
+                      : dtype == KDA_F32   ? kda::paged_simt_need(a)
+                      : a.groups > 0       ? kda::paged_prefix_tc_workspace(a.total_T, a.Hq, a.D)
+                                           : kda::paged_tc_workspace(a.D);
+  if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
+    return KDA_ERR_WORKSPACE;
+  const int s = kda::check_current_device();
+  if (s != KDA_OK) return s;
+  if (!work) return KDA_OK;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return launch_status(dtype == KDA_BF16 ? kda::launch_paged_tc(a, workspace, st)
+                                         : kda::launch_paged_simt(a, workspace, st));
+}
+
+kda::PagedArgs paged_args(const void* query, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, void* out, float* lse, float softmax_scale,
+                          int N, int total_T, int Hq, int Hkv, int D, int num_pages,
+                          int page_size, int max_pages, long long query_stride) {
+  kda::PagedArgs a{};
+  a.q = query; a.q_stride = query_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.block_table = block_table; a.cu_seqlens = cu_seqlens; a.kv_lens = kv_lens; a.out = out;
+  a.lse = lse; a.scale = softmax_scale; a.N = N; a.total_T = total_T; a.Hq = Hq; a.Hkv = Hkv;
+  a.D = D; a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages;
+  return a;
+}
+
+bool paged_shape_ok(int N, int total_T, int Hq, int Hkv, int D, int dtype) {
+  return N > 0 && total_T > 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && head_dim_ok(D) &&
+         dtype_ok(dtype);
+}
+
 }  // namespace
 
 extern "C" {
@@ -140,27 +237,75 @@ int kda_qk_norm_rope_append(const void* query, const void* key, const void* valu
                             long long query_stride, long long key_stride,
                             long long value_stride, int flags, int dtype, kda_stream_t stream) {
   kda::NormRopeArgs a;
-  int s = fill_norm_rope(a, query, key, query_weight, key_weight, cos_table, sin_table, positions,
-                         eps, T, Hq, Hkv, D, R, max_position, query_stride, key_stride, flags,
-                         dtype);
+  int s = fill_append(a, query, key, value, query_weight, key_weight, cos_table, sin_table,
+                      positions, slots, query_out, k_cache, v_cache, eps, T, Hq, Hkv, D, R,
+                      max_position, num_pages, page_size, query_stride, key_stride, value_stride,
+                      flags, dtype);
   if (s != KDA_OK) return s;
-  if (num_pages < 0) return KDA_ERR_BAD_SHAPE;
-  if (!page_size_ok(page_size)) return KDA_ERR_PAGE_SIZE;
-  if (T > 0 && (!value || !slots || !query_out || (num_pages > 0 && (!k_cache || !v_cache))))
-    return KDA_ERR_NULL_POINTER;
-  const void* const ptrs[] = {value, slots, query_out, k_cache, v_cache};
-  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
-  s = check_stride(value_stride, (long long)Hkv * D, T, dtype);
-  if (s != KDA_OK) return s;
-  if ((double)num_pages * Hkv * page_size * D >= kMaxElems) return KDA_ERR_TOO_LARGE;
   s = kda::check_current_device();
   if (s != KDA_OK) return s;
   if (T == 0) return KDA_OK;
-  a.v = value; a.v_stride = value_stride; a.slots = slots; a.q_out = query_out;
-  a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages; a.page_size = page_size;
-  a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   return launch_status(
       kda::launch_norm_rope(a, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_qk_norm_rope_append_q8(const void* query, const void* key, const void* value,
+                               const float* query_weight, const float* key_weight,
+                               const float* cos_table, const float* sin_table,
+                               const int32_t* positions, const int64_t* slots, void* query_out,
+                               void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                               float eps, int T, int Hq, int Hkv, int D, int R, int max_position,
+                               int num_pages, int page_size, long long query_stride,
+                               long long key_stride, long long value_stride, int flags,
+                               int dtype, kda_stream_t stream) {
+  kda::NormRopeArgs a;
+  const int s = fill_append(a, query, key, value, query_weight, key_weight, cos_table, sin_table,
+                            positions, slots, query_out, k_cache, v_cache, eps, T, Hq, Hkv, D, R,
+                            max_position, num_pages, page_size, query_stride, key_stride,
+                            value_stride, flags, dtype);
+  if (s != KDA_OK) return s;
+  if (T > 0 && num_pages > 0 && (!k_scale || !v_scale)) return KDA_ERR_NULL_POINTER;
+  const void* const ptrs[] = {k_scale, v_scale};
+  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
+  const int d = kda::check_current_device();
+  if (d != KDA_OK) return d;
+  if (T == 0) return KDA_OK;
+  // (without pages no token is kept, whatever the caches are)
+  if (num_pages > 0) {
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+  }
+  return launch_status(
+      kda::launch_norm_rope(a, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_paged_cache_read_q8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                            const uint8_t* v_scale, const int64_t* slots, void* key_out,
+                            void* value_out, int T, int Hkv, int D, int num_pages, int page_size,
+                            int dtype, kda_stream_t stream) {
+  if (T < 0 || Hkv <= 0 || num_pages < 0) return KDA_ERR_BAD_SHAPE;
+  if (!head_dim_ok(D)) return KDA_ERR_HEAD_DIM;
+  if (!page_size_ok(page_size)) return KDA_ERR_PAGE_SIZE;
+  if (!dtype_ok(dtype)) return KDA_ERR_DTYPE;
+  if (T > 0 && (!slots || !key_out || !value_out ||
+                (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale))))
+    return KDA_ERR_NULL_POINTER;
+  const void* const ptrs[] = {k_cache, v_cache, k_scale, v_scale, slots, key_out, value_out};
+  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
+  if ((double)num_pages * Hkv * page_size * D >= kMaxElems ||
+      (double)T * Hkv * (D / 16) > 2147483647.0)
+    return KDA_ERR_TOO_LARGE;
+  const int s = kda::check_current_device();
+  if (s != KDA_OK) return s;
+  if (T == 0) return KDA_OK;
+  kda::CacheReadArgs a{};
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale; a.v_scale = v_scale; a.slots = slots; a.k_out = key_out;
+  a.v_out = value_out; a.T = T; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages;
+  a.page_size = page_size;
+  return launch_status(
+      kda::launch_cache_read(a, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_qk_norm_rope_bwd_workspace_size(int T, int Hq, int Hkv, int D) {
@@ -198,11 +343,9 @@ int kda_qk_norm_rope_bwd(const void* query, const void* key, const float* query_
 
 size_t kda_paged_attention_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
                                               int dtype) {
-  if (N <= 0 || total_T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || !head_dim_ok(D) ||
-      !dtype_ok(dtype))
-    return 0;
+  if (!paged_shape_ok(N, total_T, Hq, Hkv, D, dtype)) return 0;
   return dtype == KDA_BF16 ? kda::paged_tc_workspace(D)
-                           : kda::paged_simt_workspace(total_T, Hq, D);
+                           : kda::paged_simt_workspace(total_T, Hq, D, false);
 }
 
 int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
@@ -212,46 +355,66 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
                             int page_size, int max_pages, int window, int sinks,
                             long long query_stride, int dtype, void* workspace,
                             size_t workspace_bytes, kda_stream_t stream) {
-  if (N < 0 || total_T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || num_pages < 0 ||
-      max_pages < 0 || window < 0 || sinks < 0)
-    return KDA_ERR_BAD_SHAPE;
-  if (!head_dim_ok(D)) return KDA_ERR_HEAD_DIM;
-  if (!page_size_ok(page_size)) return KDA_ERR_PAGE_SIZE;
-  if (!isfinite(softmax_scale)) return KDA_ERR_SCALE;
-  if (softmax_scale <= 0.f) softmax_scale = 1.0f / sqrtf((float)D);
-  if (!dtype_ok(dtype)) return KDA_ERR_DTYPE;
-  const bool work = N > 0 && total_T > 0;
-  if (work && (!query || !out || !cu_seqlens || !kv_lens ||
-               (num_pages > 0 && max_pages > 0 && (!k_cache || !v_cache || !block_table))))
-    return KDA_ERR_NULL_POINTER;
-  const void* const ptrs[] = {query, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, lse};
-  if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
-  const int s0 = check_stride(query_stride, (long long)Hq * D, total_T, dtype);
-  if (s0 != KDA_OK) return s0;
-  if ((double)num_pages * Hkv * page_size > 2147483647.0 ||
-      (double)max_pages * page_size > 2147483647.0 || (double)total_T * Hq > 2147483647.0 ||
-      (double)N * max_pages >= kMaxElems || N > 65535 || Hkv > 65535)
-    return KDA_ERR_TOO_LARGE;
-  kda::PagedArgs a{};
-  a.q = query; a.q_stride = query_stride; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.block_table = block_table; a.cu_seqlens = cu_seqlens; a.kv_lens = kv_lens; a.out = out;
-  a.lse = lse; a.scale = softmax_scale; a.N = N; a.total_T = total_T; a.Hq = Hq; a.Hkv = Hkv;
-  a.D = D; a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages;
-  // a window that no position can leave hides nothing
-  a.window = (double)window >= (double)max_pages * page_size ? 0 : window;
+  kda::PagedArgs a =
+      paged_args(query, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, lse,
+                 softmax_scale, N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
+                 query_stride);
+  a.window = window;
   a.sinks = sinks;
-  if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
-  const size_t need = !work                 ? 0
-                      : dtype == KDA_BF16 ? kda::paged_tc_workspace(D)
-                                          : kda::paged_simt_need(a);
-  if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
-    return KDA_ERR_WORKSPACE;
-  const int s = kda::check_current_device();
-  if (s != KDA_OK) return s;
-  if (!work) return KDA_OK;
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return launch_status(dtype == KDA_BF16 ? kda::launch_paged_tc(a, workspace, st)
-                                         : kda::launch_paged_simt(a, workspace, st));
+  return run_paged(a, dtype, workspace, workspace_bytes, stream);
+}
+
+int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const void* v_cache,
+                               const uint8_t* k_scale, const uint8_t* v_scale,
+                               const int32_t* block_table, const int32_t* cu_seqlens,
+                               const int32_t* kv_lens, void* out, float* lse,
+                               float softmax_scale, int N, int total_T, int Hq, int Hkv, int D,
+                               int num_pages, int page_size, int max_pages, int window,
+                               int sinks, long long query_stride, int dtype, void* workspace,
+                               size_t workspace_bytes, kda_stream_t stream) {
+  kda::PagedArgs a =
+      paged_args(query, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, lse,
+                 softmax_scale, N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
+                 query_stride);
+  a.window = window;
+  a.sinks = sinks;
+  // scales may be absent only where the caches are
+  if (!k_scale || !v_scale) {
+    if (k_cache || v_cache || (N > 0 && total_T > 0 && num_pages > 0 && max_pages > 0))
+      return KDA_ERR_NULL_POINTER;
+  }
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return run_paged(a, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t kda_paged_prefix_attention_fwd_workspace_size(int num_groups, int N, int total_T, int Hq,
+                                                     int Hkv, int D, int dtype) {
+  if (num_groups < 0 || !paged_shape_ok(N, total_T, Hq, Hkv, D, dtype)) return 0;
+  if (dtype == KDA_F32) return kda::paged_simt_workspace(total_T, Hq, D, num_groups > 0);
+  return num_groups > 0 ? kda::paged_prefix_tc_workspace(total_T, Hq, D)
+                        : kda::paged_tc_workspace(D);
+}
+
+int kda_paged_prefix_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_scale, const uint8_t* v_scale,
+                                   const int32_t* prefix_table, const int32_t* prefix_lens,
+                                   const int32_t* cu_groups, const int32_t* block_table,
+                                   const int32_t* cu_seqlens, const int32_t* kv_lens, void* out,
+                                   float* lse, float softmax_scale, int num_groups, int N,
+                                   int total_T, int Hq, int Hkv, int D, int num_pages,
+                                   int page_size, int max_prefix_pages, int max_pages,
+                                   long long query_stride, int dtype, void* workspace,
+                                   size_t workspace_bytes, kda_stream_t stream) {
+  kda::PagedArgs a =
+      paged_args(query, k_cache, v_cache, block_table, cu_seqlens, kv_lens, out, lse,
+                 softmax_scale, N, total_T, Hq, Hkv, D, num_pages, page_size, max_pages,
+                 query_stride);
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  if (!k_scale != !v_scale) return KDA_ERR_NULL_POINTER;
+  a.prefix_table = prefix_table; a.prefix_lens = prefix_lens; a.cu_groups = cu_groups;
+  a.groups = num_groups; a.max_prefix_pages = max_prefix_pages;
+  return run_paged(a, dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

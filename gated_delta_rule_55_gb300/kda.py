@@ -35,7 +35,9 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_fwd_workspace_siz
            "kda_decode_step", "kda_attention_step", "kda_qk_norm_rope_fwd",
            "kda_qk_norm_rope_append", "kda_qk_norm_rope_bwd_workspace_size",
            "kda_qk_norm_rope_bwd", "kda_paged_attention_fwd_workspace_size",
-           "kda_paged_attention_fwd",
+           "kda_paged_attention_fwd", "kda_qk_norm_rope_append_q8", "kda_paged_cache_read_q8",
+           "kda_paged_attention_q8_fwd", "kda_paged_prefix_attention_fwd_workspace_size",
+           "kda_paged_prefix_attention_fwd",
            "kda_status_string",
            "kda_version", "kda_device_error", "kda_selftest_bounded_wait")
 KDA_ATTN_NO_QK_L2NORM = 1
@@ -114,6 +116,15 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.kda_paged_attention_fwd_workspace_size.argtypes = [_I] * 6
     L.kda_paged_attention_fwd_workspace_size.restype = _Z
     L.kda_paged_attention_fwd.argtypes = ([_P] * 8 + [_F] + [_I] * 10 + [_LL, _I, _P, _Z, _P])
+    L.kda_qk_norm_rope_append_q8.argtypes = ([_P] * 14 + [_F] + [_I] * 8 + [_LL] * 3 +
+                                             [_I, _I, _P])
+    L.kda_paged_cache_read_q8.argtypes = [_P] * 7 + [_I] * 6 + [_P]
+    L.kda_paged_attention_q8_fwd.argtypes = ([_P] * 10 + [_F] + [_I] * 10 +
+                                             [_LL, _I, _P, _Z, _P])
+    L.kda_paged_prefix_attention_fwd_workspace_size.argtypes = [_I] * 7
+    L.kda_paged_prefix_attention_fwd_workspace_size.restype = _Z
+    L.kda_paged_prefix_attention_fwd.argtypes = ([_P] * 13 + [_F] + [_I] * 10 +
+                                                 [_LL, _I, _P, _Z, _P])
     L.kda_device_error.argtypes = [_I]
     L.kda_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, _P]
     L.kda_selftest_bounded_wait.restype = _I
@@ -125,6 +136,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
               "kda_recurrent_attention_fwd_ws",
               "kda_decode_step", "kda_attention_step", "kda_qk_norm_rope_fwd",
               "kda_qk_norm_rope_append", "kda_qk_norm_rope_bwd", "kda_paged_attention_fwd",
+              "kda_qk_norm_rope_append_q8", "kda_paged_cache_read_q8",
+              "kda_paged_attention_q8_fwd", "kda_paged_prefix_attention_fwd",
               "kda_version", "kda_device_error"):
         getattr(L, f).restype = _I
     L.kda_status_string.argtypes = [_I]
@@ -446,13 +459,14 @@ class _Call:
     """What the serving calls look up once: torch's types, the current device and its stream.
     A serving step makes many small calls, so their arguments are checked in few Python
     operations each."""
-    f32 = bf16 = i32 = i64 = None
+    f32 = bf16 = i32 = i64 = e4m3 = u8 = None
     device = raw_stream = where = dense = address = None
 
 
 def _setup():
     import torch
     _Call.bf16, _Call.i32, _Call.i64 = torch.bfloat16, torch.int32, torch.int64
+    _Call.e4m3, _Call.u8 = torch.float8_e4m3fn, torch.uint8
     _Call.device = torch.cuda.current_device
     _Call.where, _Call.dense = torch.Tensor.get_device, torch.Tensor.is_contiguous
     _Call.address = torch.Tensor.data_ptr
@@ -634,3 +648,82 @@ def kda_paged_attention_fwd(query, k_cache, v_cache, block_table, cu_seqlens, kv
                    "k_cache v_cache block_table cu_seqlens kv_lens out"),
         _dev(lse, _Call.f32, dev, "lse"), float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D,
         num_pages, page_size, max_pages, window, sinks, qs, code, wp, wb, st))
+
+
+def kda_qk_norm_rope_append_q8(query, key, value, query_weight, key_weight, cos_table, sin_table,
+                               positions, slots, query_out, k_cache, v_cache, k_scale, v_scale, T,
+                               Hq, Hkv, D, R, max_position, num_pages, page_size, eps=1e-6,
+                               interleaved=False, dtype=None, stream=None):
+    """kda_qk_norm_rope_append into pages of 8-bit rows: caches of torch.float8_e4m3fn, scales of
+    torch.uint8 (see include/kda.h)."""
+    code, el, dev, st = _begin(query, dtype, stream)
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    kp, ks = _rows(key, el, dev, Hkv, D, "key")
+    vp, vs = _rows(value, el, dev, Hkv, D, "value")
+    e4m3, u8 = _Call.e4m3, _Call.u8
+    _check("kda_qk_norm_rope_append_q8", lib().kda_qk_norm_rope_append_q8(
+        qp, kp, vp,
+        *_norm_rope_in(query_weight, key_weight, cos_table, sin_table, positions, dev),
+        *_devs((slots, query_out, k_cache, v_cache, k_scale, v_scale),
+               [_Call.i64, el, e4m3, e4m3, u8, u8], dev,
+               "slots query_out k_cache v_cache k_scale v_scale"), float(eps), T, Hq, Hkv, D, R,
+        max_position, num_pages, page_size, qs, ks, vs,
+        KDA_ROPE_INTERLEAVED if interleaved else 0, code, st))
+
+
+def kda_paged_cache_read_q8(k_cache, v_cache, k_scale, v_scale, slots, key_out, value_out, T, Hkv,
+                            D, num_pages, page_size, dtype=None, stream=None):
+    """Tokens of an 8-bit cache as dense rows of key_out's type (see include/kda.h)."""
+    code, el, dev, st = _begin(key_out, dtype, stream)
+    e4m3, u8 = _Call.e4m3, _Call.u8
+    _check("kda_paged_cache_read_q8", lib().kda_paged_cache_read_q8(
+        *_devs((k_cache, v_cache, k_scale, v_scale, slots, key_out, value_out),
+               [e4m3, e4m3, u8, u8, _Call.i64, el, el], dev,
+               "k_cache v_cache k_scale v_scale slots key_out value_out"), T, Hkv, D, num_pages,
+        page_size, code, st))
+
+
+def kda_paged_attention_q8_fwd(query, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                               kv_lens, out, N, total_T, Hq, Hkv, D, num_pages, page_size,
+                               max_pages, lse=None, softmax_scale=None, window=0, sinks=0,
+                               dtype=None, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache in 8 bits (see include/kda.h)."""
+    code, el, dev, st = _begin(query, dtype, stream)
+    i32, e4m3, u8 = _Call.i32, _Call.e4m3, _Call.u8
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    wp, wb = _scratch(workspace, dev)
+    _check("kda_paged_attention_q8_fwd", lib().kda_paged_attention_q8_fwd(
+        qp, *_devs((k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, out),
+                   [e4m3, e4m3, u8, u8, i32, i32, i32, el], dev,
+                   "k_cache v_cache k_scale v_scale block_table cu_seqlens kv_lens out"),
+        _dev(lse, _Call.f32, dev, "lse"), float(softmax_scale or 0.0), N, total_T, Hq, Hkv, D,
+        num_pages, page_size, max_pages, window, sinks, qs, code, wp, wb, st))
+
+
+def kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq, Hkv, D,
+                                                  dtype=KDA_BF16) -> int:
+    """Bytes of workspace kda_paged_prefix_attention_fwd needs (see include/kda.h)."""
+    return int(lib().kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq, Hkv,
+                                                                   D, dtype))
+
+
+def kda_paged_prefix_attention_fwd(query, k_cache, v_cache, prefix_table, prefix_lens, cu_groups,
+                                   block_table, cu_seqlens, kv_lens, out, num_groups, N, total_T,
+                                   Hq, Hkv, D, num_pages, page_size, max_prefix_pages, max_pages,
+                                   k_scale=None, v_scale=None, lse=None, softmax_scale=None,
+                                   dtype=None, workspace=None, stream=None):
+    """Attention of groups of sequences that share prefixes, over pages of query's type or, with
+    scales, of 8 bits (see include/kda.h)."""
+    code, el, dev, st = _begin(query, dtype, stream)
+    i32, u8 = _Call.i32, _Call.u8
+    kept = el if k_scale is None and v_scale is None else _Call.e4m3
+    qp, qs = _rows(query, el, dev, Hq, D, "query")
+    wp, wb = _scratch(workspace, dev)
+    kp, vp, *rest = _devs(
+        (k_cache, v_cache, prefix_table, prefix_lens, cu_groups, block_table, cu_seqlens, kv_lens,
+         out), [kept, kept, i32, i32, i32, i32, i32, i32, el], dev,
+        "k_cache v_cache prefix_table prefix_lens cu_groups block_table cu_seqlens kv_lens out")
+    _check("kda_paged_prefix_attention_fwd", lib().kda_paged_prefix_attention_fwd(
+        qp, kp, vp, _dev(k_scale, u8, dev, "k_scale"), _dev(v_scale, u8, dev, "v_scale"), *rest,
+        _dev(lse, _Call.f32, dev, "lse"), float(softmax_scale or 0.0), num_groups, N, total_T, Hq,
+        Hkv, D, num_pages, page_size, max_prefix_pages, max_pages, qs, code, wp, wb, st))

@@ -543,6 +543,44 @@ int kda_qk_norm_rope_append(const void* query, const void* key, const void* valu
                             long long value_stride, int flags, int dtype, kda_stream_t stream);
 
 /*
+ * kda_qk_norm_rope_append_q8 -- kda_qk_norm_rope_append into a cache that holds its rows in 8 bits.
+ *   A row (a token's key or value of one kv head) y [D] becomes D numbers of e4m3 (4 exponent and 3
+ *   mantissa bits, largest 448) and one byte b:
+ *       e = the smallest integer with max |y| <= 448 * 2^e, within [-110, 119],  b = e + 127
+ *       number_i = y_i / 2^e to nearest, halves to even;   it stands for number_i * 2^e
+ *   Keys are normed and turned in fp32 and rounded once, to the 8 bits; a number within fp32's error
+ *   of the middle between two may become either.  Magnitudes above 448 * 2^119 (2.98e38) are kept
+ *   as that.  A row with an infinity or a NaN is kept with b = 255 and stands for NaNs.
+ *
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] 8-bit numbers
+ *   k_scale, v_scale [num_pages, Hkv, page_size]    the bytes b
+ *   All other arguments, layouts and errors are those of kda_qk_norm_rope_append.
+ */
+int kda_qk_norm_rope_append_q8(const void* query, const void* key, const void* value,
+                               const float* query_weight, const float* key_weight,
+                               const float* cos_table, const float* sin_table,
+                               const int32_t* positions, const int64_t* slots, void* query_out,
+                               void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                               float eps, int T, int Hq, int Hkv, int D, int R, int max_position,
+                               int num_pages, int page_size, long long query_stride,
+                               long long key_stride, long long value_stride, int flags,
+                               int dtype, kda_stream_t stream);
+
+/*
+ * kda_paged_cache_read_q8 -- keys and values of T tokens out of such a cache, as dense rows (for a
+ *   call that takes no pages, or to write them elsewhere).
+ *
+ *   slots        [T] int64 DEVICE: page * page_size + offset; outside
+ *                [0, num_pages * page_size): the token's rows become zeros
+ *   key_out, value_out [T, Hkv, D] dtype (fp32 or bf16), written; both types hold exactly what
+ *                the append keeps
+ */
+int kda_paged_cache_read_q8(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                            const uint8_t* v_scale, const int64_t* slots, void* key_out,
+                            void* value_out, int T, int Hkv, int D, int num_pages, int page_size,
+                            int dtype, kda_stream_t stream);
+
+/*
  * kda_qk_norm_rope_bwd -- gradients of kda_qk_norm_rope_fwd.  With g the output gradient turned
  *   back and r = 1 / sqrt(mean(x^2) + eps): d_weight = sum over tokens and heads of g x r and
  *   dx = r (g w - x r^2 mean(g w x)).
@@ -613,6 +651,62 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
                             long long query_stride, int dtype, void* workspace,
                             size_t workspace_bytes, kda_stream_t stream);
 
+/*
+ * kda_paged_attention_q8_fwd -- kda_paged_attention_fwd over a cache in 8 bits
+ *   (kda_qk_norm_rope_append_q8): k_cache, v_cache [num_pages, Hkv, page_size, D] numbers, k_scale,
+ *   v_scale [num_pages, Hkv, page_size].  query and out stay in dtype.  Rows are expanded exactly,
+ *   so the result is that of kda_paged_attention_fwd over the values that the cache stands for; a
+ *   seen row with b = 255 makes what sees it NaN.  All other arguments, limits and errors are those
+ *   of kda_paged_attention_fwd, as is the workspace (kda_paged_attention_fwd_workspace_size).
+ */
+int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const void* v_cache,
+                               const uint8_t* k_scale, const uint8_t* v_scale,
+                               const int32_t* block_table, const int32_t* cu_seqlens,
+                               const int32_t* kv_lens, void* out, float* lse,
+                               float softmax_scale, int N, int total_T, int Hq, int Hkv, int D,
+                               int num_pages, int page_size, int max_pages, int window,
+                               int sinks, long long query_stride, int dtype, void* workspace,
+                               size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_paged_prefix_attention_fwd -- kda_paged_attention_fwd for sequences that share what they begin
+ *   with (a system prompt, a document): sequences cu_groups[g] .. cu_groups[g + 1] - 1 have the
+ *   prefix_lens[g] keys of prefix g in front of their own, all of which all of their new tokens see.
+ *   A prefix is worked on once for all tokens of its group, so its keys are read once and meet
+ *   full tiles of queries:
+ *       o = sum_j softmax_j(scale q . k_j) v_j   over the prefix's keys and the sequence's own
+ *
+ *   prefix_table [num_groups, max_prefix_pages] int32 DEVICE: pages of the prefixes, as block_table
+ *   prefix_lens  [num_groups] int32 DEVICE, clamped into [0, max_prefix_pages page_size]; 0: none
+ *   cu_groups    [num_groups + 1] int32 DEVICE offsets of the groups among the sequences, clamped
+ *                into [0, N]; they must not decrease (groups that overlap leave their rows
+ *                unspecified; there is no fault).  Sequences outside [cu_groups[0],
+ *                cu_groups[num_groups]) have no prefix.
+ *   block_table, cu_seqlens, kv_lens: of the sequences' own keys, the new tokens' included, as for
+ *                kda_paged_attention_fwd.  (Positions are the cache's affair: keys are appended
+ *                with those that they have behind the prefix.)
+ *   k_cache, v_cache, k_scale, v_scale: pages of dtype with both scales NULL, or in 8 bits
+ *                (kda_paged_attention_q8_fwd)
+ *   num_groups = 0: kda_paged_attention_fwd (the three prefix arguments may be NULL)
+ *   There is no window.  bf16 limit: the line counts the prefixes as sequences of all of their
+ *   groups' tokens.  num_groups at most 65535.  All else as for kda_paged_attention_fwd.
+ *   workspace    at least kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq,
+ *                Hkv, D, dtype) bytes, 256-byte aligned; the size never decreases as num_groups,
+ *                N or total_T grows.
+ */
+size_t kda_paged_prefix_attention_fwd_workspace_size(int num_groups, int N, int total_T, int Hq,
+                                                     int Hkv, int D, int dtype);
+int kda_paged_prefix_attention_fwd(const void* query, const void* k_cache, const void* v_cache,
+                                   const uint8_t* k_scale, const uint8_t* v_scale,
+                                   const int32_t* prefix_table, const int32_t* prefix_lens,
+                                   const int32_t* cu_groups, const int32_t* block_table,
+                                   const int32_t* cu_seqlens, const int32_t* kv_lens, void* out,
+                                   float* lse, float softmax_scale, int num_groups, int N,
+                                   int total_T, int Hq, int Hkv, int D, int num_pages,
+                                   int page_size, int max_prefix_pages, int max_pages,
+                                   long long query_stride, int dtype, void* workspace,
+                                   size_t workspace_bytes, kda_stream_t stream);
+
 /* Static, human-readable text for a kda_status value (never NULL). */
 const char* kda_status_string(int status);
 
@@ -631,7 +725,7 @@ int kda_version(void);
  *   detected per 16-token sub-chunk (a summed key-axis gate or decay totalling outside
  *   [-80, 16] over a sub-chunk, or a value-axis gate outside [-40, 8] over half of one,
  *   which gates in [-5, 1] rule out; that call's results are unspecified); bit 6: a bounded
- *   wait inside kda_paged_attention_fwd's tensor-core kernel gave up.  Synchronises
+ *   wait inside the tensor-core kernels of attention over pages gave up.  Synchronises
  *   the device.  reset != 0
  *   clears the mask.
  *   Returns the mask (>= 0) or KDA_ERR_DEVICE.
