@@ -172,10 +172,12 @@ size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
 size_t paged_prefix_tc_workspace(int total_T, int Hq, int D);
 cudaError_t launch_paged_tc_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_tc_q8_few(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
 unsigned int paged_q8_read_error(bool reset);
+unsigned int paged_q8_few_read_error(bool reset);
 unsigned int paged_prefix_read_error(bool reset);
 unsigned int paged_prefix_q8_read_error(bool reset);
 // Of any call of up to total_T tokens.

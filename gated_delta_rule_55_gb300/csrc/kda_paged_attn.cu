@@ -30,11 +30,14 @@ cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st
   if (a.groups > 0)
     return q8 ? launch_paged_tc_prefix_q8(a, workspace, st)
               : launch_paged_tc_prefix(a, workspace, st);
+  if (q8 && a.D == 128 && (long long)a.total_T * (a.Hq / a.Hkv) <= 16ll * a.N)
+    return launch_paged_tc_q8_few(a, workspace, st);
   return q8 ? launch_paged_tc_q8(a, workspace, st) : launch_any<false, false>(a, workspace, st);
 }
 
 unsigned int paged_read_error(bool reset) {
-  return read_error(reset) | paged_q8_read_error(reset) | paged_prefix_read_error(reset) |
+  return read_error(reset) | paged_q8_read_error(reset) | paged_q8_few_read_error(reset) |
+          paged_prefix_read_error(reset) |
          paged_prefix_q8_read_error(reset);
 }
 

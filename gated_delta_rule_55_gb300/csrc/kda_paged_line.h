@@ -10,7 +10,7 @@
 
 namespace kda {
 
-constexpr int kCtas = 152;  // one per SM
+constexpr int kCtas = 152;  // one per SM (CTAS below: a kernel with another number says so)
 
 // Sums of the line's units, none of them negative, stop here.  A line this long is not worked
 // on: offsets in order are never this long (paged_tc_index_ok), overlapping ones can be, and a
@@ -23,14 +23,16 @@ KDA_LINE_FN int line_add(int a, int b) {
 }
 
 // The first unit of CTA c's stretch of a line of `total` units.
+template <int CTAS = kCtas>
 KDA_LINE_FN int stretch(int total, int c) {
-  const int q = (int)((unsigned)total / kCtas), more = total - q * kCtas;
+  const int q = (int)((unsigned)total / CTAS), more = total - q * CTAS;
   return q * c + (c < more ? c : more);
 }
 
 // The CTA whose stretch holds a unit.
+template <int CTAS = kCtas>
 KDA_LINE_FN int stretch_of(int total, int unit) {
-  const int q = (int)((unsigned)total / kCtas), more = total - q * kCtas;  // q + 1 units each
+  const int q = (int)((unsigned)total / CTAS), more = total - q * CTAS;  // q + 1 units each
   return unit < more * (q + 1) ? unit / (q + 1)
                                : more + (unit - more * (q + 1)) / (q > 1 ? q : 1);
 }
