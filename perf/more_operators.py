@@ -399,8 +399,8 @@ def _workspace(s, kda):
     c, n = s["case"], 0
     dt = kda.KDA_F32 if c["f32"] else kda.KDA_BF16
     if c["op"] == "attn":
-        n = kda.kda_paged_attention_fwd_workspace_size(c["N"], s["cu_host"][-1], c["Hq"], c["Hkv"],
-                                                       c["D"], dtype=dt)
+        n = kda.kda_paged_attention_q8_fwd_workspace_size(
+            c["N"], s["cu_host"][-1], c["Hq"], c["Hkv"], c["D"], dtype=dt)
     elif c["op"] == "prefix":
         n = kda.kda_paged_prefix_attention_fwd_workspace_size(
             c["groups"], c["N"], s["cu_host"][-1], c["Hq"], c["Hkv"], c["D"], dtype=dt)
