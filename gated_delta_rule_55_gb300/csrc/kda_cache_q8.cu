@@ -1,7 +1,9 @@
 // Reading tokens back from a cache in 8 bits (kda_paged_cache_read_q8): keys and values of given
 // slots as dense rows of fp32 or bf16, which both hold them exactly.
 //
-// Bound by HBM: D + 1 bytes in and 2 D or 4 D out per row.  A thread has 16 numbers of a token's
+// And queries as two e4m3 terms, for attention whose keys stay in 8 bits (kda_paged_tc.cuh).
+//
+// Reading is bound by HBM: D + 1 bytes in and 2 D or 4 D out per row.  A thread has 16 numbers of a token's
 // key and value of one head, so that its loads are 16 bytes and its four loads of the two rows
 // (numbers and scales) are in flight together behind the slot's.
 #include "kda_q8.cuh"
@@ -68,7 +70,59 @@ cudaError_t launch_t(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// A query row of bf16 (8 bits of mantissa) under a power of two as the sum of two rows of e4m3 (4
+// each):  q 2^-e = hi + lo,  hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Exact where q is more than
+// 2^-10 of the row's largest, and off by at most 2^-18 of that elsewhere (e4m3 ends at 2^-9).
+// Sixteen lanes a row; hi and lo lie where the row's 256 bytes would.
+__global__ void __launch_bounds__(kThreads) query_terms_kernel(PagedArgs a, uint8_t* terms,
+                                                               float* scales) {
+  const long long row = (long long)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  const int c = threadIdx.x & 15;
+  const long long rows = (long long)a.total_T * a.Hq;
+  const long long src = row < rows ? row : rows - 1;
+  const long long tok = src / a.Hq;
+  const uint4 x = __ldcs(reinterpret_cast<const uint4*>(
+      static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride + (src - tok * a.Hq) * 128 + c * 8));
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(u[i] << 16 & 0x7fff0000u, u[i] & 0x7fff0000u));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool odd = top >= 0x7f800000u;  // an infinity or a NaN: the row's scores are NaN
+  const int e = q8::exponent(top);
+  const float f = odd ? 0.f : q8::power(-e);
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y0 = odd ? 0.f : __uint_as_float(u[i] << 16) * f;
+    const float y1 = odd ? 0.f : __uint_as_float(u[i] & 0xffff0000u) * f;
+    hi[i] = q8::pack2(y0, y1);
+    const float2 z = q8::unpack2(hi[i]);
+    lo[i] = q8::pack2(y0 - z.x, y1 - z.y);
+  }
+  if (row >= rows) return;
+  uint8_t* dst = terms + row * 256 + c * 8;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+  *reinterpret_cast<uint2*>(dst + 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  if (c == 0) scales[row] = odd ? __uint_as_float(0x7fc00000u) : q8::power(e);
+}
+
 }  // namespace
+
+size_t paged_query_terms(int total_T, int Hq) { return (size_t)total_T * Hq * (256 + sizeof(float)); }
+
+cudaError_t launch_query_terms(PagedArgs& a, void* terms, cudaStream_t st) {
+  const long long rows = (long long)a.total_T * a.Hq;
+  uint8_t* t = static_cast<uint8_t*>(terms);
+  float* scales = reinterpret_cast<float*>(t + rows * 256);
+  constexpr int per = kThreads / 16;
+  query_terms_kernel<<<(unsigned)((rows + per - 1) / per), kThreads, 0, st>>>(a, t, scales);
+  a.q = t;
+  a.q_stride = (long long)a.Hq * 128;
+  a.q_scale = scales;
+  return cudaGetLastError();
+}
 
 cudaError_t launch_cache_read(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
   return a.D == 32   ? launch_t<32>(a, bf16, st)

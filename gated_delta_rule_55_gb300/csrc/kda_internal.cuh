@@ -152,6 +152,7 @@ struct PagedArgs {
   const int32_t* prefix_lens;  // [groups]
   const int32_t* cu_groups;    // [groups + 1]
   int groups, max_prefix_pages;
+  const float* q_scale;        // [total_T, Hq]: queries as two e4m3 terms (set by the launcher)
   int G;                       // Hq / Hkv, and division by it (set by the tensor-core launcher)
   uint32_t g_mul, g_shift;
 };
@@ -170,11 +171,16 @@ cudaError_t launch_cache_read(const CacheReadArgs& a, bool bf16, cudaStream_t st
 bool paged_tc_index_ok(const PagedArgs& a);
 size_t paged_tc_workspace(int D);
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t stream);
-size_t paged_prefix_tc_workspace(int total_T, int Hq, int D);
+size_t paged_q8_tc_workspace(int total_T, int Hq, int D);
+size_t paged_prefix_tc_workspace(int total_T, int Hq, int D, bool q8);
 cudaError_t launch_paged_tc_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_q8_few(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
+// Queries of bf16 with D = 128 as two rows of e4m3 under a power of two each, for products with
+// keys in 8 bits: a.q and a.q_scale become them.  terms: paged_query_terms() bytes.
+size_t paged_query_terms(int total_T, int Hq);
+cudaError_t launch_query_terms(PagedArgs& a, void* terms, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
 unsigned int paged_q8_read_error(bool reset);
 unsigned int paged_q8_few_read_error(bool reset);

@@ -19,10 +19,15 @@ size_t paged_tc_workspace(int D) {
   return 8192 + (size_t)2 * kCtas * kRowsItem * (sizeof(float2) + D * sizeof(float));
 }
 
-// Every row's two results, where they are not cut, and where they are.
-size_t paged_prefix_tc_workspace(int total_T, int Hq, int D) {
-  return paged_tc_workspace(D) + (size_t)2 * total_T * Hq *
-                                     (sizeof(float2) + sizeof(int4) + D * sizeof(float));
+// Behind it: a query's terms (caches in 8 bits, D = 128), and every row's two results, where they
+// are not cut and where they are (prefixes).
+size_t paged_q8_tc_workspace(int total_T, int Hq, int D) {
+  return paged_tc_workspace(D) + (D == 128 ? paged_query_terms(total_T, Hq) : 0);
+}
+
+size_t paged_prefix_tc_workspace(int total_T, int Hq, int D, bool q8) {
+  return (q8 ? paged_q8_tc_workspace(total_T, Hq, D) : paged_tc_workspace(D)) +
+         (size_t)2 * total_T * Hq * (sizeof(float2) + sizeof(int4) + D * sizeof(float));
 }
 
 cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st) {
@@ -32,13 +37,12 @@ cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st
               : launch_paged_tc_prefix(a, workspace, st);
   if (q8 && a.D == 128 && (long long)a.total_T * (a.Hq / a.Hkv) <= 16ll * a.N)
     return launch_paged_tc_q8_few(a, workspace, st);
-  return q8 ? launch_paged_tc_q8(a, workspace, st) : launch_any<false, false>(a, workspace, st);
+  return q8 ? launch_paged_tc_q8(a, workspace, st) : launch_any<false, false>(a, workspace, nullptr, st);
 }
 
 unsigned int paged_read_error(bool reset) {
   return read_error(reset) | paged_q8_read_error(reset) | paged_q8_few_read_error(reset) |
-          paged_prefix_read_error(reset) |
-         paged_prefix_q8_read_error(reset);
+         paged_prefix_read_error(reset) | paged_prefix_q8_read_error(reset);
 }
 
 }  // namespace kda

@@ -5,7 +5,7 @@
 namespace kda {
 
 cudaError_t launch_paged_tc_prefix(const PagedArgs& a, void* workspace, cudaStream_t st) {
-  return launch_any<false, true>(a, workspace, st);
+  return launch_any<false, true>(a, workspace, nullptr, st);
 }
 
 unsigned int paged_prefix_read_error(bool reset) { return read_error(reset); }

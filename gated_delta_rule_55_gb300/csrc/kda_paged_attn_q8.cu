@@ -4,7 +4,8 @@
 namespace kda {
 
 cudaError_t launch_paged_tc_q8(const PagedArgs& a, void* workspace, cudaStream_t st) {
-  return launch_any<true, false>(a, workspace, st);
+  return launch_any<true, false>(a, workspace,
+                                 static_cast<uint8_t*>(workspace) + paged_tc_workspace(a.D), st);
 }
 
 unsigned int paged_q8_read_error(bool reset) { return read_error(reset); }

@@ -40,7 +40,7 @@ constexpr int kThreads = 384;  // softmax, expanders, and the warps below
 constexpr int kExpandWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
 // Registers: 80 a thread at launch, 3 x 80 = 104 + 72 + 64.
 constexpr int kRegsSoftmax = 104, kRegsExpand = 72, kRegsOther = 64;
-constexpr float kRescale = 8.0f;  // log2 growth of the maximum that O and l absorb
+constexpr float kRescale = 32.0f;  // log2 growth of the maximum that O and l absorb (kda_paged_tc.cuh)
 constexpr int kSteps = 4;         // items put down ahead
 
 constexpr int kFront = 5 * 1024;                  // barriers, the plan, scales
@@ -72,16 +72,6 @@ struct Small {
   alignas(16) float parts[2][4][kRowsItem];   // a warp's maxima, sums
 };
 static_assert(sizeof(Small) <= kFront, "front");
-
-// D[tmem] (+)= A[smem] * B[smem]^T of e4m3, issued by one thread.
-__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
   uint32_t r[N];

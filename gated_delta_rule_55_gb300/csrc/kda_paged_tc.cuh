@@ -88,16 +88,30 @@ template <bool Q8> struct Group {
 };
 // log2 growth of the maximum that O and l absorb.  (Rescaling only from some growth on, and two
 // softmax warpgroups beside two score tiles, are published ways for attention on this hardware.)
-constexpr float kRescale = 8.0f;
+// Weights, sums and O keep their relative precision whatever their size, so what bounds it is
+// overflow: 2^32 leaves values of 2^80 and 2^15 keys.  Keys of different magnitudes outgrow 2^8 in
+// some row of a warp every few tiles, and such a tile goes the long way: 2 chunks of 2048 tokens
+// behind 8192 keys in 8 bits whose magnitudes vary by e^0.7 took 1003 us.  Calls of bf16 pages
+// without prefixes keep the 2^8 that their results were made with.
+template <bool Q8, bool PRE> constexpr float kRescaleOf = Q8 || PRE ? 40.0f : 8.0f;
+// How far (log2) above the first 32 keys' maximum the standing one starts.
+template <bool Q8, bool PRE> constexpr float kAheadOf = Q8 || PRE ? 16.0f : 0.0f;
 
 template <int D, bool Q8> struct Cfg {
+  // 8 bits and D = 128: keys are products' operands as they land (kDirect), in a ring of their own;
+  // values land in the upper half of their stage and are expanded where they are.  Otherwise all
+  // tiles are in one ring, and those in 8 bits land in another one.
+  static constexpr bool kDirect = Q8 && D == 128;
   // What lies before the tiles: m and l of both units' rows (2 KB), barriers, the plan; 8 bits:
   // the scales of the tiles that have landed.
   static constexpr int kFront = (Q8 ? 4 : 3) * 1024;
   static constexpr int kStageBytes = kKeys * D * 2;
-  static constexpr int kStages = Q8 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 8;
+  static constexpr int kStages = kDirect ? 3 : Q8 ? 6 : D == 128 ? 5 : 8;  // (direct: of each)
+  static constexpr int kBars = kDirect ? 2 * kStages : kStages;
+  // A direct stage of keys: the tile, and the scales as fp32.
+  static constexpr int kKeyBytes = kDirect ? kKeys * D + kKeys * 4 : 0;
   // Tiles in 8 bits, as they land.
-  static constexpr int kRawStages = Q8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kRawStages = kDirect ? 6 : Q8 ? 6 : 0;
   static constexpr int kRawBytes = kKeys * D;
   static constexpr int kQBytes = kRowsUnit * D * 2;
   // Rows in shared memory: blocks of up to 64 columns, swizzled over their bytes.
@@ -106,8 +120,8 @@ template <int D, bool Q8> struct Cfg {
   // D <= 64 leaves Tensor Memory for weights of their own (D = 128 keeps them over the scores):
   // the next scores are then made while the softmax of the last is still running.
   static constexpr bool kOwnP = D <= 64;
-  static constexpr int kSmem =
-      kFront + 2 * kQBytes + kStages * kStageBytes + kRawStages * kRawBytes;
+  static constexpr int kSmem = kFront + 2 * kQBytes + kStages * kStageBytes +
+                               (kDirect ? kStages * kKeyBytes : kRawStages * kRawBytes);
 };
 
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
@@ -177,6 +191,9 @@ struct Order {
     if (kind == kWide) return e / 2;
     return e == 0 ? 0 : e == 2 * n - 1 ? n - 1 : e & 1 ? (e + 1) / 2 : e / 2 - 1;
   }
+  __device__ __forceinline__ bool is_key(int e) const {
+    return kind == kWide ? !(e & 1) : e == 0 || ((e & 1) && e != 2 * n - 1);
+  }
   // The unit that uses entry e (not wide: both do).
   __device__ __forceinline__ int owner(int e) const { return unit(tile_of(e)); }
 };
@@ -210,16 +227,35 @@ __device__ __forceinline__ void tmem_wait_st() {
 
 template <bool B> struct Bool { static constexpr bool value = B; };
 
+// 32 scores times their keys' scales.
+__device__ __forceinline__ void scale32(uint32_t (&s)[32], const float* c) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(c + e);
+    float x[4];
+    unpack2(mul2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f.x), x[0], x[1]);
+    unpack2(mul2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), f.y), x[2], x[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[e + i] = __float_as_uint(x[i]);
+  }
+}
+
 // Softmax weights of 32 scores: p = 2^(s sc + nb), packed to bf16; their sum (in fp32, before the
-// rounding) and the largest score, started or carried on.
-__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float sc, float nb, uint32_t* p,
-                                          float& sum, float& top, bool start) {
+// rounding) and the largest score, started or carried on.  SC: scores times their keys' scales c.
+template <bool SC>
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], const float* c, float sc, float nb,
+                                          uint32_t* p, float& sum, float& top, bool start) {
   const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(nb, nb);
   uint64_t acc[4] = {0, 0, 0, 0};
   float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  ulonglong2 f{};
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const float s0 = __uint_as_float(s[2 * e]), s1 = __uint_as_float(s[2 * e + 1]);
+    float s0 = __uint_as_float(s[2 * e]), s1 = __uint_as_float(s[2 * e + 1]);
+    if constexpr (SC) {
+      if (e % 2 == 0) f = *reinterpret_cast<const ulonglong2*>(c + 2 * e);
+      unpack2(mul2(pack2(s0, s1), e % 2 ? f.y : f.x), s0, s1);
+    }
     c4[e & 3] = max3(c4[e & 3], s0, s1);
     float x, y;
     unpack2(fma2(pack2(s0, s1), sc2, nb2), x, y);
@@ -254,6 +290,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
   using C = Cfg<D, Q8>;
   constexpr int NS = C::kStages, RB = C::kRowBytes, HALVES = D * 2 / RB;
   constexpr int NL = Q8 ? C::kRawStages : NS;  // stages of the ring that tiles land in
+  constexpr bool KD = C::kDirect;
+  constexpr float kRescale = kRescaleOf<Q8, PRE>, kAhead = kAheadOf<Q8, PRE>;
   constexpr int kThreads = Group<Q8>::kThreads, kFront = C::kFront;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   float2* s_ml = reinterpret_cast<float2*>(smem_raw);  // [2][128]: m, l of the units' rows
@@ -262,7 +300,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     Plan plan;
     Step steps[kSteps];
     uint32_t tmem;
-    alignas(16) uint8_t scales[Q8 ? C::kRawStages * kKeys : 16];  // of the tiles in 8 bits
+    alignas(16) uint8_t scales[Q8 ? NL * kKeys : 16];  // of the tiles in 8 bits
   };
   static_assert(2048 + sizeof(Small) <= kFront, "front");
   Small& small = *reinterpret_cast<Small*>(smem_raw + 2048);
@@ -271,7 +309,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
   uint32_t& s_tmem = small.tmem;
   uint8_t* sQ = smem_raw + kFront;           // two 128-row tiles
   uint8_t* sKV = sQ + 2 * C::kQBytes;        // the ring
-  uint8_t* sRaw = sKV + NS * C::kStageBytes;  // and that of tiles in 8 bits
+  uint8_t* sRaw = sKV + NS * C::kStageBytes;  // and that of tiles in 8 bits; or that of keys,
+  float* sKeyScale = reinterpret_cast<float*>(sRaw + NS * C::kRawBytes);  // [NS][128] (direct)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMmaWarp) tmem_alloc(&s_tmem, kTmemCols);
@@ -281,7 +320,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     tma_prefetch_desc(&vmap);
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < C::kBars; ++i) {
       mbar_init(&bars.kv_full[i], Q8 ? 4 : 1);
       mbar_init(&bars.kv_empty[i], 2);  // both units let an entry go
     }
@@ -328,6 +367,24 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     if (lane == 0) mbar_arrive(&bars.step_empty[j % kSteps]);
   };
 
+  // Barrier (and stage) and phase of a tile's keys and values, `pos` entries before its step.  (Direct:
+  // stages of keys, then of values.)
+  struct Place {
+    uint32_t at, phase;
+  };
+  auto ring = [](uint32_t i, uint32_t first) {
+    return Place{first + i % NS, (i / NS) & 1};
+  };
+  auto key_place = [&](const Order& o, uint32_t pos, int t) {
+    return KD ? ring(pos / 2 + t, 0) : ring(pos + o.key(t), 0);
+  };
+  auto value_place = [&](const Order& o, uint32_t pos, int t) {
+    return KD ? ring(pos / 2 + t, NS) : ring(pos + o.value(t), 0);
+  };
+  auto entry_place = [&](const Order& o, uint32_t pos, int e) {
+    return KD ? ring(pos / 2 + o.tile_of(e), o.is_key(e) ? 0 : NS) : ring(pos + e, 0);
+  };
+
   if (Q8 && warp >= kExpandWarp) {
     if constexpr (Q8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Group<Q8>::kRegsExpand));
@@ -338,43 +395,60 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     for (uint32_t j = 0;; ++j) {
       const Step* st = step(j);
       if (!st) break;
-      const int n = 2 * Order(*st).n;
+      const Order o(*st);
+      const int n = 2 * o.n;
 #pragma unroll 1
-      for (int e = 0; e < n; ++e, ++pos) {
-        const uint32_t from = pos % NL, to = pos % NS;
-        wait_or_die(&bars.raw_full[from], (pos / NL) & 1, dead);
-        const q8::Scale16 sc(small.scales[from * kKeys + r]);
-        uint4 w[D / 16];
-        const uint8_t* src = sRaw + from * C::kRawBytes;
+      for (int e = 0; e < n; ++e) {
+        const Place to = entry_place(o, pos, e);
+        const Place from = KD ? to : Place{(pos + e) % NL, ((pos + e) / NL) & 1};
+        wait_or_die(&bars.raw_full[from.at], from.phase, dead);
+        const uint32_t byte = small.scales[from.at * kKeys + r];
+        if (KD && o.is_key(e)) {
+          sKeyScale[to.at * kKeys + r] = q8::scale(byte);
+        } else {
+          const q8::Scale16 sc(byte);
+          uint8_t* dst = sKV + (KD ? to.at - NS : to.at) * C::kStageBytes;
+          const uint8_t* src = KD ? dst + C::kRawBytes : sRaw + from.at * C::kRawBytes;
+          uint4 w[D / 16];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          w[c] = *reinterpret_cast<const uint4*>(src + raw_offset<D>(r, c));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.raw_empty[from]);
-        wait_or_die(&bars.kv_empty[to], ((pos / NS) & 1) ^ 1, dead);
-        uint8_t* dst = sKV + to * C::kStageBytes;
-        auto put = [&](auto big) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t y[8];
-            q8::expand4_in_order<decltype(big)::value>(w[c].x, sc, y[0], y[1]);
-            q8::expand4_in_order<decltype(big)::value>(w[c].y, sc, y[2], y[3]);
-            q8::expand4_in_order<decltype(big)::value>(w[c].z, sc, y[4], y[5]);
-            q8::expand4_in_order<decltype(big)::value>(w[c].w, sc, y[6], y[7]);
-            *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c)) =
-                make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c + 1)) =
-                make_uint4(y[4], y[5], y[6], y[7]);
+          for (int c = 0; c < D / 16; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(src + raw_offset<D>(r, c));
+          if (!KD) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.raw_empty[from.at]);
+            wait_or_die(&bars.kv_empty[to.at], to.phase ^ 1, dead);
           }
-        };
-        if (__any_sync(0xffffffffu, sc.big))
-          put(Bool<true>{});
-        else
-          put(Bool<false>{});
-        fence_async_smem();
+          auto put = [&](auto big) {
+            constexpr bool B = decltype(big)::value;
+            auto four = [&](uint32_t x, uint32_t& lo, uint32_t& hi) {
+              if (KD)  // (values: their columns change places)
+                q8::expand4<B>(x, sc, lo, hi);
+              else
+                q8::expand4_in_order<B>(x, sc, lo, hi);
+            };
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[8];
+              four(w[c].x, y[0], y[1]);
+              four(w[c].y, y[2], y[3]);
+              four(w[c].z, y[4], y[5]);
+              four(w[c].w, y[6], y[7]);
+              *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c)) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c + 1)) =
+                  make_uint4(y[4], y[5], y[6], y[7]);
+            }
+          };
+          if (__any_sync(0xffffffffu, sc.big))
+            put(Bool<true>{});
+          else
+            put(Bool<false>{});
+          fence_async_smem();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.kv_full[to]);
+        if (lane == 0) mbar_arrive(&bars.kv_full[to.at]);
       }
+      pos += n;
       step_done(j);
     }
     }
@@ -385,8 +459,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       // Lane 8 x + p looks up and copies page p of the tiles x, x + 4, ..., four tiles ahead.
       const int quarter = lane >> 3, pi = lane & 7;
       uint64_t *const landed = Q8 ? bars.raw_full : bars.kv_full;
-      uint64_t *const gone = Q8 ? bars.raw_empty : bars.kv_empty;
+      uint64_t *const gone = Q8 && !KD ? bars.raw_empty : bars.kv_empty;
       uint32_t pos = 0, sg = 0, ph = 0;  // entries pushed, the next one's stage and phase
+      uint32_t keys_pushed = 0;
       for (uint32_t j = 0;; ++j) {
         const Step* st = step(j);
         if (!st) break;
@@ -419,6 +494,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         look_up(quarter);
         settle();
         const bool wide = o.kind == kWide;
+        const uint32_t base = pos;
 #pragma unroll 1
         for (int t = -1; t < o.n; ++t) {
 #pragma unroll
@@ -426,31 +502,38 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             const bool keys = (z == 0) != wide;  // the next tile's; or this tile's values
             const int y = keys ? t + 1 : t;
             if (y < 0 || y >= o.n) continue;
-            wait_or_die(&gone[sg], ph ^ 1, dead);
+            const Place at = !KD    ? Place{sg, ph}
+                             : keys ? key_place(o, base, y)
+                                    : value_place(o, base, y);
+            wait_or_die(&gone[at.at], at.phase ^ 1, dead);
             const bool mine = (y & 3) == quarter && row >= 0;
             const unsigned need = __ballot_sync(0xffffffffu, mine);
-            uint64_t* bar = &landed[sg];
+            uint64_t* bar = &landed[at.at];
             if (lane == 0)
               mbar_arrive_expect_tx(bar, uint32_t(__popc(need)) *
                                              uint32_t(Q8 ? ps * (D + 1) : HALVES * ps * RB));
             __syncwarp();
             if (Q8 && mine && !dead) {
-              tma_load_2d(sRaw + sg * C::kRawBytes + pi * ps * D, keys ? &kmap : &vmap, bar, 0, row);
-              bulk_load(small.scales + sg * kKeys + pi * ps,
+              uint8_t* dst = KD && !keys
+                                 ? sKV + (at.at - NS) * C::kStageBytes + C::kRawBytes
+                                 : sRaw + at.at * C::kRawBytes;
+              tma_load_2d(dst + pi * ps * D, keys ? &kmap : &vmap, bar, 0, row);
+              bulk_load(small.scales + at.at * kKeys + pi * ps,
                         (keys ? a.k_scale : a.v_scale) + row, ps, bar);
             }
             if (!Q8 && mine && !dead) {
-              uint8_t* dst = sKV + sg * C::kStageBytes + pi * ps * RB;
+              uint8_t* dst = sKV + at.at * C::kStageBytes + pi * ps * RB;
 #pragma unroll
               for (int hf = 0; hf < HALVES; ++hf)
                 tma_load_2d(dst + hf * (kKeys * RB), keys ? &kmap : &vmap, bar, hf * 64, row);
             }
             __syncwarp();
-            if (++sg == NL) {
+            if (!KD && ++sg == NL) {
               sg = 0;
               ph ^= 1;
             }
             ++pos;
+            if (keys) ++keys_pushed;
           }
           if (t >= 0) {
             settle();
@@ -461,7 +544,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         step_done(j);
       }
       // leave no copy in flight behind a give-up
-      if (dead)
+      if (dead && KD)
+        for (uint32_t v = 0; v < 2; ++v)
+          for (uint32_t end = v ? pos - keys_pushed : keys_pushed, i = end > NS ? end - NS : 0;
+               i < end; ++i)
+            mbar_wait(&landed[v * NS + i % NS], (i / NS) & 1, 100000000ull);
+      if (dead && !KD)
         for (uint32_t i = pos > NL ? pos - NL : 0; i < pos; ++i)
           mbar_wait(&landed[i % NL], (i / NL) & 1, 100000000ull);
     } else if (warp < kQueryWarp) {
@@ -470,28 +558,42 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       // are made warp-uniform before the issuing branch: from values of one lane, eight
       // products took 800 to 1200 cycles to issue, twice their run time.
       const int u = warp - kMmaWarp;
-      const uint32_t idesc_s = make_idesc(1, 128, kKeys);
+      const uint32_t idesc_s = make_idesc(KD ? 0 : 1, 128, kKeys);
       const uint32_t idesc_o = make_idesc(1, 128, D, false, true);
       const uint32_t tmu = __shfl_sync(0xffffffffu, tm + 128 * u, 0);
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
       const bool leader = elect_one();
       uint32_t pos = 0, seen = 0, np = 0, items = 0, wides = 0, turns = 0, nscores = 0;
-      // Ring entries up to `at` have landed.  Every entry is waited for in turn, and the other
-      // unit's are let go at once: a stage is refilled only when both units have passed it, so
-      // no barrier is ever more than the one phase away that a parity can tell.
-      auto ready = [&](uint32_t at, const Order& o) {
-        for (; (int)(at - seen) >= 0; ++seen) {
-          wait_or_die(&bars.kv_full[seen % NS], (seen / NS) & 1, dead);
-          if (o.kind != kWide && o.owner((int)(seen - pos)) != u && leader)
-            mbar_arrive(&bars.kv_empty[seen % NS]);
+      uint32_t k_last = 0;  // stage of the last scores' keys
+      // Ring entries up to number e of the step have landed.  Every entry is waited for in turn, and
+      // the other unit's are let go at once: a stage is refilled only when both units have passed
+      // it, so no barrier is ever more than the one phase away that a parity can tell.
+      auto ready = [&](int e, const Order& o) {
+        for (; (int)(pos + e - seen) >= 0; ++seen) {
+          const int x = (int)(seen - pos);
+          const Place at = entry_place(o, pos, x);
+          wait_or_die(&bars.kv_full[at.at], at.phase, dead);
+          if (o.kind != kWide && o.owner(x) != u && leader) mbar_arrive(&bars.kv_empty[at.at]);
         }
       };
-      auto stage = [&](uint32_t at) {
-        return __shfl_sync(0xffffffffu, kv0 + at % NS * C::kStageBytes, 0);
+      auto key_stage = [&](const Place& p) {
+        return __shfl_sync(0xffffffffu,
+                           KD ? smem_u32(sRaw) + p.at * C::kRawBytes : kv0 + p.at * C::kStageBytes,
+                           0);
+      };
+      auto value_stage = [&](const Place& p) {
+        return __shfl_sync(0xffffffffu, kv0 + (KD ? p.at - NS : p.at) * C::kStageBytes, 0);
       };
       auto scores = [&](uint32_t q, uint32_t k) {  // S = Q K^T
         const uint64_t kd = make_sdesc(k, 16, 8 * RB, C::kSwizzle);
         const uint64_t qd = make_sdesc(q, 16, 8 * RB, C::kSwizzle);
+        if constexpr (KD) {  // the queries' two terms, in the halves of their tile
+#pragma unroll
+          for (int s = 0; s < 2 * (D / 32); ++s)
+            mma_ss_f8(tmu + kColS, qd + (s / 4) * (kRowsUnit * 128 / 16) + (s % 4) * 2,
+                      kd + (s % 4) * 2, idesc_s, s > 0);
+          return;
+        }
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           // the K step's 32 bytes, in 16-byte units; 64-column blocks are 16 KB apart
@@ -535,15 +637,17 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         wides += !split;
         if (first < n) {
           // the first scores
-          const uint32_t k_at = pos + o.key(o.tile(u, first));
-          ready(k_at, o);
+          const int t = o.tile(u, first);
+          const Place k_at = key_place(o, pos, t);
+          ready((int)o.key(t), o);
           scores_free();
           tc_fence_after();
-          const uint32_t k = stage(k_at);
+          const uint32_t k = key_stage(k_at);
+          k_last = k_at.at;
           if (leader) {
             if (!dead) scores(q, k);
             mma_commit(&bars.s_full[u]);
-            mma_commit(&bars.kv_empty[k_at % NS]);
+            if (!KD) mma_commit(&bars.kv_empty[k_at.at]);
             if (first + by >= n) {
               mma_commit(&bars.q_empty[tile]);
               if (tile) mma_commit(&bars.q_empty[tile]);
@@ -556,12 +660,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         // a tile's values, then the unit's next scores
         for (int i = first; i < n; i += by) {
           const bool more = i + by < n;
-          const uint32_t v_at = pos + o.value(o.tile(u, i));
-          const uint32_t k_at = pos + o.key(o.tile(u, i + by));
+          const int t = o.tile(u, i), t1 = o.tile(u, i + by);
+          const Place v_at = value_place(o, pos, t), k_at = key_place(o, pos, t1);
+          const int v_e = (int)o.value(t), k_e = (int)o.key(t1);
           auto next_scores = [&](uint32_t k) {  // by the leader
             if (!dead) scores(q, k);
             mma_commit(&bars.s_full[u]);
-            mma_commit(&bars.kv_empty[k_at % NS]);
+            mma_commit(&bars.kv_empty[k_at.at]);
             if (i + 2 * by >= n) {
               mma_commit(&bars.q_empty[tile]);
               if (tile) mma_commit(&bars.q_empty[tile]);
@@ -569,28 +674,28 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           };
           if constexpr (C::kOwnP) {
             if (more) {
-              ready(k_at, o);
+              ready(k_e, o);
               scores_free();
               tc_fence_after();
-              const uint32_t k = stage(k_at);
+              const uint32_t k = key_stage(k_at);
               if (leader) next_scores(k);
               __syncwarp();
             }
-            ready(v_at, o);
-            const uint32_t v = stage(v_at);
+            ready(v_e, o);
+            const uint32_t v = value_stage(v_at);
             wait_or_die(&bars.p_full[u], np & 1, dead);
             ++np;
             tc_fence_after();
             if (leader) {
               if (!dead) values(v, i == first, true, true);
               mma_commit(&bars.o_full[u]);
-              mma_commit(&bars.kv_empty[v_at % NS]);
+              mma_commit(&bars.kv_empty[v_at.at]);
             }
             __syncwarp();
           } else {
-            ready(v_at, o);
-            if (more) ready(k_at, o);
-            const uint32_t v = stage(v_at), k = stage(k_at);
+            ready(v_e, o);
+            if (more) ready(k_e, o);
+            const uint32_t v = value_stage(v_at), k = key_stage(k_at);
             // the lower half of the keys' weights comes first
             wait_or_die(&bars.ph_full[u], np & 1, dead);
             // A wide item's units take turns: interleaved, both would get their scores late and
@@ -616,17 +721,20 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               }
               if (kind == kWide) mbar_arrive(&bars.turn[u ^ 1]);
               mma_commit(more ? &bars.s_full[u] : &bars.o_full[u]);
-              mma_commit(&bars.kv_empty[v_at % NS]);
-              if (more) mma_commit(&bars.kv_empty[k_at % NS]);
+              mma_commit(&bars.kv_empty[v_at.at]);
+              // (direct keys: their scales were in use until the weights were there)
+              if (KD) mma_commit(&bars.kv_empty[k_last]);
+              if (!KD && more) mma_commit(&bars.kv_empty[k_at.at]);
               if (more && i + 2 * by >= n) {
                 mma_commit(&bars.q_empty[tile]);
                 if (tile) mma_commit(&bars.q_empty[tile]);
               }
             }
             __syncwarp();
+            k_last = k_at.at;
           }
         }
-        ready(pos + 2 * o.n - 1, o);
+        ready(2 * o.n - 1, o);
         pos += 2 * o.n;
         step_done(j);
       }
@@ -733,7 +841,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     const uint32_t tS = tm + kColS + 128 * u + lanebits, tO = tm + kColO + 128 * u + lanebits;
     const uint32_t tO0 = tm + kColO + lanebits, tO1 = tO0 + 128;
     const uint32_t tP = C::kOwnP ? tm + kColP64 + 128 * u + lanebits : tS;
-    const float sc = a.scale * kLog2E;
+    float sc = a.scale * kLog2E;
     uint32_t pos = 0, ns = 0, no = 0, joins = 0;
     auto join = [&]() {  // all softmax warps
       __syncwarp();
@@ -755,6 +863,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const int tk = div_g(a, row);
 
       // 1. The unit's tiles.
+      if (KD)  // the power of two of the row's terms
+        sc = a.scale * kLog2E *
+             __ldg(a.q_scale + (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G));
       float m = -INFINITY, l = 0.f;
       int mine = 0;
       // (a prefix is seen to its last key by all)
@@ -764,10 +875,26 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const int pos_last = limit(w.pos0 + div_g(a, w.g.row0 + base + nr - 1));
       for (int i = split ? u : 0; i < n; i += split ? 2 : 1) {
         const int ks = tile_start(w.g, w.v0 + i);
+        const int tile = order.tile(u, i);
+        const float* cols = nullptr;
+        if (KD) {
+          const Place at = key_place(order, pos, tile);
+          wait_or_die(&bars.kv_full[at.at], at.phase, dead);  // (written by the expanders)
+          cols = sKeyScale + at.at * kKeys;
+        }
         wait_or_die(&bars.s_full[u], ns & 1, dead);
         ++ns;
         tc_fence_after();
         bool halves = false;  // the lower half of the weights has been handed over
+        // Scores from column c on, waited for, times the keys' scales.
+        auto finish = [&](uint32_t(&s)[32], int c) {
+          tmem_ld32_finish(s);
+          if (KD) scale32(s, cols + c);
+        };
+        auto weights = [&](const uint32_t(&s)[32], int c, float nb, uint32_t* p, float& sum,
+                           float& top, bool start) {
+          weights32<KD>(s, cols + c, sc, nb, p, sum, top, start);
+        };
         // The scores are in the warp's registers (or it has no rows): the next may come.
         auto scores_read = [&]() {
           if (C::kOwnP) {
@@ -817,13 +944,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             // no maximum yet: that of the first 32 keys
             uint32_t s[32];
             tmem_ld32_start(tS, s);
-            tmem_ld32_finish(s);
+            finish(s, 0);
             float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < 32; c += 2)
               c4[c / 2 & 3] =
                   max3(c4[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             m = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
+            if (kAhead > 0.f) m += kAhead / sc;
           }
           if (!C::kOwnP && whole) {
             // Weights against the maximum so far, which almost always stands, while the
@@ -838,10 +966,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             tmem_ld32_start(tS, s[0]);
             tmem_ld32_finish(s[0]);
             tmem_ld32_start(tS + 32, s[1]);
-            weights32(s[0], sc, nb, p, sum, top, true);
+            weights(s[0], 0, nb, p, sum, top, true);
             tmem_ld32_finish(s[1]);
             tmem_ld32_start(tS + 64, s[0]);
-            weights32(s[1], sc, nb, p + 16, sum, top, false);
+            weights(s[1], 32, nb, p + 16, sum, top, false);
             done = !__any_sync(0xffffffffu, outgrown());
             if (done) {
               tmem_st32_nowait(tP, p);
@@ -854,9 +982,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             tmem_ld32_finish(s[0]);
             if (done) {
               tmem_ld32_start(tS + 96, s[1]);
-              weights32(s[0], sc, nb, p, sum, top, true);
+              weights(s[0], 64, nb, p, sum, top, true);
               tmem_ld32_finish(s[1]);
-              weights32(s[1], sc, nb, p + 16, sum, top, false);
+              weights(s[1], 96, nb, p + 16, sum, top, false);
               if (__any_sync(0xffffffffu, outgrown())) {
                 // The upper half has outgrown the range: once the lower half's product is in O,
                 // O and l are scaled down and the upper half's weights made again.
@@ -867,8 +995,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 const float nb2 = m == -INFINITY ? 0.f : -m * sc;
                 tmem_ld32_start(tS + 64, s[0]);
                 tmem_ld32_finish(s[0]);
-                weights32(s[0], sc, nb2, p, sum, top, true);
-                weights32(s[1], sc, nb2, p + 16, sum, top, false);
+                weights(s[0], 64, nb2, p, sum, top, true);
+                weights(s[1], 96, nb2, p + 16, sum, top, false);
               }
               tmem_st32_nowait(tP + 32, p);
               l += sum;
@@ -883,15 +1011,15 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             tmem_ld32_start(tS, s[0]);
             tmem_ld32_finish(s[0]);
             tmem_ld32_start(tS + 32, s[1]);
-            weights32(s[0], sc, nb, p[0], sum, top, true);
+            weights(s[0], 0, nb, p[0], sum, top, true);
             tmem_ld32_finish(s[1]);
             tmem_ld32_start(tS + 64, s[0]);
-            weights32(s[1], sc, nb, p[0] + 16, sum, top, false);
+            weights(s[1], 0, nb, p[0] + 16, sum, top, false);
             tmem_ld32_finish(s[0]);
             tmem_ld32_start(tS + 96, s[1]);
-            weights32(s[0], sc, nb, p[1], sum, top, false);
+            weights(s[0], 0, nb, p[1], sum, top, false);
             tmem_ld32_finish(s[1]);
-            weights32(s[1], sc, nb, p[1] + 16, sum, top, false);
+            weights(s[1], 0, nb, p[1] + 16, sum, top, false);
             done = !__any_sync(0xffffffffu, r < nr && top > m && (top - m) * sc > kRescale);
             if (done) {
               scores_read();
@@ -940,7 +1068,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             auto weigh = [&](const uint32_t(&s)[32], int q) {
               uint32_t p[16];
               float sum, top;
-              weights32(s, sc, nb, p, sum, top, true);
+              weights32<false>(s, nullptr, sc, nb, p, sum, top, true);
               l += sum;
               tmem_st16_nowait(tP + 16 * q, p);
             };
@@ -968,7 +1096,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll 1
               for (int q = 0; q < 4; ++q) {
                 tmem_ld32_start(tS + 32 * q, s);
-                tmem_ld32_finish(s);
+                finish(s, 32 * q);
                 if (!whole) mask(s, q);
                 largest(s);
               }
@@ -976,7 +1104,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll 1
               for (int q = 0; q < 4; ++q) {
                 tmem_ld32_start(tS + 32 * q, s);
-                tmem_ld32_finish(s);
+                finish(s, 32 * q);
                 if (q == 3) scores_read();
                 if (!whole) mask(s, q);
                 weigh(s, q);
@@ -989,11 +1117,11 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         // scores: the products before them have used every earlier entry of the ring, so the
         // value stage's barrier is in the phase that is waited for.
         if (ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks)) {
-          const uint32_t at = pos + order.value(order.tile(u, i));
-          wait_or_die(&bars.kv_full[at % NS], (at / NS) & 1, dead);
+          const Place at = value_place(order, pos, tile);
+          wait_or_die(&bars.kv_full[at.at], at.phase, dead);
           const int key = ks + r;
           if (key >= w.g.kr.hi || (key < w.g.kr.lo && key >= w.g.kr.sinks)) {
-            uint8_t* vrow = sKV + (at % NS) * C::kStageBytes + r * RB;
+            uint8_t* vrow = sKV + (KD ? at.at - NS : at.at) * C::kStageBytes + r * RB;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
@@ -1064,6 +1192,13 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
           }
           if (!valid) continue;
+          if (KD) {  // (the expanded values' order)
+            uint32_t x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = o[q8::place(e)];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = x[e];
+          }
           if (PRE || cut0 || cut1) {
             float* dst = PRE && !cut0 && !cut1 ? rows.o + side * D : part_o + prow * D;
 #pragma unroll
@@ -1200,9 +1335,13 @@ bool query_map(CUtensorMap* map, const PagedArgs& a) {
 }
 
 template <int D, bool Q8, bool PRE>
-cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
+cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream_t st) {
   set_divisor(a);
   const uint32_t G = (uint32_t)a.G;
+  if constexpr (Cfg<D, Q8>::kDirect) {
+    const cudaError_t e = launch_query_terms(a, query_terms, st);
+    if (e != cudaSuccess) return e;
+  }
   CUtensorMap qmap{}, kmap{}, vmap{};
   // Rows by TMA where the items are large: a call with one token for each of its sequences has
   // a few rows in each, which are copied one by one.
@@ -1250,11 +1389,12 @@ cudaError_t launch_t(PagedArgs a, void* workspace, cudaStream_t st) {
                             (const float2*)ml);
 }
 
+// query_terms: 8 bits and D = 128, room for paged_query_terms() bytes.
 template <bool Q8, bool PRE>
-cudaError_t launch_any(const PagedArgs& a, void* workspace, cudaStream_t st) {
-  return a.D == 32   ? launch_t<32, Q8, PRE>(a, workspace, st)
-         : a.D == 64 ? launch_t<64, Q8, PRE>(a, workspace, st)
-                     : launch_t<128, Q8, PRE>(a, workspace, st);
+cudaError_t launch_any(const PagedArgs& a, void* workspace, void* query_terms, cudaStream_t st) {
+  return a.D == 32   ? launch_t<32, Q8, PRE>(a, workspace, query_terms, st)
+         : a.D == 64 ? launch_t<64, Q8, PRE>(a, workspace, query_terms, st)
+                     : launch_t<128, Q8, PRE>(a, workspace, query_terms, st);
 }
 
 static_assert(sizeof(Header) * kCtas <= 8192, "headers");

@@ -131,8 +131,10 @@ int run_paged(kda::PagedArgs a, int dtype, void* workspace, size_t workspace_byt
   if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;
   const size_t need = !work                ? 0
                       : dtype == KDA_F32   ? kda::paged_simt_need(a)
-                      : a.groups > 0       ? kda::paged_prefix_tc_workspace(a.total_T, a.Hq, a.D)
-                                           : kda::paged_tc_workspace(a.D);
+                      : a.groups > 0
+                          ? kda::paged_prefix_tc_workspace(a.total_T, a.Hq, a.D, a.k_scale)
+                      : a.k_scale ? kda::paged_q8_tc_workspace(a.total_T, a.Hq, a.D)
+                                  : kda::paged_tc_workspace(a.D);
   if (need > 0 && (!workspace || !aligned256(workspace) || workspace_bytes < need))
     return KDA_ERR_WORKSPACE;
   const int s = kda::check_current_device();
@@ -364,6 +366,13 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
   return run_paged(a, dtype, workspace, workspace_bytes, stream);
 }
 
+size_t kda_paged_attention_q8_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
+                                                 int dtype) {
+  if (!paged_shape_ok(N, total_T, Hq, Hkv, D, dtype)) return 0;
+  return dtype == KDA_BF16 ? kda::paged_q8_tc_workspace(total_T, Hq, D)
+                           : kda::paged_simt_workspace(total_T, Hq, D, false);
+}
+
 int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const void* v_cache,
                                const uint8_t* k_scale, const uint8_t* v_scale,
                                const int32_t* block_table, const int32_t* cu_seqlens,
@@ -392,8 +401,8 @@ size_t kda_paged_prefix_attention_fwd_workspace_size(int num_groups, int N, int 
                                                      int Hkv, int D, int dtype) {
   if (num_groups < 0 || !paged_shape_ok(N, total_T, Hq, Hkv, D, dtype)) return 0;
   if (dtype == KDA_F32) return kda::paged_simt_workspace(total_T, Hq, D, num_groups > 0);
-  return num_groups > 0 ? kda::paged_prefix_tc_workspace(total_T, Hq, D)
-                        : kda::paged_tc_workspace(D);
+  return num_groups > 0 ? kda::paged_prefix_tc_workspace(total_T, Hq, D, true)
+                        : kda::paged_q8_tc_workspace(total_T, Hq, D);
 }
 
 int kda_paged_prefix_attention_fwd(const void* query, const void* k_cache, const void* v_cache,

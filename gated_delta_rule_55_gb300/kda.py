@@ -36,7 +36,8 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_fwd_workspace_siz
            "kda_qk_norm_rope_append", "kda_qk_norm_rope_bwd_workspace_size",
            "kda_qk_norm_rope_bwd", "kda_paged_attention_fwd_workspace_size",
            "kda_paged_attention_fwd", "kda_qk_norm_rope_append_q8", "kda_paged_cache_read_q8",
-           "kda_paged_attention_q8_fwd", "kda_paged_prefix_attention_fwd_workspace_size",
+           "kda_paged_attention_q8_fwd_workspace_size", "kda_paged_attention_q8_fwd",
+           "kda_paged_prefix_attention_fwd_workspace_size",
            "kda_paged_prefix_attention_fwd",
            "kda_status_string",
            "kda_version", "kda_device_error", "kda_selftest_bounded_wait")
@@ -119,6 +120,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     L.kda_qk_norm_rope_append_q8.argtypes = ([_P] * 14 + [_F] + [_I] * 8 + [_LL] * 3 +
                                              [_I, _I, _P])
     L.kda_paged_cache_read_q8.argtypes = [_P] * 7 + [_I] * 6 + [_P]
+    L.kda_paged_attention_q8_fwd_workspace_size.argtypes = [_I] * 6
+    L.kda_paged_attention_q8_fwd_workspace_size.restype = _Z
     L.kda_paged_attention_q8_fwd.argtypes = ([_P] * 10 + [_F] + [_I] * 10 +
                                              [_LL, _I, _P, _Z, _P])
     L.kda_paged_prefix_attention_fwd_workspace_size.argtypes = [_I] * 7
@@ -681,6 +684,11 @@ def kda_paged_cache_read_q8(k_cache, v_cache, k_scale, v_scale, slots, key_out, 
                [e4m3, e4m3, u8, u8, _Call.i64, el, el], dev,
                "k_cache v_cache k_scale v_scale slots key_out value_out"), T, Hkv, D, num_pages,
         page_size, code, st))
+
+
+def kda_paged_attention_q8_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype=KDA_BF16) -> int:
+    """Bytes of workspace kda_paged_attention_q8_fwd needs (0: none; see include/kda.h)."""
+    return int(lib().kda_paged_attention_q8_fwd_workspace_size(N, total_T, Hq, Hkv, D, dtype))
 
 
 def kda_paged_attention_q8_fwd(query, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,

@@ -657,8 +657,13 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   v_scale [num_pages, Hkv, page_size].  query and out stay in dtype.  Rows are expanded exactly,
  *   so the result is that of kda_paged_attention_fwd over the values that the cache stands for; a
  *   seen row with b = 255 makes what sees it NaN.  All other arguments, limits and errors are those
- *   of kda_paged_attention_fwd, as is the workspace (kda_paged_attention_fwd_workspace_size).
+ *   of kda_paged_attention_fwd; the workspace's size is kda_paged_attention_q8_fwd_workspace_size's,
+ *   which never decreases as N or total_T grows.  bf16 with D = 128 multiplies queries in two terms
+ *   of 8 bits, which are off by at most 2^-18 of the row's largest element where an element is less
+ *   than 2^-10 of it, and exact otherwise.
  */
+size_t kda_paged_attention_q8_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
+                                                 int dtype);
 int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const void* v_cache,
                                const uint8_t* k_scale, const uint8_t* v_scale,
                                const int32_t* block_table, const int32_t* cu_seqlens,

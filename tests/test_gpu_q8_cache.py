@@ -282,7 +282,7 @@ def make(seqs, Hq, Hkv, D, page, dt, seed=0, fill=None, std=1.0, **kw):
 
 
 def call(d, ws=None, **kw):
-    n = kda.kda_paged_attention_fwd_workspace_size(
+    n = kda.kda_paged_attention_q8_fwd_workspace_size(
         d["N"], d["T"], d["Hq"], d["Hkv"], d["D"],
         dtype=kda.KDA_F32 if d["dt"] == "f32" else kda.KDA_BF16)
     if ws is None and n:
@@ -322,7 +322,7 @@ def test_one_key_is_read_exactly(dt, D):
     table = torch.arange(N, dtype=torch.int32, device="cuda")[:, None].contiguous()
     cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
     kv = torch.ones(N, dtype=torch.int32, device="cuda")
-    n = kda.kda_paged_attention_fwd_workspace_size(
+    n = kda.kda_paged_attention_q8_fwd_workspace_size(
         N, N, H, H, D, dtype=kda.KDA_F32 if dt == "f32" else kda.KDA_BF16)
     ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
     zero = torch.full_like(vs, 127)
@@ -505,7 +505,7 @@ def test_repeat_stream_and_replay_give_the_same_bits(dt, D):
         call(d)
     s.synchronize()
     assert torch.equal(a, d["out"]) and torch.equal(l, d["lse"])
-    n = kda.kda_paged_attention_fwd_workspace_size(
+    n = kda.kda_paged_attention_q8_fwd_workspace_size(
         d["N"], d["T"], 8, 2, D, dtype=kda.KDA_F32 if dt == "f32" else kda.KDA_BF16)
     ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
     gr = torch.cuda.CUDAGraph()
@@ -531,7 +531,7 @@ def test_two_calls_at_once():
     for d in ds:
         call(d)
         want.append(d["out"].clone())
-        n = kda.kda_paged_attention_fwd_workspace_size(d["N"], d["T"], 8, 2, d["D"])
+        n = kda.kda_paged_attention_q8_fwd_workspace_size(d["N"], d["T"], 8, 2, d["D"])
         ws.append(torch.empty(n, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]

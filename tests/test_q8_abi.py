@@ -134,6 +134,27 @@ def test_prefix_workspace_of_the_largest_batch_serves_smaller_ones(L, dtype, Hq,
                                      maxpp=maxp, qs=Hq * D, dtype=dtype, wb=wb) == -9
 
 
+@pytest.mark.parametrize("dtype", [kda.KDA_F32, kda.KDA_BF16])
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (4, 4, 64)])
+def test_q8_workspace_of_the_largest_batch_serves_smaller_ones(L, dtype, Hq, Hkv, D):  # noqa: F811
+    import torch
+
+    def size(N, T):
+        return kda.kda_paged_attention_q8_fwd_workspace_size(N, T, Hq, Hkv, D, dtype)
+
+    Ns, Ts = [1, 2, 16, 300], [1, 15, 17, 64, 1024, 70000]
+    for i, N in enumerate(Ns):
+        for j, T in enumerate(Ts):
+            assert size(Ns[max(i - 1, 0)], T) <= size(N, T)
+            assert size(N, Ts[max(j - 1, 0)]) <= size(N, T)
+            if not torch.cuda.is_available():  # (the addresses are never to reach a device)
+                for wb in (size(N, T), size(Ns[-1], Ts[-1])):
+                    assert _attn(L, N=N, T=T, Hq=Hq, Hkv=Hkv, D=D, qs=Hq * D, dtype=dtype,
+                                 wb=wb) == -9
+    if dtype == kda.KDA_BF16 and D == 128:
+        assert _attn(L, wb=kda.kda_paged_attention_fwd_workspace_size(2, 5, 8, 2, 128)) == -12
+
+
 def test_binding_refuses_other_types():
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, 4, 64)
