@@ -1,5 +1,11 @@
 // Attention over a paged cache of bf16 on the tensor cores (kda_paged_attention_fwd), and what the
 // kinds of call share.
+namespace kda {
+namespace {
+constexpr bool kPrefixes = false;
+}  // namespace
+}  // namespace kda
+
 #include "kda_paged_tc.cuh"
 
 namespace kda {
@@ -9,7 +15,7 @@ bool paged_tc_index_ok(const PagedArgs& a) {
   const double rows = (double)a.total_T * (a.Hq / a.Hkv) / kRowsItem;
   auto units = [&](int n, int pages) {
     const double tiles = (double)pages * a.page_size / kKeys + kOverheadMost + 2;
-    return (rows + n) * tiles * a.Hkv;
+    return (rows + n) * tiles * a.Hkv * (a.groups > 0 ? 3 : 1);  // (units of a tile, at most)
   };
   return units(a.N, a.max_pages) + (a.groups > 0 ? units(a.groups, a.max_prefix_pages) : 0.0) <
          2147483647.0;

@@ -1,5 +1,11 @@
 // Attention behind shared prefixes, caches in 8 bits, on the tensor cores
 // (kda_paged_prefix_attention_fwd).
+namespace kda {
+namespace {
+constexpr bool kPrefixes = true;
+}  // namespace
+}  // namespace kda
+
 #include "kda_paged_tc.cuh"
 
 namespace kda {

@@ -1,4 +1,10 @@
 // Attention over a paged cache in 8 bits on the tensor cores (kda_paged_attention_q8_fwd).
+namespace kda {
+namespace {
+constexpr bool kPrefixes = false;
+}  // namespace
+}  // namespace kda
+
 #include "kda_paged_tc.cuh"
 
 namespace kda {

@@ -3,6 +3,8 @@
 // Included behind the including kernel's numbers:
 //   kRowsItem    query rows of an item, at most
 //   kStretches   CTAs of the line
+//   kTile        units of the line that a tile counts; kTileMost, one of an item with more than
+//                kRowsFew rows
 //   kOverhead    units that an item counts beside its tiles; kOverheadMost, one of D = 128 with more
 //                than kRowsFew rows
 #pragma once
@@ -41,7 +43,16 @@ struct Geometry {
   KeyRange kr;
   int t_lo, ns, nt;  // first window tile, sink tiles before it, tiles in all
   int extra;         // units of the line before its tiles
-  __device__ __forceinline__ int units() const { return nt + extra; }
+  // A tile's units: it is worked on where the first of them lies.
+  __device__ __forceinline__ int cost() const {
+    return kTile == kTileMost || rows <= kRowsFew ? kTile : kTileMost;
+  }
+  __device__ __forceinline__ int units() const { return nt * cost() + extra; }
+  // Tiles that begin among the item's first x units.
+  __device__ __forceinline__ int begun(int x) const {
+    const int c = cost();
+    return x <= extra ? 0 : c == 1 ? x - extra : min((x - extra + c - 1) / c, nt);
+  }
 };
 
 __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, int G, int rt) {
@@ -87,6 +98,8 @@ struct Walker {
   int n, h, rt, v0, v1;
   int left;   // units of the stretch from the item's first one on
   int units;  // units of the item in the stretch
+  int end;       // the stretch's
+  int start_at;  // the item's first tile in the line
   Seq s;
   Geometry g;
   int c1, c2, kv1;  // the next sequence's offsets and keys
@@ -99,19 +112,23 @@ struct Walker {
   // is the stretch's last item then, and the next CTA takes it whole).
   __device__ __forceinline__ bool enter(const PagedArgs& a, int x) {
     g = geometry(a, s, a.G, rt);
-    const int last = min(g.nt + g.extra, x + left);
+    const int last = min(g.units(), x + left);
     units = last - x;
-    v0 = max(x - g.extra, 0);
-    v1 = max(last - g.extra, 0);
+    v0 = g.begun(x);
+    v1 = g.begun(last);
+    start_at = end - left - x + g.extra;
     return v1 > v0;
   }
   __device__ __forceinline__ bool start(const PagedArgs& a, const Plan& p) {
+    end = p.end;
     left = p.end - p.first;
     if (left <= 0 || p.n < 0) return false;
     n = p.n; h = p.h; rt = p.rt;
     s = p.s;
     ahead(a);
-    return enter(a, p.x);
+    if (enter(a, p.x)) return true;
+    // (only units of a tile that the CTA before has)
+    return kTileMost > 1 && left > units && next(a);
   }
   __device__ __forceinline__ bool next(const PagedArgs& a) {
     left -= units;

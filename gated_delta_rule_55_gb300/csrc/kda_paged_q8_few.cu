@@ -26,6 +26,7 @@ namespace {
 constexpr int kStretches = 2 * kCtas;  // two CTAs per SM
 constexpr int kRowsItem = 16;
 constexpr int kRowsFew = kRowsItem;
+constexpr int kTile = 1, kTileMost = 1;
 constexpr int kOverhead = 2, kOverheadMost = 2;  // units of the line that an item counts
 }  // namespace
 }  // namespace kda
@@ -344,7 +345,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           hd.h = w.h;
           hd.nt = w.g.nt;
           hd.bos = w.s.bos;
-          hd.start = s.plan.end - w.v1;
+          hd.start = w.start_at;
           hd.total = s.plan.total;
         }
         live = w.next(a);

@@ -66,7 +66,12 @@ constexpr int kRowsFew = 128;
 // counts 3: 12 sequences of 1 to 600 tokens, 32 + 8 heads, take 125 us for 132 with 2 and 145
 // with 1; 256 single tokens 111 us with 2, 114 with 3; the mixed batch above 35.0 with 2, 35.7
 // with 3.
-constexpr int kOverhead = 2, kOverheadMost = 3;
+//
+// Behind prefixes, where the rows of a group fill wide items beside the narrow ones of the
+// sequences' own keys, a wide tile counts 3 and a narrow one 2: as equals, the CTAs with the prefix
+// of 64 single tokens behind 16384 keys took 56 us, the others 37.
+constexpr int kTile = kPrefixes ? 2 : 1, kTileMost = kPrefixes ? 3 : 1;
+constexpr int kOverhead = kPrefixes ? 4 : 2, kOverheadMost = kPrefixes ? 15 : 3;
 }  // namespace
 }  // namespace kda
 
@@ -127,13 +132,6 @@ template <int D, bool Q8> struct Cfg {
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // + 128 * unit
 constexpr uint32_t kColP64 = kColO + 64;                     // weights, D <= 64
 
-// A call with prefixes: what is known of each row, its prefix's first, [2][total_T][Hq].
-struct Rows {
-  int4* at;    // the item's first tile in the line, its tiles (0: not cut), row, the line's length
-  float2* ml;  // of items that are not cut: m and l
-  float* o;    // [.][D]
-};
-
 // What a CTA's units work on together; made by the query warp, kSteps of them ahead at most.
 enum Kind : int {
   kEnd,    // nothing more
@@ -144,6 +142,7 @@ enum Kind : int {
 struct Item {
   int n, h, bos, pos0;  // sequence, kv head, first token and its position
   int v0, v1;           // its tiles in the stretch
+  int start_at;         // its first tile in the line
   Geometry g;
 };
 struct Step {
@@ -152,6 +151,22 @@ struct Step {
   __device__ __forceinline__ int tiles(int i) const { return it[i].v1 - it[i].v0; }
 };
 constexpr int kSteps = 4;
+
+// A call with prefixes: what is known of each row, its prefix's first, [2][total_T][Hq].
+struct Rows {
+  int4* at;    // row_at()
+  float2* ml;  // of items that are not cut: m and l
+  float* o;    // [.][D]
+};
+// Where a row's parts are: the item's first tile in the line, its tiles (0: not cut); row in the
+// item, units of a tile, this CTA (that it starts in) and the number of CTAs to its last tile's; the
+// line's length.
+__device__ __forceinline__ int4 row_at(const Item& w, bool cut, int row, int total) {
+  const int c = blockIdx.x, unit = w.g.cost();
+  const int parts =
+      cut ? stretch_of<kStretches>(total, w.start_at + unit * (w.g.nt - 1)) - c + 1 : 1;
+  return make_int4(w.start_at, cut ? w.g.nt : 0, row | unit << 8 | c << 12 | parts << 20, total);
+}
 // Two narrow items next to each other are worked on side by side when neither has more than
 // kSkew tiles more than the other: their starts and ends then pass beside the other's tiles.  What
 // is left of a longer one would go through one unit alone.
@@ -764,7 +779,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           if (lane == 0) {
             Item& it = next.it[x];
             it.n = w.n; it.h = w.h; it.bos = w.s.bos; it.pos0 = w.s.pos0;
-            it.v0 = w.v0; it.v1 = w.v1;
+            it.v0 = w.v0; it.v1 = w.v1; it.start_at = w.start_at;
             it.g = w.g;
           }
           if (w.v0 == 0 && w.v1 < w.g.nt) {  // starts here and goes on: only the last item does
@@ -773,7 +788,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             hd.h = w.h;
             hd.nt = w.g.nt;
             hd.bos = w.s.bos;
-            hd.start = plan.end - w.v1;
+            hd.start = w.start_at;
             hd.total = plan.total;
           }
           live = w.next(a);
@@ -1224,7 +1239,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         }
         if (valid && (!split || u == 0)) {
           if (PRE && !cut0)
-            rows.at[side] = make_int4(plan.end - w.v1, cut1 ? w.g.nt : 0, base + r, plan.total);
+            rows.at[side] = row_at(w, cut1, base + r, plan.total);
           if (cut0 || cut1)
             part_ml[prow] = make_float2(m * sc, l);
           else if (PRE)
@@ -1250,73 +1265,99 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 }
 
 // Joins what a row has of its prefix and of its own keys, each of which lies whole in `rows` or in
-// parts with the CTAs that its item was cut among.  A thread has four columns of a row.  (Whatever
-// the numbers of a row that no item had are, they are made places inside the workspace.)
+// parts with the CTAs that its item was cut among.  A warp a row: half of its lanes look at a side's
+// CTAs each, so that all parts' (m, l) are one round trip to memory and their columns, D / 32 of
+// them a lane, another.  (Whatever the numbers of a row that no item had are, they are made places
+// inside the workspace.)
 template <int D>
 __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
                                                          const float* part_o,
                                                          const float2* part_ml) {
-  constexpr int PIECES = D / 4, U = 4;
-  const long long all = (long long)a.total_T * a.Hq;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long row = i / PIECES;
-  const int e = (int)(i % PIECES);
+  constexpr int C = D / 32, U = 8;
+  const int all = a.total_T * a.Hq;
+  const int lane = threadIdx.x & 31, side = lane >> 4;
+  const int row = (int)((blockIdx.x * 256u + threadIdx.x) >> 5);
+  if (row >= all) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= all || !token_owned(a, row / a.Hq)) return;
-  const bool grouped = token_grouped(a, row / a.Hq);
-  const int4 at0 = rows.at[grouped ? row : all + row], at1 = rows.at[all + row];
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int4 at = rows.at[(long long)side * all + row];
+  const int tok = (int)((unsigned)row / (unsigned)a.Hq);
+  const bool mine = token_owned(a, tok), grouped = token_grouped(a, tok);
+  if (!mine) return;
+  const bool any = side || grouped, whole = at.y <= 0;
+  const int unit = at.z >> 8 & 15, c = min(at.z >> 12 & 255, kCtas - 1);
+  const int parts = !any ? 0 : whole ? 1 : min(at.z >> 20 & 255, kCtas - c);
+  // the first tile that begins in a CTA's stretch or behind it
+  auto first_of = [&](int cta) {
+    const int x = stretch(max(at.w, 0), cta) - at.x;
+    return x <= 0 ? 0 : min(unit == kTile ? (x + kTile - 1) / kTile
+                                          : (x + kTileMost - 1) / kTileMost, at.y);
+  };
+  float m = -INFINITY, l = 0.f, o[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) o[e] = 0.f;
 #pragma unroll 1
-  for (int side = grouped ? 0 : 1; side < 2; ++side) {
-    const int4 at = side ? at1 : at0;
-    const bool whole = at.y <= 0;
-    const int total = max(at.w, 1), start = min(max(at.x, 0), total - 1);
-    const int last = (int)min((long long)start + max(at.y, 1) - 1, (long long)total - 1);
-    const int c = min(stretch_of(total, start), kCtas - 1);
-    const int parts = whole ? 1 : min(stretch_of(total, last), kCtas - 1) - c + 1;
+  for (int i = lane & 15; __any_sync(0xffffffffu, i < parts); i += 16) {
+    const int cta = min(c + i, kCtas - 1);
+    const bool there = i < parts && (whole || first_of(cta + 1) > first_of(cta));
+    const int p = (2 * cta + (i == 0)) * kRowsItem + (at.z & 255);
+    const float2* pm = whole ? rows.ml + (long long)side * all + row : part_ml + p;
+    const float2 ml = there ? *pm : make_float2(-INFINITY, 0.f);
+    // (rows.o lies behind part_o)
+    const long long at_o =
+        whole ? (rows.o - part_o) + ((long long)side * all + row) * D : (long long)p * D;
+    const bool some = ml.y != 0.f;  // (a part that saw nothing has no say)
+    float mn = some ? ml.x : -INFINITY;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+    mn = fmaxf(mn, m);
+    const float b = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - b);
+    const float g = some ? fast_exp2(ml.x - b) : 0.f;
+    m = mn;
+    l = l * f + warp_sum(some ? ml.y * g : 0.f);
+#pragma unroll
+    for (int e = 0; e < C; ++e) o[e] *= f;
+    unsigned todo = __ballot_sync(0xffffffffu, some);
 #pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += U) {
-      float2 ml[U];
-      float4 x[U];
-      float mn = m;
+    while (todo) {
+      float x[U][C], w[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int cta = min(c + i0 + k, kCtas - 1);
-        const int lo = stretch(total, cta) - start, hi = stretch(total, cta + 1) - start;
-        const bool there = whole ? k == 0 : i0 + k < parts && min(hi, at.y) > max(lo, 0);
-        const long long p = (long long)(2 * cta + (i0 + k == 0)) * kRowsItem + (at.z & 255);
-        const float2* pm = whole ? rows.ml + side * all + row : part_ml + p;
-        const float* po = whole ? rows.o + (side * all + row) * D : part_o + p * D;
-        ml[k] = there ? *pm : make_float2(-INFINITY, 0.f);
-        x[k] = there ? *reinterpret_cast<const float4*>(po + 4 * e)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool take = todo != 0;
+        const int src = take ? __ffs(todo) - 1 : 0;
+        w[k] = __shfl_sync(0xffffffffu, g, src);
+        const float* po = part_o + __shfl_sync(0xffffffffu, at_o, src) + C * lane;
+        if (!take) w[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < C; ++e) x[k][e] = 0.f;
+        if (take) {
+          if constexpr (C == 4) {
+            const float4 y = __ldcs(reinterpret_cast<const float4*>(po));
+            x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+          } else if constexpr (C == 2) {
+            const float2 y = __ldcs(reinterpret_cast<const float2*>(po));
+            x[k][0] = y.x; x[k][1] = y.y;
+          } else {
+            x[k][0] = __ldcs(po);
+          }
+        }
+        todo &= todo - 1;
       }
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (ml[k].y != 0.f) mn = fmaxf(mn, ml[k].x);  // (a part that saw nothing has no say)
-      const float b = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - b);
-      m = mn;
-      l *= f;
-      o.x *= f; o.y *= f; o.z *= f; o.w *= f;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (ml[k].y != 0.f) {
-          const float g = fast_exp2(ml[k].x - b);
-          l += ml[k].y * g;
-          o.x += x[k].x * g;
-          o.y += x[k].y * g;
-          o.z += x[k].z * g;
-          o.w += x[k].w * g;
-        }
+        for (int e = 0; e < C; ++e) o[e] += x[k][e] * w[k];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
-  uint2 w;
-  w.x = pack_bf16(o.x * inv, o.y * inv);
-  w.y = pack_bf16(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * e) = w;
-  if (e == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)row * D + C * lane;
+  if constexpr (C == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  else if constexpr (C == 2)
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
+  else
+    *dst = __float2bfloat16_rn(o[0] * inv);
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // Query rows: 128 rows of a kv head as a box of whole tokens, where its query heads divide 128.
@@ -1377,7 +1418,7 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
   if (e != cudaSuccess) return e;
   if constexpr (!PRE) return launch_join<D>(a, headers, po, ml, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((all * (D / 4) + 255) / 256));
+  cfg.gridDim = dim3((unsigned)((all + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
