@@ -152,6 +152,7 @@ struct PagedArgs {
   const int32_t* prefix_lens;  // [groups]
   const int32_t* cu_groups;    // [groups + 1]
   int groups, max_prefix_pages;
+  int alone;                   // some group may be long enough to go alone (set by the launcher)
   const float* q_scale;        // [total_T, Hq]: queries as two e4m3 terms (set by the launcher)
   int G;                       // Hq / Hkv, and division by it (set by the tensor-core launcher)
   uint32_t g_mul, g_shift;

@@ -10,6 +10,8 @@ struct Seq {
   int len;   // new tokens
   int kv;    // keys of the sequence, the new tokens' included
   int pos0;  // position of its first new token (negative: more new tokens than keys)
+  int list, pre;  // the prefix that its items take along with its own keys, and its keys (list < 0:
+                  // none; kda_paged_plan.cuh)
 };
 
 // Lists of keys: those of the shared prefixes, which all tokens of a group of sequences see, and
@@ -44,6 +46,8 @@ __device__ __forceinline__ Seq make_seq(const PagedArgs& a, int lo, int hi, int 
   const long long cap = (long long)(prefix ? a.max_prefix_pages : a.max_pages) * a.page_size;
   s.kv = (int)min((long long)max(kv, 0), a.num_pages > 0 ? cap : 0ll);
   s.pos0 = s.kv - (prefix ? 1 : s.len);
+  s.list = -1;
+  s.pre = 0;
   return s;
 }
 __device__ __forceinline__ Seq load_seq(const PagedArgs& a, int i) {

@@ -17,7 +17,10 @@ bool paged_tc_index_ok(const PagedArgs& a) {
     const double tiles = (double)pages * a.page_size / kKeys + kOverheadMost + 2;
     return (rows + n) * tiles * a.Hkv * (a.groups > 0 ? 3 : 1);  // (units of a tile, at most)
   };
-  return units(a.N, a.max_pages) + (a.groups > 0 ? units(a.groups, a.max_prefix_pages) : 0.0) <
+  // (sequences may take their prefix along)
+  const int along = a.groups > 0 ? a.max_prefix_pages : 0;
+  if ((double)a.max_pages + along > 2147483647.0) return false;
+  return units(a.N, a.max_pages + along) + (a.groups > 0 ? units(a.groups, a.max_prefix_pages) : 0.0) <
          2147483647.0;
 }
 

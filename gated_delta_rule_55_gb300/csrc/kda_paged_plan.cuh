@@ -5,6 +5,7 @@
 //   kStretches   CTAs of the line
 //   kTile        units of the line that a tile counts; kTileMost, one of an item with more than
 //                kRowsFew rows
+//   kPrefixes    whether calls have prefixes
 //   kOverhead    units that an item counts beside its tiles; kOverheadMost, one of D = 128 with more
 //                than kRowsFew rows
 #pragma once
@@ -41,7 +42,8 @@ __device__ __forceinline__ int div_g(const PagedArgs& a, int x) {
 struct Geometry {
   int row0, rows;  // query rows of the item
   KeyRange kr;
-  int t_lo, ns, nt;  // first window tile, sink tiles before it, tiles in all
+  int t_lo, ns, nt;  // first window tile, sink (prefix) tiles before it, tiles in all
+  int list;          // the prefix whose tiles come first, kr.sinks keys of it (< 0: none)
   int extra;         // units of the line before its tiles
   // A tile's units: it is worked on where the first of them lies.
   __device__ __forceinline__ int cost() const {
@@ -55,6 +57,44 @@ struct Geometry {
   }
 };
 
+// A group whose sequences have kAlone rows and more on average fills the products' tiles without its
+// neighbours: its sequences take the prefix along with their own keys, as one list of tiles, and
+// there is nothing to join.  (2300 tokens of 8 sequences behind 8191 keys, 32 + 8 heads of 128: 250
+// us when their prefix was worked on for all of them.)
+constexpr int kAlone = 768;
+
+__device__ __forceinline__ bool group_alone(const PagedArgs& a, int g) {
+  const int g0 = min(max(a.cu_groups[g], 0), a.N), g1 = min(max(a.cu_groups[g + 1], 0), a.N);
+  const long long lo = a.cu_seqlens[g0], hi = a.cu_seqlens[g1];
+  return g1 > g0 && (hi - lo) * a.G >= (long long)kAlone * (g1 - g0);
+}
+// List i from its raw numbers.
+__device__ __forceinline__ Seq list_seq(const PagedArgs& a, int i, int lo, int hi, int kv) {
+  Seq s = make_seq(a, lo, hi, kv, i < a.groups);
+  if (kPrefixes && a.alone) {
+    if (i < a.groups) {
+      if (group_alone(a, i)) s.len = 0;
+    } else {
+      const int n = i - a.groups;
+      int g = 0;  // the last group that begins at n or before it
+      for (int end = a.groups; end - g > 1;) {
+        const int mid = (g + end) >> 1;
+        (a.cu_groups[mid] <= n ? g : end) = mid;
+      }
+      if (a.cu_groups[g] <= n && n < a.cu_groups[g + 1] && group_alone(a, g)) {
+        s.list = g;
+        s.pre = make_seq(a, 0, 0, a.prefix_lens[g], true).kv;
+      }
+    }
+  }
+  return s;
+}
+__device__ __forceinline__ Seq load_list(const PagedArgs& a, int i) {
+  int lo, hi, kv;
+  raw_seq(a, i, lo, hi, kv);
+  return list_seq(a, i, lo, hi, kv);
+}
+
 __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, int G, int rt) {
   Geometry g;
   const int rows = s.len * G;
@@ -64,6 +104,12 @@ __device__ __forceinline__ Geometry geometry(const PagedArgs& a, const Seq& s, i
   g.kr = key_range(a, s, div_g(a, g.row0), div_g(a, g.row0 + g.rows - 1));
   g.t_lo = g.kr.lo / kKeys;
   g.ns = min((g.kr.sinks + kKeys - 1) / kKeys, g.t_lo);
+  g.list = -1;
+  if (kPrefixes) {  // (no window: neither sinks nor tiles that it hides)
+    g.list = s.list;
+    g.kr.sinks = s.pre;
+    g.ns = (s.pre + kKeys - 1) / kKeys;
+  }
   // an item without keys still has one (empty) tile: its rows get their zeros
   g.nt = max(g.ns + (g.kr.hi + kKeys - 1) / kKeys - g.t_lo, 1);
   return g;
@@ -75,6 +121,11 @@ __device__ __forceinline__ Seq shfl_seq(const Seq& s, int src) {
   t.len = __shfl_sync(0xffffffffu, s.len, src);
   t.kv = __shfl_sync(0xffffffffu, s.kv, src);
   t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
+  t.list = t.pre = 0;
+  if (kPrefixes) {
+    t.list = __shfl_sync(0xffffffffu, s.list, src);
+    t.pre = __shfl_sync(0xffffffffu, s.pre, src);
+  }
   return t;
 }
 
@@ -139,7 +190,7 @@ struct Walker {
         h = 0;
         do {  // (the line has more units, so a later sequence has tokens)
           if (++n >= lists(a)) return false;
-          s = make_seq(a, c1, c2, kv1, n < a.groups);
+          s = list_seq(a, n, c1, c2, kv1);
           ahead(a);
         } while (s.len == 0);
       }
@@ -212,7 +263,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
     if (count <= kFew) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (warp + k * W < count) s[k] = load_seq(a, r * kPlanSeqs + warp + k * W);
+        if (warp + k * W < count) s[k] = load_list(a, r * kPlanSeqs + warp + k * W);
 #pragma unroll 1
       for (int k = 0; k < 2; ++k)
         if (warp + k * W < count) {
@@ -222,7 +273,7 @@ __device__ void make_plan(const PagedArgs& a, Plan& plan, int* s_units) {
         }
     } else {
       const int i = threadIdx.x;
-      if (i < count) s[0] = load_seq(a, r * kPlanSeqs + i);
+      if (i < count) s[0] = load_list(a, r * kPlanSeqs + i);
       const int nrt = i < count ? row_tiles(s[0], G) : 0;
       per[0] = 0;
       if (nrt <= 4)

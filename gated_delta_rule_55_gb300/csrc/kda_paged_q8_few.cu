@@ -26,6 +26,7 @@ namespace {
 constexpr int kStretches = 2 * kCtas;  // two CTAs per SM
 constexpr int kRowsItem = 16;
 constexpr int kRowsFew = kRowsItem;
+constexpr bool kPrefixes = false;
 constexpr int kTile = 1, kTileMost = 1;
 constexpr int kOverhead = 2, kOverheadMost = 2;  // units of the line that an item counts
 }  // namespace

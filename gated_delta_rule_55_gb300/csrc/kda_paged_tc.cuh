@@ -158,14 +158,16 @@ struct Rows {
   float2* ml;  // of items that are not cut: m and l
   float* o;    // [.][D]
 };
-// Where a row's parts are: the item's first tile in the line, its tiles (0: not cut); row in the
-// item, units of a tile, this CTA (that it starts in) and the number of CTAs to its last tile's; the
-// line's length.
+// Where a row's parts are: the item's first tile in the line, its tiles (0: not cut; -1: nor has it
+// another side, so that it is done); row in the item, units of a tile, this CTA (that it starts in),
+// the number of CTAs to its last tile's, and whether it has no other side; the line's length.
 __device__ __forceinline__ int4 row_at(const Item& w, bool cut, int row, int total) {
   const int c = blockIdx.x, unit = w.g.cost();
   const int parts =
       cut ? stretch_of<kStretches>(total, w.start_at + unit * (w.g.nt - 1)) - c + 1 : 1;
-  return make_int4(w.start_at, cut ? w.g.nt : 0, row | unit << 8 | c << 12 | parts << 20, total);
+  const int alone = w.g.list >= 0;
+  return make_int4(w.start_at, cut ? w.g.nt : -alone,
+                   row | unit << 8 | c << 12 | parts << 20 | alone << 28, total);
 }
 // Two narrow items next to each other are worked on side by side when neither has more than
 // kSkew tiles more than the other: their starts and ends then pass beside the other's tiles.  What
@@ -495,10 +497,14 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             x = o.unit(t);
             w = st->it[x];
           }
-          const int k0 = tile_start(w.g, w.v0 + (pair ? o.place(t) : t)) + pi * ps;
-          if (k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks)) return;
+          const int v = w.v0 + (pair ? o.place(t) : t);
+          const int k0 = tile_start(w.g, v) + pi * ps;
+          const bool along = PRE && v < w.g.ns;  // a prefix's tile before the own ones
+          if (PRE ? k0 >= (along ? w.g.kr.sinks : w.g.kr.hi)
+                  : k0 >= w.g.kr.hi || (k0 + ps <= w.g.kr.lo && k0 >= w.g.kr.sinks))
+            return;
           head = w.h;
-          const int32_t* table = PRE ? table_of(a, w.n)
+          const int32_t* table = PRE ? table_of(a, along ? w.g.list : w.n)
                                      : a.block_table + (long long)w.n * a.max_pages;
           page = __ldg(table + k0 / kKeys * ppt + pi);
         };
@@ -890,6 +896,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const int pos_last = limit(w.pos0 + div_g(a, w.g.row0 + base + nr - 1));
       for (int i = split ? u : 0; i < n; i += split ? 2 : 1) {
         const int ks = tile_start(w.g, w.v0 + i);
+        const bool along = PRE && w.v0 + i < w.g.ns;  // a prefix's tile before the own ones
         const int tile = order.tile(u, i);
         const float* cols = nullptr;
         if (KD) {
@@ -933,8 +940,10 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         if (active) {
           // a tile needs masks where some row of the unit does not see all of it
           const bool whole =
-              ks + kKeys <= pos_first + 1 &&
-              (a.window == 0 || ks > max(pos_last, 0) - a.window || ks + kKeys <= a.sinks);
+              along ? ks + kKeys <= w.g.kr.sinks
+                    : ks + kKeys <= pos_first + 1 &&
+                          (a.window == 0 || ks > max(pos_last, 0) - a.window ||
+                           ks + kKeys <= a.sinks);
           bool done = false;
           // O and l to another maximum (mine > 0, or O is not there yet).
           bool lower = false;  // the product of the tile's lower half is in O
@@ -1049,7 +1058,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             // maximum first, then the weights.
             // Bits of the keys that the thread's row sees: not in the future, and in the
             // window or among the sinks.
-            const int hi = whole ? kKeys : mypos - ks + 1;  // keys [0, hi) of the tile
+            // keys [0, hi) of the tile
+            const int hi = whole ? kKeys : along ? w.g.kr.sinks - ks : mypos - ks + 1;
             const int lo = a.window && !whole ? max(mypos, 0) - a.window - ks + 1 : 0;
             const int sk = a.window ? a.sinks - ks : 0;
             auto bits = [&](int q) -> uint32_t {
@@ -1131,11 +1141,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         // zero times what the cache holds there need not be zero).  Behind the wait for the
         // scores: the products before them have used every earlier entry of the ring, so the
         // value stage's barrier is in the phase that is waited for.
-        if (ks + kKeys > w.g.kr.hi || (ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks)) {
+        const int behind = along ? w.g.kr.sinks : w.g.kr.hi;
+        if (ks + kKeys > behind || (!PRE && ks < w.g.kr.lo && ks + kKeys > w.g.kr.sinks)) {
           const Place at = value_place(order, pos, tile);
           wait_or_die(&bars.kv_full[at.at], at.phase, dead);
           const int key = ks + r;
-          if (key >= w.g.kr.hi || (key < w.g.kr.lo && key >= w.g.kr.sinks)) {
+          if (key >= behind || (!PRE && key < w.g.kr.lo && key >= w.g.kr.sinks)) {
             uint8_t* vrow = sKV + (KD ? at.at - NS : at.at) * C::kStageBytes + r * RB;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
@@ -1184,6 +1195,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       }
       tc_fence_after();
       const bool cut0 = w.v0 > 0, cut1 = w.v1 < w.g.nt;
+      // the rows' other side is to be joined
+      const bool sides = PRE && w.g.list < 0;
       if (active) {
         const bool valid = r < nr;
         const long long orow =
@@ -1214,7 +1227,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = x[e];
           }
-          if (PRE || cut0 || cut1) {
+          if (sides || cut0 || cut1) {
             float* dst = PRE && !cut0 && !cut1 ? rows.o + side * D : part_o + prow * D;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) store32(dst + c + e, o + e);
@@ -1242,7 +1255,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             rows.at[side] = row_at(w, cut1, base + r, plan.total);
           if (cut0 || cut1)
             part_ml[prow] = make_float2(m * sc, l);
-          else if (PRE)
+          else if (sides)
             rows.ml[side] = make_float2(m * sc, l);
           else if (a.lse)
             a.lse[orow] =
@@ -1282,8 +1295,9 @@ __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
   const int4 at = rows.at[(long long)side * all + row];
   const int tok = (int)((unsigned)row / (unsigned)a.Hq);
   const bool mine = token_owned(a, tok), grouped = token_grouped(a, tok);
-  if (!mine) return;
-  const bool any = side || grouped, whole = at.y <= 0;
+  if (!mine || __shfl_sync(0xffffffffu, at.y, 16) < 0) return;  // (a warp alike)
+  const bool alone = __shfl_sync(0xffffffffu, at.z, 16) >> 28 & 1;
+  const bool any = side || (grouped && !alone), whole = at.y <= 0;
   const int unit = at.z >> 8 & 15, c = min(at.z >> 12 & 255, kCtas - 1);
   const int parts = !any ? 0 : whole ? 1 : min(at.z >> 20 & 255, kCtas - c);
   // the first tile that begins in a CTA's stretch or behind it
@@ -1379,6 +1393,7 @@ template <int D, bool Q8, bool PRE>
 cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream_t st) {
   set_divisor(a);
   const uint32_t G = (uint32_t)a.G;
+  a.alone = PRE && (long long)a.total_T * G >= kAlone;
   if constexpr (Cfg<D, Q8>::kDirect) {
     const cudaError_t e = launch_query_terms(a, query_terms, st);
     if (e != cudaSuccess) return e;

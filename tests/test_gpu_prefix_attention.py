@@ -301,3 +301,46 @@ def test_one_workspace_for_all_batches(dt, q8):
         call(d, ws=(ws.data_ptr(), n))
         check(d)
         assert (ws[n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("G,Hkv", [(4, 1), (8, 2)])
+def test_groups_that_fill_tiles_alone(D, q8, G, Hkv):
+    """Long sequences, which take their prefix along, beside groups of short ones, which share it:
+    groups on both sides of the border, with a short sequence among long ones, without a prefix,
+    without tokens, and sequences outside all groups."""
+    n = 1000 // G  # tokens of a long sequence
+    for page in (16, 64):
+        d = make([300, 129, 0, 500, 77, 40],
+                 [(3, 3), (n, n), (n + 17, 2 * n), (1, 90), (n, n - 40), (1, 1), (2 * n, 2 * n),
+                  (2, 2), (4, 70), (0, 5), (n, n + 1), (1, 7)], G * Hkv, Hkv, D, page, "bf16", q8,
+                 groups=[1, 3, 6, 7, 9, 10, 11], seed=n + D, pad=2, fill=True)
+        call(d)
+        check(d)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("P", [1, 127, 128, 129, 1500])
+def test_a_prefix_taken_along(q8, P):
+    """Prefix lengths around a tile in front of a long sequence's own keys, cut among many blocks."""
+    d = make([P], [(300, 300), (257, 900)], 8, 2, 128, 64, "bf16", q8, seed=P)
+    call(d)
+    check(d)
+    a = d["out"].clone()
+    for _ in range(3):
+        call(d)
+        assert torch.equal(a, d["out"])
+
+
+def test_bad_groups_of_long_sequences_stay_inside():
+    d = make([100, 60, 30], [(200, 300), (190, 200), (210, 210)], 8, 2, 64, 16, "bf16", False, pad=2)
+    n = size(d)
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    for cg in ([2, 1, 3, 0], [3, 0, 0, 2], [-4, 2, 1, 9], [0, 3, 2, 3], [1, 1, 1, 1]):
+        d["cg"].copy_(torch.tensor(cg, dtype=torch.int32))
+        d["out"].fill_(7)
+        call(d, ws=(ws.data_ptr(), n))
+        torch.cuda.synchronize()
+        assert (host(d["out"])[d["live"]:] == 7).all() and (ws[n:] == 0x5A).all()
+    assert kda.kda_device_error() == 0
