@@ -426,40 +426,36 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
           const q8::Scale16 sc(byte);
           uint8_t* dst = sKV + (KD ? to.at - NS : to.at) * C::kStageBytes;
           const uint8_t* src = KD ? dst + C::kRawBytes : sRaw + from.at * C::kRawBytes;
-          uint4 w[D / 16];
+          const bool big = __any_sync(0xffffffffu, sc.big);
+          if (!KD) wait_or_die(&bars.kv_empty[to.at], to.phase ^ 1, dead);
+          // In a loop: little code.  (Direct: the pieces that are written over the row's bytes are
+          // behind those that have been read.)
+          uint4 w = *reinterpret_cast<const uint4*>(src + raw_offset<D>(r, 0));
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            if (c + 1 < D / 16)
+              w = *reinterpret_cast<const uint4*>(src + raw_offset<D>(r, c + 1));
+            uint32_t y[8];
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(src + raw_offset<D>(r, c));
+            for (int k = 0; k < 4; ++k) {
+              if (KD)  // (values: their columns change places)
+                q8::expand4<false>(x[k], sc, y[2 * k], y[2 * k + 1]);
+              else
+                q8::expand4_in_order<false>(x[k], sc, y[2 * k], y[2 * k + 1]);
+            }
+            if (big)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = q8::mul_bf16x2(y[k], sc.more);
+            *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c + 1)) =
+                make_uint4(y[4], y[5], y[6], y[7]);
+          }
           if (!KD) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.raw_empty[from.at]);
-            wait_or_die(&bars.kv_empty[to.at], to.phase ^ 1, dead);
           }
-          auto put = [&](auto big) {
-            constexpr bool B = decltype(big)::value;
-            auto four = [&](uint32_t x, uint32_t& lo, uint32_t& hi) {
-              if (KD)  // (values: their columns change places)
-                q8::expand4<B>(x, sc, lo, hi);
-              else
-                q8::expand4_in_order<B>(x, sc, lo, hi);
-            };
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t y[8];
-              four(w[c].x, y[0], y[1]);
-              four(w[c].y, y[2], y[3]);
-              four(w[c].z, y[4], y[5]);
-              four(w[c].w, y[6], y[7]);
-              *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c)) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(dst + piece_offset<D>(r, 2 * c + 1)) =
-                  make_uint4(y[4], y[5], y[6], y[7]);
-            }
-          };
-          if (__any_sync(0xffffffffu, sc.big))
-            put(Bool<true>{});
-          else
-            put(Bool<false>{});
           fence_async_smem();
         }
         __syncwarp();
@@ -1017,10 +1013,30 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
                 lower = true;
                 rescale(outgrown() ? top : m);
                 const float nb2 = m == -INFINITY ? 0.f : -m * sc;
-                tmem_ld32_start(tS + 64, s[0]);
-                tmem_ld32_finish(s[0]);
-                weights(s[0], 64, nb2, p, sum, top, true);
-                weights(s[1], 96, nb2, p + 16, sum, top, false);
+                if constexpr (KD) {  // (rare, and little code)
+                  sum = 0.f;
+#pragma unroll 1
+                  for (int q = 0; q < 2; ++q) {
+                    tmem_ld32_start(tS + 64 + 32 * q, s[0]);
+                    finish(s[0], 64 + 32 * q);
+                    float part, t2;
+                    weights32<false>(s[0], nullptr, sc, nb2, p, part, t2, true);
+                    sum += part;
+                    if (q == 0)
+#pragma unroll
+                      for (int e = 0; e < 16; ++e) s[1][e] = p[e];
+                  }
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    p[16 + e] = p[e];
+                    p[e] = s[1][e];
+                  }
+                } else {
+                  tmem_ld32_start(tS + 64, s[0]);
+                  tmem_ld32_finish(s[0]);
+                  weights(s[0], 64, nb2, p, sum, top, true);
+                  weights(s[1], 96, nb2, p + 16, sum, top, false);
+                }
               }
               tmem_st32_nowait(tP + 32, p);
               l += sum;
