@@ -30,6 +30,7 @@ struct Header {  // a CTA's part of the line, for the joining kernel
   int nt;         // its tiles
   int start, total;  // place of its first tile in the line, the line's length
   int bos;        // its sequence's first token
+  int unit;       // units of a tile
 };
 
 // ------------------------------------------------------------------- items of the line
@@ -479,25 +480,28 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, bool
 // slot, the following ones in their first.  Blocks (c, .): the item that starts in CTA c's
 // stretch; a thread has four columns of a row and takes four parts at a time, all their loads in
 // flight together (eight: 39.8 against 37.5 us for a call with 150 items cut in two).
+// (c, y of ny): the block's number.
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Header* headers,
-                                                         const float* part_o,
-                                                         const float2* part_ml) {
+__device__ __forceinline__ void join_items(const PagedArgs& a, const Header* headers,
+                                           const float* part_o, const float2* part_ml, int c,
+                                           int y, int ny) {
   constexpr int PIECES = D / 4, U = 4;
-  const int c = blockIdx.x;
-  // launched while the first kernel runs: wait for its results
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Header hd = headers[c];
   if (hd.rows == 0) return;
+  const int unit = kTileMost == 1 ? 1 : hd.unit;
   // CTAs from this one to the one it ends in
-  const int parts = stretch_of<kStretches>(hd.total, hd.start + hd.nt - 1) - c + 1;
-  for (int at = blockIdx.y * 256 + threadIdx.x; at < hd.rows * PIECES; at += gridDim.y * 256) {
+  const int parts = stretch_of<kStretches>(hd.total, hd.start + unit * (hd.nt - 1)) - c + 1;
+  // The first of its tiles that begins in CTA k's stretch or behind it.
+  auto first_of = [&](int k) {
+    const int x = stretch<kStretches>(hd.total, k) - hd.start;
+    return unit == 1 ? x : x <= 0 ? 0 : (x + unit - 1) / unit;
+  };
+  for (int at = y * 256 + threadIdx.x; at < hd.rows * PIECES; at += ny * 256) {
     const int r = at / PIECES, e = at % PIECES;
     // Row of the i-th part in the partial results, -1 if that CTA has no tile of the item.
     auto place = [&](int i) -> int {
       const int k = c + i;
-      const int first = stretch<kStretches>(hd.total, k) - hd.start;
-      const int last = min(stretch<kStretches>(hd.total, k + 1) - hd.start, hd.nt);
+      const int first = first_of(k), last = min(first_of(k + 1), hd.nt);
       return i < parts && last > max(first, 0) ? (2 * k + (i == 0)) * kRowsItem + r : -1;
     };
     float m = -INFINITY, l = 0.f;
@@ -542,6 +546,15 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Head
     if (e == 0 && a.lse)
       a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedArgs a, const Header* headers,
+                                                         const float* part_o,
+                                                         const float2* part_ml) {
+  // launched while the first kernel runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  join_items<D>(a, headers, part_o, part_ml, blockIdx.x, blockIdx.y, gridDim.y);
 }
 
 // Pages of a cache: boxes of a page's rows, of up to 64 columns of bf16 or of all D bytes.

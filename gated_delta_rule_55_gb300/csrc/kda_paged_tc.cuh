@@ -86,10 +86,10 @@ constexpr int kExpandWarp = 12;  // and 13 to 15: caches in 8 bits
 
 // Two softmax warpgroups, one of the warps above, and one that expands 8-bit tiles.  Registers:
 // 168 a thread at launch (3 x 128 threads), moved to the softmax warpgroups: 2 x 216 + 72 = 3 x 168;
-// with the fourth warpgroup 128: 2 x 176 + 72 + 88 = 4 x 128.
+// with the fourth warpgroup 128: 2 x 184 + 72 + 72 = 4 x 128.
 template <bool Q8> struct Group {
   static constexpr int kThreads = Q8 ? 512 : 384;
-  static constexpr int kRegsSoftmax = Q8 ? 176 : 216, kRegsOther = 72, kRegsExpand = 88;
+  static constexpr int kRegsSoftmax = Q8 ? 184 : 216, kRegsOther = 72, kRegsExpand = 72;
 };
 // log2 growth of the maximum that O and l absorb.  (Rescaling only from some growth on, and two
 // softmax warpgroups beside two score tiles, are published ways for attention on this hardware.)
@@ -158,16 +158,15 @@ struct Rows {
   float2* ml;  // of items that are not cut: m and l
   float* o;    // [.][D]
 };
-// Where a row's parts are: the item's first tile in the line, its tiles (0: not cut; -1: nor has it
-// another side, so that it is done); row in the item, units of a tile, this CTA (that it starts in),
-// the number of CTAs to its last tile's, and whether it has no other side; the line's length.
+// Where a row's parts are: the item's first tile in the line, its tiles (0: not cut; -1: it has no
+// other side, and is joined as an item where it is cut); row in the item, units of a tile, this CTA
+// (that it starts in), the number of CTAs to its last tile's; the line's length.
 __device__ __forceinline__ int4 row_at(const Item& w, bool cut, int row, int total) {
   const int c = blockIdx.x, unit = w.g.cost();
   const int parts =
       cut ? stretch_of<kStretches>(total, w.start_at + unit * (w.g.nt - 1)) - c + 1 : 1;
-  const int alone = w.g.list >= 0;
-  return make_int4(w.start_at, cut ? w.g.nt : -alone,
-                   row | unit << 8 | c << 12 | parts << 20 | alone << 28, total);
+  return make_int4(w.start_at, w.g.list >= 0 ? -1 : cut ? w.g.nt : 0,
+                   row | unit << 8 | c << 12 | parts << 20, total);
 }
 // Two narrow items next to each other are worked on side by side when neither has more than
 // kSkew tiles more than the other: their starts and ends then pass beside the other's tiles.  What
@@ -260,8 +259,9 @@ __device__ __forceinline__ void scale32(uint32_t (&s)[32], const float* c) {
 // Softmax weights of 32 scores: p = 2^(s sc + nb), packed to bf16; their sum (in fp32, before the
 // rounding) and the largest score, started or carried on.  SC: scores times their keys' scales c.
 template <bool SC>
-__device__ __forceinline__ void weights32(const uint32_t (&s)[32], const float* c, float sc, float nb,
-                                          uint32_t* p, float& sum, float& top, bool start) {
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], const float* c, float sc,
+                                          float nb, uint32_t* p, float& sum, float& top,
+                                          bool start) {
   const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(nb, nb);
   uint64_t acc[4] = {0, 0, 0, 0};
   float c4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -384,8 +384,8 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
     if (lane == 0) mbar_arrive(&bars.step_empty[j % kSteps]);
   };
 
-  // Barrier (and stage) and phase of a tile's keys and values, `pos` entries before its step.  (Direct:
-  // stages of keys, then of values.)
+  // Barrier (and stage) and phase of a tile's keys and values, `pos` entries before its step.
+  // (Direct: stages of keys, then of values.)
   struct Place {
     uint32_t at, phase;
   };
@@ -784,7 +784,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
             it.v0 = w.v0; it.v1 = w.v1; it.start_at = w.start_at;
             it.g = w.g;
           }
-          if (w.v0 == 0 && w.v1 < w.g.nt) {  // starts here and goes on: only the last item does
+          // starts here and goes on: only the last item does (and its rows have no other side)
+          if (w.v0 == 0 && w.v1 < w.g.nt && (!PRE || w.g.list >= 0)) {
+            hd.unit = w.g.cost();
             hd.rows = w.g.rows;
             hd.row0 = w.g.row0;
             hd.h = w.h;
@@ -1295,99 +1297,128 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 
 // Joins what a row has of its prefix and of its own keys, each of which lies whole in `rows` or in
 // parts with the CTAs that its item was cut among.  A warp a row: half of its lanes look at a side's
-// CTAs each, so that all parts' (m, l) are one round trip to memory and their columns, D / 32 of
-// them a lane, another.  (Whatever the numbers of a row that no item had are, they are made places
-// inside the workspace.)
+// CTAs each, so that all parts' (m, l) and their columns, D / 32 of them a lane, are one round trip
+// to memory.  A warp has `per` rows, one after the other.  The first `joins` blocks, a multiple of
+// the CTAs, join the items whose rows have no other side.  (Whatever the numbers of a row that no
+// item had are, they are made places inside the workspace.)
 template <int D>
-__global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
+__global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows, int per,
+                                                         int joins, const Header* headers,
                                                          const float* part_o,
                                                          const float2* part_ml) {
   constexpr int C = D / 32, U = 8;
+  if ((int)blockIdx.x < joins) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    join_items<D>(a, headers, part_o, part_ml, blockIdx.x % kCtas, blockIdx.x / kCtas,
+                  joins / kCtas);
+    return;
+  }
   const int all = a.total_T * a.Hq;
   const int lane = threadIdx.x & 31, side = lane >> 4;
-  const int row = (int)((blockIdx.x * 256u + threadIdx.x) >> 5);
-  if (row >= all) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 at = rows.at[(long long)side * all + row];
-  const int tok = (int)((unsigned)row / (unsigned)a.Hq);
-  const bool mine = token_owned(a, tok), grouped = token_grouped(a, tok);
-  if (!mine || __shfl_sync(0xffffffffu, at.y, 16) < 0) return;  // (a warp alike)
-  const bool alone = __shfl_sync(0xffffffffu, at.z, 16) >> 28 & 1;
-  const bool any = side || (grouped && !alone), whole = at.y <= 0;
-  const int unit = at.z >> 8 & 15, c = min(at.z >> 12 & 255, kCtas - 1);
-  const int parts = !any ? 0 : whole ? 1 : min(at.z >> 20 & 255, kCtas - c);
-  // the first tile that begins in a CTA's stretch or behind it
-  auto first_of = [&](int cta) {
-    const int x = stretch(max(at.w, 0), cta) - at.x;
-    return x <= 0 ? 0 : min(unit == kTile ? (x + kTile - 1) / kTile
-                                          : (x + kTileMost - 1) / kTileMost, at.y);
+  const int first = (int)(((blockIdx.x - joins) * 256u + threadIdx.x) >> 5) * per;
+  if (first >= all) return;
+  auto owned = [&](int row, bool& grouped) {
+    const int tok = (int)((unsigned)row / (unsigned)a.Hq);
+    grouped = token_grouped(a, tok);
+    return token_owned(a, tok);
   };
-  float m = -INFINITY, l = 0.f, o[C];
-#pragma unroll
-  for (int e = 0; e < C; ++e) o[e] = 0.f;
+  bool grouped = false;
+  if (per == 1 && !owned(first, grouped)) return;
+  // launched while the first kernel runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  unsigned open = 1;  // rows that are not done
+  if (per > 1)
+    open = __ballot_sync(0xffffffffu,
+                         lane < per && first + lane < all &&
+                             rows.at[(long long)all + min(first + lane, all - 1)].y >= 0);
 #pragma unroll 1
-  for (int i = lane & 15; __any_sync(0xffffffffu, i < parts); i += 16) {
-    const int cta = min(c + i, kCtas - 1);
-    const bool there = i < parts && (whole || first_of(cta + 1) > first_of(cta));
-    const int p = (2 * cta + (i == 0)) * kRowsItem + (at.z & 255);
-    const float2* pm = whole ? rows.ml + (long long)side * all + row : part_ml + p;
-    const float2 ml = there ? *pm : make_float2(-INFINITY, 0.f);
-    // (rows.o lies behind part_o)
-    const long long at_o =
-        whole ? (rows.o - part_o) + ((long long)side * all + row) * D : (long long)p * D;
-    const bool some = ml.y != 0.f;  // (a part that saw nothing has no say)
-    float mn = some ? ml.x : -INFINITY;
+  for (; open; open &= open - 1) {
+    const int row = first + __ffs(open) - 1;
+    if (per > 1 && !owned(row, grouped)) continue;
+    const int4 at = rows.at[(long long)side * all + row];
+    if (__shfl_sync(0xffffffffu, at.y, 16) < 0) continue;  // (a warp alike)
+    const bool any = side || grouped, whole = at.y <= 0;
+    const int unit = at.z >> 8 & 15, c = min(at.z >> 12 & 255, kCtas - 1);
+    const int parts = !any ? 0 : whole ? 1 : min(at.z >> 20 & 255, kCtas - c);
+    // the first tile that begins in a CTA's stretch or behind it
+    auto first_of = [&](int cta) {
+      const int x = stretch(max(at.w, 0), cta) - at.x;
+      return x <= 0 ? 0 : min(unit == kTile ? (x + kTile - 1) / kTile
+                                            : (x + kTileMost - 1) / kTileMost, at.y);
+    };
+    float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-    mn = fmaxf(mn, m);
-    const float b = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - b);
-    const float g = some ? fast_exp2(ml.x - b) : 0.f;
-    m = mn;
-    l = l * f + warp_sum(some ? ml.y * g : 0.f);
-#pragma unroll
-    for (int e = 0; e < C; ++e) o[e] *= f;
-    unsigned todo = __ballot_sync(0xffffffffu, some);
+    for (int e = 0; e < C; ++e) o[e] = 0.f;
 #pragma unroll 1
-    while (todo) {
-      float x[U][C], w[U];
+    for (int i = lane & 15; __any_sync(0xffffffffu, i < parts); i += 16) {
+      const int cta = min(c + i, kCtas - 1);
+      const bool there = i < parts && (whole || first_of(cta + 1) > first_of(cta));
+      const int p = (2 * cta + (i == 0)) * kRowsItem + (at.z & 255);
+      const float2* pm = whole ? rows.ml + (long long)side * all + row : part_ml + p;
+      // (rows.o lies behind part_o)
+      const long long at_o =
+          whole ? (rows.o - part_o) + ((long long)side * all + row) * D : (long long)p * D;
+      const float2 ml = there ? __ldcs(pm) : make_float2(-INFINITY, 0.f);
+      unsigned todo = __ballot_sync(0xffffffffu, there);
+      // the columns of up to U parts; src: their lanes
+      float x[U][C];
+      int src[U];
+      auto fetch = [&]() {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const bool take = todo != 0;
-        const int src = take ? __ffs(todo) - 1 : 0;
-        w[k] = __shfl_sync(0xffffffffu, g, src);
-        const float* po = part_o + __shfl_sync(0xffffffffu, at_o, src) + C * lane;
-        if (!take) w[k] = 0.f;
+        for (int k = 0; k < U; ++k) {
+          src[k] = todo ? __ffs(todo) - 1 : -1;
+          const float* po = part_o + __shfl_sync(0xffffffffu, at_o, max(src[k], 0)) + C * lane;
 #pragma unroll
-        for (int e = 0; e < C; ++e) x[k][e] = 0.f;
-        if (take) {
-          if constexpr (C == 4) {
-            const float4 y = __ldcs(reinterpret_cast<const float4*>(po));
-            x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
-          } else if constexpr (C == 2) {
-            const float2 y = __ldcs(reinterpret_cast<const float2*>(po));
-            x[k][0] = y.x; x[k][1] = y.y;
-          } else {
-            x[k][0] = __ldcs(po);
+          for (int e = 0; e < C; ++e) x[k][e] = 0.f;
+          if (todo) {
+            if constexpr (C == 4) {
+              const float4 y = __ldcs(reinterpret_cast<const float4*>(po));
+              x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+            } else if constexpr (C == 2) {
+              const float2 y = __ldcs(reinterpret_cast<const float2*>(po));
+              x[k][0] = y.x; x[k][1] = y.y;
+            } else {
+              x[k][0] = __ldcs(po);
+            }
           }
+          todo &= todo - 1;
         }
-        todo &= todo - 1;
+      };
+      fetch();
+      const bool some = ml.y != 0.f;  // (a part that saw nothing has no say)
+      float mn = some ? ml.x : -INFINITY;
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+      mn = fmaxf(mn, m);
+      const float b = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - b);
+      const float g = some ? fast_exp2(ml.x - b) : 0.f;
+      m = mn;
+      l = l * f + warp_sum(some ? ml.y * g : 0.f);
+#pragma unroll
+      for (int e = 0; e < C; ++e) o[e] *= f;
+#pragma unroll 1
+      while (src[0] >= 0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float w = __shfl_sync(0xffffffffu, g, max(src[k], 0));
+#pragma unroll
+          for (int e = 0; e < C; ++e) o[e] += x[k][e] * (src[k] < 0 ? 0.f : w);
+        }
+        fetch();
       }
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-#pragma unroll
-        for (int e = 0; e < C; ++e) o[e] += x[k][e] * w[k];
     }
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)row * D + C * lane;
+    if constexpr (C == 4)
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else if constexpr (C == 2)
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
+    else
+      *dst = __float2bfloat16_rn(o[0] * inv);
+    if (lane == 0 && a.lse)
+      a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (long long)row * D + C * lane;
-  if constexpr (C == 4)
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-  else if constexpr (C == 2)
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
-  else
-    *dst = __float2bfloat16_rn(o[0] * inv);
-  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // Query rows: 128 rows of a kv head as a box of whole tokens, where its query heads divide 128.
@@ -1449,7 +1480,10 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
   if (e != cudaSuccess) return e;
   if constexpr (!PRE) return launch_join<D>(a, headers, po, ml, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((all + 7) / 8));
+  // A warp looks at several rows, most of which may be done, where there are more than the SMs have
+  // room for warps (with few, one after the other takes longer: 130 tokens of 16 heads 34 us for 27).
+  const int per = a.alone && all > kCtas * 64 ? 4 : 1, joins = a.alone ? 8 * kCtas : 0;
+  cfg.gridDim = dim3((unsigned)(joins + (all + 8 * per - 1) / (8 * per)));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -1457,7 +1491,8 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, a, rows, (const float*)po,
+  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<D>, a, rows, per, joins,
+                            (const Header*)headers, (const float*)po,
                             (const float2*)ml);
 }
 
