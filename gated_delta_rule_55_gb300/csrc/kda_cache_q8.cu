@@ -11,58 +11,73 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // of a block
 
-__device__ __forceinline__ void put(float* dst, const uint4& w, float s) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = q8::unpack2(x[i]), b = q8::unpack2(x[i] >> 16);
-    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(a.x * s, a.y * s, b.x * s, b.y * s));
+// 32 bytes: a whole sector, where the address allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    __stcs(static_cast<uint4*>(p), make_uint4(x[0], x[1], x[2], x[3]));
+    __stcs(static_cast<uint4*>(p) + 1, make_uint4(x[4], x[5], x[6], x[7]));
   }
 }
-__device__ __forceinline__ void put(__nv_bfloat16* dst, const uint4& w, float s) {
+__device__ __forceinline__ void put(float* dst, const uint4& w, float s, bool whole) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    uint32_t y[4];
+  for (int i = 0; i < 2; ++i) {
+    uint32_t y[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 a = q8::unpack2(x[i + j / 2] >> (j % 2 * 16));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x * s, a.y * s);
-      y[j] = *reinterpret_cast<const uint32_t*>(&b);
+      const float2 a = q8::unpack2(x[2 * i + j / 2] >> (j % 2 * 16));
+      y[2 * j] = __float_as_uint(a.x * s);
+      y[2 * j + 1] = __float_as_uint(a.y * s);
     }
-    __stcs(reinterpret_cast<uint4*>(dst) + i / 2, make_uint4(y[0], y[1], y[2], y[3]));
+    store32(dst + 8 * i, y, whole);
   }
 }
+__device__ __forceinline__ void put(__nv_bfloat16* dst, const uint4& w, float s, bool whole) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 a = q8::unpack2(x[j / 2] >> (j % 2 * 16));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(a.x * s, a.y * s);
+    y[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  store32(dst, y, whole);
+}
 
+// A block has pieces of one token: a thread 16 numbers of its key and value of one head.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheReadArgs a) {
   constexpr int PIECES = D / 16;
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long row = i / PIECES;  // token * Hkv + head
-  if (row >= (long long)a.T * a.Hkv) return;
-  const int tok = (int)(row / a.Hkv), h = (int)(row - (long long)tok * a.Hkv);
-  const int c = (int)(i % PIECES) * 16;
+  const int i = blockIdx.y * kThreads + threadIdx.x;
+  if (i >= a.Hkv * PIECES) return;
+  const int h = i / PIECES, c = i % PIECES * 16;
+  const long long tok = blockIdx.x;
   const long long slot = __ldg(a.slots + tok);
   uint4 k = make_uint4(0, 0, 0, 0), v = k;
   uint32_t ks = q8::kBias, vs = q8::kBias;
   if (slot >= 0 && slot < (long long)a.num_pages * a.page_size) {
-    const long long page = slot / a.page_size;
-    const long long at = (page * a.Hkv + h) * a.page_size + (slot - page * a.page_size);
-    k = __ldcs(reinterpret_cast<const uint4*>(a.k_cache + at * D + c));
-    v = __ldcs(reinterpret_cast<const uint4*>(a.v_cache + at * D + c));
-    ks = a.k_scale[at];
-    vs = a.v_scale[at];
+    const long long page = slot >> a.page_shift;
+    const long long at = (page * a.Hkv + h) * a.page_size + (slot - (page << a.page_shift));
+    k = __ldg(reinterpret_cast<const uint4*>(a.k_cache + at * D + c));
+    v = __ldg(reinterpret_cast<const uint4*>(a.v_cache + at * D + c));
+    ks = __ldg(a.k_scale + at);
+    vs = __ldg(a.v_scale + at);
   }
-  put(static_cast<T*>(a.k_out) + row * D + c, k, q8::scale(ks));
-  put(static_cast<T*>(a.v_out) + row * D + c, v, q8::scale(vs));
+  const long long row = tok * a.Hkv + h;
+  T *kd = static_cast<T*>(a.k_out) + row * D + c, *vd = static_cast<T*>(a.v_out) + row * D + c;
+  put(kd, k, q8::scale(ks), (reinterpret_cast<uintptr_t>(kd) & 31) == 0);
+  put(vd, v, q8::scale(vs), (reinterpret_cast<uintptr_t>(vd) & 31) == 0);
 }
 
 template <int D>
 cudaError_t launch_t(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
-  const long long n = (long long)a.T * a.Hkv * (D / 16);
-  const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+  const dim3 grid((unsigned)a.T, (unsigned)((a.Hkv * (D / 16) + kThreads - 1) / kThreads));
   if (bf16)
     cache_read_kernel<__nv_bfloat16, D><<<grid, kThreads, 0, st>>>(a);
   else
@@ -74,9 +89,10 @@ cudaError_t launch_t(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
 // each):  q 2^-e = hi + lo,  hi = e4m3(q 2^-e), lo = e4m3(q 2^-e - hi).  Exact where q is more than
 // 2^-10 of the row's largest, and off by at most 2^-18 of that elsewhere (e4m3 ends at 2^-9).
 // Sixteen lanes a row; hi and lo lie where the row's 256 bytes would.
-__global__ void __launch_bounds__(kThreads) query_terms_kernel(PagedArgs a, uint8_t* terms,
+constexpr int kTermThreads = 256;
+__global__ void __launch_bounds__(kTermThreads) query_terms_kernel(PagedArgs a, uint8_t* terms,
                                                                float* scales) {
-  const long long row = (long long)blockIdx.x * (kThreads / 16) + threadIdx.x / 16;
+  const long long row = (long long)blockIdx.x * (kTermThreads / 16) + threadIdx.x / 16;
   const int c = threadIdx.x & 15;
   const long long rows = (long long)a.total_T * a.Hq;
   const long long src = row < rows ? row : rows - 1;
@@ -116,8 +132,8 @@ cudaError_t launch_query_terms(PagedArgs& a, void* terms, cudaStream_t st) {
   const long long rows = (long long)a.total_T * a.Hq;
   uint8_t* t = static_cast<uint8_t*>(terms);
   float* scales = reinterpret_cast<float*>(t + rows * 256);
-  constexpr int per = kThreads / 16;
-  query_terms_kernel<<<(unsigned)((rows + per - 1) / per), kThreads, 0, st>>>(a, t, scales);
+  constexpr int per = kTermThreads / 16;
+  query_terms_kernel<<<(unsigned)((rows + per - 1) / per), kTermThreads, 0, st>>>(a, t, scales);
   a.q = t;
   a.q_stride = (long long)a.Hq * 128;
   a.q_scale = scales;

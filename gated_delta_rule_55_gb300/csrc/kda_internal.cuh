@@ -129,7 +129,7 @@ struct CacheReadArgs {
   const int64_t* slots;        // [T]
   void* k_out;                 // [T, Hkv, D]
   void* v_out;
-  int T, Hkv, D, num_pages, page_size;
+  int T, Hkv, D, num_pages, page_size, page_shift;
 };
 
 // Attention over a paged cache (kda_paged_attention_fwd, _q8_fwd, kda_paged_prefix_attention_fwd).

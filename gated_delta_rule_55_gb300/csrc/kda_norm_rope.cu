@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
       for (int i = 0; i < kUnroll; ++i) {
         const int r = h + i * RPW + rw;
         if constexpr (Q8) {
+          if (h + i * RPW >= h1) break;  // (a warp alike; a row in 8 bits is more than a copy)
           float x[VE];
           unpack_row<T, D>(ra[i], rb[i], x);
           store_row_q8<T, D>(dst8 + r * dst_head, scale8 + (long long)r * a.page_size, l, x, li,
@@ -278,17 +279,31 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int row = now + i * RPW + rw;
+      if (Q8 && now + i * RPW >= h1) break;
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < VE; ++e) ss += x[i][e] * x[i][e];
-      const float r = rsqrtf(row_sum<L>(ss) * (1.0f / D) + a.eps);
-      float y[VE];
+      const float v = row_sum<L>(ss) * (1.0f / D) + a.eps;
+      float r = rsqrtf(v), y[VE];
+      if (Q8 && kind == 1) {
+        // Of these only 8 bits stay, but which of two neighbours is nearest can hang on the last bit:
+        // r by a Newton step with its residual exact, and multiplied last.
+        const float h = v * r, rest = fmaf(v, r, -h);
+        r = fmaf(0.5f * r, fmaf(-h, r, 1.0f) - rest * r, r);
 #pragma unroll
-      for (int k = 0; k < PE; ++k) {
-        const int e0 = Ln::template lo<IL>(k), e1 = Ln::template hi<IL>(k);
-        const float x0 = x[i][e0] * r, x1 = x[i][e1] * r;
-        y[e0] = x0 * p0[k] - x1 * p1[k];
-        y[e1] = x0 * p2[k] + x1 * p3[k];
+        for (int k = 0; k < PE; ++k) {
+          const int e0 = Ln::template lo<IL>(k), e1 = Ln::template hi<IL>(k);
+          y[e0] = (x[i][e0] * p0[k] - x[i][e1] * p1[k]) * r;
+          y[e1] = (x[i][e0] * p2[k] + x[i][e1] * p3[k]) * r;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < PE; ++k) {
+          const int e0 = Ln::template lo<IL>(k), e1 = Ln::template hi<IL>(k);
+          const float x0 = x[i][e0] * r, x1 = x[i][e1] * r;
+          y[e0] = x0 * p0[k] - x1 * p1[k];
+          y[e1] = x0 * p2[k] + x1 * p3[k];
+        }
       }
       if (Q8 && kind == 1)  // (warp-uniform)
         store_row_q8<T, D>(dst8 + row * dst_head, scale8 + (long long)row * a.page_size, l, y, li,

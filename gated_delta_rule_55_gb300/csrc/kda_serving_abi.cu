@@ -13,6 +13,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool page_size_ok(int s) { return s == 16 || s == 32 || s == 64 || s == 128; }
+int page_shift_of(int s) { return s == 16 ? 4 : s == 32 ? 5 : s == 64 ? 6 : 7; }
 bool dtype_ok(int t) { return t == KDA_F32 || t == KDA_BF16; }
 
 template <size_t K>
@@ -87,7 +88,7 @@ int fill_append(kda::NormRopeArgs& a, const void* query, const void* key, const 
   if ((double)num_pages * Hkv * page_size * D >= kMaxElems) return KDA_ERR_TOO_LARGE;
   a.v = value; a.v_stride = value_stride; a.slots = slots; a.q_out = query_out;
   a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages; a.page_size = page_size;
-  a.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  a.page_shift = page_shift_of(page_size);
   return KDA_OK;
 }
 
@@ -295,7 +296,7 @@ int kda_paged_cache_read_q8(const void* k_cache, const void* v_cache, const uint
   const void* const ptrs[] = {k_cache, v_cache, k_scale, v_scale, slots, key_out, value_out};
   if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
   if ((double)num_pages * Hkv * page_size * D >= kMaxElems ||
-      (double)T * Hkv * (D / 16) > 2147483647.0)
+      (double)Hkv * (D / 16) > 65535.0 * 64)
     return KDA_ERR_TOO_LARGE;
   const int s = kda::check_current_device();
   if (s != KDA_OK) return s;
@@ -305,7 +306,7 @@ int kda_paged_cache_read_q8(const void* k_cache, const void* v_cache, const uint
   a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.k_scale = k_scale; a.v_scale = v_scale; a.slots = slots; a.k_out = key_out;
   a.v_out = value_out; a.T = T; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages;
-  a.page_size = page_size;
+  a.page_size = page_size; a.page_shift = page_shift_of(page_size);
   return launch_status(
       kda::launch_cache_read(a, dtype == KDA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
