@@ -92,6 +92,7 @@ cudaError_t launch_t(const CacheReadArgs& a, bool bf16, cudaStream_t st) {
 constexpr int kTermThreads = 256;
 __global__ void __launch_bounds__(kTermThreads) query_terms_kernel(PagedArgs a, uint8_t* terms,
                                                                float* scales) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the products may be set up
   const long long row = (long long)blockIdx.x * (kTermThreads / 16) + threadIdx.x / 16;
   const int c = threadIdx.x & 15;
   const long long rows = (long long)a.total_T * a.Hq;

@@ -39,9 +39,9 @@ namespace {
 
 constexpr int D = 128;
 constexpr int kThreads = 384;  // softmax, expanders, and the warps below
-constexpr int kExpandWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10;
-// Registers: 80 a thread at launch, 3 x 80 = 104 + 72 + 64.
-constexpr int kRegsSoftmax = 104, kRegsExpand = 72, kRegsOther = 64;
+constexpr int kExpandWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10 /* and 11 */;
+// Registers: 80 a thread at launch, 3 x 80 = 112 + 64 + 64.
+constexpr int kRegsSoftmax = 112, kRegsExpand = 64, kRegsOther = 64;
 constexpr float kRescale = 32.0f;  // log2 growth of the maximum that O and l absorb (kda_paged_tc.cuh)
 constexpr int kSteps = 4;         // items put down ahead
 
@@ -121,6 +121,27 @@ template <int N> __device__ __forceinline__ void tmem_st(uint32_t taddr, const f
 
 template <int N> struct Int { static constexpr int value = N; };
 
+// N values of each lane, each joined over the warp's lanes: a lane gives half of its values away and
+// takes the other half's from its partner until one is left, number e of them, which `out` then has
+// (N - 1 exchanges and those for the lanes that are left; 5 N one by one).
+template <int N, class F>
+__device__ __forceinline__ void join_lanes(float (&v)[N], float* out, F op) {
+  const int lane = threadIdx.x & 31;
+  int e = 0, o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float y = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], o);
+      v[i] = op(up ? v[i + n] : v[i], y);
+    }
+    if (up) e += n;
+  }
+  for (; o > 0; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  if ((lane & (32 / N - 1)) == 0) out[e] = v[0];
+}
+
 __global__ void __launch_bounds__(kThreads, 2)
 paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, Header* headers, float* part_o,
@@ -147,7 +168,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       mbar_init(&s.vr_full[i], 1);
       mbar_init(&s.v_full[i], 4);
       mbar_init(&s.v_empty[i], 1);
-      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_full[i], 2);  // half of the rows by each query warp
       mbar_init(&s.q_empty[i], 5);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.s_empty[i], 4);
@@ -158,7 +179,8 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     mbar_init(&s.vote, 4);
     for (int i = 0; i < kSteps; ++i) {
       mbar_init(&s.step_full[i], 1);
-      mbar_init(&s.step_empty[i], 10);  // load, products, expanders, softmax: one for each warp
+      // load, products, second query warp, expanders, softmax: one for each warp
+      mbar_init(&s.step_empty[i], 11);
     }
     fence_mbar_init();
   }
@@ -179,6 +201,69 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   auto step_done = [&](uint32_t j) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.step_empty[j % kSteps]);
+  };
+
+  // A half of item i's query rows as their two terms: 16 lanes a row, 8 numbers a lane.
+  auto convert = [&](uint32_t i, int half) {
+    const uint32_t b = i & 1;
+    const Step& it = s.steps[i % kSteps];
+    const int rows = it.g.rows, row0 = it.g.row0, bos = it.bos, h = it.h, pos0 = it.pos0;
+    uint8_t* q = sQ + b * kQBytes;
+    const int c = lane & 15;
+    wait_or_die(&s.q_empty[b], ((i >> 1) & 1) ^ 1, dead);
+    constexpr int U = 4, kHalf = kRowsItem / 2;  // pairs of rows in flight
+    static_assert(kHalf == 2 * U, "a half at a time");
+#pragma unroll 1
+    for (int r0 = half * kHalf; r0 < min(rows, (half + 1) * kHalf); r0 += 2 * U) {
+      uint4 x[U];
+      int at[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = min(r0 + 2 * k + (lane >> 4), rows - 1);
+        const int tk = div_g(a, row0 + r), hg = row0 + r - tk * a.G;
+        at[k] = pos0 + tk;
+        x[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                               (long long)(bos + tk) * a.q_stride +
+                                               (long long)(h * a.G + hg) * D + c * 8);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = r0 + 2 * k + (lane >> 4);
+        const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = max(top, max(u[e] << 16 & 0x7fff0000u, u[e] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool odd = top >= 0x7f800000u;  // an infinity or a NaN: the row's scores are NaN
+        const int e = q8::exponent(top);
+        const float f = odd ? 0.f : q8::power(-e);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float y0 = odd ? 0.f : bf16_lo(u[p]) * f, y1 = odd ? 0.f : bf16_hi(u[p]) * f;
+          hi[p] = q8::pack2(y0, y1);
+          const float2 z = q8::unpack2(hi[p]);
+          lo[p] = q8::pack2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f);
+        }
+        if (r < rows) {
+          uint8_t* dst = q + (r >> 3) * 1024 + (r & 7) * 128 +
+                         (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2*>(dst + kRowsItem * 128) =
+              make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          if (c == 0) {
+            s.row_scale[b][r] =
+                odd ? __uint_as_float(0x7fc00000u) : q8::power(e) * (a.scale * kLog2E);
+            s.row_pos[b][r] = at[k];
+          }
+        }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full[b]);
   };
 
   if (warp >= kLoadWarp)
@@ -322,6 +407,11 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         np = tp < tq ? nx.v1 - nx.v0 : 0;
       }
     }
+  } else if (warp > kQueryWarp) {
+    for (uint32_t j = 0; step(j); ++j) {
+      convert(j, 1);
+      step_done(j);
+    }
   } else if (warp == kQueryWarp) {
     // The items, one ahead of the query rows of each.
     Walker w;
@@ -356,67 +446,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         mbar_arrive(&s.step_full[j % kSteps]);
       }
       __syncwarp();
-      // the rows of the item before: 16 lanes a row, 8 numbers a lane
-      if (j > 0) {
-        const uint32_t i = j - 1, b = i & 1;
-        const Step& it = s.steps[i % kSteps];
-        const int rows = it.g.rows, row0 = it.g.row0, bos = it.bos, h = it.h, pos0 = it.pos0;
-        uint8_t* q = sQ + b * kQBytes;
-        const int c = lane & 15;
-        wait_or_die(&s.q_empty[b], ((i >> 1) & 1) ^ 1, dead);
-        constexpr int U = 4;  // pairs of rows in flight
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 2 * U) {
-          uint4 x[U];
-          int at[U];
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int r = min(r0 + 2 * k + (lane >> 4), rows - 1);
-            const int tk = div_g(a, row0 + r), hg = row0 + r - tk * a.G;
-            at[k] = pos0 + tk;
-            x[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   (long long)(bos + tk) * a.q_stride +
-                                                   (long long)(h * a.G + hg) * D + c * 8);
-          }
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int r = r0 + 2 * k + (lane >> 4);
-            const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = max(top, max(u[e] << 16 & 0x7fff0000u, u[e] & 0x7fff0000u));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const bool odd = top >= 0x7f800000u;  // an infinity or a NaN: the row's scores are NaN
-            const int e = q8::exponent(top);
-            const float f = odd ? 0.f : q8::power(-e);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              const float y0 = odd ? 0.f : bf16_lo(u[p]) * f, y1 = odd ? 0.f : bf16_hi(u[p]) * f;
-              hi[p] = q8::pack2(y0, y1);
-              const float2 z = q8::unpack2(hi[p]);
-              lo[p] = q8::pack2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f);
-            }
-            if (r < rows) {
-              uint8_t* dst = q + (r >> 3) * 1024 + (r & 7) * 128 +
-                             (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              *reinterpret_cast<uint2*>(dst + kRowsItem * 128) =
-                  make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-              if (c == 0) {
-                s.row_scale[b][r] =
-                    odd ? __uint_as_float(0x7fc00000u) : q8::power(e) * (a.scale * kLog2E);
-                s.row_pos[b][r] = at[k];
-              }
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.q_full[b]);
-      }
+      if (j > 0) convert(j - 1, 0);  // the rows of the item before
       if (!here) break;
     }
     if (lane == 0) headers[blockIdx.x] = hd;
@@ -437,17 +467,17 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
         const uint32_t b = t & 1;
         wait_or_die(&s.vr_full[b], (t >> 1) & 1, dead);
         uint8_t* slot = sV + b * kVBytes;
-        uint4 w[D / 16];
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          w[c] = *reinterpret_cast<const uint4*>(slot + kKBytes + raw_offset<D>(r, c));
-#pragma unroll
+        // In a loop: little code, which a small call has to fetch.  (The pieces that are written over
+        // the row's bytes are behind those that have been read.)
+        uint4 w = *reinterpret_cast<const uint4*>(slot + kKBytes + raw_offset<D>(r, 0));
+#pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          if (c + 1 < D / 16)
+            w = *reinterpret_cast<const uint4*>(slot + kKBytes + raw_offset<D>(r, c + 1));
           uint32_t y[8];
-          q8::expand4<false>(w[c].x, one, y[0], y[1]);
-          q8::expand4<false>(w[c].y, one, y[2], y[3]);
-          q8::expand4<false>(w[c].z, one, y[4], y[5]);
-          q8::expand4<false>(w[c].w, one, y[6], y[7]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q8::expand4<false>(x[k], one, y[2 * k], y[2 * k + 1]);
           *reinterpret_cast<uint4*>(slot + piece_offset<D>(r, 2 * c)) =
               make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(slot + piece_offset<D>(r, 2 * c + 1)) =
@@ -500,9 +530,19 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           const float ck = q8::scale(s.k_scale[b][r]);
           wait_or_die(&s.s_full[b], ph, dead);
           tc_fence_after();
-          float x[NR], lo[NR];
-          tmem_ld<NR>(tm + kColS + 32 * b + lanebits, x);
-          tmem_ld<NR>(tm + kColS + 32 * b + kRowsItem + lanebits, lo);
+          float x[NR];
+          {
+            constexpr int W = NR < 8 ? NR : 8;
+            const uint32_t tS = tm + kColS + 32 * b + lanebits;
+#pragma unroll
+            for (int e = 0; e < NR; e += W) {
+              float hi[W], lo[W];
+              tmem_ld<W>(tS + e, hi);
+              tmem_ld<W>(tS + kRowsItem + e, lo);
+#pragma unroll
+              for (int k = 0; k < W; ++k) x[e + k] = fmaf(lo[k], 0.0625f, hi[k]);
+            }
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -516,7 +556,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           bool grown = false;
 #pragma unroll
           for (int e = 0; e < NR; ++e) {
-            x[e] = fmaf(lo[e], 0.0625f, x[e]) * (ck * s.row_scale[qb][e]);
+            x[e] *= ck * s.row_scale[qb][e];
             if (!whole && !visible(a, s.row_pos[qb][e], key)) {
               seen &= ~(1u << e);
               x[e] = -INFINITY;
@@ -530,17 +570,12 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           meet();
           const int4 v = *vt;
           if (v.x | v.y | v.z | v.w) {
-            float* mine = s.parts[nv & 1][warp];
+            float f[NR];
 #pragma unroll
-            for (int e = 0; e < NR; ++e) {
-              float y = x[e];
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-              if (lane == 0) mine[e] = y;
-            }
+            for (int e = 0; e < NR; ++e) f[e] = x[e];
+            join_lanes(f, s.parts[nv & 1][warp], [](float y, float z) { return fmaxf(y, z); });
             const float(*all)[kRowsItem] = s.parts[nv & 1];
             meet();
-            float f[NR];
 #pragma unroll
             for (int e = 0; e < NR; ++e) {
               const float y = fmaxf(fmaxf(all[0][e], all[1][e]), fmaxf(all[2][e], all[3][e]));
@@ -579,12 +614,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           if (lane == 0) mbar_arrive(&s.p_full);
         }
         // The item's result: the keys' sums joined, columns of O by each thread.
-        float* mine = s.parts[nv & 1][warp];
-#pragma unroll
-        for (int e = 0; e < NR; ++e) {
-          const float y = warp_sum(l[e]);
-          if (lane == 0) mine[e] = y;
-        }
+        join_lanes(l, s.parts[nv & 1][warp], [](float y, float z) { return y + z; });
         const float(*all)[kRowsItem] = s.parts[nv & 1];
         meet();
         wait_or_die(&s.pv_done, (t - 1) & 1, dead);
@@ -598,21 +628,26 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           mbar_arrive(&s.q_empty[qb]);
         }
         const bool cut0 = w.v0 > 0, cut = cut0 || w.v1 < w.g.nt;
-#pragma unroll
-        for (int e = 0; e < NR; ++e) {
-          if (e >= nr) break;
+        // In a loop that passes the values along: little code.
+#pragma unroll 1
+        for (int e = 0; e < nr; ++e) {
           const float sum = (all[0][e] + all[1][e]) + (all[2][e] + all[3][e]);
           const int row = w.g.row0 + e, tk = div_g(a, row);
           const long long orow = (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
           if (cut) {
             const long long p = (long long)(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRowsItem + e;
-            part_o[p * D + d] = o[e];
-            if (r == e) part_ml[p] = make_float2(m[e], sum);
+            part_o[p * D + d] = o[0];
+            if (r == 0) part_ml[p] = make_float2(m[0], sum);
           } else {
             static_cast<__nv_bfloat16*>(a.out)[orow * D + d] =
-                __float2bfloat16_rn(sum == 0.f ? 0.f : o[e] * (1.0f / sum));
-            if (r == e && a.lse)
-              a.lse[orow] = sum == 0.f ? -INFINITY : (m[e] + log2f(sum)) * 0.6931471805599453f;
+                __float2bfloat16_rn(sum == 0.f ? 0.f : o[0] * (1.0f / sum));
+            if (r == 0 && a.lse)
+              a.lse[orow] = sum == 0.f ? -INFINITY : (m[0] + log2f(sum)) * 0.6931471805599453f;
+          }
+#pragma unroll
+          for (int k = 0; k + 1 < NR; ++k) {
+            o[k] = o[k + 1];
+            m[k] = m[k + 1];
           }
         }
       };

@@ -370,6 +370,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up
+  if (KD) asm volatile("griddepcontrol.wait;" ::: "memory");  // for the queries' terms
   const uint32_t tm = s_tmem;
   bool dead = false;
   // The CTA's j-th step (null: none, or the warp has given up), and that the warp is done with it.
@@ -1474,9 +1475,24 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
     rows.at = reinterpret_cast<int4*>(rows.o + 2 * all * D);
     rows.ml = reinterpret_cast<float2*>(rows.at + 2 * all);
   }
-  kernel<<<kCtas, Group<Q8>::kThreads, C::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes, headers, po,
-                                                       ml, rows);
-  e = cudaGetLastError();
+  if constexpr (C::kDirect) {
+    // set up beside the kernel that makes the queries' terms
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kCtas);
+    cfg.blockDim = dim3(Group<Q8>::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, qmap, kmap, vmap, q_boxes, headers, po, ml, rows);
+  } else {
+    kernel<<<kCtas, Group<Q8>::kThreads, C::kSmem, st>>>(a, qmap, kmap, vmap, q_boxes, headers, po,
+                                                         ml, rows);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   if constexpr (!PRE) return launch_join<D>(a, headers, po, ml, st);
   cudaLaunchConfig_t cfg{};
