@@ -685,10 +685,6 @@ cudaError_t launch_paged_tc_q8_few(const PagedArgs& args, void* workspace, cudaS
   cudaError_t e = cudaFuncSetAttribute(paged_q8_few_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // (without it an SM may be set up for one CTA's shared memory: 139 us for 64 single tokens)
-  e = cudaFuncSetAttribute(paged_q8_few_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
   paged_q8_few_kernel<<<kStretches, kThreads, kSmem, st>>>(a, kmap, vmap, headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -111,7 +111,8 @@ template <int D, bool Q8> struct Cfg {
   // the scales of the tiles that have landed.
   static constexpr int kFront = (Q8 ? 4 : 3) * 1024;
   static constexpr int kStageBytes = kKeys * D * 2;
-  static constexpr int kStages = kDirect ? 3 : Q8 ? 6 : D == 128 ? 5 : 8;  // (direct: of each)
+  // (direct: of each, and no fewer: a unit's values wait for its next keys, two tiles on)
+  static constexpr int kStages = kDirect ? 3 : Q8 ? 6 : D == 128 ? 5 : 8;
   static constexpr int kBars = kDirect ? 2 * kStages : kStages;
   // A direct stage of keys: the tile, and the scales as fp32.
   static constexpr int kKeyBytes = kDirect ? kKeys * D + kKeys * 4 : 0;
@@ -883,9 +884,11 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const int tk = div_g(a, row);
 
       // 1. The unit's tiles.
-      if (KD)  // the power of two of the row's terms
+      if (KD) {  // with the power of two of the row's terms
         sc = a.scale * kLog2E *
              __ldg(a.q_scale + (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G));
+        if (sc < 1.2e-38f) sc = 1.2e-38f;  // (zero times a hidden key's -inf would be NaN)
+      }
       float m = -INFINITY, l = 0.f;
       int mine = 0;
       // (a prefix is seen to its last key by all)
@@ -974,7 +977,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
               c4[c / 2 & 3] =
                   max3(c4[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             m = fmaxf(max3(c4[0], c4[1], c4[2]), c4[3]);
-            if (kAhead > 0.f) m += kAhead / sc;
+            if (kAhead > 0.f) m += fminf(kAhead / sc, 1e30f);  // (sc may be next to nothing)
           }
           if (!C::kOwnP && whole) {
             // Weights against the maximum so far, which almost always stands, while the

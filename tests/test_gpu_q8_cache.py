@@ -558,3 +558,85 @@ def test_empty_calls(dt):
                                    d["out"], 1, 2, 2, 1, 64, 0, 16, 0, workspace=ws)
     torch.cuda.synchronize()
     assert (d["out"] == 0).all()
+
+
+# --------------------------------------------------------------------------- few rows, odd queries
+
+@pytest.mark.parametrize("G,Hkv", [(1, 3), (2, 2), (3, 1), (4, 2), (5, 1), (8, 1), (9, 1), (12, 1),
+                                   (16, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5), (1, 200)])
+def test_few_rows(G, Hkv, window, sinks):
+    """Up to 16 rows of a sequence, items of 16 where some have more; no keys, fewer keys than tokens,
+    many tiles, several items in a block and cut ones."""
+    d = make([(1, 1), (1, 129), (2, 300), (1, 0), (3, 1), (0, 7), (2, 2000), (1, 128), (1, 5000)] +
+             [(0, 3)] * 6, G * Hkv, Hkv, 128, 64, "bf16", seed=G + window, pad=2, fill="scale")
+    assert d["T"] * G <= 16 * d["N"]  # (16 rows a sequence on average, or fewer)
+    call(d, window=window, sinks=sinks)
+    pa.check(d, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("slope", [20.0, 150.0, 600.0, -300.0])
+def test_rising_scores_of_few_rows_and_of_chunks(slope):
+    """Scores that grow along the keys: the standing maximum moves, by less and more than what is
+    taken without scaling anew."""
+    for seqs in ([(1, 1500), (2, 1500), (1, 130)], [(200, 1500), (130, 130), (1, 1500)]):
+        d = make(seqs, 2, 1, 128, 64, "bf16", seed=13)
+        k = np.zeros(tuple(d["kb"].shape))
+        for n in range(3):
+            for j in range(int(d["kv_h"][n])):
+                k[int(d["table_h"][n, j // 64]), :, j % 64] = slope * j / 1500 / 128
+        b, s = q8_ref.quantise(k)
+        d["kb"], d["ks"] = e4m3(b), torch.from_numpy(s).cuda()
+        d["kc"] = torch.from_numpy(q8_ref.value(b, s)).cuda()
+        d["q"].copy_(torch.rand_like(d["q"].float()) + 0.5)
+        call(d, softmax_scale=1.0)
+        pa.check(d, scale=1.0)
+
+
+@pytest.mark.parametrize("dt,D", KINDS)
+@pytest.mark.parametrize("tokens", [1, 150])
+def test_queries_of_all_magnitudes(dt, D, tokens):
+    """Rows of zeros, of the smallest and of large numbers, and of numbers of very different sizes; an
+    infinity or a NaN in one row stays in it.  Scores of e^+-87 at most, so that nothing overflows."""
+    d = make([(tokens, 400), (tokens, 300), (tokens, 200)], 4, 1, D, 64, dt, seed=5)
+    q = d["q"].float().clone()
+    q[0, 0] = 0
+    q[0, 1] *= 1e-30
+    q[0, 2] *= 3.0
+    q[0, 3, ::2] *= 2.0 ** -9
+    d["q"].copy_(q)
+    call(d)
+    pa.check(d)
+    # next to no scale: all keys alike
+    call(d, softmax_scale=1e-30)
+    pa.check(d, scale=1e-30)
+    a = d["out"].clone()
+    d["q"][tokens, 2, 3] = float("inf")
+    d["q"][tokens, 1, 0] = float("nan")
+    call(d, softmax_scale=1e-30)
+    same = torch.ones(d["T"], 4, dtype=torch.bool, device="cuda")
+    same[tokens, 1:3] = False
+    assert torch.equal(a[same], d["out"][same])
+    assert torch.isnan(d["out"][tokens, 1]).all() and not torch.isfinite(d["out"][tokens, 2]).any()
+
+
+@pytest.mark.parametrize("tokens", [1, 100])
+def test_graphs_that_share_a_workspace(tokens):
+    """Two captured calls with one buffer, replayed in turn."""
+    ds = [make([(tokens, 700), (tokens, 900), (1, 64)], 8, 2, 128, 64, "bf16", seed=70),
+          make([(tokens, int(k)) for k in range(140, 1500, 99)], 8, 2, 128, 32, "bf16", seed=71)]
+    n = max(kda.kda_paged_attention_q8_fwd_workspace_size(d["N"], d["T"], 8, 2, 128) for d in ds)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    graphs, want = [], []
+    for d in ds:
+        call(d)
+        want.append(d["out"].clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(d, ws=ws)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        ds[i]["out"].fill_(3)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ds[i]["out"], want[i])

@@ -69,6 +69,267 @@ def test_landing_ring(raw, stages):
                 del roles[r], weights[r]
 
 
+def interleave(rnd, roles, events, limit=300_000):
+    """Runs coroutines in random turns; events(): what the hardware may do meanwhile."""
+    weights = [rnd.choice([1, 1, 5, 20]) for _ in roles]
+    idle = 0
+    while roles:
+        events()
+        r = rnd.choices(range(len(roles)), weights)[0]
+        idle += 1
+        assert idle < limit, "no end"
+        try:
+            next(roles[r])
+        except StopIteration:
+            del roles[r], weights[r]
+
+
+def test_two_stages_of_keys_are_not_enough():
+    """A unit's values wait for its next keys, two tiles on, while the other's keys are held."""
+    with pytest.raises(AssertionError, match="no end"):
+        test_keys_and_values_in_rings_of_their_own(2)
+
+
+@pytest.mark.parametrize("stages", [3, 4])
+def test_keys_and_values_in_rings_of_their_own(stages):
+    """Direct keys: a step's tiles in the order of one ring, keys and values each with stages of
+    their own; keys are let go with the values of their tile."""
+    for seed in range(200):
+        rnd = random.Random(seed)
+        steps = []
+        for _ in range(rnd.randint(1, 6)):
+            n, x = rnd.choice([1, 1, 2, 3, 5]), rnd.random()
+            steps.append(pm.Step("wide", n) if x < 0.4 else pm.Step("split", n) if x < 0.7 else
+                         pm.Step("pair", n, rnd.choice([1, 2, 4])))
+        bars = lambda c: [pm.Bar(c) for _ in range(2 * stages)]  # noqa: E731
+        raw, full, empty = bars(1), bars(4), bars(2)
+        holds, flying, commits = [None] * 2 * stages, [], [[], []]
+
+        def place(s, base, e):
+            keys, t = list(s.loads())[e]
+            i = base + t
+            return (0 if keys else stages) + i % stages, i // stages
+
+        def load():
+            base = 0
+            for s in steps:
+                for e in range(2 * s.n):
+                    at, k = place(s, base, e)
+                    yield from pm.free(empty[at], k)
+                    holds[at] = (base, e)
+                    flying.append(raw[at])
+                    yield
+                base += s.n
+
+        def expand():
+            base = 0
+            for s in steps:
+                for e in range(2 * s.n):
+                    at, k = place(s, base, e)
+                    yield from pm.full(raw[at], k)
+                    assert holds[at] == (base, e)
+                    yield
+                    full[at].arrive()
+                base += s.n
+
+        def products(u):
+            base = 0
+            for s in steps:
+                seen = 0
+                split, wide = s.kind == "split", s.kind == "wide"
+                n = s.n if split else s.tiles[u]
+                first, by = (u, 2) if split else (0, 1)
+
+                def ready(e):
+                    nonlocal seen
+                    while seen <= e:
+                        at, k = place(s, base, seen)
+                        yield from pm.full(full[at], k)
+                        if not wide and s.owner(seen) != u:
+                            empty[at].arrive()
+                        seen += 1
+
+                if first < n:
+                    yield from ready(s.key(s.tile(u, first)))
+                for i in range(first, n, by):
+                    t = s.tile(u, i)
+                    yield from ready(s.value(t))
+                    if i + by < n:
+                        yield from ready(s.key(s.tile(u, i + by)))
+                    for _ in range(rnd.randint(0, 6)):  # the softmax, which reads the keys' scales
+                        yield
+                    for e in (s.value(t), s.key(t)):
+                        at, _ = place(s, base, e)
+                        assert holds[at] == (base, e)
+                        commits[u].append(empty[at])
+                yield from ready(2 * s.n - 1)
+                base += s.n
+
+        def events():
+            if flying and rnd.random() < 0.3:
+                flying.pop(rnd.randrange(len(flying))).arrive()
+            for c in commits:
+                if c and rnd.random() < 0.3:
+                    c.pop(0).arrive()
+
+        interleave(rnd, [load(), products(0), products(1)] + [expand() for _ in range(4)], events)
+
+
+def test_pipeline_of_few_rows():
+    """The kernel for few rows: load, products (scores a tile ahead), two query warps, expanders and
+    softmax warps that meet at every tile."""
+    W = 2  # warps of the softmax and of the expanders (the kernel has four)
+    for seed in range(250):
+        rnd = random.Random(seed)
+        items = [rnd.choice([1, 1, 1, 2, 3, 6]) for _ in range(rnd.randint(1, 10))]
+        two = lambda c: [pm.Bar(c), pm.Bar(c)]  # noqa: E731
+        k_full, k_empty, vr_full, v_full, v_empty = two(1), two(1 + W), two(1), two(W), two(1)
+        q_full, q_empty, s_full, s_empty, o_empty = two(2), two(1 + W), two(1), two(W), two(W)
+        p_full, pv_done, vote = pm.Bar(W), pm.Bar(1), pm.Bar(W)
+        step_full, step_empty = [pm.Bar(1) for _ in range(4)], [pm.Bar(3 + 2 * W) for _ in range(4)]
+        slots, keys, vals, scores = [None] * 4, [None] * 2, [None] * 2, [None] * 2
+        flying, commits = [], []
+
+        def get(j):
+            yield from pm.full(step_full[j % 4], j // 4)
+            assert slots[j % 4][0] == j
+            return slots[j % 4][1]
+
+        def load():
+            kp = vp = j = 0
+            while (n := (yield from get(j))) is not None:
+                for t in range(-1, n):
+                    for isk in (True, False):
+                        y = t + 1 if isk else t
+                        if not 0 <= y < n:
+                            continue
+                        p = kp if isk else vp
+                        yield from pm.free((k_empty if isk else v_empty)[p & 1], p >> 1)
+                        (keys if isk else vals)[p & 1] = p
+                        flying.append((k_full if isk else vr_full)[p & 1])
+                        kp, vp = kp + isk, vp + (not isk)
+                step_empty[j % 4].arrive()
+                j += 1
+
+        def convert(i):
+            yield from pm.free(q_empty[i & 1], i >> 1)
+            yield
+            q_full[i & 1].arrive()
+
+        def query():
+            for j in range(len(items) + 1):
+                yield from pm.free(step_empty[j % 4], j // 4)
+                slots[j % 4] = (j, items[j] if j < len(items) else None)
+                yield
+                step_full[j % 4].arrive()
+                if j:
+                    yield from convert(j - 1)
+
+        def second():
+            j = 0
+            while (yield from get(j)) is not None:
+                yield from convert(j)
+                step_empty[j % 4].arrive()
+                j += 1
+
+        def products():
+            jq = tq = iq = jp = tp = ip = 0
+            sq = yield from get(0)
+            sizes = {0: sq}
+
+            def issue():
+                nonlocal jq, tq, iq, sq
+                if sq is None:
+                    return
+                if iq == 0:
+                    yield from pm.full(q_full[jq & 1], jq >> 1)
+                yield from pm.full(k_full[tq & 1], tq >> 1)
+                yield from pm.free(s_empty[tq & 1], tq >> 1)
+                assert keys[tq & 1] == tq
+                scores[tq & 1] = tq
+                iq += 1
+                commits.extend([s_full[tq & 1], k_empty[tq & 1]])
+                if iq == sq:
+                    commits.append(q_empty[jq & 1])
+                tq += 1
+                if iq == sq:
+                    iq, jq = 0, jq + 1
+                    sq = sizes[jq] = yield from get(jq)
+
+            yield from issue()
+            while tp < tq:
+                yield from issue()
+                if ip == 0:
+                    yield from pm.free(o_empty[jp & 1], jp >> 1)
+                yield from pm.full(v_full[tp & 1], tp >> 1)
+                yield from pm.full(p_full, tp)
+                assert vals[tp & 1] == tp
+                commits.extend([pv_done, v_empty[tp & 1]])
+                tp, ip = tp + 1, ip + 1
+                if ip == sizes[jp]:
+                    step_empty[jp % 4].arrive()
+                    ip, jp = 0, jp + 1
+
+        def expand():
+            t = j = 0
+            while (n := (yield from get(j))) is not None:
+                for _ in range(n):
+                    yield from pm.full(vr_full[t & 1], t >> 1)
+                    assert vals[t & 1] == t
+                    yield
+                    v_full[t & 1].arrive()
+                    t += 1
+                step_empty[j % 4].arrive()
+                j += 1
+
+        grown = {}
+
+        def softmax():
+            t = nv = j = 0
+
+            def meet():
+                nonlocal nv
+                vote.arrive()
+                yield from pm.full(vote, nv)
+                nv += 1
+
+            while (n := (yield from get(j))) is not None:
+                yield from pm.full(q_full[j & 1], j >> 1)
+                for i in range(n):
+                    yield from pm.full(k_full[t & 1], t >> 1)
+                    yield from pm.full(s_full[t & 1], t >> 1)
+                    assert scores[t & 1] == t and keys[t & 1] == t
+                    yield
+                    s_empty[t & 1].arrive()
+                    k_empty[t & 1].arrive()
+                    yield from meet()
+                    if grown.setdefault(t, i == 0 or rnd.random() < 0.2):
+                        yield from meet()
+                        if i:
+                            yield from pm.full(pv_done, t - 1)
+                    yield from pm.full(vr_full[t & 1], t >> 1)
+                    if t:
+                        yield from pm.full(pv_done, t - 1)
+                    yield
+                    p_full.arrive()
+                    t += 1
+                yield from meet()
+                yield from pm.full(pv_done, t - 1)
+                o_empty[j & 1].arrive()
+                q_empty[j & 1].arrive()
+                step_empty[j % 4].arrive()
+                j += 1
+
+        def events():
+            if flying and rnd.random() < 0.3:
+                flying.pop(rnd.randrange(len(flying))).arrive()
+            if commits and rnd.random() < 0.4:
+                commits.pop(0).arrive()
+
+        interleave(rnd, [load(), query(), second(), products()] + [expand() for _ in range(W)] +
+                   [softmax() for _ in range(W)], events)
+
+
 def test_the_definition_of_a_row():
     rng = np.random.default_rng(0)
     y = rng.standard_normal((200, 32)) * 2.0 ** rng.integers(-140, 120, (200, 1))
