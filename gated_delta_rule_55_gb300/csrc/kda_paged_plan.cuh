@@ -494,7 +494,8 @@ __device__ __forceinline__ void join_items(const PagedArgs& a, const Header* hea
   // The first of its tiles that begins in CTA k's stretch or behind it.
   auto first_of = [&](int k) {
     const int x = stretch<kStretches>(hd.total, k) - hd.start;
-    return unit == 1 ? x : x <= 0 ? 0 : (x + unit - 1) / unit;
+    if (kTileMost == 1) return x;
+    return x <= 0 ? 0 : unit == kTile ? (x + kTile - 1) / kTile : (x + kTileMost - 1) / kTileMost;
   };
   for (int at = y * 256 + threadIdx.x; at < hd.rows * PIECES; at += ny * 256) {
     const int r = at / PIECES, e = at % PIECES;
