@@ -296,7 +296,7 @@ int kda_paged_cache_read_q8(const void* k_cache, const void* v_cache, const uint
   const void* const ptrs[] = {k_cache, v_cache, k_scale, v_scale, slots, key_out, value_out};
   if (!all_aligned16(ptrs)) return KDA_ERR_MISALIGNED;
   if ((double)num_pages * Hkv * page_size * D >= kMaxElems ||
-      (double)Hkv * (D / 16) > 65535.0 * 64)
+      (double)T * Hkv * D >= kMaxElems || (double)Hkv * (D / 16) > 65535.0 * 64)
     return KDA_ERR_TOO_LARGE;
   const int s = kda::check_current_device();
   if (s != KDA_OK) return s;
