@@ -9,6 +9,9 @@
 // a long key range is cut into parts (for few rows) whose (m, l, o) are joined by a second
 // kernel, and blocks share an SM.  5 sequences of 1..17 tokens over up to 700 keys, 4 + 4 heads
 // of 64: 11.5 us.  Chunks take taller tiles (below), which the FMA pipes bound.
+//
+// Rows in 8 bits are expanded to fp32 on their way into shared memory.  With prefixes the parts of
+// both of a row's lists are joined by the second kernel.
 #include "kda_paged.cuh"
 #include "kda_q8.cuh"
 
@@ -673,8 +676,10 @@ size_t paged_simt_workspace(int total_T, int Hq, int D, bool prefix) {
 cudaError_t launch_paged_simt(const PagedArgs& a, void* workspace, cudaStream_t st) {
   const bool q8 = a.k_scale != nullptr;
   switch (a.D) {
-    case 32: return q8 ? launch_t<32, true>(a, workspace, st) : launch_t<32, false>(a, workspace, st);
-    case 64: return q8 ? launch_t<64, true>(a, workspace, st) : launch_t<64, false>(a, workspace, st);
+    case 32:
+      return q8 ? launch_t<32, true>(a, workspace, st) : launch_t<32, false>(a, workspace, st);
+    case 64:
+      return q8 ? launch_t<64, true>(a, workspace, st) : launch_t<64, false>(a, workspace, st);
     default:
       return q8 ? launch_t<128, true>(a, workspace, st) : launch_t<128, false>(a, workspace, st);
   }

@@ -1,5 +1,5 @@
 // The line of key tiles that attention over a paged cache cuts among its CTAs
-// (kda_paged_attn.cu).  Plain integer arithmetic, so that the host can compile it too.
+// (kda_paged_plan.cuh).  Plain integer arithmetic, so that the host can compile it too.
 #pragma once
 
 #ifdef __CUDACC__

@@ -6,8 +6,8 @@
 //   kTile        units of the line that a tile counts; kTileMost, one of an item with more than
 //                kRowsFew rows
 //   kPrefixes    whether calls have prefixes
-//   kOverhead    units that an item counts beside its tiles; kOverheadMost, one of D = 128 with more
-//                than kRowsFew rows
+//   kOverhead    units that an item counts beside its tiles; kOverheadMost, one of D = 128 with
+//                more than kRowsFew rows
 #pragma once
 
 #include "chunk_common.cuh"
@@ -58,10 +58,10 @@ struct Geometry {
   }
 };
 
-// A group whose sequences have kAlone rows and more on average fills the products' tiles without its
-// neighbours: its sequences take the prefix along with their own keys, as one list of tiles, and
-// there is nothing to join.  (2300 tokens of 8 sequences behind 8191 keys, 32 + 8 heads of 128: 250
-// us when their prefix was worked on for all of them.)
+// A group whose sequences have kAlone rows and more on average fills the products' tiles without
+// its neighbours: its sequences take the prefix along with their own keys, as one list of tiles,
+// and there is nothing to join.  (2300 tokens of 8 sequences behind 8191 keys, 32 + 8 heads of 128:
+// 250 us when their prefix was worked on for all of them.)
 constexpr int kAlone = 768;
 
 __device__ __forceinline__ bool group_alone(const PagedArgs& a, int g) {
@@ -440,8 +440,8 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint6
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }

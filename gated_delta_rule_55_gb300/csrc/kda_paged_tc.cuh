@@ -48,6 +48,23 @@
 //   cut, barriers, first loads) takes 4; then items' starts and ends.
 //   One token over 1000 keys: 12 us of latencies in a row.
 //
+// Caches in 8 bits (Q8).  D = 128: a key tile is an operand as it lands, e4m3 with e4m3, the
+// queries as two terms hi + lo of that type (made before, kda_cache_q8.cu), whose two products take
+// the tensor cores as long as one of bf16; the scores are multiplied by their keys' scales, and a
+// fourth warpgroup expands value tiles to bf16 where they landed, a thread for each key's row.  The
+// columns of four change places on the way (kda_q8.cuh), and O's change back as it is read.  2
+// chunks of 2048 tokens behind 8192 keys, 32 + 8 heads: 538 us, 61% of a library product's rate
+// (over bf16 pages 394 to 406: the expanding takes 105 us of the softmax warps' issue slots, the
+// keys' scales 37); with keys expanded too 932.  The expanding is a loop (unrolled: 618).  D <= 64:
+// keys and values land in a ring of their own and are expanded, with their scales, into that of the
+// products.
+//
+// Shared prefixes (PRE).  A row has two lists of keys, its group's prefix and its own, both of them
+// items of the line; each item leaves its rows' (m, l, O), whole or in parts, and paged_rows_kernel
+// joins a row's two sides.  64 single tokens behind 16384 shared and 16..1024 own keys, 32 + 8
+// heads of 128: 54 us for 30 of bytes.  8 chunks of 100..512 tokens behind 8191 keys: 233 to 241 us
+// (161 of flops); their groups go alone (kda_paged_plan.cuh).
+//
 // Softmax weights are rounded to bf16 for the product (their sum is taken before, in fp32).
 // Keys that no row of the item sees (behind the last one, outside the window, pages that are
 // not loaded) have weight zero and their values are overwritten with zeros in shared memory,
@@ -84,8 +101,8 @@ constexpr int kRowsUnit = 128;   // query rows of a unit
 constexpr int kLoadWarp = 8, kMmaWarp = 9 /* and 10: one per unit */, kQueryWarp = 11;
 constexpr int kExpandWarp = 12;  // and 13 to 15: caches in 8 bits
 
-// Two softmax warpgroups, one of the warps above, and one that expands 8-bit tiles.  Registers:
-// 168 a thread at launch (3 x 128 threads), moved to the softmax warpgroups: 2 x 216 + 72 = 3 x 168;
+// Two softmax warpgroups, one of the warps above, and one that expands 8-bit tiles.  Registers: 168
+// a thread at launch (3 x 128 threads), moved to the softmax warpgroups: 2 x 216 + 72 = 3 x 168;
 // with the fourth warpgroup 128: 2 x 184 + 72 + 72 = 4 x 128.
 template <bool Q8> struct Group {
   static constexpr int kThreads = Q8 ? 512 : 384;
@@ -584,9 +601,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
       const bool leader = elect_one();
       uint32_t pos = 0, seen = 0, np = 0, items = 0, wides = 0, turns = 0, nscores = 0;
       uint32_t k_last = 0;  // stage of the last scores' keys
-      // Ring entries up to number e of the step have landed.  Every entry is waited for in turn, and
-      // the other unit's are let go at once: a stage is refilled only when both units have passed
-      // it, so no barrier is ever more than the one phase away that a parity can tell.
+      // Ring entries up to number e of the step have landed.  Every entry is waited for in turn,
+      // and the other unit's are let go at once: a stage is refilled only when both units have
+      // passed it, so no barrier is ever more than the one phase away that a parity can tell.
       auto ready = [&](int e, const Order& o) {
         for (; (int)(pos + e - seen) >= 0; ++seen) {
           const int x = (int)(seen - pos);
@@ -1300,11 +1317,11 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 }
 
 // Joins what a row has of its prefix and of its own keys, each of which lies whole in `rows` or in
-// parts with the CTAs that its item was cut among.  A warp a row: half of its lanes look at a side's
-// CTAs each, so that all parts' (m, l) and their columns, D / 32 of them a lane, are one round trip
-// to memory.  A warp has `per` rows, one after the other.  The first `joins` blocks, a multiple of
-// the CTAs, join the items whose rows have no other side.  (Whatever the numbers of a row that no
-// item had are, they are made places inside the workspace.)
+// parts with the CTAs that its item was cut among.  A warp a row: half of its lanes look at a
+// side's CTAs each, so that all parts' (m, l) and their columns, D / 32 of them a lane, are one
+// round trip to memory.  A warp has `per` rows, one after the other.  The first `joins` blocks, a
+// multiple of the CTAs, join the items whose rows have no other side.  (Whatever the numbers of a
+// row that no item had are, they are made places inside the workspace.)
 template <int D>
 __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows, int per,
                                                          int joins, const Header* headers,
@@ -1461,9 +1478,9 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
   float* po = reinterpret_cast<float*>(ml + (size_t)2 * kCtas * kRowsItem);
   // D <= 64: chunks of 2048 behind 8192 keys, 32 + 4 heads of 64: 320 us for 352 with one pass over
   // whole tiles, 148 for 162 with D = 32.  Masked tiles are faster unrolled, which the one pass
-  // does not go with; under a window they can be many (a third in the windowed batch above: 36.2 us for
-  // 35.1).  How many there are lies in device memory, so any window counts as narrow: a chunk under
-  // a wide one forgoes the gain.
+  // does not go with; under a window they can be many (a third in the windowed batch above: 36.2 us
+  // for 35.1).  How many there are lies in device memory, so any window counts as narrow: a chunk
+  // under a wide one forgoes the gain.
   using C = Cfg<D, Q8>;
   auto kernel = paged_tc_kernel<D, PRE && C::kOwnP, Q8, PRE>;  // (prefixes: no window)
   if constexpr (C::kOwnP && !PRE)
@@ -1500,7 +1517,8 @@ cudaError_t launch_t(PagedArgs a, void* workspace, void* query_terms, cudaStream
   if constexpr (!PRE) return launch_join<D>(a, headers, po, ml, st);
   cudaLaunchConfig_t cfg{};
   // A warp looks at several rows, most of which may be done, where there are more than the SMs have
-  // room for warps (with few, one after the other takes longer: 130 tokens of 16 heads 34 us for 27).
+  // room for warps (with few, one after the other takes longer: 130 tokens of 16 heads 34 us for
+  // 27).
   const int per = a.alone && all > kCtas * 64 ? 4 : 1, joins = a.alone ? 8 * kCtas : 0;
   cfg.gridDim = dim3((unsigned)(joins + (all + 8 * per - 1) / (8 * per)));
   cfg.blockDim = dim3(256);

@@ -548,9 +548,11 @@ int kda_qk_norm_rope_append(const void* query, const void* key, const void* valu
  *   mantissa bits, largest 448) and one byte b:
  *       e = the smallest integer with max |y| <= 448 * 2^e, within [-110, 119],  b = e + 127
  *       number_i = y_i / 2^e to nearest, halves to even;   it stands for number_i * 2^e
- *   Keys are normed and turned in fp32 and rounded once, to the 8 bits; a number within fp32's error
- *   of the middle between two may become either.  Magnitudes above 448 * 2^119 (2.98e38) are kept
- *   as that.  A row with an infinity or a NaN is kept with b = 255 and stands for NaNs.
+ *   (the numbers 0x7f and 0xff, e4m3's NaNs, are never written, and what attention makes of them
+ *   is not specified)
+ *   Keys are normed and turned in fp32 and rounded once, to the 8 bits; a number within fp32's
+ *   error of the middle between two may become either.  Magnitudes above 448 * 2^119 (2.98e38) are
+ *   kept as that.  A row with an infinity or a NaN is kept with b = 255 and stands for NaNs.
  *
  *   k_cache, v_cache [num_pages, Hkv, page_size, D] 8-bit numbers
  *   k_scale, v_scale [num_pages, Hkv, page_size]    the bytes b
@@ -657,10 +659,12 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   v_scale [num_pages, Hkv, page_size].  query and out stay in dtype.  Rows are expanded exactly,
  *   so the result is that of kda_paged_attention_fwd over the values that the cache stands for; a
  *   seen row with b = 255 makes what sees it NaN.  All other arguments, limits and errors are those
- *   of kda_paged_attention_fwd; the workspace's size is kda_paged_attention_q8_fwd_workspace_size's,
- *   which never decreases as N or total_T grows.  bf16 with D = 128 multiplies queries in two terms
- *   of 8 bits, which are off by at most 2^-18 of the row's largest element where an element is less
- *   than 2^-10 of it, and exact otherwise.
+ *   of kda_paged_attention_fwd; the workspace's size is
+ *   kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N or total_T grows.
+ *   bf16 with D = 128 multiplies queries in two terms of 8 bits, which are off by at most 2^-17 of
+ *   the row's largest element where an element is less than 2^-9 of it, and exact otherwise (rows
+ *   below 2^-102 aside); its running maximum absorbs a growth of 2^40, so that values above 2^80
+ *   may overflow on the way (kda_paged_attention_fwd: 2^8).
  */
 size_t kda_paged_attention_q8_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
                                                  int dtype);
@@ -674,9 +678,9 @@ int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const voi
                                size_t workspace_bytes, kda_stream_t stream);
 
 /*
- * kda_paged_prefix_attention_fwd -- kda_paged_attention_fwd for sequences that share what they begin
- *   with (a system prompt, a document): sequences cu_groups[g] .. cu_groups[g + 1] - 1 have the
- *   prefix_lens[g] keys of prefix g in front of their own, all of which all of their new tokens see.
+ * kda_paged_prefix_attention_fwd -- kda_paged_attention_fwd for sequences that share what they
+ *   begin with (a system prompt, a document): sequences cu_groups[g] .. cu_groups[g + 1] - 1 have
+ *   the prefix_lens[g] keys of prefix g in front of their own, which all of their new tokens see.
  *   A prefix is worked on once for all tokens of its group, so its keys are read once and meet
  *   full tiles of queries:
  *       o = sum_j softmax_j(scale q . k_j) v_j   over the prefix's keys and the sequence's own
@@ -693,8 +697,9 @@ int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const voi
  *   k_cache, v_cache, k_scale, v_scale: pages of dtype with both scales NULL, or in 8 bits
  *                (kda_paged_attention_q8_fwd)
  *   num_groups = 0: kda_paged_attention_fwd (the three prefix arguments may be NULL)
- *   There is no window.  bf16 limit: the line counts the prefixes as sequences of all of their
- *   groups' tokens.  num_groups at most 65535.  All else as for kda_paged_attention_fwd.
+ *   There is no window.  bf16 counts three times the units of kda_paged_attention_fwd's limit,
+ *   at max_prefix_pages + max_pages, and adds those of num_groups sequences of all tokens at
+ *   max_prefix_pages.  num_groups at most 65535.  All else as for kda_paged_attention_fwd.
  *   workspace    at least kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq,
  *                Hkv, D, dtype) bytes, 256-byte aligned; the size never decreases as num_groups,
  *                N or total_T grows.

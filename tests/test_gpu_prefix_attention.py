@@ -1,6 +1,6 @@
 """kda_paged_prefix_attention_fwd against the fp64 definition, over pages of bf16, fp32 and 8 bits.
 
-Tolerances: those of kda_paged_attention_fwd (test_gpu_paged_attention.py) over all keys that a token
+Tolerances: those of kda_paged_attention_fwd (test_gpu_paged_attention.py) over all keys a token
 sees, and for the joining of its two parts 2^-20 of A = sum p |v| (two factors e^{m_i - m} and the
 quotient, each of fp32)."""
 import numpy as np

@@ -566,7 +566,7 @@ def test_empty_calls(dt):
                                    (16, 2)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5), (1, 200)])
 def test_few_rows(G, Hkv, window, sinks):
-    """Up to 16 rows of a sequence, items of 16 where some have more; no keys, fewer keys than tokens,
+    """Up to 16 rows of a sequence, items of 16 where some have more; none, fewer keys than tokens,
     many tiles, several items in a block and cut ones."""
     d = make([(1, 1), (1, 129), (2, 300), (1, 0), (3, 1), (0, 7), (2, 2000), (1, 128), (1, 5000)] +
              [(0, 3)] * 6, G * Hkv, Hkv, 128, 64, "bf16", seed=G + window, pad=2, fill="scale")
@@ -596,8 +596,8 @@ def test_rising_scores_of_few_rows_and_of_chunks(slope):
 @pytest.mark.parametrize("dt,D", KINDS)
 @pytest.mark.parametrize("tokens", [1, 150])
 def test_queries_of_all_magnitudes(dt, D, tokens):
-    """Rows of zeros, of the smallest and of large numbers, and of numbers of very different sizes; an
-    infinity or a NaN in one row stays in it.  Scores of e^+-87 at most, so that nothing overflows."""
+    """Rows of zeros, of the smallest and of large numbers, and of numbers of very different sizes;
+    an infinity or a NaN in one row stays in it.  Scores of e^+-87 at most, so that nothing overflows."""
     d = make([(tokens, 400), (tokens, 300), (tokens, 200)], 4, 1, D, 64, dt, seed=5)
     q = d["q"].float().clone()
     q[0, 0] = 0
