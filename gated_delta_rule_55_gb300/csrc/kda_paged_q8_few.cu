@@ -1,5 +1,5 @@
-// Attention of few new tokens (single ones, or a handful) over a paged cache in 8 bits, D = 128, on
-// the tensor cores: kda_paged_attention_q8_fwd where kda_paged_tc.cuh's tiles of 128 query rows
+// Attention of few new tokens (single ones, or a handful) over a paged cache in 8 bits, D = 64 or
+// 128, on the tensor cores: kda_paged_attention_q8_fwd where kda_paged_tc.cuh's tiles of 128 query rows
 // would be almost empty.
 //
 // The products are turned round: keys and values are the 128 rows of the tiles, the query rows (16
@@ -18,7 +18,7 @@
 // weights: bf16(p 2^scale(v)).
 //
 // One CTA is one line's stretch (kda_paged_plan.cuh) with a ring of two tiles of keys and two of
-// values, half of an SM's shared memory; two CTAs share an SM, and one's chain of waits (scores,
+// values (D = 64: three), half of an SM's shared memory; two CTAs share an SM, and one's chain of waits (scores,
 // softmax, values) passes beside the other's.
 //
 // What bounds it, and measured (alone on the GPU, 32 + 8 heads): 64 single tokens over 512..8192
@@ -27,7 +27,9 @@
 // keys 83 us, where items' starts and ends count; one token over 1000 keys 11.5 us of latencies in
 // a row.  The code is kept small (loops for the expanding and the results): a small call has to
 // fetch it first.  With the expanding unrolled the long caches take 2% less, the short ones 15%
-// more.
+// more.  D = 64: the 64 single tokens 83 us (161 through tiles of 128 query rows, 104 over bf16
+// pages) for 41 of bytes, one token over 1000 keys 10.9 (13.2): a tile is half of the bytes in the
+// same chain of waits.
 #include "kda_paged_line.h"
 
 namespace kda {
@@ -46,7 +48,6 @@ constexpr int kOverhead = 2, kOverheadMost = 2;  // units of the line that an it
 namespace kda {
 namespace {
 
-constexpr int D = 128;
 constexpr int kThreads = 384;  // softmax, expanders, and the warps below
 constexpr int kExpandWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kQueryWarp = 10 /* and 11 */;
 // Registers: 80 a thread at launch, 3 x 80 = 112 + 64 + 64.
@@ -55,11 +56,17 @@ constexpr float kRescale = 32.0f;  // log2 growth of the maximum that O and l ab
 constexpr int kSteps = 4;         // items put down ahead
 
 constexpr int kFront = 5 * 1024;                  // barriers, the plan, scales
-constexpr int kQBytes = 2 * kRowsItem * D;        // hi rows, lo rows
 constexpr int kPBytes = kRowsItem * kKeys * 2;
-constexpr int kKBytes = kKeys * D, kVBytes = kKeys * D * 2;
-constexpr int kSmem = kFront + 2 * kQBytes + kPBytes + 2 * kKBytes + 2 * kVBytes;
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+constexpr int kLand = kKeys * 128;  // where a slot's values land: D = 128, in its upper half
+template <int D> struct Cfg {
+  static constexpr int kStages = D == 128 ? 2 : 3;   // tiles of keys, of values
+  static constexpr int kQBytes = 2 * kRowsItem * D;  // hi rows, lo rows
+  static constexpr int kKBytes = kKeys * D;
+  static constexpr int kVBytes = D == 128 ? 2 * kLand : kLand + kKBytes;
+  static constexpr int kSmem = kFront + 2 * kQBytes + kPBytes + kStages * (kKBytes + kVBytes);
+  static constexpr uint32_t kSwizzleK = D == 128 ? kSwizzle128 : 4;  // its rows: 128 or 64 bytes
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+};
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 128;  // two of 32 (hi, lo), two of 16
 
 struct Step {
@@ -69,20 +76,20 @@ struct Step {
   Geometry g;
 };
 
-struct Small {
-  uint64_t k_full[2], k_empty[2], vr_full[2], v_full[2], v_empty[2], q_full[2], q_empty[2],
+template <int NS> struct Small {
+  uint64_t k_full[NS], k_empty[NS], vr_full[NS], v_full[NS], v_empty[NS], q_full[2], q_empty[2],
       s_full[2], s_empty[2], o_empty[2], p_full, pv_done, vote, step_full[kSteps],
       step_empty[kSteps];
   Plan plan;
   Step steps[kSteps];
   uint32_t tmem;
-  alignas(16) uint8_t k_scale[2][kKeys], v_scale[2][kKeys];
+  alignas(16) uint8_t k_scale[NS][kKeys], v_scale[NS][kKeys];
   alignas(16) float row_scale[2][kRowsItem];  // 2^e scale log2(e)
   alignas(16) int row_pos[2][kRowsItem];
   alignas(16) int votes[2][4];
   alignas(16) float parts[2][4][kRowsItem];   // a warp's maxima, sums
 };
-static_assert(sizeof(Small) <= kFront, "front");
+static_assert(sizeof(Small<3>) <= kFront, "front");
 
 template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
   uint32_t r[N];
@@ -151,16 +158,20 @@ __device__ __forceinline__ void join_lanes(float (&v)[N], float* out, F op) {
   if ((lane & (32 / N - 1)) == 0) out[e] = v[0];
 }
 
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, Header* headers, float* part_o,
                     float2* part_ml) {
+  using C = Cfg<D>;
+  constexpr int NS = C::kStages, kQBytes = C::kQBytes, kKBytes = C::kKBytes,
+                kVBytes = C::kVBytes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Small& s = *reinterpret_cast<Small*>(smem_raw);
+  Small<NS>& s = *reinterpret_cast<Small<NS>*>(smem_raw);
   uint8_t* sQ = smem_raw + kFront;   // two stages
   uint8_t* sP = sQ + 2 * kQBytes;
-  uint8_t* sK = sP + kPBytes;        // two tiles, as they land
-  uint8_t* sV = sK + 2 * kKBytes;    // two tiles: they land in the upper half
+  uint8_t* sK = sP + kPBytes;        // tiles, as they land
+  uint8_t* sV = sK + NS * kKBytes;   // tiles as the products read them, and as they land
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == kMmaWarp) {
     tmem_alloc(&s.tmem, kTmemCols);
@@ -171,12 +182,14 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     tma_prefetch_desc(&vmap);
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.k_empty[i], 5);  // the scores' product, and the softmax warps
       mbar_init(&s.vr_full[i], 1);
       mbar_init(&s.v_full[i], 4);
       mbar_init(&s.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], 2);  // half of the rows by each query warp
       mbar_init(&s.q_empty[i], 5);
       mbar_init(&s.s_full[i], 1);
@@ -212,23 +225,23 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     if (lane == 0) mbar_arrive(&s.step_empty[j % kSteps]);
   };
 
-  // A half of item i's query rows as their two terms: 16 lanes a row, 8 numbers a lane.
+  // A half of item i's query rows as their two terms: 8 numbers a lane.
   auto convert = [&](uint32_t i, int half) {
     const uint32_t b = i & 1;
     const Step& it = s.steps[i % kSteps];
     const int rows = it.g.rows, row0 = it.g.row0, bos = it.bos, h = it.h, pos0 = it.pos0;
     uint8_t* q = sQ + b * kQBytes;
-    const int c = lane & 15;
+    constexpr int L = D / 8, W = 32 / L;  // lanes of a row, rows of the warp
+    constexpr int kHalf = kRowsItem / 2, U = kHalf / W;
+    const int c = lane & (L - 1);
     wait_or_die(&s.q_empty[b], ((i >> 1) & 1) ^ 1, dead);
-    constexpr int U = 4, kHalf = kRowsItem / 2;  // pairs of rows in flight
-    static_assert(kHalf == 2 * U, "a half at a time");
-#pragma unroll 1
-    for (int r0 = half * kHalf; r0 < min(rows, (half + 1) * kHalf); r0 += 2 * U) {
+    const int r0 = half * kHalf;
+    if (r0 < rows) {
       uint4 x[U];
       int at[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int r = min(r0 + 2 * k + (lane >> 4), rows - 1);
+        const int r = min(r0 + W * k + lane / L, rows - 1);
         const int tk = div_g(a, row0 + r), hg = row0 + r - tk * a.G;
         at[k] = pos0 + tk;
         x[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
@@ -237,14 +250,15 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int r = r0 + 2 * k + (lane >> 4);
+        const int r = r0 + W * k + lane / L;
         const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           top = max(top, max(u[e] << 16 & 0x7fff0000u, u[e] & 0x7fff0000u));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = L / 2; o > 0; o >>= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const bool odd = top >= 0x7f800000u;  // an infinity or a NaN: the row's scores are NaN
         const int e = q8::exponent(top);
         const float f = odd ? 0.f : q8::power(-e);
@@ -257,10 +271,9 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           lo[p] = q8::pack2((y0 - z.x) * 16.f, (y1 - z.y) * 16.f);
         }
         if (r < rows) {
-          uint8_t* dst = q + (r >> 3) * 1024 + (r & 7) * 128 +
-                         (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+          uint8_t* dst = q + raw_offset<D>(r, c >> 1) + (c & 1) * 8;
           *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2*>(dst + kRowsItem * 128) =
+          *reinterpret_cast<uint2*>(dst + kRowsItem * D) =
               make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
           if (c == 0) {
             s.row_scale[b][r] =
@@ -313,8 +326,8 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           const bool keys = z == 0;
           const int y = keys ? t + 1 : t;
           if (y < 0 || y >= n) continue;
-          const uint32_t at = keys ? kp++ : vp++, slot = at & 1;
-          wait_or_die(keys ? &s.k_empty[slot] : &s.v_empty[slot], ((at >> 1) & 1) ^ 1, dead);
+          const uint32_t at = keys ? kp++ : vp++, slot = at % NS;
+          wait_or_die(keys ? &s.k_empty[slot] : &s.v_empty[slot], ((at / NS) & 1) ^ 1, dead);
           const bool mine = (y & 3) == quarter && row >= 0;
           const unsigned need = __ballot_sync(0xffffffffu, mine);
           uint64_t* bar = keys ? &s.k_full[slot] : &s.vr_full[slot];
@@ -322,7 +335,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             mbar_arrive_expect_tx(bar, uint32_t(__popc(need)) * uint32_t(ps * (D + 1)));
           __syncwarp();
           if (mine && !dead) {
-            uint8_t* dst = keys ? sK + slot * kKBytes : sV + slot * kVBytes + kKBytes;
+            uint8_t* dst = keys ? sK + slot * kKBytes : sV + slot * kVBytes + kLand;
             tma_load_2d(dst + pi * ps * D, keys ? &kmap : &vmap, bar, 0, row);
             bulk_load((keys ? s.k_scale[slot] : s.v_scale[slot]) + pi * ps,
                       (keys ? a.k_scale : a.v_scale) + row, ps, bar);
@@ -339,16 +352,16 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     // leave no copy in flight behind a give-up
     if (dead) {
-      for (uint32_t i = kp > 2 ? kp - 2 : 0; i < kp; ++i)
-        mbar_wait(&s.k_full[i & 1], (i >> 1) & 1, 100000000ull);
-      for (uint32_t i = vp > 2 ? vp - 2 : 0; i < vp; ++i)
-        mbar_wait(&s.vr_full[i & 1], (i >> 1) & 1, 100000000ull);
+      for (uint32_t i = kp > NS ? kp - NS : 0; i < kp; ++i)
+        mbar_wait(&s.k_full[i % NS], (i / NS) & 1, 100000000ull);
+      for (uint32_t i = vp > NS ? vp - NS : 0; i < vp; ++i)
+        mbar_wait(&s.vr_full[i % NS], (i / NS) & 1, 100000000ull);
     }
   } else if (warp == kMmaWarp) {
     // Products: a tile's scores one tile ahead of the values.  The whole warp walks and waits, one
     // lane issues, from warp-uniform addresses.
     const uint32_t idesc_s = make_idesc(0, 128, 2 * kRowsItem);
-    const uint32_t idesc_o = make_idesc(1, 128, kRowsItem, true, false);
+    const uint32_t idesc_o = make_idesc(1, D, kRowsItem, true, false);
     const uint32_t tmu = __shfl_sync(0xffffffffu, tm, 0);
     const uint32_t q0 = smem_u32(sQ), p0 = smem_u32(sP), k0 = smem_u32(sK), v0 = smem_u32(sV);
     const bool leader = elect_one();
@@ -359,14 +372,14 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     auto scores = [&]() {
       if (!sq) return;
       if (iq == 0) wait_or_die(&s.q_full[jq & 1], (jq >> 1) & 1, dead);
-      const uint32_t b = tq & 1, ph = (tq >> 1) & 1;
-      wait_or_die(&s.k_full[b], ph, dead);
-      wait_or_die(&s.s_empty[b], ph ^ 1, dead);
+      const uint32_t b = tq & 1, slot = tq % NS;
+      wait_or_die(&s.k_full[slot], (tq / NS) & 1, dead);
+      wait_or_die(&s.s_empty[b], ((tq >> 1) & 1) ^ 1, dead);
       tc_fence_after();
-      const uint64_t kd = make_sdesc(__shfl_sync(0xffffffffu, k0 + b * kKBytes, 0), 16, 1024,
-                                     kSwizzle128);
+      const uint64_t kd = make_sdesc(__shfl_sync(0xffffffffu, k0 + slot * kKBytes, 0), 16, 8 * D,
+                                     C::kSwizzleK);
       const uint64_t qd = make_sdesc(__shfl_sync(0xffffffffu, q0 + (jq & 1) * kQBytes, 0), 16,
-                                     1024, kSwizzle128);
+                                     8 * D, C::kSwizzleK);
       const uint32_t to = __shfl_sync(0xffffffffu, tmu + kColS + 32 * b, 0);
       ++iq;
       if (leader) {
@@ -374,7 +387,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) mma_ss_f8(to, kd + 2 * x, qd + 2 * x, idesc_s, x > 0);
         mma_commit(&s.s_full[b]);
-        mma_commit(&s.k_empty[b]);
+        mma_commit(&s.k_empty[slot]);
         if (iq == nq) mma_commit(&s.q_empty[jq & 1]);
       }
       __syncwarp();
@@ -388,9 +401,9 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     scores();
     while (tp < tq) {
       scores();
-      const uint32_t b = tp & 1;
+      const uint32_t b = tp % NS;
       if (ip == 0) wait_or_die(&s.o_empty[jp & 1], ((jp >> 1) & 1) ^ 1, dead);
-      wait_or_die(&s.v_full[b], (tp >> 1) & 1, dead);
+      wait_or_die(&s.v_full[b], (tp / NS) & 1, dead);
       wait_or_die(&s.p_full, tp & 1, dead);
       tc_fence_after();
       const uint64_t vd = make_sdesc(__shfl_sync(0xffffffffu, v0 + b * kVBytes, 0), kKeys * 128,
@@ -460,9 +473,9 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     }
     if (lane == 0) headers[blockIdx.x] = hd;
   } else if (warp >= kExpandWarp && warp < kLoadWarp) {
-    // A thread has a key's row of each tile of values: its bytes, in the slot's upper half, into
-    // registers, and the row as bf16 over the slot in the products' layout (whose pieces in the
-    // upper half lie where the row's own bytes did).
+    // A thread has a key's row of each tile of values: its bytes, where they landed, into registers,
+    // and the row as bf16 into the slot in the products' layout (whose pieces in the upper half, D =
+    // 128, lie where the row's own bytes did).
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
     const int r = tid - 32 * kExpandWarp;
     const q8::Scale16 one(q8::kBias);
@@ -473,17 +486,17 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
       const int n = st->v1 - st->v0;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++t) {
-        const uint32_t b = t & 1;
-        wait_or_die(&s.vr_full[b], (t >> 1) & 1, dead);
+        const uint32_t b = t % NS;
+        wait_or_die(&s.vr_full[b], (t / NS) & 1, dead);
         uint8_t* slot = sV + b * kVBytes;
         // In a loop: little code, which a small call has to fetch.  (The pieces that are written
         // over the row's bytes are behind those that have been read.)
-        uint4 w = *reinterpret_cast<const uint4*>(slot + kKBytes + raw_offset<D>(r, 0));
+        uint4 w = *reinterpret_cast<const uint4*>(slot + kLand + raw_offset<D>(r, 0));
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
           if (c + 1 < D / 16)
-            w = *reinterpret_cast<const uint4*>(slot + kKBytes + raw_offset<D>(r, c + 1));
+            w = *reinterpret_cast<const uint4*>(slot + kLand + raw_offset<D>(r, c + 1));
           uint32_t y[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) q8::expand4<false>(x[k], one, y[2 * k], y[2 * k + 1]);
@@ -500,8 +513,10 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
     }
   } else if (warp < kExpandWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int r = tid;            // the thread's key in the tile, and its lane of O,
-    const int d = q8::place(tid);  // which is that of this column
+    const int r = tid;  // the thread's key in the tile
+    // The column whose lane of O is the thread's: with D = 64 a warp has sixteen.
+    const int d = q8::place(D == 128 ? tid : warp * 16 + (lane & 15));
+    const bool has = D == 128 || lane < 16;
     const uint32_t lanebits = uint32_t(warp) << 21;  // (32 * warp) << 16
     uint8_t* const prow = sP + (r >> 6) * (kRowsItem * 128) + (r & 7) * 2;
     const uint32_t pchunk = uint32_t(r >> 3 & 7) << 4;
@@ -534,10 +549,10 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
         for (int i = 0; i < n; ++i, ++t) {
           const int ks = tile_start(w.g, w.v0 + i), key = ks + r;
-          const uint32_t b = t & 1, ph = (t >> 1) & 1;
-          wait_or_die(&s.k_full[b], ph, dead);
-          const float ck = q8::scale(s.k_scale[b][r]);
-          wait_or_die(&s.s_full[b], ph, dead);
+          const uint32_t b = t & 1, slot = t % NS, ph = (t / NS) & 1;
+          wait_or_die(&s.k_full[slot], ph, dead);
+          const float ck = q8::scale(s.k_scale[slot][r]);
+          wait_or_die(&s.s_full[b], (t >> 1) & 1, dead);
           tc_fence_after();
           float x[NR];
           {
@@ -556,7 +571,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&s.s_empty[b]);
-            mbar_arrive(&s.k_empty[b]);
+            mbar_arrive(&s.k_empty[slot]);
           }
           const bool whole =
               ks + kKeys <= pos_first + 1 &&
@@ -603,8 +618,8 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
               tmem_st<NR>(tO, o);
             }
           }
-          wait_or_die(&s.vr_full[b], ph, dead);
-          const float cv = q8::scale(s.v_scale[b][r]);
+          wait_or_die(&s.vr_full[slot], ph, dead);
+          const float cv = q8::scale(s.v_scale[slot][r]);
 #pragma unroll
           for (int e = 0; e < NR; ++e) {
             const float p = fast_exp2(x[e] - (m[e] == -INFINITY ? 0.f : m[e]));
@@ -645,11 +660,12 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
           const long long orow = (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G);
           if (cut) {
             const long long p = (long long)(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRowsItem + e;
-            part_o[p * D + d] = o[0];
+            if (has) part_o[p * D + d] = o[0];
             if (r == 0) part_ml[p] = make_float2(m[0], sum);
           } else {
-            static_cast<__nv_bfloat16*>(a.out)[orow * D + d] =
-                __float2bfloat16_rn(sum == 0.f ? 0.f : o[0] * (1.0f / sum));
+            if (has)
+              static_cast<__nv_bfloat16*>(a.out)[orow * D + d] =
+                  __float2bfloat16_rn(sum == 0.f ? 0.f : o[0] * (1.0f / sum));
             if (r == 0 && a.lse)
               a.lse[orow] = sum == 0.f ? -INFINITY : (m[0] + log2f(sum)) * 0.6931471805599453f;
           }
@@ -675,15 +691,11 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
   if (warp == kMmaWarp) tmem_dealloc(tm, kTmemCols);
 }
 
-}  // namespace
-
 static_assert(sizeof(Header) * kStretches <= 16384, "headers");
-static_assert(16384 + 2 * kStretches * kRowsItem * (8 + 4 * D) <= 152 * 512 * (8 + 4 * D),
-              "inside the workspace of the other kernel");
+static_assert(kStretches * kRowsItem <= 152 * 256, "inside the workspace of the other kernel");
 
-cudaError_t launch_paged_tc_q8_few(const PagedArgs& args, void* workspace, cudaStream_t st) {
-  PagedArgs a = args;
-  set_divisor(a);
+template <int D>
+cudaError_t launch_t(const PagedArgs& a, void* workspace, cudaStream_t st) {
   CUtensorMap kmap{}, vmap{};
   if (a.num_pages > 0 && a.max_pages > 0)
     if (!cache_map<true>(&kmap, a.k_cache, a) || !cache_map<true>(&vmap, a.v_cache, a))
@@ -691,13 +703,22 @@ cudaError_t launch_paged_tc_q8_few(const PagedArgs& args, void* workspace, cudaS
   Header* headers = static_cast<Header*>(workspace);
   float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + 16384);
   float* po = reinterpret_cast<float*>(ml + (size_t)2 * kStretches * kRowsItem);
-  cudaError_t e = cudaFuncSetAttribute(paged_q8_few_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(
+      paged_q8_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  paged_q8_few_kernel<<<kStretches, kThreads, kSmem, st>>>(a, kmap, vmap, headers, po, ml);
+  paged_q8_few_kernel<D>
+      <<<kStretches, kThreads, Cfg<D>::kSmem, st>>>(a, kmap, vmap, headers, po, ml);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<D>(a, headers, po, ml, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc_q8_few(const PagedArgs& args, void* workspace, cudaStream_t st) {
+  PagedArgs a = args;
+  set_divisor(a);
+  return a.D == 64 ? launch_t<64>(a, workspace, st) : launch_t<128>(a, workspace, st);
 }
 
 unsigned int paged_q8_few_read_error(bool reset) { return read_error(reset); }

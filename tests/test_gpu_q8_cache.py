@@ -565,26 +565,28 @@ def test_empty_calls(dt):
 @pytest.mark.parametrize("G,Hkv", [(1, 3), (2, 2), (3, 1), (4, 2), (5, 1), (8, 1), (9, 1), (12, 1),
                                    (16, 2)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5), (1, 200)])
-def test_few_rows(G, Hkv, window, sinks):
+@pytest.mark.parametrize("D", [128, 64])
+def test_few_rows(G, Hkv, window, sinks, D):
     """Up to 16 rows of a sequence, items of 16 where some have more; none, fewer keys than tokens,
     many tiles, several items in a block and cut ones."""
     d = make([(1, 1), (1, 129), (2, 300), (1, 0), (3, 1), (0, 7), (2, 2000), (1, 128), (1, 5000)] +
-             [(0, 3)] * 6, G * Hkv, Hkv, 128, 64, "bf16", seed=G + window, pad=2, fill="scale")
+             [(0, 3)] * 6, G * Hkv, Hkv, D, 64, "bf16", seed=G + window, pad=2, fill="scale")
     assert d["T"] * G <= 16 * d["N"]  # (16 rows a sequence on average, or fewer)
     call(d, window=window, sinks=sinks)
     pa.check(d, window=window, sinks=sinks)
 
 
 @pytest.mark.parametrize("slope", [20.0, 150.0, 600.0, -300.0])
-def test_rising_scores_of_few_rows_and_of_chunks(slope):
+@pytest.mark.parametrize("D", [128, 64])
+def test_rising_scores_of_few_rows_and_of_chunks(slope, D):
     """Scores that grow along the keys: the standing maximum moves, by less and more than what is
     taken without scaling anew."""
     for seqs in ([(1, 1500), (2, 1500), (1, 130)], [(200, 1500), (130, 130), (1, 1500)]):
-        d = make(seqs, 2, 1, 128, 64, "bf16", seed=13)
+        d = make(seqs, 2, 1, D, 64, "bf16", seed=13)
         k = np.zeros(tuple(d["kb"].shape))
         for n in range(3):
             for j in range(int(d["kv_h"][n])):
-                k[int(d["table_h"][n, j // 64]), :, j % 64] = slope * j / 1500 / 128
+                k[int(d["table_h"][n, j // 64]), :, j % 64] = slope * j / 1500 / D
         b, s = q8_ref.quantise(k)
         d["kb"], d["ks"] = e4m3(b), torch.from_numpy(s).cuda()
         d["kc"] = torch.from_numpy(q8_ref.value(b, s)).cuda()
@@ -621,11 +623,12 @@ def test_queries_of_all_magnitudes(dt, D, tokens):
 
 
 @pytest.mark.parametrize("tokens", [1, 100])
-def test_graphs_that_share_a_workspace(tokens):
+@pytest.mark.parametrize("D", [128, 64])
+def test_graphs_that_share_a_workspace(tokens, D):
     """Two captured calls with one buffer, replayed in turn."""
-    ds = [make([(tokens, 700), (tokens, 900), (1, 64)], 8, 2, 128, 64, "bf16", seed=70),
-          make([(tokens, int(k)) for k in range(140, 1500, 99)], 8, 2, 128, 32, "bf16", seed=71)]
-    n = max(kda.kda_paged_attention_q8_fwd_workspace_size(d["N"], d["T"], 8, 2, 128) for d in ds)
+    ds = [make([(tokens, 700), (tokens, 900), (1, 64)], 8, 2, D, 64, "bf16", seed=70),
+          make([(tokens, int(k)) for k in range(140, 1500, 99)], 8, 2, D, 32, "bf16", seed=71)]
+    n = max(kda.kda_paged_attention_q8_fwd_workspace_size(d["N"], d["T"], 8, 2, D) for d in ds)
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     graphs, want = [], []
     for d in ds:

@@ -175,19 +175,22 @@ def test_keys_and_values_in_rings_of_their_own(stages):
         interleave(rnd, [load(), products(0), products(1)] + [expand() for _ in range(4)], events)
 
 
-def test_pipeline_of_few_rows():
+@pytest.mark.parametrize("stages", [2, 3])
+def test_pipeline_of_few_rows(stages):
     """The kernel for few rows: load, products (scores a tile ahead), two query warps, expanders and
     softmax warps that meet at every tile."""
     W = 2  # warps of the softmax and of the expanders (the kernel has four)
     for seed in range(250):
         rnd = random.Random(seed)
         items = [rnd.choice([1, 1, 1, 2, 3, 6]) for _ in range(rnd.randint(1, 10))]
-        two = lambda c: [pm.Bar(c), pm.Bar(c)]  # noqa: E731
-        k_full, k_empty, vr_full, v_full, v_empty = two(1), two(1 + W), two(1), two(W), two(1)
+        S = stages  # of keys, of values
+        two = lambda c, n=2: [pm.Bar(c) for _ in range(n)]  # noqa: E731
+        k_full, k_empty, vr_full = two(1, S), two(1 + W, S), two(1, S)
+        v_full, v_empty = two(W, S), two(1, S)
         q_full, q_empty, s_full, s_empty, o_empty = two(2), two(1 + W), two(1), two(W), two(W)
         p_full, pv_done, vote = pm.Bar(W), pm.Bar(1), pm.Bar(W)
         step_full, step_empty = [pm.Bar(1) for _ in range(4)], [pm.Bar(3 + 2 * W) for _ in range(4)]
-        slots, keys, vals, scores = [None] * 4, [None] * 2, [None] * 2, [None] * 2
+        slots, keys, vals, scores = [None] * 4, [None] * S, [None] * S, [None] * 2
         flying, commits = [], []
 
         def get(j):
@@ -204,9 +207,9 @@ def test_pipeline_of_few_rows():
                         if not 0 <= y < n:
                             continue
                         p = kp if isk else vp
-                        yield from pm.free((k_empty if isk else v_empty)[p & 1], p >> 1)
-                        (keys if isk else vals)[p & 1] = p
-                        flying.append((k_full if isk else vr_full)[p & 1])
+                        yield from pm.free((k_empty if isk else v_empty)[p % S], p // S)
+                        (keys if isk else vals)[p % S] = p
+                        flying.append((k_full if isk else vr_full)[p % S])
                         kp, vp = kp + isk, vp + (not isk)
                 step_empty[j % 4].arrive()
                 j += 1
@@ -243,12 +246,12 @@ def test_pipeline_of_few_rows():
                     return
                 if iq == 0:
                     yield from pm.full(q_full[jq & 1], jq >> 1)
-                yield from pm.full(k_full[tq & 1], tq >> 1)
+                yield from pm.full(k_full[tq % S], tq // S)
                 yield from pm.free(s_empty[tq & 1], tq >> 1)
-                assert keys[tq & 1] == tq
+                assert keys[tq % S] == tq
                 scores[tq & 1] = tq
                 iq += 1
-                commits.extend([s_full[tq & 1], k_empty[tq & 1]])
+                commits.extend([s_full[tq & 1], k_empty[tq % S]])
                 if iq == sq:
                     commits.append(q_empty[jq & 1])
                 tq += 1
@@ -261,10 +264,10 @@ def test_pipeline_of_few_rows():
                 yield from issue()
                 if ip == 0:
                     yield from pm.free(o_empty[jp & 1], jp >> 1)
-                yield from pm.full(v_full[tp & 1], tp >> 1)
+                yield from pm.full(v_full[tp % S], tp // S)
                 yield from pm.full(p_full, tp)
-                assert vals[tp & 1] == tp
-                commits.extend([pv_done, v_empty[tp & 1]])
+                assert vals[tp % S] == tp
+                commits.extend([pv_done, v_empty[tp % S]])
                 tp, ip = tp + 1, ip + 1
                 if ip == sizes[jp]:
                     step_empty[jp % 4].arrive()
@@ -274,10 +277,10 @@ def test_pipeline_of_few_rows():
             t = j = 0
             while (n := (yield from get(j))) is not None:
                 for _ in range(n):
-                    yield from pm.full(vr_full[t & 1], t >> 1)
-                    assert vals[t & 1] == t
+                    yield from pm.full(vr_full[t % S], t // S)
+                    assert vals[t % S] == t
                     yield
-                    v_full[t & 1].arrive()
+                    v_full[t % S].arrive()
                     t += 1
                 step_empty[j % 4].arrive()
                 j += 1
@@ -296,18 +299,18 @@ def test_pipeline_of_few_rows():
             while (n := (yield from get(j))) is not None:
                 yield from pm.full(q_full[j & 1], j >> 1)
                 for i in range(n):
-                    yield from pm.full(k_full[t & 1], t >> 1)
+                    yield from pm.full(k_full[t % S], t // S)
                     yield from pm.full(s_full[t & 1], t >> 1)
-                    assert scores[t & 1] == t and keys[t & 1] == t
+                    assert scores[t & 1] == t and keys[t % S] == t
                     yield
                     s_empty[t & 1].arrive()
-                    k_empty[t & 1].arrive()
+                    k_empty[t % S].arrive()
                     yield from meet()
                     if grown.setdefault(t, i == 0 or rnd.random() < 0.2):
                         yield from meet()
                         if i:
                             yield from pm.full(pv_done, t - 1)
-                    yield from pm.full(vr_full[t & 1], t >> 1)
+                    yield from pm.full(vr_full[t % S], t // S)
                     if t:
                         yield from pm.full(pv_done, t - 1)
                     yield
