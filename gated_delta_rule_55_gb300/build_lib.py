@@ -18,12 +18,11 @@ SOURCES = ["kda_abi.cu", "kda_decode.cu", "kda_chunk_simt.cu", "kda_chunk_tc.cu"
            "kda_chunk_split.cu", "kda_noalloc.cu", "kda_recurrent.cu", "kda_backward.cu",
            "kda_gla.cu", "kda_gla_chunk.cu", "kda_chunk_bwd.cu", "kda_selftest.cu", "kda_step.cu",
            "kda_norm_rope.cu", "kda_cache_q8.cu", "kda_paged_attn.cu", "kda_paged_attn_q8.cu",
-           "kda_paged_q8_few.cu",
-           "kda_paged_attn_prefix.cu", "kda_paged_attn_prefix_q8.cu", "kda_paged_attn_simt.cu",
-           "kda_serving_abi.cu"]
+           "kda_paged_q8_few.cu", "kda_paged_q8_few32.cu", "kda_paged_attn_prefix.cu",
+           "kda_paged_attn_prefix_q8.cu", "kda_paged_attn_simt.cu", "kda_serving_abi.cu"]
 HEADERS = ["kda_internal.cuh", "tc_prims.cuh", "chunk_common.cuh", "chunk_records.cuh",
            "kda_paged.cuh", "kda_paged_line.h", "kda_paged_tc.cuh", "kda_paged_plan.cuh",
-           "kda_q8.cuh"]
+           "kda_paged_q8_few.cuh", "kda_q8.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -176,6 +176,7 @@ size_t paged_q8_tc_workspace(int total_T, int Hq, int D);
 size_t paged_prefix_tc_workspace(int total_T, int Hq, int D, bool q8);
 cudaError_t launch_paged_tc_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_q8_few(const PagedArgs& a, void* workspace, cudaStream_t stream);
+cudaError_t launch_paged_tc_q8_few32(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix(const PagedArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_paged_tc_prefix_q8(const PagedArgs& a, void* workspace, cudaStream_t stream);
 // Queries of bf16 with D = 128 as two rows of e4m3 under a power of two each, for products with
@@ -185,6 +186,7 @@ cudaError_t launch_query_terms(PagedArgs& a, void* terms, cudaStream_t stream);
 unsigned int paged_read_error(bool reset);
 unsigned int paged_q8_read_error(bool reset);
 unsigned int paged_q8_few_read_error(bool reset);
+unsigned int paged_q8_few32_read_error(bool reset);
 unsigned int paged_prefix_read_error(bool reset);
 unsigned int paged_prefix_q8_read_error(bool reset);
 // Of any call of up to total_T tokens.

@@ -44,18 +44,21 @@ cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st
   if (a.groups > 0)
     return q8 ? launch_paged_tc_prefix_q8(a, workspace, st)
               : launch_paged_tc_prefix(a, workspace, st);
-  // 16 rows a sequence on average or fewer: 64 single tokens (4 rows) 98 us for 230, 101 sequences
-  // of one token but one of 300 (15.8 on average) 329 for 370; 64 of 5 tokens (20) 253 for 231.
-  // D = 64: 64 single tokens 83 us for 161.
-  if (q8 && a.D >= 64 && (long long)a.total_T * (a.Hq / a.Hkv) <= 16ll * a.N)
-    return launch_paged_tc_q8_few(a, workspace, st);
+  // By the rows of a sequence on average, items of 16, of 32 or of 256 rows.  64 sequences, 32 + 8
+  // heads: D = 128, 16 rows 113 us for 241 (items of 32, 20 rows: 172 for 253 with items of 16), 32
+  // rows 176 for 241, 36 rows 244; D = 64, 4 rows 82 for 161, 20 rows 136, 32 rows 147 for 162.
+  const long long rows = (long long)a.total_T * (a.Hq / a.Hkv);
+  if (q8 && a.D >= 64 && rows <= 32ll * a.N)
+    return rows <= 16ll * a.N ? launch_paged_tc_q8_few(a, workspace, st)
+                              : launch_paged_tc_q8_few32(a, workspace, st);
   return q8 ? launch_paged_tc_q8(a, workspace, st)
             : launch_any<false, false>(a, workspace, nullptr, st);
 }
 
 unsigned int paged_read_error(bool reset) {
   return read_error(reset) | paged_q8_read_error(reset) | paged_q8_few_read_error(reset) |
-         paged_prefix_read_error(reset) | paged_prefix_q8_read_error(reset);
+         paged_q8_few32_read_error(reset) | paged_prefix_read_error(reset) |
+         paged_prefix_q8_read_error(reset);
 }
 
 }  // namespace kda

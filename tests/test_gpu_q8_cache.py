@@ -576,12 +576,30 @@ def test_few_rows(G, Hkv, window, sinks, D):
     pa.check(d, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("G,Hkv,few", [(1, 2, 32), (4, 2, 8), (5, 1, 6), (8, 1, 4), (9, 1, 3),
+                                       (16, 2, 2), (17, 1, 1), (32, 1, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5), (1, 200)])
+@pytest.mark.parametrize("D", [128, 64])
+def test_up_to_32_rows(G, Hkv, few, window, sinks, D):
+    """Items of 32 rows, full ones, those of a row more than a half and less; none, fewer keys than
+    tokens, many tiles, several items in a block and cut ones.  (few: tokens of 32 rows.)"""
+    seqs = [(few, 1), (few, 129), (few // 2 + 1, 300), (few, 0), (few + 1, 1), (few, 7), (1, 2000),
+            (few, 128), (few, 5000), (0, 3), (few + 2, 700)] + [(few, 60)] * 4
+    T = sum(q for q, _ in seqs)
+    seqs += [(0, 3)] * max(0, (T * G + 31) // 32 - len(seqs))
+    d = make(seqs, G * Hkv, Hkv, D, 64, "bf16", seed=G + window, pad=2, fill="scale")
+    assert 16 * d["N"] < T * G <= 32 * d["N"]  # (17 to 32 rows a sequence on average)
+    call(d, window=window, sinks=sinks)
+    pa.check(d, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("slope", [20.0, 150.0, 600.0, -300.0])
 @pytest.mark.parametrize("D", [128, 64])
 def test_rising_scores_of_few_rows_and_of_chunks(slope, D):
     """Scores that grow along the keys: the standing maximum moves, by less and more than what is
     taken without scaling anew."""
-    for seqs in ([(1, 1500), (2, 1500), (1, 130)], [(200, 1500), (130, 130), (1, 1500)]):
+    for seqs in ([(1, 1500), (2, 1500), (1, 130)], [(15, 1500), (12, 130), (16, 1500)],
+                 [(200, 1500), (130, 130), (1, 1500)]):
         d = make(seqs, 2, 1, D, 64, "bf16", seed=13)
         k = np.zeros(tuple(d["kb"].shape))
         for n in range(3):
@@ -596,7 +614,7 @@ def test_rising_scores_of_few_rows_and_of_chunks(slope, D):
 
 
 @pytest.mark.parametrize("dt,D", KINDS)
-@pytest.mark.parametrize("tokens", [1, 150])
+@pytest.mark.parametrize("tokens", [1, 7, 150])
 def test_queries_of_all_magnitudes(dt, D, tokens):
     """Rows of zeros, of the smallest and of large numbers, and of numbers of very different sizes;
     an infinity or a NaN in one row stays in it.  Scores of e^+-87 at most, so that nothing overflows."""
@@ -622,7 +640,7 @@ def test_queries_of_all_magnitudes(dt, D, tokens):
     assert torch.isnan(d["out"][tokens, 1]).all() and not torch.isfinite(d["out"][tokens, 2]).any()
 
 
-@pytest.mark.parametrize("tokens", [1, 100])
+@pytest.mark.parametrize("tokens", [1, 5, 100])
 @pytest.mark.parametrize("D", [128, 64])
 def test_graphs_that_share_a_workspace(tokens, D):
     """Two captured calls with one buffer, replayed in turn."""

@@ -175,10 +175,11 @@ def test_keys_and_values_in_rings_of_their_own(stages):
         interleave(rnd, [load(), products(0), products(1)] + [expand() for _ in range(4)], events)
 
 
-@pytest.mark.parametrize("stages", [2, 3])
-def test_pipeline_of_few_rows(stages):
+@pytest.mark.parametrize("stages,wide", [(2, False), (3, False), (2, True), (3, True)])
+def test_pipeline_of_few_rows(stages, wide):
     """The kernel for few rows: load, products (scores a tile ahead), two query warps, expanders and
-    softmax warps that meet at every tile."""
+    softmax warps that meet at every tile.  Wide: weights over their tile of keys, query rows in one
+    place."""
     W = 2  # warps of the softmax and of the expanders (the kernel has four)
     for seed in range(250):
         rnd = random.Random(seed)
@@ -187,7 +188,8 @@ def test_pipeline_of_few_rows(stages):
         two = lambda c, n=2: [pm.Bar(c) for _ in range(n)]  # noqa: E731
         k_full, k_empty, vr_full = two(1, S), two(1 + W, S), two(1, S)
         v_full, v_empty = two(W, S), two(1, S)
-        q_full, q_empty, s_full, s_empty, o_empty = two(2), two(1 + W), two(1), two(W), two(W)
+        q_full, q_empty, s_full = two(2), two(W if wide else 1 + W), two(1)
+        s_empty, o_empty, q_read, held = two(W), two(W), pm.Bar(1), [None]
         p_full, pv_done, vote = pm.Bar(W), pm.Bar(1), pm.Bar(W)
         step_full, step_empty = [pm.Bar(1) for _ in range(4)], [pm.Bar(3 + 2 * W) for _ in range(4)]
         slots, keys, vals, scores = [None] * 4, [None] * S, [None] * S, [None] * 2
@@ -216,6 +218,10 @@ def test_pipeline_of_few_rows(stages):
 
         def convert(i):
             yield from pm.free(q_empty[i & 1], i >> 1)
+            if wide:
+                yield from pm.free(q_read, i)
+                assert held[0] in (None, i - 1, i)
+                held[0] = i
             yield
             q_full[i & 1].arrive()
 
@@ -251,9 +257,10 @@ def test_pipeline_of_few_rows(stages):
                 assert keys[tq % S] == tq
                 scores[tq & 1] = tq
                 iq += 1
-                commits.extend([s_full[tq & 1], k_empty[tq % S]])
+                assert not wide or held[0] == jq
+                commits.extend([s_full[tq & 1]] if wide else [s_full[tq & 1], k_empty[tq % S]])
                 if iq == sq:
-                    commits.append(q_empty[jq & 1])
+                    commits.append(q_read if wide else q_empty[jq & 1])
                 tq += 1
                 if iq == sq:
                     iq, jq = 0, jq + 1
@@ -266,8 +273,8 @@ def test_pipeline_of_few_rows(stages):
                     yield from pm.free(o_empty[jp & 1], jp >> 1)
                 yield from pm.full(v_full[tp % S], tp // S)
                 yield from pm.full(p_full, tp)
-                assert vals[tp % S] == tp
-                commits.extend([pv_done, v_empty[tp % S]])
+                assert vals[tp % S] == tp and (not wide or keys[tp % S] == ("p", tp))
+                commits.extend([pv_done, v_empty[tp % S]] + ([k_empty[tp % S]] if wide else []))
                 tp, ip = tp + 1, ip + 1
                 if ip == sizes[jp]:
                     step_empty[jp % 4].arrive()
@@ -301,7 +308,7 @@ def test_pipeline_of_few_rows(stages):
                 for i in range(n):
                     yield from pm.full(k_full[t % S], t // S)
                     yield from pm.full(s_full[t & 1], t >> 1)
-                    assert scores[t & 1] == t and keys[t % S] == t
+                    assert scores[t & 1] == t and keys[t % S] in (t, ("p", t))
                     yield
                     s_empty[t & 1].arrive()
                     k_empty[t % S].arrive()
@@ -314,6 +321,8 @@ def test_pipeline_of_few_rows(stages):
                     if t:
                         yield from pm.full(pv_done, t - 1)
                     yield
+                    if wide:
+                        keys[t % S] = ("p", t)
                     p_full.arrive()
                     t += 1
                 yield from meet()
