@@ -47,8 +47,11 @@ cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st
   // By the rows of a sequence on average, items of 16, of 32 or of 256 rows.  64 sequences, 32 + 8
   // heads: D = 128, 16 rows 113 us for 241 (items of 32, 20 rows: 172 for 253 with items of 16), 32
   // rows 176 for 241, 36 rows 244; D = 64, 4 rows 82 for 161, 20 rows 136, 32 rows 147 for 162.
+  // Smaller items are more of them, whose line has to fit the indices as well (paged_tc_index_ok).
   const long long rows = (long long)a.total_T * (a.Hq / a.Hkv);
-  if (q8 && a.D >= 64 && rows <= 32ll * a.N)
+  const double line =
+      (rows / 16.0 + a.N) * a.Hkv * ((double)a.max_pages * a.page_size / kKeys + 4);
+  if (q8 && a.D >= 64 && rows <= 32ll * a.N && line < 2147483647.0)
     return rows <= 16ll * a.N ? launch_paged_tc_q8_few(a, workspace, st)
                               : launch_paged_tc_q8_few32(a, workspace, st);
   return q8 ? launch_paged_tc_q8(a, workspace, st)

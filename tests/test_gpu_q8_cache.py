@@ -593,6 +593,29 @@ def test_up_to_32_rows(G, Hkv, few, window, sinks, D):
     pa.check(d, window=window, sinks=sinks)
 
 
+def test_few_rows_of_a_batch_whose_tables_are_near_the_limit():
+    """Block tables so wide that items of 16 rows could pass the 31 bits of the line, while those of
+    256 rows, which the limit is about, could not."""
+    d = make([(1, 70), (1, 0), (1, 300)], 64, 4, 128, 128, "bf16", seed=3)
+    N, pages = 65535, 6000
+    assert (N * 16 / 16 + N) * 4 * (pages + 4) > 2 ** 31 > (N * 16 / 256 + N) * 4 * (pages + 5)
+    table = d["table"].new_zeros((N, pages))
+    table[:3, :d["table"].shape[1]] = d["table"]
+    cu = torch.full((N + 1,), 3, dtype=torch.int32, device="cuda")
+    cu[:4] = d["cu"]
+    kv = torch.zeros(N, dtype=torch.int32, device="cuda")
+    kv[:3] = d["kv"]
+    q = torch.zeros((N, 64, 128), dtype=torch.bfloat16, device="cuda")
+    q[:3] = d["q"]
+    out, lse = torch.empty_like(q), torch.empty((N, 64), device="cuda")
+    ws = torch.empty(kda.kda_paged_attention_q8_fwd_workspace_size(N, N, 64, 4, 128),
+                     dtype=torch.uint8, device="cuda")
+    kda.kda_paged_attention_q8_fwd(q, d["kb"], d["vb"], d["ks"], d["vs"], table, cu, kv, out, N, N,
+                                   64, 4, 128, d["kb"].shape[0], 128, pages, lse=lse, workspace=ws)
+    d["out"], d["lse"] = out[:3].contiguous(), lse[:3].contiguous()
+    pa.check(d)
+
+
 @pytest.mark.parametrize("slope", [20.0, 150.0, 600.0, -300.0])
 @pytest.mark.parametrize("D", [128, 64])
 def test_rising_scores_of_few_rows_and_of_chunks(slope, D):
