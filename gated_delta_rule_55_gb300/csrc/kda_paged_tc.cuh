@@ -1336,7 +1336,7 @@ __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
   }
   const int all = a.total_T * a.Hq;
   const int lane = threadIdx.x & 31, side = lane >> 4;
-  const int first = (int)(((blockIdx.x - joins) * 256u + threadIdx.x) >> 5) * per;
+  const long long first = first_row(blockIdx.x - joins, threadIdx.x >> 5, per);
   if (first >= all) return;
   auto owned = [&](int row, bool& grouped) {
     const int tok = (int)((unsigned)row / (unsigned)a.Hq);
@@ -1344,17 +1344,17 @@ __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
     return token_owned(a, tok);
   };
   bool grouped = false;
-  if (per == 1 && !owned(first, grouped)) return;
+  if (per == 1 && !owned((int)first, grouped)) return;
   // launched while the first kernel runs: wait for its results
   asm volatile("griddepcontrol.wait;" ::: "memory");
   unsigned open = 1;  // rows that are not done
   if (per > 1)
     open = __ballot_sync(0xffffffffu,
                          lane < per && first + lane < all &&
-                             rows.at[(long long)all + min(first + lane, all - 1)].y >= 0);
+                             rows.at[all + min(first + lane, all - 1ll)].y >= 0);
 #pragma unroll 1
   for (; open; open &= open - 1) {
-    const int row = first + __ffs(open) - 1;
+    const int row = (int)first + __ffs(open) - 1;
     if (per > 1 && !owned(row, grouped)) continue;
     const int4 at = rows.at[(long long)side * all + row];
     if (__shfl_sync(0xffffffffu, at.y, 16) < 0) continue;  // (a warp alike)

@@ -68,3 +68,38 @@ def test_a_long_line_of_overlapping_sequences_is_seen(line):
     for k in range(12):  # doubling: 2^12 sequences
         total = line([("+", total or per, total or per)])[0]
     assert total == MOST
+
+
+ROWS = r"""
+#include <cstdio>
+#include "kda_paged_line.h"
+int main() {
+  unsigned block;
+  int warp, per;
+  while (std::scanf("%u %d %d", &block, &warp, &per) == 3)
+    std::printf("%lld\n", kda::first_row(block, warp, per));
+}
+"""
+
+
+@pytest.mark.parametrize("per", [1, 4])
+def test_rows_that_are_joined_are_numbered_beyond_32_bits(tmp_path, per):
+    """Every row of the largest call, 2^31 - 1, has a warp, and one only: the first rows of
+    neighbouring warps are `per` apart over all blocks, where threads counted in 32 bits begin again
+    (2^24 blocks of 256, 2^29 rows of four a warp)."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    (tmp_path / "rows.cpp").write_text(ROWS)
+    csrc = os.path.join(build_lib.PKG, "csrc")
+    subprocess.run([cxx, "-O1", "-fsanitize=undefined", "-fno-sanitize-recover", "-I", csrc,
+                    str(tmp_path / "rows.cpp"), "-o", str(tmp_path / "rows")], check=True)
+    last = (MOST + 8 * per - 1) // (8 * per) - 1  # the last block
+    blocks = [b for x in (0, 2 ** 24, 2 ** 26, last) for b in (x - 1, x, x + 1) if 0 <= b <= last]
+    at = [(b, w) for b in sorted(set(blocks)) for w in range(8)]
+    r = subprocess.run([str(tmp_path / "rows")], text=True, capture_output=True, check=True,
+                       input="\n".join(f"{b} {w} {per}" for b, w in at))
+    assert [int(x) for x in r.stdout.split()] == [(8 * b + w) * per for b, w in at]
+    assert (8 * last + 7) * per + per >= MOST > 8 * last * per
+    wrapped = [((b * 256 + 32 * w) % 2 ** 32 >> 5) * per for b, w in at]
+    assert wrapped[:8] == [(8 * b + w) * per for b, w in at[:8]] and len(set(wrapped)) < len(at)
