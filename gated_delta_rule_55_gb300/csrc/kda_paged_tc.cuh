@@ -1337,16 +1337,17 @@ __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
   const int all = a.total_T * a.Hq;
   const int lane = threadIdx.x & 31, side = lane >> 4;
   const long long first = first_row(blockIdx.x - joins, threadIdx.x >> 5, per);
-  if (first >= all) return;
   auto owned = [&](int row, bool& grouped) {
     const int tok = (int)((unsigned)row / (unsigned)a.Hq);
     grouped = token_grouped(a, tok);
     return token_owned(a, tok);
   };
   bool grouped = false;
-  if (per == 1 && !owned((int)first, grouped)) return;
-  // launched while the first kernel runs: wait for its results
+  const bool live = first < all && (per > 1 || owned((int)first, grouped));
+  // launched while the first kernel runs: wait for its results.  (Without rows too: were every block
+  // gone before the first kernel's end, what follows in the stream could begin beside it.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;
   unsigned open = 1;  // rows that are not done
   if (per > 1)
     open = __ballot_sync(0xffffffffu,

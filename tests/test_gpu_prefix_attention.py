@@ -344,3 +344,24 @@ def test_bad_groups_of_long_sequences_stay_inside():
         torch.cuda.synchronize()
         assert (host(d["out"])[d["live"]:] == 7).all() and (ws[n:] == 0x5A).all()
     assert kda.kda_device_error() == 0
+
+
+@pytest.mark.parametrize("D,q8", [(64, False), (128, True)])
+def test_a_call_without_tokens_has_ended_before_what_follows(D, q8):
+    """No row is in a sequence, so nothing is joined: the workspace is the caller's again behind the
+    call in the stream, and the next call's with it."""
+    d = make([100], [(2, 100), (1, 40)], 2, 1, D, 16, "bf16", q8, pad=2)
+    call(d)
+    want, cu = d["out"].clone(), d["cu"].clone()
+    ws = torch.empty(size(d), dtype=torch.uint8, device="cuda")
+    for _ in range(100):
+        d["cu"].zero_()
+        d["out"].fill_(7)
+        call(d, ws=ws)
+        ws.fill_(0x5A)
+        d["cu"].copy_(cu)
+        torch.cuda.synchronize()
+        assert (ws == 0x5A).all() and (d["out"] == 7).all()
+        call(d, ws=ws)
+        assert torch.equal(d["out"], want)
+    assert kda.kda_device_error() == 0
