@@ -127,6 +127,13 @@ int run_paged(kda::PagedArgs a, int dtype, void* workspace, size_t workspace_byt
       (double)a.groups * a.max_prefix_pages >= kMaxElems || a.N > 65535 || a.groups > 65535 ||
       a.Hkv > 65535)
     return KDA_ERR_TOO_LARGE;
+  // The last tile's end stays in 31 bits, and so do the positions that tokens have behind all of a
+  // prefix (the calls over 8-bit pages and behind prefixes).
+  if ((a.k_scale || a.groups > 0) &&
+      ((double)a.max_pages * a.page_size > 2147483520.0 ||
+       (double)a.max_prefix_pages * a.page_size > 2147483520.0 ||
+       (a.groups > 0 && (double)a.max_prefix_pages * a.page_size + a.total_T > 2147483647.0)))
+    return KDA_ERR_TOO_LARGE;
   // a window that no position can leave hides nothing
   if ((double)a.window >= (double)a.max_pages * a.page_size) a.window = 0;
   if (dtype == KDA_BF16 && !kda::paged_tc_index_ok(a)) return KDA_ERR_TOO_LARGE;

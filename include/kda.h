@@ -659,7 +659,8 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   v_scale [num_pages, Hkv, page_size].  query and out stay in dtype.  Rows are expanded exactly,
  *   so the result is that of kda_paged_attention_fwd over the values that the cache stands for; a
  *   seen row with b = 255 makes what sees it NaN.  All other arguments, limits and errors are those
- *   of kda_paged_attention_fwd; the workspace's size is
+ *   of kda_paged_attention_fwd, and max_pages page_size is at most 2^31 - 128 (KDA_ERR_TOO_LARGE);
+ *   the workspace's size is
  *   kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N or total_T grows.
  *   bf16 with D >= 64 may multiply queries in two terms of 8 bits, which are off by at most 2^-17
  *   of the row's largest element where an element is less than 2^-9 of it, and exact otherwise
@@ -699,7 +700,9 @@ int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const voi
  *   num_groups = 0: kda_paged_attention_fwd (the three prefix arguments may be NULL)
  *   There is no window.  bf16 counts three times the units of kda_paged_attention_fwd's limit,
  *   at max_prefix_pages + max_pages, and adds those of num_groups sequences of all tokens at
- *   max_prefix_pages.  num_groups at most 65535.  All else as for kda_paged_attention_fwd.
+ *   max_prefix_pages.  num_groups at most 65535.  With groups, max_pages page_size and
+ *   max_prefix_pages page_size are at most 2^31 - 128, max_prefix_pages page_size + total_T below
+ *   2^31 (KDA_ERR_TOO_LARGE).  All else as for kda_paged_attention_fwd.
  *   workspace    at least kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq,
  *                Hkv, D, dtype) bytes, 256-byte aligned; the size never decreases as num_groups,
  *                N or total_T grows.

@@ -163,3 +163,24 @@ def test_binding_refuses_other_types():
     with pytest.raises(ValueError, match="dtype"):
         kda.kda_paged_cache_read_q8(x, x, x, x, x, x.half(), x, 2, 4, 64, 1, 16)
     assert sa.FAKE == FAKE
+
+
+def test_lists_whose_positions_would_pass_31_bits(L):  # noqa: F811
+    """A list of 2^31 - 1 keys has a tile that ends at 2^31, and a token behind a prefix of that many
+    the position 2^31 - 2 + its number: both would wrap."""
+    page = 16
+    most = (2 ** 31 - 128) // page
+    for dtype in (0, 1):
+        assert _attn(L, page=page, maxp=most + 1, N=1, Hkv=1, dtype=dtype) == -11
+        for over in (dict(maxp=most + 1), dict(maxpp=most + 1), dict(maxpp=most, T=200)):
+            a = dict(page=page, N=1, Hkv=1, Hq=1, D=32, qs=32, dtype=dtype, ws=None)
+            a.update(over)
+            assert _attn(L, True, **a) == -11
+            assert _attn(L, True, ks=None, vs=None, **a) == -11
+    # at the limits the next check refuses (no workspace)
+    a = dict(page=page, N=1, Hkv=1, Hq=1, D=32, qs=32, ws=None)
+    assert _attn(L, maxp=most, **a) == -12
+    assert _attn(L, True, maxp=most, maxpp=4, **a) == -12
+    assert _attn(L, True, maxp=4, maxpp=most, T=127, **a) == -12
+    # without prefixes, over pages of query's type: as before
+    assert _attn(L, True, ks=None, vs=None, groups=0, maxp=most + 1, **a) == -12
