@@ -285,9 +285,11 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(NormRopeArgs a, 
       for (int e = 0; e < VE; ++e) ss += x[i][e] * x[i][e];
       const float v = row_sum<L>(ss) * (1.0f / D) + a.eps;
       float r = rsqrtf(v), y[VE];
-      if (Q8 && kind == 1) {
+      if (Q8 && kind == 1 && v < INFINITY) {
         // Of these only 8 bits stay, but which of two neighbours is nearest can hang on the last
-        // bit: r by a Newton step with its residual exact, and multiplied last.
+        // bit: r by a Newton step with its residual exact, and multiplied last.  (Squares whose sum
+        // leaves fp32 go the other way, whose r = 0 makes zeros; here zero times infinity would
+        // make NaNs.)
         const float h = v * r, rest = fmaf(v, r, -h);
         r = fmaf(0.5f * r, fmaf(-h, r, 1.0f) - rest * r, r);
 #pragma unroll

@@ -552,7 +552,9 @@ int kda_qk_norm_rope_append(const void* query, const void* key, const void* valu
  *   is not specified)
  *   Keys are normed and turned in fp32 and rounded once, to the 8 bits; a number within fp32's
  *   error of the middle between two may become either.  Magnitudes above 448 * 2^119 (2.98e38) are
- *   kept as that.  A row with an infinity or a NaN is kept with b = 255 and stands for NaNs.
+ *   kept as that.  A row with an infinity or a NaN is kept with b = 255 and stands for NaNs.  A key
+ *   whose sum of squares leaves fp32 (elements of 1.6e18 and more) is kept as zeros, which is what
+ *   kda_qk_norm_rope_append makes of it.
  *
  *   k_cache, v_cache [num_pages, Hkv, page_size, D] 8-bit numbers
  *   k_scale, v_scale [num_pages, Hkv, page_size]    the bytes b

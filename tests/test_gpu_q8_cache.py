@@ -684,3 +684,41 @@ def test_graphs_that_share_a_workspace(tokens, D):
         graphs[i].replay()
         torch.cuda.synchronize()
         assert torch.equal(ds[i]["out"], want[i])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("R", [0, 32])
+def test_keys_whose_squares_leave_fp32(dt, D, R):
+    """Finite keys whose sum of squares overflows: 1 / rms is zero, so they become rows of zeros, as
+    kda_qk_norm_rope_append makes them; 255 is for rows that hold an infinity or a NaN.  A row of
+    1e18 at the head's last element alone, whose square does not overflow, is normed."""
+    rng = np.random.default_rng(3)
+    rows = [np.full(D, 3.3e38), np.full(D, -3e38), rng.standard_normal(D) * 1e30,
+            np.r_[np.zeros(D - 1), 3e19], np.r_[-2e38, np.ones(D - 1)], np.r_[np.zeros(D - 1), 1e18],
+            np.r_[np.full(D - 1, 3e38), np.inf], np.r_[np.nan, np.full(D - 1, 3e38)],
+            np.full(D, -np.inf), rng.standard_normal(D)]
+    k = torch.from_numpy(np.stack(rows)[:, None]).to("cuda", DT[dt])
+    T = len(rows)
+    a = append(T, 2, 1, D, R, 16, dt, False, k=k, seed=11)
+    kc, vc = (torch.full((a["pages"], 1, 16, D), 7.0, dtype=DT[dt], device="cuda")
+              for _ in range(2))
+    kda.kda_qk_norm_rope_append(*a["head"], torch.empty_like(a["qo"]), kc, vc, *a["tail"], **a["kw"])
+    want = host(kc)[:, 0].reshape(-1, D)
+    got = q8_ref.value(raw(a["kb"]), raw(a["ks"]))[:, 0].reshape(-1, D)
+    byte = raw(a["ks"])[:, 0].reshape(-1)
+    slots = a["slots"].tolist()
+    assert sum(0 <= s < a["pages"] * 16 for s in slots) == T - 2
+    for t, s in enumerate(slots):
+        if not 0 <= s < a["pages"] * 16:
+            continue
+        if t < 5:
+            assert (want[s] == 0).all() and (got[s] == 0).all() and byte[s] == q8_ref.LO + 127
+        elif t in (6, 7, 8):
+            assert byte[s] == 255 and not np.isfinite(want[s]).all()
+        else:
+            # one rounding to e4m3 (2^-4), one to bf16 (2^-8), and fp32's of norm and rotation
+            lim = (2.0 ** -4 + 2.0 ** -8 + 2.0 ** -15) * np.abs(want[s]) + 2.0 ** -9 * \
+                2.0 ** (int(byte[s]) - 127) + (D + 24) * 2.0 ** -24 * np.abs(want[s]).max()
+            assert byte[s] != 255 and np.abs(want[s]).max() > 0.1
+            assert (np.abs(got[s] - want[s]) <= lim).all()
