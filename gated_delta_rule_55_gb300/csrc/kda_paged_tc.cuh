@@ -116,6 +116,11 @@ template <bool Q8> struct Group {
 // behind 8192 keys in 8 bits whose magnitudes vary by e^0.7 took 1003 us.  Calls of bf16 pages
 // without prefixes keep the 2^8 that their results were made with.
 template <bool Q8, bool PRE> constexpr float kRescaleOf = Q8 || PRE ? 40.0f : 8.0f;
+// Direct keys (8 bits, D = 128): scores of e4m3 rows, up to 448^2 128 < 2^25, are multiplied by
+// their keys' scales, up to 2^119, before the query row's own scale, so the keys' are kept 2^16
+// lower and the rows' 2^16 higher: keys of all magnitudes stay inside fp32, the smallest scale
+// (2^-110) a normal number.
+constexpr float kKeyDown = 0x1p-16f, kRowUp = 0x1p16f;
 // How far (log2) above the first 32 keys' maximum the standing one starts.
 template <bool Q8, bool PRE> constexpr float kAheadOf = Q8 || PRE ? 16.0f : 0.0f;
 
@@ -440,7 +445,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
         wait_or_die(&bars.raw_full[from.at], from.phase, dead);
         const uint32_t byte = small.scales[from.at * kKeys + r];
         if (KD && o.is_key(e)) {
-          sKeyScale[to.at * kKeys + r] = q8::scale(byte);
+          sKeyScale[to.at * kKeys + r] = q8::scale(byte) * kKeyDown;
         } else {
           const q8::Scale16 sc(byte);
           uint8_t* dst = sKV + (KD ? to.at - NS : to.at) * C::kStageBytes;
@@ -902,9 +907,12 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 
       // 1. The unit's tiles.
       if (KD) {  // with the power of two of the row's terms
-        sc = a.scale * kLog2E *
-             __ldg(a.q_scale + (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G));
+        const float x = a.scale * kLog2E;
+        const float y =
+            __ldg(a.q_scale + (long long)(w.bos + tk) * a.Hq + w.h * a.G + (row - tk * a.G));
+        sc = x > 1.f ? x * y * kRowUp : x * kRowUp * y;  // (neither order leaves fp32 on the way)
         if (sc < 1.2e-38f) sc = 1.2e-38f;  // (zero times a hidden key's -inf would be NaN)
+        if (sc > 3.4e38f) sc = 3.4e38f;    // (and infinity times a score of zero)
       }
       float m = -INFINITY, l = 0.f;
       int mine = 0;

@@ -666,8 +666,9 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N or total_T grows.
  *   bf16 with D >= 64 may multiply queries in two terms of 8 bits, which are off by at most 2^-17
  *   of the row's largest element where an element is less than 2^-9 of it, and exact otherwise
- *   (rows below 2^-102 aside); bf16's running maximum absorbs a growth of 2^40, so that values
- *   above 2^80 may overflow on the way (kda_paged_attention_fwd: 2^8).
+ *   (rows below 2^-102 aside); there a query's elements times softmax_scale must stay below 2^119.
+ *   bf16's running maximum absorbs a growth of 2^40, so that values above 2^80 may overflow on the
+ *   way (kda_paged_attention_fwd: 2^8).
  */
 size_t kda_paged_attention_q8_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
                                                  int dtype);

@@ -12,6 +12,7 @@ pytestmark = pytest.mark.gpu
 import gated_delta_rule_55_gb300 as kda  # noqa: E402
 import q8_ref  # noqa: E402
 import test_gpu_paged_attention as pa  # noqa: E402
+import test_gpu_q8_cache as q8_cache  # noqa: E402
 from gpu_helpers import ensure_built  # noqa: E402
 
 DT = pa.DT
@@ -364,4 +365,30 @@ def test_a_call_without_tokens_has_ended_before_what_follows(D, q8):
         assert (ws == 0x5A).all() and (d["out"] == 7).all()
         call(d, ws=ws)
         assert torch.equal(d["out"], want)
+    assert kda.kda_device_error() == 0
+
+
+@pytest.mark.parametrize("k,q", q8_cache.EXTREMES)
+@pytest.mark.parametrize("tokens", [2, 200])
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_of_all_magnitudes(D, tokens, k, q):
+    """test_gpu_q8_cache.py's, behind prefixes that are shared (2 tokens) or taken along (200)."""
+    d = make([500, 90], [(tokens, 300), (tokens, tokens), (tokens, 300)], 4, 1, D, 64, "bf16", True,
+             groups=[0, 2, 3], seed=22)
+    b, s, sign = q8_cache.keys_of_one_magnitude(d["kc"].shape, k, 6)
+    k = float(q8_ref.value(b, s).max())
+    d["kc"] = torch.from_numpy(b).cuda().view(torch.float8_e4m3fn)
+    d["ks"] = torch.from_numpy(s).cuda()
+    d["q"].fill_(q)
+    call(d)
+    out, lse = host(d["out"]), host(d["lse"])
+    for n, (g, p) in enumerate([(0, 500), (0, 500), (1, 90)]):
+        kv, t0 = int(d["kv_h"][n]), int(d["cu_h"][n])
+        sg, v = (np.concatenate([q8_ref.rows_of(x, d["pt_h"][g], p, 64)[:, 0],
+                                 q8_ref.rows_of(x, d["table_h"][n], kv, 64)[:, 0]])
+                 for x in (sign, d["vx"]))
+        for i in range(tokens):
+            m = p + kv - tokens + i + 1
+            for h in range(4):
+                q8_cache.check_one_magnitude(out[t0 + i, h], lse[t0 + i, h], k, q, sg[:m], v[:m], D)
     assert kda.kda_device_error() == 0

@@ -722,3 +722,56 @@ def test_keys_whose_squares_leave_fp32(dt, D, R):
                 2.0 ** (int(byte[s]) - 127) + (D + 24) * 2.0 ** -24 * np.abs(want[s]).max()
             assert byte[s] != 255 and np.abs(want[s]).max() > 0.1
             assert (np.abs(got[s] - want[s]) <= lim).all()
+
+
+EXTREMES = [(2.0 ** 114, 2.0 ** -102), (2.98e38, 2.0 ** -102), (2.0 ** 100, 2.0 ** -90),
+            (2.0 ** -110, 2.0 ** 122)]
+
+
+def keys_of_one_magnitude(shape, k, seed):
+    """Rows of one number, k or -k, in 8 bits: (numbers, scale bytes, signs [pages, Hkv, page])."""
+    sign = np.where(np.random.default_rng(seed).random(shape[:3]) < 0.5, -1.0, 1.0)
+    b, s = q8_ref.quantise(np.broadcast_to(sign[..., None] * k, shape))
+    return b, s, sign
+
+
+def check_one_magnitude(out, lse, k, q, sign, V, D):
+    """One query row of elements q against keys of k sign_j: scores are +-S, S = q k sqrt(D) of 2^15 or
+    more, so the result is the mean of the values of the visible keys with the larger score.  A
+    score in log2 has an error of up to 8 roundings (products, maxima, joined parts): the weights of
+    equal ones differ by that at most, and a mean of any weights lies between its values."""
+    S = q * k * D ** 0.5
+    best = sign == sign.max()
+    v, err = V[best], 2.0 ** -21 * S * 1.4427
+    A = np.abs(v).mean(0)
+    slack = 2.0 ** -7 * (A + np.abs(v).max(0) * 2.0 ** -8)
+    assert np.isfinite(out).all()
+    assert (out >= v.min(0) - slack).all() and (out <= v.max(0) + slack).all()
+    if err < 0.1:
+        assert (np.abs(out - v.mean(0)) <= 2 * err * A + 2.0 ** -8 * (A + np.abs(v.mean(0)))).all()
+    want = sign.max() * S + np.log(best.sum())
+    assert abs(lse - want) <= 2.0 ** -19 * S + 1e-3
+
+
+@pytest.mark.parametrize("k,q", EXTREMES)
+@pytest.mark.parametrize("tokens", [1, 6, 150])
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 128)])
+def test_keys_of_all_magnitudes(dt, D, tokens, k, q):
+    """Keys up to the largest that a row can hold beside small queries, and the other way round: their
+    products are in range, so no way to them may leave it."""
+    d = make([(tokens, 700), (tokens, tokens), (tokens, 300)], 4, 1, D, 64, dt, seed=21)
+    b, s, sign = keys_of_one_magnitude(d["kb"].shape, k, 5)
+    k = float(q8_ref.value(b, s).max())
+    d["kb"], d["ks"] = e4m3(b), torch.from_numpy(s).cuda()
+    d["q"].fill_(q)
+    call(d)
+    out, lse, V = host(d["out"]), host(d["lse"]), host(d["vc"])
+    for n in range(3):
+        kv, t0 = int(d["kv_h"][n]), int(d["cu_h"][n])
+        sg = q8_ref.rows_of(sign, d["table_h"][n], kv, 64)[:, 0]
+        v = q8_ref.rows_of(V, d["table_h"][n], kv, 64)[:, 0]
+        for i in range(tokens):
+            m = kv - tokens + i + 1
+            for h in range(4):
+                check_one_magnitude(out[t0 + i, h], lse[t0 + i, h], k, q, sg[:m], v[:m], D)
+    assert kda.kda_device_error() == 0
