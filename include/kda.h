@@ -667,8 +667,8 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   bf16 with D >= 64 may multiply queries in two terms of 8 bits, which are off by at most 2^-17
  *   of the row's largest element where an element is less than 2^-9 of it, and exact otherwise
  *   (rows below 2^-102 aside); there a query's elements times softmax_scale must stay below 2^119.
- *   bf16's running maximum absorbs a growth of 2^40, so that values above 2^80 may overflow on the
- *   way (kda_paged_attention_fwd: 2^8).
+ *   bf16's running maximum absorbs a growth of 2^32, so that results may overflow on the way where
+ *   the largest value times the keys seen passes 2^95 (kda_paged_attention_fwd: 2^8, 2^119).
  */
 size_t kda_paged_attention_q8_fwd_workspace_size(int N, int total_T, int Hq, int Hkv, int D,
                                                  int dtype);

@@ -392,3 +392,27 @@ def test_keys_of_all_magnitudes(D, tokens, k, q):
             for h in range(4):
                 q8_cache.check_one_magnitude(out[t0 + i, h], lse[t0 + i, h], k, q, sg[:m], v[:m], D)
     assert kda.kda_device_error() == 0
+
+
+@pytest.mark.parametrize("top", q8_cache.RISES)
+@pytest.mark.parametrize("at", [40, 700])
+@pytest.mark.parametrize("D,q8,large", [(64, True, 2.0 ** 84), (128, True, 2.0 ** 84)])
+def test_large_values_under_rising_scores(D, q8, large, at, top):
+    """test_gpu_q8_cache.py's, behind prefixes, shared and taken along: a growth of what the call
+    absorbs over values that leave room for it and the keys (less than 2^11)."""
+    i32 = q8_cache.i32
+    for tokens, Hkv in ((2, 80), (200, 24)):
+        r = q8_cache.Rise([1200, 300, 500, 800, 600], Hkv, D, top, at, large, q8)
+        q, cu, out, lse = r.queries([tokens] * 3, 4)
+        a = (2, 3, len(q), 4 * Hkv, Hkv, D)
+        ws = torch.empty(kda.kda_paged_prefix_attention_fwd_workspace_size(*a), dtype=torch.uint8,
+                         device="cuda")
+        w = r.table.shape[1]
+        kda.kda_paged_prefix_attention_fwd(
+            q, r.kc, r.vc, i32(r.table[:2]), i32(r.lists[:2]), i32([0, 2, 3]), i32(r.table[2:]),
+            i32(cu), i32(r.lists[2:]), out, *a, r.pages, 64, w, w, k_scale=r.ks, v_scale=r.vs,
+            lse=lse, softmax_scale=q8_cache.LN2, workspace=ws)
+        for n, g in enumerate([0, 0, 1]):
+            rows = [np.concatenate(x) for x in zip(r.of(g), r.of(2 + n))]
+            q8_cache.check_rise(out[cu[n]:cu[n + 1]], lse[cu[n]:cu[n + 1]], *rows, D)
+    assert kda.kda_device_error() == 0

@@ -775,3 +775,93 @@ def test_keys_of_all_magnitudes(dt, D, tokens, k, q):
             for h in range(4):
                 check_one_magnitude(out[t0 + i, h], lse[t0 + i, h], k, q, sg[:m], v[:m], D)
     assert kda.kda_device_error() == 0
+
+
+RISES = [15.0, 30.0, 36.0, 44.0, 48.0, 52.0, 56.0, 60.0, 72.0]
+LN2 = float(np.float32(np.log(2)))
+
+
+class Rise:
+    """Lists of keys in pages of 64 whose scores, in log2, are 0 and from key `at` of each list on
+    `top`, the same for every query, and whose values are `large` times 1/2 to 1: the largest sums
+    that values can have.  In 8 bits, or (q8 False) in bf16."""
+
+    def __init__(self, lists, Hkv, D, top, at, large, q8=True):
+        ensure_built()
+        need, rng = [-(-n // 64) for n in lists], np.random.default_rng(7)
+        self.lists, self.Hkv, self.D, self.pages = lists, Hkv, D, sum(need)
+        self.table = np.zeros((len(lists), max(need)), np.int32)
+        k = np.zeros((self.pages, Hkv, 64, 1))
+        for i, m in enumerate(need):
+            self.table[i, :m] = sum(need[:i]) + np.arange(m)
+            j = np.arange(64 * m).reshape(m, 1, 64, 1)
+            k[self.table[i, :m]] = np.where(j < at, 0.0, top)
+        x = {"k": k, "v": rng.uniform(0.5, 1.0, k.shape) * large}
+        for n in "kv":
+            shape = (*k.shape[:3], D)
+            if q8:
+                b, s = q8_ref.quantise(x[n])
+                x[n] = q8_ref.value(b, s)
+                full, s = torch.zeros(shape, dtype=torch.uint8), torch.from_numpy(s).cuda()
+                b = torch.from_numpy(b)
+            else:
+                b, s = torch.from_numpy(x[n]).to(torch.bfloat16), None
+                x[n] = host(b)
+                full = torch.zeros(shape, dtype=torch.bfloat16)
+            full[..., :1 if n == "k" else D] = b  # keys: all in the first column
+            setattr(self, n + "c", full.cuda().view(torch.float8_e4m3fn) if q8 else full.cuda())
+            setattr(self, n + "s", s)
+        self.x = x
+
+    def of(self, i):
+        """Scores and values [keys, Hkv] of a list."""
+        return [q8_ref.rows_of(self.x[n], self.table[i], self.lists[i], 64)[..., 0] for n in "kv"]
+
+    def queries(self, tokens, G):
+        """Queries whose score is a key's first element, offsets, and places for the results."""
+        cu = np.concatenate([[0], np.cumsum(tokens)])
+        q = torch.zeros(cu[-1], G * self.Hkv, self.D, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 0] = 1
+        return q, cu, torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+
+
+def check_rise(out, lse, k, v, D):
+    """A sequence's tokens, [tokens, Hq, D], against sums along its scores and values.  Tolerances as
+    test_gpu_paged_attention.compare's."""
+    k, v, tokens = torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), out.shape[0]
+    out = out.double().view(tokens, k.shape[1], -1, D)  # [tokens, Hkv, G, D]
+    p = torch.exp2(k - k.max())
+    l, o = (x.cumsum(0)[-tokens:] for x in (p, p * v))
+    want = (o / l)[:, :, None, None]
+    dl = (D + 8) * 2.0 ** -24 * float(k.max()) * LN2
+    lim = 2 * dl + (len(k) + 64) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -7
+    bad = ~((out - want).abs() <= lim * want)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3], out[bad][:3])
+    want = (float(k.max()) * LN2 + l.log())[:, :, None]
+    lse = lse.double().view(tokens, k.shape[1], -1)
+    assert ((lse - want).abs() <= dl + 2.0 ** -22 * (want.abs() + 3 + len(k) / 16)).all()
+
+
+def i32(x):
+    return torch.from_numpy(np.asarray(x, np.int32)).cuda()
+
+
+@pytest.mark.parametrize("at,top,large", [(at, top, 2.0 ** 84) for at in (40, 700) for top in RISES] +
+                         [(40, top, 2.0 ** -107) for top in (0.0, 15.0, 60.0)])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_large_values_under_rising_scores(D, at, top, large):
+    """Scores that rise by 2^top at once, up to what the standing maximum absorbs and beyond, over
+    1500 (less than 2^11) values of up to 2^84: nothing overflows on the way.  Many heads, so that
+    one block has most of a row's keys.  And over the smallest values."""
+    for tokens, Hkv in (([1, 2], 100), ([12, 16], 100), ([130, 200], 50)):
+        r = Rise([1500, 1400], Hkv, D, top, at, large)
+        q, cu, out, lse = r.queries(tokens, 2)
+        ws = torch.empty(kda.kda_paged_attention_q8_fwd_workspace_size(2, len(q), 2 * Hkv, Hkv, D),
+                         dtype=torch.uint8, device="cuda")
+        kda.kda_paged_attention_q8_fwd(
+            q, r.kc, r.vc, r.ks, r.vs, i32(r.table), i32(cu), i32(r.lists), out, 2, len(q),
+            2 * Hkv, Hkv, D, r.pages, 64, r.table.shape[1], lse=lse, softmax_scale=LN2,
+            workspace=ws)
+        for n in range(2):
+            check_rise(out[cu[n]:cu[n + 1]], lse[cu[n]:cu[n + 1]], *r.of(n), D)
+    assert kda.kda_device_error() == 0
