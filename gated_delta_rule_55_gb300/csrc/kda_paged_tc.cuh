@@ -114,15 +114,15 @@ template <bool Q8> struct Group {
 // overflow: 2^32 leaves values times keys seen of 2^95 (values of 2^80 and 2^15 keys).  Keys of
 // different magnitudes outgrow 2^8 in some row of a warp every few tiles, and such a tile goes the
 // long way: 2 chunks of 2048 tokens behind 8192 keys in 8 bits whose magnitudes vary by e^0.7 took
-// 1003 us.  Calls of bf16 pages without prefixes keep the 2^8 that their results were made with.
-template <bool Q8, bool PRE> constexpr float kRescaleOf = Q8 || PRE ? 32.0f : 8.0f;
+// 1003 us.  bf16 pages, whose values may be larger, keep to 2^8, with prefixes as without.
+template <bool Q8> constexpr float kRescaleOf = Q8 ? 32.0f : 8.0f;
 // Direct keys (8 bits, D = 128): scores of e4m3 rows, up to 448^2 128 < 2^25, are multiplied by
 // their keys' scales, up to 2^119, before the query row's own scale, so the keys' are kept 2^16
 // lower and the rows' 2^16 higher: keys of all magnitudes stay inside fp32, the smallest scale
 // (2^-110) a normal number.
 constexpr float kKeyDown = 0x1p-16f, kRowUp = 0x1p16f;
 // How far (log2) above the first 32 keys' maximum the standing one starts.
-template <bool Q8, bool PRE> constexpr float kAheadOf = Q8 || PRE ? 24.0f : 0.0f;
+template <bool Q8> constexpr float kAheadOf = Q8 ? 24.0f : 0.0f;
 
 template <int D, bool Q8> struct Cfg {
   // 8 bits and D = 128: keys are products' operands as they land (kDirect), in a ring of their own;
@@ -331,7 +331,7 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
   constexpr int NS = C::kStages, RB = C::kRowBytes, HALVES = D * 2 / RB;
   constexpr int NL = Q8 ? C::kRawStages : NS;  // stages of the ring that tiles land in
   constexpr bool KD = C::kDirect;
-  constexpr float kRescale = kRescaleOf<Q8, PRE>, kAhead = kAheadOf<Q8, PRE>;
+  constexpr float kRescale = kRescaleOf<Q8>, kAhead = kAheadOf<Q8>;
   constexpr int kThreads = Group<Q8>::kThreads, kFront = C::kFront;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   float2* s_ml = reinterpret_cast<float2*>(smem_raw);  // [2][128]: m, l of the units' rows

@@ -705,7 +705,8 @@ int kda_paged_attention_q8_fwd(const void* query, const void* k_cache, const voi
  *   at max_prefix_pages + max_pages, and adds those of num_groups sequences of all tokens at
  *   max_prefix_pages.  num_groups at most 65535.  With groups, max_pages page_size and
  *   max_prefix_pages page_size are at most 2^31 - 128, max_prefix_pages page_size + total_T below
- *   2^31 (KDA_ERR_TOO_LARGE).  All else as for kda_paged_attention_fwd.
+ *   2^31 (KDA_ERR_TOO_LARGE).  All else as for kda_paged_attention_fwd, or over pages in 8 bits for
+ *   kda_paged_attention_q8_fwd.
  *   workspace    at least kda_paged_prefix_attention_fwd_workspace_size(num_groups, N, total_T, Hq,
  *                Hkv, D, dtype) bytes, 256-byte aligned; the size never decreases as num_groups,
  *                N or total_T grows.

@@ -394,9 +394,10 @@ def test_keys_of_all_magnitudes(D, tokens, k, q):
     assert kda.kda_device_error() == 0
 
 
-@pytest.mark.parametrize("top", q8_cache.RISES)
+@pytest.mark.parametrize("q8,top,large", [(True, top, 2.0 ** 84) for top in q8_cache.RISES] +
+                         [(False, top, 2.0 ** 108) for top in (7.0, 9.0, 30.0, 44.0, 52.0, 72.0)])
 @pytest.mark.parametrize("at", [40, 700])
-@pytest.mark.parametrize("D,q8,large", [(64, True, 2.0 ** 84), (128, True, 2.0 ** 84)])
+@pytest.mark.parametrize("D", [32, 64, 128])
 def test_large_values_under_rising_scores(D, q8, large, at, top):
     """test_gpu_q8_cache.py's, behind prefixes, shared and taken along: a growth of what the call
     absorbs over values that leave room for it and the keys (less than 2^11)."""
