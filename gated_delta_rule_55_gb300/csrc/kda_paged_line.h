@@ -37,8 +37,8 @@ KDA_LINE_FN int stretch_of(int total, int unit) {
                                : more + (unit - more * (q + 1)) / (q > 1 ? q : 1);
 }
 
-// The first row of a warp of the kernel that joins rows, eight warps a block with `per` rows each, in
-// 64 bits: a call of up to 2^31 - 1 rows has more than 2^24 blocks, whose threads, counted in 32
+// The first row of a warp of the kernel that joins rows, eight warps a block with `per` rows each,
+// in 64 bits: a call of up to 2^31 - 1 rows has more than 2^24 blocks, whose threads, counted in 32
 // bits, would begin again at the first rows.  (May lie behind the last row.)
 KDA_LINE_FN long long first_row(unsigned block, int warp, int per) {
   return ((long long)block * 8 + warp) * per;

@@ -524,7 +524,7 @@ paged_q8_few_kernel(PagedArgs a, const __grid_constant__ CUtensorMap kmap,
             w = *reinterpret_cast<const uint4*>(slot + kLand + raw_offset<D>(r, c + 1));
           uint32_t y[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q8::expand4<false>(x[k], one, y[2 * k], y[2 * k + 1]);
+          for (int k = 0; k < 4; ++k) q8::expand4(x[k], one, y[2 * k], y[2 * k + 1]);
           *reinterpret_cast<uint4*>(slot + piece_offset<D>(r, 2 * c)) =
               make_uint4(y[0], y[1], y[2], y[3]);
           *reinterpret_cast<uint4*>(slot + piece_offset<D>(r, 2 * c + 1)) =

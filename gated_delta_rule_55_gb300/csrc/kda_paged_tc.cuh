@@ -464,9 +464,9 @@ paged_tc_kernel(PagedArgs a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (KD)  // (values: their columns change places)
-                q8::expand4<false>(x[k], sc, y[2 * k], y[2 * k + 1]);
+                q8::expand4(x[k], sc, y[2 * k], y[2 * k + 1]);
               else
-                q8::expand4_in_order<false>(x[k], sc, y[2 * k], y[2 * k + 1]);
+                q8::expand4_in_order(x[k], sc, y[2 * k], y[2 * k + 1]);
             }
             if (big)
 #pragma unroll
@@ -1352,8 +1352,8 @@ __global__ void __launch_bounds__(256) paged_rows_kernel(PagedArgs a, Rows rows,
   };
   bool grouped = false;
   const bool live = first < all && (per > 1 || owned((int)first, grouped));
-  // launched while the first kernel runs: wait for its results.  (Without rows too: were every block
-  // gone before the first kernel's end, what follows in the stream could begin beside it.)
+  // launched while the first kernel runs: wait for its results.  (Without rows too: were every
+  // block gone before the first kernel's end, what follows in the stream could begin beside it.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
   unsigned open = 1;  // rows that are not done

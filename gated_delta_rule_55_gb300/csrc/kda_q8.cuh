@@ -70,34 +70,24 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 // Four numbers (a register of them) as two registers of bf16 pairs: the first and third, the second
-// and fourth (place()).  In this order a number's
-// bits move by the same distance in both halves of a register, and half of the moves are products
-// by powers of two, which pass beside the logic operations.  BIG: the second product too.
-template <bool BIG>
+// and fourth (place()).  In this order a number's bits move by the same distance in both halves of a
+// register, and half of the moves are products by powers of two, which pass beside the logic
+// operations.  (The first product: a caller that may meet big scales makes the second.)
 __device__ __forceinline__ void expand4(uint32_t w, const Scale16& s, uint32_t& even,
                                         uint32_t& odd) {
   constexpr uint32_t kSign = 0x80008000u, kRest = 0x07f007f0u;
   even = mul_bf16x2((w * 256u & kSign) | (w * 16u & kRest), s.m);
   odd = mul_bf16x2((w & kSign) | (w >> 4 & kRest), s.m);
-  if (BIG) {
-    even = mul_bf16x2(even, s.more);
-    odd = mul_bf16x2(odd, s.more);
-  }
 }
 __device__ __forceinline__ constexpr int place(int i) {  // of number i among the results
   return (i & ~3) | (i & 1) << 1 | (i >> 1 & 1);
 }
 
-template <bool BIG>
 __device__ __forceinline__ void expand4_in_order(uint32_t w, const Scale16& s, uint32_t& lo,
                                                  uint32_t& hi) {
   const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);  // b << 8
   lo = mul_bf16x2((x & 0x80008000u) | (x >> 4 & 0x07f007f0u), s.m);
   hi = mul_bf16x2((y & 0x80008000u) | (y >> 4 & 0x07f007f0u), s.m);
-  if (BIG) {
-    lo = mul_bf16x2(lo, s.more);
-    hi = mul_bf16x2(hi, s.more);
-  }
 }
 
 }  // namespace q8

@@ -695,7 +695,8 @@ def test_keys_whose_squares_leave_fp32(dt, D, R):
     1e18 at the head's last element alone, whose square does not overflow, is normed."""
     rng = np.random.default_rng(3)
     rows = [np.full(D, 3.3e38), np.full(D, -3e38), rng.standard_normal(D) * 1e30,
-            np.r_[np.zeros(D - 1), 3e19], np.r_[-2e38, np.ones(D - 1)], np.r_[np.zeros(D - 1), 1e18],
+            np.r_[np.zeros(D - 1), 3e19], np.r_[-2e38, np.ones(D - 1)],
+            np.r_[np.zeros(D - 1), 1e18],
             np.r_[np.full(D - 1, 3e38), np.inf], np.r_[np.nan, np.full(D - 1, 3e38)],
             np.full(D, -np.inf), rng.standard_normal(D)]
     k = torch.from_numpy(np.stack(rows)[:, None]).to("cuda", DT[dt])
@@ -703,7 +704,8 @@ def test_keys_whose_squares_leave_fp32(dt, D, R):
     a = append(T, 2, 1, D, R, 16, dt, False, k=k, seed=11)
     kc, vc = (torch.full((a["pages"], 1, 16, D), 7.0, dtype=DT[dt], device="cuda")
               for _ in range(2))
-    kda.kda_qk_norm_rope_append(*a["head"], torch.empty_like(a["qo"]), kc, vc, *a["tail"], **a["kw"])
+    kda.kda_qk_norm_rope_append(*a["head"], torch.empty_like(a["qo"]), kc, vc, *a["tail"],
+                                **a["kw"])
     want = host(kc)[:, 0].reshape(-1, D)
     got = q8_ref.value(raw(a["kb"]), raw(a["ks"]))[:, 0].reshape(-1, D)
     byte = raw(a["ks"])[:, 0].reshape(-1)
@@ -736,8 +738,8 @@ def keys_of_one_magnitude(shape, k, seed):
 
 
 def check_one_magnitude(out, lse, k, q, sign, V, D):
-    """One query row of elements q against keys of k sign_j: scores are +-S, S = q k sqrt(D) of 2^15 or
-    more, so the result is the mean of the values of the visible keys with the larger score.  A
+    """One query row of elements q against keys of k sign_j: scores are +-S, S = q k sqrt(D) of 2^13
+    or more, so the result is the mean of the values of the visible keys with the larger score.  A
     score in log2 has an error of up to 8 roundings (products, maxima, joined parts): the weights of
     equal ones differ by that at most, and a mean of any weights lies between its values."""
     S = q * k * D ** 0.5
@@ -757,8 +759,8 @@ def check_one_magnitude(out, lse, k, q, sign, V, D):
 @pytest.mark.parametrize("tokens", [1, 6, 150])
 @pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 128)])
 def test_keys_of_all_magnitudes(dt, D, tokens, k, q):
-    """Keys up to the largest that a row can hold beside small queries, and the other way round: their
-    products are in range, so no way to them may leave it."""
+    """Keys up to the largest that a row can hold beside small queries, and the other way round:
+    their products are in range, so no way to them may leave it."""
     d = make([(tokens, 700), (tokens, tokens), (tokens, 300)], 4, 1, D, 64, dt, seed=21)
     b, s, sign = keys_of_one_magnitude(d["kb"].shape, k, 5)
     k = float(q8_ref.value(b, s).max())
@@ -826,8 +828,8 @@ class Rise:
 
 
 def check_rise(out, lse, k, v, D):
-    """A sequence's tokens, [tokens, Hq, D], against sums along its scores and values.  Tolerances as
-    test_gpu_paged_attention.compare's."""
+    """A sequence's tokens, [tokens, Hq, D], against sums along its scores and values.  Tolerances
+    as test_gpu_paged_attention.compare's."""
     k, v, tokens = torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), out.shape[0]
     out = out.double().view(tokens, k.shape[1], -1, D)  # [tokens, Hkv, G, D]
     p = torch.exp2(k - k.max())
@@ -846,7 +848,8 @@ def i32(x):
     return torch.from_numpy(np.asarray(x, np.int32)).cuda()
 
 
-@pytest.mark.parametrize("at,top,large", [(at, top, 2.0 ** 84) for at in (40, 700) for top in RISES] +
+@pytest.mark.parametrize("at,top,large",
+                         [(at, top, 2.0 ** 84) for at in (40, 700) for top in RISES] +
                          [(40, top, 2.0 ** -107) for top in (0.0, 15.0, 60.0)])
 @pytest.mark.parametrize("D", [32, 64, 128])
 def test_large_values_under_rising_scores(D, at, top, large):

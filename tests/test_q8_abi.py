@@ -166,8 +166,8 @@ def test_binding_refuses_other_types():
 
 
 def test_lists_whose_positions_would_pass_31_bits(L):  # noqa: F811
-    """A list of 2^31 - 1 keys has a tile that ends at 2^31, and a token behind a prefix of that many
-    the position 2^31 - 2 + its number: both would wrap."""
+    """A list of 2^31 - 1 keys has a tile that ends at 2^31, and a token behind a prefix of that
+    many the position 2^31 - 2 + its number: both would wrap."""
     page = 16
     most = (2 ** 31 - 128) // page
     for dtype in (0, 1):
