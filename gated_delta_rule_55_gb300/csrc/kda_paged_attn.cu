@@ -47,6 +47,13 @@ cudaError_t launch_paged_tc(const PagedArgs& a, void* workspace, cudaStream_t st
   // By the rows of a sequence on average, items of 16, of 32 or of 256 rows.  64 sequences, 32 + 8
   // heads: D = 128, 16 rows 113 us for 241 (items of 32, 20 rows: 172 for 253 with items of 16), 32
   // rows 176 for 241, 36 rows 244; D = 64, 4 rows 82 for 161, 20 rows 136, 32 rows 147 for 162.
+  // The lengths lie in device memory, so the host has only the average, and one kernel takes all
+  // sequences of a call.  Where they are of two kinds that costs one of them, D = 128: 64 single
+  // tokens over 512..8192 keys with a chunk of 512 behind 8192 (35 rows on average: tiles of 256
+  // rows) 335 us, alone 110 and 80, over bf16 pages 281; 200 single tokens with that chunk (14
+  // rows: items of 16, for each of which the chunk's keys are read again) 641, alone 291 and 80,
+  // bf16 673; 255 over 100..1000 keys with a chunk of 1700 behind 4096 (31 rows: items of 32) 825,
+  // alone 76 and 148, bf16 236.  Two calls, one for each kind, take the sum of what they take alone.
   // Smaller items are more of them, whose line has to fit the indices as well (paged_tc_index_ok).
   const long long rows = (long long)a.total_T * (a.Hq / a.Hkv);
   const double line =

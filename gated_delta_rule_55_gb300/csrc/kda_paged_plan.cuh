@@ -62,6 +62,13 @@ struct Geometry {
 // its neighbours: its sequences take the prefix along with their own keys, as one list of tiles,
 // and there is nothing to join.  (2300 tokens of 8 sequences behind 8191 keys, 32 + 8 heads of 128:
 // 250 us when their prefix was worked on for all of them.)
+//
+// Sequences of 256, 512, 768, 1024 rows, prefix taken along / shared, us: 8 sequences behind 8191
+// keys, D = 128, 68 / 73, 114 / 132, 158 / 194, 200 / 254; behind 2000 keys 41 / 45, 53 / 71, 68 /
+// 101, 83 / 130; 3 sequences behind 4000 keys 36 / 30, 40 / 44, 52 / 59, 63 / 74; 8 behind 4000, D =
+// 64, 39 / 58, 60 / 100, 82 / 139, 102 / 181; over 8-bit pages 60 / 67, 97 / 116, 129 / 171, 164 /
+// 224.  So between 512 rows and the border sharing costs 10 to 40%; a prefix taken along is read
+// once for each sequence, which more sequences of fewer rows pay for.
 constexpr int kAlone = 768;
 
 __device__ __forceinline__ bool group_alone(const PagedArgs& a, int g) {

@@ -24,7 +24,7 @@
 // (which are then free only behind the values' product), query rows in one place.
 //
 // What bounds it, and measured (alone on the GPU, 32 + 8 heads): 64 single tokens over 512..8192
-// keys HBM, 97 us, 5.6 TB/s of the 6.8 of a copy (305 through tiles of 128 query rows), 14 of them
+// keys HBM, 97 us, 5.6 TB/s of the 6.8 of a copy (233 through tiles of 128 query rows), 14 of them
 // the start and the join; 16 tokens over 30000 keys 163 us, 6.1 TB/s; 256 tokens over 100..1000
 // keys 77 us, where items' starts and ends count; one token over 1000 keys 11.3 us of latencies in
 // a row.  More rows, over the 512..8192 keys: 4 tokens (16 rows) 113 us, 5 (20 rows) 172, 8 (32)

@@ -666,7 +666,13 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N or total_T grows.
  *   bf16 with D >= 64 may multiply queries in two terms of 8 bits, which are off by at most 2^-17
  *   of the row's largest element where an element is less than 2^-9 of it, and exact otherwise
- *   (rows below 2^-102 aside); there a query's elements times softmax_scale must stay below 2^119.
+ *   (rows below 2^-102 aside); there a query's elements times softmax_scale must stay below 2^119,
+ *   and times a seen key's largest element inside fp32.
+ *   Half of the bytes of bf16 pages.  In bf16 the time is less for single tokens and a few drafted
+ *   ones over long caches, and more where tiles of values are expanded for many query rows: chunks,
+ *   D = 32, 5 to 8 drafted tokens of 4 query heads a kv head with D = 64.  One kernel is chosen for
+ *   a call, by its tokens over its sequences: many single tokens and a long chunk are faster as two
+ *   calls.
  *   bf16's running maximum absorbs a growth of 2^32, so that results may overflow on the way where
  *   the largest value times the keys seen passes 2^95 (kda_paged_attention_fwd: 2^8, 2^119).
  */
