@@ -661,9 +661,9 @@ int kda_paged_attention_fwd(const void* query, const void* k_cache, const void* 
  *   v_scale [num_pages, Hkv, page_size].  query and out stay in dtype.  Rows are expanded exactly,
  *   so the result is that of kda_paged_attention_fwd over the values that the cache stands for; a
  *   seen row with b = 255 makes what sees it NaN.  All other arguments, limits and errors are those
- *   of kda_paged_attention_fwd, and max_pages page_size is at most 2^31 - 128 (KDA_ERR_TOO_LARGE);
- *   the workspace's size is
- *   kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N or total_T grows.
+ *   of kda_paged_attention_fwd, and max_pages page_size is at most 2^31 - 128 (KDA_ERR_TOO_LARGE).
+ *   The workspace's size is kda_paged_attention_q8_fwd_workspace_size's, which never decreases as N
+ *   or total_T grows.
  *   bf16 with D >= 64 may multiply queries in two terms of 8 bits, which are off by at most 2^-17
  *   of the row's largest element where an element is less than 2^-9 of it, and exact otherwise
  *   (rows below 2^-102 aside); there a query's elements times softmax_scale must stay below 2^119,
